@@ -52,6 +52,8 @@ struct DevBuffers {
   void* scan = nullptr;   // two-level scan buffers (its first bytes: an all-zero value tensor)
   size_t scan_bytes = 0;
   size_t scan_zeroed = 0;
+  void* ssm = nullptr;  // gdn_ssm_scan's workspace
+  size_t ssm_bytes = 0;
   cudaStream_t aux = nullptr;  // second stream for pass A's transition run
   cudaEvent_t fork = nullptr, join = nullptr;
   int sms = 0;
@@ -393,6 +395,21 @@ bool take_injected_alloc_failure() {
   while (n > 0 && !g_fail_allocs.compare_exchange_weak(n, n - 1)) {
   }
   return n > 0;
+}
+
+int ensure_ssm_workspace(int dev, size_t need, void** ws) {
+  if (dev < 0 || dev >= kMaxDevices) return GDN_ERR_ARG;
+  std::lock_guard<std::mutex> lock(g_mu);
+  DevBuffers& d = g_dev[dev];
+  const size_t had = d.ssm_bytes;
+  const int rc = ensure(d.ssm, d.ssm_bytes, need);
+  if (rc != GDN_OK) return rc;
+  if (d.ssm_bytes != had) {  // a new allocation: its status words
+    const cudaError_t e = cudaMemset(d.ssm, 0, 256);
+    if (e != cudaSuccess) return set_cuda_error(e, GDN_ERR_LAUNCH);
+  }
+  *ws = d.ssm;
+  return GDN_OK;
 }
 
 }  // namespace gdn
@@ -805,10 +822,12 @@ int gdn_device_status(int* status) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return set_cuda_error(e, GDN_ERR_LAUNCH);
   if (dev < 0 || dev >= kMaxDevices) return GDN_ERR_ARG;
-  void* words[2] = {nullptr, gdn::static_scratch_address(dev)};  // the workspace's, the static array's
+  // the workspaces', the static array's
+  void* words[3] = {nullptr, gdn::static_scratch_address(dev), nullptr};
   {
     std::lock_guard<std::mutex> lock(g_mu);
     words[0] = g_dev[dev].ws;
+    words[2] = g_dev[dev].ssm;
   }
   e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return set_cuda_error(e, GDN_ERR_LAUNCH);
@@ -847,6 +866,7 @@ void gdn_release_workspace(void) {
   if (d.ws) cudaFree(d.ws);
   if (d.stage) cudaFree(d.stage);
   if (d.scan) cudaFree(d.scan);
+  if (d.ssm) cudaFree(d.ssm);
   if (d.fork) cudaEventDestroy(d.fork);
   if (d.join) cudaEventDestroy(d.join);
   if (d.aux) cudaStreamDestroy(d.aux);

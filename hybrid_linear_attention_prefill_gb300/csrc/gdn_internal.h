@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stddef.h>
 
 namespace gdn {
 
@@ -21,5 +22,9 @@ void* static_scratch_address(int dev);
 // Test hook behind gdn_debug_fail_allocations: true when the next library allocation
 // is to fail (and counts it down).
 bool take_injected_alloc_failure();
+
+// gdn_ssm_scan's library-owned workspace on device `dev`, grown to at least `need` bytes (its first
+// 256 bytes are status words, zero when new): GDN_OK or the error code to return.
+int ensure_ssm_workspace(int dev, size_t need, void** ws);
 
 }  // namespace gdn

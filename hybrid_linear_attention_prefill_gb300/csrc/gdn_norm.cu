@@ -1,0 +1,184 @@
+// Root-mean-square norm with the residual's addition, to bf16 or to e4m3 with scales (sm_103a):
+//
+//   r = x + residual,   y = r / sqrt(mean(r^2) + eps) w,
+//   e4m3: scale = max(max |y|, 2^-96) / 448 over a row or a group of columns, q = y / scale.
+//
+// Every element is read and written once for a handful of operations, so HBM bandwidth bounds it
+// (one row: the latency of the loads and of the block's reductions).  A row stays in registers
+// between its two reductions.
+#include <cuda_fp8.h>
+
+#include "gdn_common.cuh"
+
+namespace gdn {
+
+namespace {
+
+__device__ __forceinline__ void widen8(const uint4& r, float (&f)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
+  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+}
+
+constexpr int kNormMinThreads = 128;
+
+}  // namespace
+
+// TPR threads a row (a power of two, 32..1024), VPT vectors of eight columns a thread; vector v of
+// the row belongs to thread v % TPR, so a group of 32, 64 or 128 columns is 4, 8 or 16 consecutive
+// lanes.  Blocks of max(TPR, 128) threads.
+template <int VPT, bool E4M3>
+__global__ void __launch_bounds__(1024)
+gdn_add_norm_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __nv_bfloat16* residual,
+                    const __nv_bfloat16* __restrict__ weight, __nv_bfloat16* residual_out, void* __restrict__ out,
+                    float* __restrict__ scales, int rows, int D, int tpr, int group, int ngroups, float eps) {
+  __shared__ float part[32];
+  __shared__ uint32_t part_max[32];
+  const int nv = D / 8;
+  const int rib = threadIdx.x / tpr, tid = threadIdx.x - rib * tpr;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int wpr = tpr >> 5, w0 = rib * wpr;  // this row's warps in the block
+  const long long row = (long long)blockIdx.x * (blockDim.x / tpr) + rib;
+  const bool live = row < rows;
+
+  float r[VPT][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = tid + j * tpr;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[j][i] = 0.f;
+    if (live && v < nv) {
+      widen8(*reinterpret_cast<const uint4*>(x + row * xs + 8 * v), r[j]);
+      if (residual != nullptr) {
+        float f[8];
+        widen8(*reinterpret_cast<const uint4*>(residual + row * D + 8 * v), f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[j][i] += f[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = tid + j * tpr;
+    if (residual_out != nullptr && live && v < nv) *reinterpret_cast<uint4*>(residual_out + row * D + 8 * v) = narrow8(r[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(r[j][i], r[j][i], ss);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (wpr > 1) {
+    if (lane == 0) part[warp] = ss;
+    __syncthreads();
+    ss = lane < wpr ? part[w0 + lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  }
+  const float rstd = 1.f / sqrtf(ss / (float)D + eps);
+
+  // y in place; its largest magnitude as bits (a NaN's are above every number's, so it stays)
+  uint32_t mx[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = tid + j * tpr;
+    mx[j] = 0;
+    if (live && v < nv) {
+      float w[8];
+      widen8(*reinterpret_cast<const uint4*>(weight + 8 * v), w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        r[j][i] = r[j][i] * rstd * w[i];
+        mx[j] = max(mx[j], __float_as_uint(r[j][i]) & 0x7fffffffu);
+      }
+    }
+  }
+  if constexpr (!E4M3) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = tid + j * tpr;
+      if (live && v < nv)
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + row * D + 8 * v) = narrow8(r[j]);
+    }
+  } else {
+    if (group == 0) {  // one scale a row
+#pragma unroll
+      for (int j = 1; j < VPT; ++j) mx[0] = max(mx[0], mx[j]);
+      mx[0] = __reduce_max_sync(0xffffffffu, mx[0]);
+      if (wpr > 1) {
+        if (lane == 0) part_max[warp] = mx[0];
+        __syncthreads();
+        mx[0] = __reduce_max_sync(0xffffffffu, lane < wpr ? part_max[w0 + lane] : 0u);
+      }
+#pragma unroll
+      for (int j = 1; j < VPT; ++j) mx[j] = mx[0];
+    } else {
+      for (int o = 1; o < group / 8; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) mx[j] = max(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], o));
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = tid + j * tpr;
+      if (!live || v >= nv) continue;
+      // 2^-96 keeps scale and 1 / scale normal numbers; NaN bits compare above it
+      const float scale = __uint_as_float(max(mx[j], __float_as_uint(0x1p-96f))) / 448.f;
+      const float inv = 1.f / scale;
+      uint32_t q[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const __nv_fp8x2_storage_t a =
+            __nv_cvt_float2_to_fp8x2(make_float2(r[j][4 * i] * inv, r[j][4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(
+            make_float2(r[j][4 * i + 2] * inv, r[j][4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+        q[i] = (uint32_t)a | ((uint32_t)b << 16);
+      }
+      *reinterpret_cast<uint2*>(static_cast<unsigned char*>(out) + row * D + 8 * v) = make_uint2(q[0], q[1]);
+      if (group == 0) {
+        if (v == 0) scales[row] = scale;
+      } else if (v % (group / 8) == 0) {
+        scales[row * ngroups + v / (group / 8)] = scale;
+      }
+    }
+  }
+}
+
+template <int VPT>
+static cudaError_t add_norm_v(const void* x, long long xs, const void* residual, const void* weight,
+                              void* residual_out, void* out, float* scales, int rows, int D, int tpr, int group,
+                              float eps, bool e4m3, cudaStream_t st) {
+  using bf = __nv_bfloat16;
+  const int threads = tpr < kNormMinThreads ? kNormMinThreads : tpr;
+  const unsigned grid = (unsigned)((rows + threads / tpr - 1) / (threads / tpr));
+  const int ngroups = group ? (D + group - 1) / group : 1;
+  if (e4m3)
+    gdn_add_norm_kernel<VPT, true><<<grid, threads, 0, st>>>(
+        static_cast<const bf*>(x), xs, static_cast<const bf*>(residual), static_cast<const bf*>(weight),
+        static_cast<bf*>(residual_out), out, scales, rows, D, tpr, group, ngroups, eps);
+  else
+    gdn_add_norm_kernel<VPT, false><<<grid, threads, 0, st>>>(
+        static_cast<const bf*>(x), xs, static_cast<const bf*>(residual), static_cast<const bf*>(weight),
+        static_cast<bf*>(residual_out), out, scales, rows, D, tpr, group, ngroups, eps);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_add_norm(const void* x, long long xs, const void* residual, const void* weight, void* residual_out,
+                            void* out, float* scales, int rows, int D, int group, float eps, bool e4m3,
+                            cudaStream_t st) {
+  const int nv = D / 8;
+  int tpr = 32;  // two vectors a thread up to 1024 threads a row
+  while (tpr < 1024 && 2 * tpr < nv) tpr <<= 1;
+  const int vpt = (nv + tpr - 1) / tpr;
+  if (vpt <= 1) return add_norm_v<1>(x, xs, residual, weight, residual_out, out, scales, rows, D, tpr, group, eps, e4m3, st);
+  if (vpt <= 2) return add_norm_v<2>(x, xs, residual, weight, residual_out, out, scales, rows, D, tpr, group, eps, e4m3, st);
+  if (vpt <= 4) return add_norm_v<4>(x, xs, residual, weight, residual_out, out, scales, rows, D, tpr, group, eps, e4m3, st);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace gdn

@@ -1,0 +1,56 @@
+// What the selective state space scan and its single-token step share.
+#pragma once
+
+#include "gdn_common.cuh"
+
+namespace gdn {
+
+// A call's tensors (token strides in elements).
+struct SsmArgs {
+  const __nv_bfloat16* x;   // [Ttot, Hv, dv]
+  const void* dt;           // [Ttot, Hv], bf16 or fp32
+  const float* A;           // [Hv]
+  const __nv_bfloat16* Bm;  // [Ttot, Hk, dk]
+  const __nv_bfloat16* Cm;  // [Ttot, Hk, dk]
+  const float* D;           // [Hv] or null
+  const __nv_bfloat16* z;   // [Ttot, Hv, dv] or null
+  const float* dt_bias;     // [Hv] or null
+  __nv_bfloat16* out;       // [Ttot, Hv, dv], contiguous
+  long long xs, dts, bs, cs, zs;
+  int Hk, Hv, dv;
+  int softplus, dt_f32;
+};
+
+// The step of (token, head): softplus(dt + bias), or dt + bias.
+__device__ __forceinline__ float ssm_dt(const SsmArgs& a, long long t, int h) {
+  const long long at = t * a.dts + h;
+  float d = a.dt_f32 ? static_cast<const float*>(a.dt)[at]
+                     : __bfloat162float(static_cast<const __nv_bfloat16*>(a.dt)[at]);
+  if (a.dt_bias != nullptr) d += a.dt_bias[h];
+  if (a.softplus) d = d > 20.f ? d : log1pf(expf(d));  // beyond 20 they agree to fp32
+  return d;
+}
+
+__device__ __forceinline__ float ssm_silu(float v) { return v / (1.f + __expf(-v)); }
+
+// E (1, 2 or 4) consecutive fp32 of a state row.
+template <int E>
+__device__ __forceinline__ void ssm_load_row(const float* p, float (&s)[E]) {
+  if constexpr (E == 4) {
+    const float4 t = *reinterpret_cast<const float4*>(p);
+    s[0] = t.x; s[1] = t.y; s[2] = t.z; s[3] = t.w;
+  } else if constexpr (E == 2) {
+    const float2 t = *reinterpret_cast<const float2*>(p);
+    s[0] = t.x; s[1] = t.y;
+  } else {
+    s[0] = *p;
+  }
+}
+template <int E>
+__device__ __forceinline__ void ssm_store_row(float* p, const float (&s)[E]) {
+  if constexpr (E == 4) *reinterpret_cast<float4*>(p) = make_float4(s[0], s[1], s[2], s[3]);
+  else if constexpr (E == 2) *reinterpret_cast<float2*>(p) = make_float2(s[0], s[1]);
+  else *p = s[0];
+}
+
+}  // namespace gdn

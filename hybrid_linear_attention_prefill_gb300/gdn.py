@@ -7,7 +7,10 @@ turns tensors into pointers.  There is no fallback: if the library cannot be loa
 Functions keep the C names: ``gdn_prefill``, ``gdn_prefill_host``,
 ``gdn_abi_version``, ``gdn_strerror``, ``gdn_last_cuda_error``,
 ``gdn_workspace_bytes``, ``gdn_scan_segments``, ``gdn_release_workspace``.  ``prefill`` is a convenience
-wrapper that allocates the outputs with PyTorch and checks the status.
+wrapper that allocates the outputs with PyTorch and checks the status, and so are ``causal_conv``,
+``causal_conv_step``, ``ssm_scan``, ``ssm_step`` and ``add_norm`` for the operators around the recurrence;
+these take tensors with their strides, check types and shapes (``ValueError``), and write into given
+output buffers where the caller has them.
 """
 
 from __future__ import annotations
@@ -38,6 +41,10 @@ GDN_STATUS_PREP_LOAD_TIMEOUT = 4
 GDN_STATUS_BAD_CU_SEQLENS = 8
 GDN_STATUS_NONFINITE_STATE = 16
 GDN_STATUS_SMALL_STATE = 32
+GDN_CONV_SILU = 1
+GDN_SSM_SOFTPLUS = 1
+GDN_SSM_DT_F32 = 2
+GDN_NORM_E4M3 = 1
 
 
 def GDN_FLAG_SEGMENTS(n: int) -> int:
@@ -49,7 +56,8 @@ EXPORTED = ("gdn_abi_version", "gdn_strerror", "gdn_last_cuda_error", "gdn_prefi
             "gdn_prefill_host", "gdn_prefill_static", "gdn_prefill_ws", "gdn_prefill_ex", "gdn_decode",
             "gdn_set_phase_events", "gdn_workspace_bytes", "gdn_scan_segments", "gdn_release_workspace",
             "gdn_device_status", "gdn_selftest_wait_timeout", "gdn_selftest_static_wait_timeout",
-            "gdn_debug_fail_allocations")
+            "gdn_debug_fail_allocations", "gdn_conv", "gdn_conv_step", "gdn_ssm_scan", "gdn_ssm_workspace_bytes",
+            "gdn_ssm_step", "gdn_add_norm")
 
 _lock = threading.Lock()
 _lib = None
@@ -114,6 +122,20 @@ def load(build_if_missing: bool = False):
         lib.gdn_selftest_static_wait_timeout.restype = i
         lib.gdn_debug_fail_allocations.argtypes = [i]
         lib.gdn_debug_fail_allocations.restype = i
+        ll, u = ctypes.c_longlong, ctypes.c_uint
+        lib.gdn_conv.argtypes = [vp, ll, vp, vp, ip, vp, vp, vp, i, i, i, i, u, vp]
+        lib.gdn_conv.restype = i
+        lib.gdn_conv_step.argtypes = [vp, ll, vp, vp, vp, vp, i, i, i, u, vp]
+        lib.gdn_conv_step.restype = i
+        ssm = [vp, ll, vp, ll, fp, vp, ll, vp, ll, fp, vp, ll, fp]
+        lib.gdn_ssm_scan.argtypes = ssm + [ip, fp, vp, fp, i, i, i, i, i, i, u, vp, ctypes.c_size_t, vp]
+        lib.gdn_ssm_scan.restype = i
+        lib.gdn_ssm_workspace_bytes.argtypes = [i] * 7
+        lib.gdn_ssm_workspace_bytes.restype = ctypes.c_size_t
+        lib.gdn_ssm_step.argtypes = ssm + [fp, vp, i, i, i, i, i, u, vp]
+        lib.gdn_ssm_step.restype = i
+        lib.gdn_add_norm.argtypes = [vp, ll, vp, vp, vp, vp, fp, i, i, i, ctypes.c_float, u, vp]
+        lib.gdn_add_norm.restype = i
         lib.gdn_release_workspace.argtypes = []
         lib.gdn_release_workspace.restype = None
         _lib = lib
@@ -275,3 +297,242 @@ def prefill(q, k, v, g, beta, cu_seqlens=None, init_state=None, *, B=None, want_
     fin = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=q.device) if want_final else None
     check(gdn_prefill(q, k, v, g, beta, cu_seqlens, init_state, out, fin, B, T, Hk, Hv, dk, dv, stream))
     return out, fin
+
+
+# ---- the operators around the recurrence -----------------------------------------------------
+
+
+def gdn_conv(x, x_stride, weight, bias, cu_seqlens, init_state, out, final_state, B, T, C, K, flags,
+             stream=None) -> int:
+    """Short causal convolution of a prompt; returns the status."""
+    return load().gdn_conv(_ptr(x), int(x_stride), _ptr(weight), _ptr(bias), _ptr(cu_seqlens), _ptr(init_state),
+                           _ptr(out), _ptr(final_state), int(B), int(T), int(C), int(K), int(flags), _stream(stream))
+
+
+def gdn_conv_step(x, x_stride, weight, bias, state, out, B, C, K, flags, stream=None) -> int:
+    """One token per sequence of the convolution, state updated in place; returns the status."""
+    return load().gdn_conv_step(_ptr(x), int(x_stride), _ptr(weight), _ptr(bias), _ptr(state), _ptr(out), int(B),
+                                int(C), int(K), int(flags), _stream(stream))
+
+
+def gdn_ssm_scan(x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, D, z, z_stride, dt_bias, cu_seqlens,
+                 init_state, out, final_state, B, T, Hk, Hv, dk, dv, flags, workspace=None, workspace_bytes=0,
+                 stream=None) -> int:
+    """Selective state space scan of a prompt; returns the status."""
+    return load().gdn_ssm_scan(_ptr(x), int(x_stride), _ptr(dt), int(dt_stride), _ptr(A), _ptr(Bm), int(b_stride),
+                               _ptr(Cm), int(c_stride), _ptr(D), _ptr(z), int(z_stride), _ptr(dt_bias),
+                               _ptr(cu_seqlens), _ptr(init_state), _ptr(out), _ptr(final_state), int(B), int(T),
+                               int(Hk), int(Hv), int(dk), int(dv), int(flags), _ptr(workspace),
+                               int(workspace_bytes), _stream(stream))
+
+
+def gdn_ssm_workspace_bytes(B, T, Hk, Hv, dk, dv, packed) -> int:
+    return load().gdn_ssm_workspace_bytes(B, T, Hk, Hv, dk, dv, int(bool(packed)))
+
+
+def gdn_ssm_step(x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, D, z, z_stride, dt_bias, state, out, B,
+                 Hk, Hv, dk, dv, flags, stream=None) -> int:
+    """One token per sequence of the scan, state updated in place; returns the status."""
+    return load().gdn_ssm_step(_ptr(x), int(x_stride), _ptr(dt), int(dt_stride), _ptr(A), _ptr(Bm), int(b_stride),
+                               _ptr(Cm), int(c_stride), _ptr(D), _ptr(z), int(z_stride), _ptr(dt_bias), _ptr(state),
+                               _ptr(out), int(B), int(Hk), int(Hv), int(dk), int(dv), int(flags), _stream(stream))
+
+
+def gdn_add_norm(x, x_stride, residual, weight, residual_out, out, scales, rows, D, group, eps, flags,
+                 stream=None) -> int:
+    """Root-mean-square norm with the residual's addition; returns the status."""
+    return load().gdn_add_norm(_ptr(x), int(x_stride), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(out),
+                               _ptr(scales), int(rows), int(D), int(group), float(eps), int(flags), _stream(stream))
+
+
+def _want(cond, what) -> None:
+    if not cond:
+        raise ValueError(what)
+
+
+def _plain(t, name, dtype, shape, like) -> None:
+    """A contiguous tensor of this type and shape on `like`'s device."""
+    if t.dtype is not dtype or tuple(t.shape) != shape or t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {shape} on {like.device} is wanted, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _rows(t, name, dtypes, shape, like) -> int:
+    """Row stride of a tensor of this shape whose rows are contiguous (a slice of a wider one may be)."""
+    if t.dtype not in dtypes or tuple(t.shape) != shape or t.device != like.device:
+        raise ValueError(f"{name}: a {' or '.join(map(str, dtypes))} tensor of shape {shape} on {like.device} is "
+                         f"wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    st, width = t.stride(), 1
+    for n, s in zip(shape[:0:-1], st[:0:-1]):
+        if n != 1 and s != width:
+            raise ValueError(f"{name}: the elements of a row have to be contiguous (strides {st})")
+        width *= n
+    return st[0] if shape[0] > 1 else width
+
+
+def _batch(x, cu_seqlens, B):
+    """(sequences, tokens per sequence or in all) of a dense or packed batch of x's rows."""
+    import torch
+
+    n = x.shape[0]
+    if cu_seqlens is None:
+        B = 1 if B is None else int(B)
+        _want(B >= 0 and (n % B == 0 if B else n == 0), "the tokens have to divide into B sequences")
+        return B, n // B if B else 0
+    _want(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 1, "cu_seqlens: B + 1 boundaries")
+    _plain(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), x)
+    return cu_seqlens.numel() - 1, n
+
+
+def causal_conv(x, weight, bias=None, cu_seqlens=None, init_state=None, *, B=None, silu=True, out=None,
+                final_state=None, want_final=True, stream=None):
+    """Short causal convolution of a dense batch of B sequences, or a packed one, with silu.
+
+    x: bf16 [Ttot, C] (rows may be a slice of wider ones); weight: bf16 [C, K], K of 2 to 4; bias: bf16 [C];
+    init_state: bf16 [B, K-1, C], the inputs before each sequence, oldest first.  Returns (out bf16
+    [Ttot, C], final_state bf16 [B, K-1, C] or None), in `out` and `final_state` where given.
+    """
+    import torch
+
+    bf16 = torch.bfloat16
+    _want(x.dim() == 2 and weight.dim() == 2, "x: [Ttot, C], weight: [C, K]")
+    C, K = weight.shape
+    xs = _rows(x, "x", (bf16,), (x.shape[0], C), x)
+    B, T = _batch(x, cu_seqlens, B)
+    _plain(weight, "weight", bf16, (C, K), x)
+    if bias is not None:
+        _plain(bias, "bias", bf16, (C,), x)
+    if init_state is not None:
+        _plain(init_state, "init_state", bf16, (B, K - 1, C), x)
+    if out is None:
+        out = torch.empty((x.shape[0], C), dtype=bf16, device=x.device)
+    else:
+        _plain(out, "out", bf16, (x.shape[0], C), x)
+    if final_state is not None:
+        _plain(final_state, "final_state", bf16, (B, K - 1, C), x)
+    elif want_final:
+        final_state = torch.empty((B, K - 1, C), dtype=bf16, device=x.device)
+    check(gdn_conv(x, xs, weight, bias, cu_seqlens, init_state, out, final_state, B, T, C, K,
+                   GDN_CONV_SILU if silu else 0, stream))
+    return out, final_state
+
+
+def causal_conv_step(x, weight, state, bias=None, *, silu=True, out=None, stream=None):
+    """One token of each of B sequences: x bf16 [B, C]; state bf16 [B, K-1, C], updated in place."""
+    import torch
+
+    bf16 = torch.bfloat16
+    _want(x.dim() == 2 and weight.dim() == 2, "x: [B, C], weight: [C, K]")
+    C, K = weight.shape
+    B = x.shape[0]
+    xs = _rows(x, "x", (bf16,), (B, C), x)
+    _plain(weight, "weight", bf16, (C, K), x)
+    _plain(state, "state", bf16, (B, K - 1, C), x)
+    if bias is not None:
+        _plain(bias, "bias", bf16, (C,), x)
+    if out is None:
+        out = torch.empty((B, C), dtype=bf16, device=x.device)
+    else:
+        _plain(out, "out", bf16, (B, C), x)
+    check(gdn_conv_step(x, xs, weight, bias, state, out, B, C, K, GDN_CONV_SILU if silu else 0, stream))
+    return out
+
+
+def _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out):
+    """Shapes, row strides and `out` of the scan and its step."""
+    import torch
+
+    bf16, f32 = torch.bfloat16, torch.float32
+    _want(x.dim() == 3 and Bm.dim() == 3, "x: [Ttot, Hv, dv], Bm and Cm: [Ttot, Hk, dk]")
+    n, Hv, dv = x.shape
+    Hk, dk = Bm.shape[1:]
+    strides = (_rows(x, "x", (bf16,), (n, Hv, dv), x), _rows(dt, "dt", (bf16, f32), (n, Hv), x),
+               _rows(Bm, "Bm", (bf16,), (n, Hk, dk), x), _rows(Cm, "Cm", (bf16,), (n, Hk, dk), x),
+               0 if z is None else _rows(z, "z", (bf16,), (n, Hv, dv), x))
+    _plain(A, "A", f32, (Hv,), x)
+    if D is not None:
+        _plain(D, "D", f32, (Hv,), x)
+    if dt_bias is not None:
+        _plain(dt_bias, "dt_bias", f32, (Hv,), x)
+    if out is None:
+        out = torch.empty((n, Hv, dv), dtype=bf16, device=x.device)
+    else:
+        _plain(out, "out", bf16, (n, Hv, dv), x)
+    return (Hk, Hv, dk, dv), strides, out, GDN_SSM_DT_F32 if dt.dtype is f32 else 0
+
+
+def ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, cu_seqlens=None, init_state=None, *, B=None,
+             softplus=True, out=None, final_state=None, want_final=True, workspace=None, stream=None):
+    """Selective state space scan of a dense batch of B sequences, or a packed one.
+
+    x, z: bf16 [Ttot, Hv, dv]; dt: bf16 or fp32 [Ttot, Hv]; A, D, dt_bias: fp32 [Hv]; Bm, Cm: bf16
+    [Ttot, Hk, dk] (token rows may be slices of wider ones); init_state: fp32 [B, Hv, dv, dk].
+    `workspace`: a byte tensor of gdn_ssm_workspace_bytes(...), for calls that overlap or are captured.
+    Returns (out bf16 [Ttot, Hv, dv], final_state fp32 [B, Hv, dv, dk] or None).
+    """
+    import torch
+
+    dims, (xs, ds, bs, cs, zs), out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out)
+    Hk, Hv, dk, dv = dims
+    B, T = _batch(x, cu_seqlens, B)
+    for name, t in (("init_state", init_state), ("final_state", final_state)):
+        if t is not None:
+            _plain(t, name, torch.float32, (B, Hv, dv, dk), x)
+    if final_state is None and want_final:
+        final_state = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=x.device)
+    check(gdn_ssm_scan(x, xs, dt, ds, A, Bm, bs, Cm, cs, D, z, zs, dt_bias, cu_seqlens, init_state, out, final_state,
+                       B, T, Hk, Hv, dk, dv, flags | (GDN_SSM_SOFTPLUS if softplus else 0), workspace,
+                       0 if workspace is None else workspace.numel() * workspace.element_size(), stream))
+    return out, final_state
+
+
+def ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softplus=True, out=None, stream=None):
+    """One token of each of B sequences of the scan: state fp32 [B, Hv, dv, dk], updated in place."""
+    import torch
+
+    dims, (xs, ds, bs, cs, zs), out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out)
+    Hk, Hv, dk, dv = dims
+    _plain(state, "state", torch.float32, (x.shape[0], Hv, dv, dk), x)
+    check(gdn_ssm_step(x, xs, dt, ds, A, Bm, bs, Cm, cs, D, z, zs, dt_bias, state, out, x.shape[0], Hk, Hv, dk, dv,
+                       flags | (GDN_SSM_SOFTPLUS if softplus else 0), stream))
+    return out
+
+
+def add_norm(x, weight, residual=None, *, eps=1e-6, group=0, e4m3=False, out=None, scales=None, residual_out=None,
+             stream=None):
+    """Root-mean-square norm of x (+ residual), to bf16, or to e4m3 with a scale per row (group 0) or per
+    32, 64 or 128 columns.
+
+    x: bf16 [rows, D] (rows may be slices of wider ones); weight: bf16 [D]; residual: bf16 [rows, D].
+    `e4m3` follows from `out` where that is given.  Returns (out, scales or None, residual_out or None);
+    residual_out may be `residual` itself.
+    """
+    import torch
+
+    bf16, f32, f8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+    _want(x.dim() == 2, "x: [rows, D]")
+    rows, D = x.shape
+    xs = _rows(x, "x", (bf16,), (rows, D), x)
+    _plain(weight, "weight", bf16, (D,), x)
+    if out is None:
+        out = torch.empty((rows, D), dtype=f8 if e4m3 else bf16, device=x.device)
+    else:
+        e4m3 = out.dtype is f8
+        _plain(out, "out", f8 if e4m3 else bf16, (rows, D), x)
+    if e4m3:
+        shape = (rows, -(-D // group) if group else 1)
+        if scales is None:
+            scales = torch.empty(shape, dtype=f32, device=x.device)
+        else:
+            _plain(scales, "scales", f32, shape, x)
+    else:
+        scales = None
+    if residual is not None:
+        _plain(residual, "residual", bf16, (rows, D), x)
+        if residual_out is None:
+            residual_out = torch.empty((rows, D), dtype=bf16, device=x.device)
+    if residual_out is not None:
+        _plain(residual_out, "residual_out", bf16, (rows, D), x)
+    check(gdn_add_norm(x, xs, residual, weight, residual_out, out, scales, rows, D, group, eps,
+                       GDN_NORM_E4M3 if e4m3 else 0, stream))
+    return out, scales, residual_out

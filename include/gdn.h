@@ -332,6 +332,126 @@ size_t gdn_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv, int pac
 /* Release the calling device's workspace and staging buffers (synchronises the device). */
 void gdn_release_workspace(void);
 
+/* ---------------------------------------------------------------------------------------
+ * The operators around the recurrence in a hybrid layer: the short causal convolution over
+ * the channels that feed it, the selective state space scan (the other recurrence of such
+ * layers), each for prompts and for single tokens, and the norm that opens a layer.
+ *
+ * All pointers are DEVICE memory, owned by the caller and not retained; every call is
+ * asynchronous on `stream`, never synchronises the host, and returns GDN_OK or, before
+ * anything is launched, GDN_ERR_ARG / GDN_ERR_ALIGN (or GDN_ERR_LAUNCH from a launch).
+ * Activations are bf16; sums, states of the scan and softplus / exp values are fp32.  A
+ * `*_stride` is the distance between consecutive tokens in elements, so that an operand can
+ * be a slice of a wider projection or convolution output; within a token the elements are
+ * contiguous.  bf16 activations start on 16 bytes and, with more than one token, their
+ * strides are multiples of 8 elements (GDN_ERR_ALIGN otherwise); dt has no such rule.
+ * Outputs are contiguous and must not overlap the inputs unless stated.
+ * ------------------------------------------------------------------------------------- */
+
+/* Flags of gdn_conv and gdn_conv_step. */
+#define GDN_CONV_SILU 1u /* out = silu(convolution), else the convolution itself */
+
+/*
+ * gdn_conv -- short causal convolution of every channel over the tokens of its sequence:
+ *
+ *     y[t, c] = act( bias[c] + sum_{k < K} weight[c, k] x[t - K + 1 + k, c] )
+ *
+ *   x            bf16 [Ttot, C], token stride x_stride
+ *   weight       bf16 [C, K];  bias bf16 [C] or NULL
+ *   cu_seqlens   int32 [B + 1] or NULL, as for gdn_prefill (dense: B sequences of T tokens;
+ *                packed: T tokens in all; out-of-order entries read and write nothing out of
+ *                range, their results are unspecified)
+ *   init_state   bf16 [B, K - 1, C] or NULL: the inputs before each sequence, oldest first
+ *                (NULL = zeros)
+ *   out          bf16 [Ttot, C];  must not overlap x
+ *   final_state  bf16 [B, K - 1, C] or NULL: the last K - 1 inputs of each sequence (of its
+ *                state, where it is shorter); must not overlap init_state (GDN_ERR_ARG)
+ *
+ * K is 2, 3 or 4, C a multiple of 8.  Sums in fp32, one rounding to bf16.
+ */
+int gdn_conv(const void *x, long long x_stride, const void *weight, const void *bias,
+             const int32_t *cu_seqlens, const void *init_state, void *out, void *final_state,
+             int B, int T, int C, int K, unsigned flags, void *stream);
+
+/*
+ * gdn_conv_step -- gdn_conv for one token per sequence: x and out [B, C], state bf16
+ * [B, K - 1, C] read and overwritten with the last K - 1 inputs.
+ */
+int gdn_conv_step(const void *x, long long x_stride, const void *weight, const void *bias, void *state,
+                  void *out, int B, int C, int K, unsigned flags, void *stream);
+
+/* Flags of gdn_ssm_scan and gdn_ssm_step. */
+#define GDN_SSM_SOFTPLUS 1u /* the step is softplus(dt + dt_bias), else dt + dt_bias */
+#define GDN_SSM_DT_F32 2u   /* dt is fp32, else bf16 */
+
+/*
+ * gdn_ssm_scan -- selective state space scan of a prompt, one decay per (token, value head):
+ *
+ *     S_t = exp(s_t A_h) S_{t-1} + s_t x_t B_t^T        s_t = softplus(dt_t + dt_bias_h)
+ *     y_t = (S_t C_t + D_h x_t) silu(z_t)
+ *
+ * with S a dv x dk fp32 state.  B and C belong to key heads: value head h reads key head
+ * h / (Hv / Hk).
+ *
+ *   x            bf16 [Ttot, Hv, dv];  dt [Ttot, Hv] bf16 or fp32 (any alignment of its type)
+ *   A            fp32 [Hv] (negative: a decay);  Bm, Cm bf16 [Ttot, Hk, dk]
+ *   D            fp32 [Hv] or NULL (no skip term);  dt_bias fp32 [Hv] or NULL
+ *   z            bf16 [Ttot, Hv, dv] or NULL (no gate)
+ *   cu_seqlens   as for gdn_conv; malformed entries also set GDN_STATUS_BAD_CU_SEQLENS
+ *   init_state   fp32 [B, Hv, dv, dk] or NULL (zeros)
+ *   out          bf16 [Ttot, Hv, dv]
+ *   final_state  fp32 [B, Hv, dv, dk] or NULL; may alias init_state.  A sequence of no tokens
+ *                returns its initial state.
+ *
+ * dk and dv are 32, 64 or 128 each.  A sequence's results do not depend on the values of other
+ * tokens of a packed batch, infinities and NaN included.
+ *
+ * workspace: gdn_ssm_workspace_bytes(...) bytes of device memory, 256-byte aligned, not shared
+ * with concurrent calls, or NULL for the library's own grow-only one (shared by the calls on a
+ * device: order calls whose work could overlap, as for gdn_prefill).  With a workspace the call
+ * allocates nothing and can be captured into a CUDA graph; GDN_ERR_SCRATCH when it is too
+ * small.  Its first word collects status bits; gdn_device_status reports those of the
+ * library's own.
+ */
+int gdn_ssm_scan(const void *x, long long x_stride, const void *dt, long long dt_stride, const float *A,
+                 const void *Bm, long long b_stride, const void *Cm, long long c_stride, const float *D,
+                 const void *z, long long z_stride, const float *dt_bias, const int32_t *cu_seqlens,
+                 const float *init_state, void *out, float *final_state, int B, int T, int Hk, int Hv,
+                 int dk, int dv, unsigned flags, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace gdn_ssm_scan needs for these sizes on the current device (0 on bad arguments). */
+size_t gdn_ssm_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv, int packed);
+
+/*
+ * gdn_ssm_step -- gdn_ssm_scan for one token per sequence (x, z, out [B, Hv, dv], dt [B, Hv],
+ * Bm, Cm [B, Hk, dk]); state fp32 [B, Hv, dv, dk], 16-byte aligned, updated in place.
+ */
+int gdn_ssm_step(const void *x, long long x_stride, const void *dt, long long dt_stride, const float *A,
+                 const void *Bm, long long b_stride, const void *Cm, long long c_stride, const float *D,
+                 const void *z, long long z_stride, const float *dt_bias, float *state, void *out, int B,
+                 int Hk, int Hv, int dk, int dv, unsigned flags, void *stream);
+
+/* Flags of gdn_add_norm. */
+#define GDN_NORM_E4M3 1u /* out is e4m3 with scales, else bf16 */
+
+/*
+ * gdn_add_norm -- root-mean-square norm with the residual's addition:
+ *
+ *     r = x + residual;   y = r / sqrt(mean(r^2) + eps) weight
+ *
+ *   x         bf16 [rows, D], row stride x_stride;  residual bf16 [rows, D] or NULL (r = x)
+ *   weight    bf16 [D]
+ *   residual_out  bf16 [rows, D] or NULL: r, rounded; may be `residual` itself
+ *   out       bf16 [rows, D], or with GDN_NORM_E4M3 8-bit [rows, D] (y / scale, saturated)
+ *   scales    fp32 [rows, ceil(D / group)] with GDN_NORM_E4M3: max(max |y|, 2^-96) / 448 over each
+ *             `group` of columns (32, 64 or 128; 0: one scale per row)
+ *
+ * D is a multiple of 8 up to 32,768.  y is computed from the unrounded sum and rounded once.  A NaN
+ * in a group makes its scale NaN.
+ */
+int gdn_add_norm(const void *x, long long x_stride, const void *residual, const void *weight, void *residual_out,
+                 void *out, float *scales, int rows, int D, int group, float eps, unsigned flags, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
