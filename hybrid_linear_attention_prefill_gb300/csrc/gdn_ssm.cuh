@@ -31,6 +31,21 @@ __device__ __forceinline__ float ssm_dt(const SsmArgs& a, long long t, int h) {
   return d;
 }
 
+// A decay by e^l, l <= 0, as keep S + (more S + what is added).  Above a half that is S + (e^l - 1) S:
+// e^l itself, rounded near 1, is off the same way for every token or chunk of a slowly decaying state,
+// which then adds up (2^-25 of it each time over thousands), while a sum's rounding errors have either
+// sign.  Below a half the difference would cancel, and e^l S is taken as it is.
+struct SsmDecay {
+  float keep, more;
+};
+__device__ __forceinline__ SsmDecay ssm_decay(float l) {
+  const bool near_one = l > -0.6931f;
+  return {near_one ? 1.f : 0.f, near_one ? expm1f(l) : expf(l)};
+}
+__device__ __forceinline__ float ssm_decayed(const SsmDecay& d, float s, float add) {
+  return fmaf(d.keep, s, fmaf(d.more, s, add));
+}
+
 __device__ __forceinline__ float ssm_silu(float v) { return v / (1.f + __expf(-v)); }
 
 // E (1, 2 or 4) consecutive fp32 of a state row.

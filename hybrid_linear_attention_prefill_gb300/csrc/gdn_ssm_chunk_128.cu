@@ -1,0 +1,9 @@
+// The chunked selective scan's kernels for a state of 128 columns.
+#include "gdn_ssm_chunk_kernels.cuh"
+
+namespace gdn {
+namespace ssm {
+template cudaError_t launch_dk<128>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const SsmArgs&,
+                                    const Segs&, float*, float*, const float*, float*, int*, int, int, cudaStream_t);
+}  // namespace ssm
+}  // namespace gdn

@@ -1,99 +1,221 @@
-// Selective state space scan of a prompt (sm_103a), token by token:
+// Launches of the selective state space scan of a prompt (gdn_ssm_chunk.cuh): tensor maps, the choice of
+// segments, and the pass that joins them.
 //
-//   S_t = exp(s_t A) S_{t-1} + s_t x_t B_t^T,   y_t = (S_t C_t + D x_t) silu(z_t)
-//
-// A warp holds four rows of one (sequence, value head)'s dv x dk state in registers, dk / 32
-// consecutive elements a lane, and walks the sequence's tokens; the row sums S C go by warp
-// shuffles.  The chain of tokens bounds it.
-#include "gdn_common.cuh"
-#include "gdn_ssm.cuh"
+// A CTA carries the state of its heads through a segment's chunks one after the other.  Where sequences
+// and heads are too few to fill the device, sequences are cut into segments: one pass sums every segment
+// from a zero state (x, B and dt only, about 0.4 of a chunk's time), gdn_ssm_join_kernel turns the sums
+// into start states, and the output pass runs every segment from its own.
+#include <algorithm>
+
+#include "../../include/gdn.h"
+#include "gdn_internal.h"
+#include "gdn_ssm_chunk.cuh"
 
 namespace gdn {
 
-namespace {
-constexpr int kScanWarps = 4;
-constexpr int kScanRows = 4;
-}  // namespace
+cudaError_t launch_chunk_table(const int32_t*, int, int, int32_t*, int32_t*, int*, cudaStream_t);
 
-// grid: (B * dv / 16, Hv)
+namespace ssm {
 template <int DK>
-__global__ void __launch_bounds__(32 * kScanWarps)
-gdn_ssm_scan_kernel(const SsmArgs a, const int32_t* __restrict__ cu, const float* init, float* fin, int* err, int B,
-                    int T) {
-  constexpr int E = DK / 32, R = kScanRows;
-  const int slices = a.dv / (kScanWarps * R);
-  const int b = blockIdx.x / slices, h = blockIdx.y;
-  const int hk = h / (a.Hv / a.Hk);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = ((blockIdx.x - b * slices) * kScanWarps + warp) * R;
-  const SeqChunk q = seq_bounds(cu, b, T);
-  if (cu != nullptr && h == 0 && blockIdx.x == b * slices && threadIdx.x == 0) {
-    const int lo = cu[b], hi = cu[b + 1];
-    if (lo < 0 || hi < lo || hi > T || (b == 0 && lo != 0) || (b == B - 1 && hi != T)) atomicOr(err, 8);
-  }
-  const size_t at = (((size_t)b * a.Hv + h) * a.dv + row) * DK + lane * E;
-  const float skip = a.D != nullptr ? a.D[h] : 0.f, decay_rate = a.A[h];
-  // the state, and what its last sums rounded away (a slowly decaying state adds thousands of tokens)
-  float s[R][E], lost[R][E];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) s[r][e] = lost[r][e] = 0.f;
-    if (init != nullptr) ssm_load_row<E>(init + at + r * DK, s[r]);
-  }
-  for (long long t = q.bos; t < q.bos + q.len; ++t) {
-    const float step = ssm_dt(a, t, h);
-    const float decay_m1 = expm1f(step * decay_rate);
-    float bv[E], cv[E], y[R];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      bv[e] = __bfloat162float(a.Bm[t * a.bs + hk * DK + lane * E + e]);
-      cv[e] = __bfloat162float(a.Cm[t * a.cs + hk * DK + lane * E + e]);
+cudaError_t launch_dk(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const SsmArgs&, const Segs&, float*,
+                      float*, const float*, float*, int*, int, int, cudaStream_t);
+}
+
+namespace {
+
+constexpr int kJoinThreads = 256;
+
+struct Plan {
+  int hpc = 1;    // heads a CTA
+  int len = 0;    // chunks a segment (0: whole sequences)
+  int slots = 0;  // segments
+};
+
+// Heads a CTA and the segments' length, from the sizes alone (a packed batch's lengths are on the device:
+// taken as equal).  In units of an output pass's chunk step, a segmented call costs its waves times the
+// segment's chunks, 0.4 of that again for the sums, and about two steps for the join.
+Plan make_plan(int B, int T, int Hk, int Hv, int dv, bool packed, int sms) {
+  Plan p;
+  p.hpc = dv < 128 && (Hv / Hk) % 2 == 0 ? 2 : 1;
+  const long long hb = Hv / p.hpc;
+  p.slots = B;
+  if (B == 0 || T == 0) return p;
+  const int nc = packed ? std::max(1, (int)(((long long)T + B - 1) / B + ssm::kQ - 1) / ssm::kQ)
+                        : (T + ssm::kQ - 1) / ssm::kQ;
+  auto waves = [&](long long ctas) { return (ctas + sms - 1) / sms; };
+  double best = (double)waves(hb * B) * nc;
+  for (int n = 2; n <= nc; ++n) {  // segments a sequence
+    const int len = (nc + n - 1) / n;
+    if (n > 2 && (nc + n - 2) / (n - 1) == len) continue;  // the same length as with fewer
+    const long long segs = (nc + len - 1) / len;
+    const double cost = (double)len * (waves(hb * B * segs) + 0.4 * waves(hb * B * (segs - 1))) + 2.0;
+    if (cost < best) {
+      best = cost;
+      p.len = len;
     }
+    if (hb * B * segs > 4LL * sms) break;
+  }
+  if (p.len != 0) {
+    const int per = p.len * ssm::kQ;
+    p.slots = packed ? T / per + B : B * ((T + per - 1) / per);
+  }
+  return p;
+}
+
+// Segment start states from the segments' sums E and decays, in place: S_start(0) = the initial state,
+// S_start(k + 1) = decay_k S_start(k) + E_k.  One thread per four state elements of a (sequence, head).
+// grid: (B * Hv, blocks over dv * dk / 4)
+__global__ void __launch_bounds__(kJoinThreads)
+gdn_ssm_join_kernel(const ssm::Segs g, const float* __restrict__ init, float* __restrict__ seg_state,
+                    const float* __restrict__ seg_decay, int Hv, int nstate) {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int b = blockIdx.x / Hv, h = blockIdx.x - b * Hv;
+  const int e = blockIdx.y * kJoinThreads + threadIdx.x;
+  int slot0 = 0, n;
+  if (g.cu == nullptr) {
+    n = ssm::seg_count(g, g.T);
+    slot0 = b * n;
+  } else {
+    n = ssm::seg_count(g, seq_bounds(g.cu, b, g.T).len);
+    const int lane = threadIdx.x & 31;  // segments of the sequences before: every warp sums them
+    int sum = 0;
+    for (int i = lane; i < b; i += 32) sum += ssm::seg_count(g, seq_bounds(g.cu, i, g.T).len);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float u = step * __bfloat162float(a.x[t * a.xs + h * a.dv + row + r]);
-      y[r] = 0.f;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    slot0 = sum;
+    if (slot0 > g.slots) slot0 = g.slots;
+    if (n > g.slots - slot0) n = g.slots - slot0;  // malformed boundaries
+  }
+  if (4 * e >= nstate) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (init != nullptr) s = *reinterpret_cast<const float4*>(init + ((size_t)b * Hv + h) * nstate + 4 * e);
+  constexpr int kAhead = 4;
+  float4 v[kAhead];
+  SsmDecay m[kAhead];
+  auto at = [&](int k) { return seg_state + ((size_t)(slot0 + k) * Hv + h) * nstate + 4 * e; };
+  for (int k0 = 0; k0 < n; k0 += kAhead) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float inc = fmaf(decay_m1, s[r][e], u * bv[e]) + lost[r][e];
-        const float next = s[r][e] + inc;
-        lost[r][e] = inc - (next - s[r][e]);
-        s[r][e] = next;
-        y[r] = fmaf(s[r][e], cv[e], y[r]);
+    for (int u = 0; u < kAhead; ++u)
+      if (k0 + u + 1 < n) {
+        v[u] = *reinterpret_cast<const float4*>(at(k0 + u));
+        m[u] = ssm_decay(seg_decay[(size_t)(slot0 + k0 + u) * Hv + h] * 0.6931471805599453f);
+      }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (k0 + u >= n) break;
+      *reinterpret_cast<float4*>(at(k0 + u)) = s;
+      if (k0 + u + 1 < n) {
+        s.x = ssm_decayed(m[u], s.x, v[u].x);
+        s.y = ssm_decayed(m[u], s.y, v[u].y);
+        s.z = ssm_decayed(m[u], s.z, v[u].z);
+        s.w = ssm_decayed(m[u], s.w, v[u].w);
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int r = 0; r < R; ++r) y[r] += __shfl_xor_sync(0xffffffffu, y[r], o);
-    if (lane < R) {
-      float v = y[0];
-#pragma unroll
-      for (int r = 1; r < R; ++r) v = lane == r ? y[r] : v;
-      v = fmaf(skip, __bfloat162float(a.x[t * a.xs + h * a.dv + row + lane]), v);
-      if (a.z != nullptr) v *= ssm_silu(__bfloat162float(a.z[t * a.zs + h * a.dv + row + lane]));
-      a.out[((size_t)t * a.Hv + h) * a.dv + row + lane] = __float2bfloat16_rn(v);
-    }
-  }
-  if (fin != nullptr) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) ssm_store_row<E>(fin + at + r * DK, s[r]);
   }
 }
 
-size_t ssm_scan_workspace(int B, int T, int Hk, int Hv, int dk, int dv, int packed) { return 256; }
+int device_sms() {
+  static std::atomic<int> known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return 0;
+    }
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Workspace: [256 B status words][packed: chunk table and dispatch order][segment states][segment decays]
+struct Layout {
+  size_t states, decays, total;
+};
+Layout layout(const Plan& p, int B, int Hv, int dk, int dv, bool packed) {
+  Layout l;
+  l.states = 256 + (packed ? chunk_table_bytes(B) : 0);
+  const size_t n = p.len != 0 ? (size_t)p.slots * Hv : 0;
+  l.decays = l.states + align256(n * dv * dk * 4);
+  l.total = l.decays + align256(n * 4);
+  return l;
+}
+
+bool token_map(CUtensorMap* m, const void* base, long long stride, long long width, long long tokens) {
+  const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)tokens};
+  const cuuint64_t strides[1] = {(cuuint64_t)(tokens > 1 ? stride : (width + 7) / 8 * 8) * 2};
+  const cuuint32_t box[2] = {64, ssm::kQ};
+  return make_map16(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace
+
+size_t ssm_scan_workspace(int B, int T, int Hk, int Hv, int dk, int dv, int packed) {
+  const int sms = device_sms();
+  // without a device: enough for any (a segment of one chunk for every chunk)
+  Plan p = make_plan(B, T, Hk, Hv, dv, packed != 0, sms > 0 ? sms : 1 << 20);
+  return layout(p, B, Hv, dk, dv, packed != 0).total;
+}
 
 cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* init, float* fin, void* ws, int B, int T,
                             int dk, cudaStream_t st) {
-  const dim3 grid((unsigned)(B * (a.dv / (kScanWarps * kScanRows))), a.Hv);
+  const int sms = device_sms();
+  if (sms == 0) return cudaErrorNoDevice;
+  const bool packed = cu != nullptr;
+  const Plan p = make_plan(B, T, a.Hk, a.Hv, a.dv, packed, sms);
+  const Layout l = layout(p, B, a.Hv, dk, a.dv, packed);
+  unsigned char* w = static_cast<unsigned char*>(ws);
   int* err = static_cast<int*>(ws);
-  switch (dk) {
-    case 32: gdn_ssm_scan_kernel<32><<<grid, 32 * kScanWarps, 0, st>>>(a, cu, init, fin, err, B, T); break;
-    case 64: gdn_ssm_scan_kernel<64><<<grid, 32 * kScanWarps, 0, st>>>(a, cu, init, fin, err, B, T); break;
-    default: gdn_ssm_scan_kernel<128><<<grid, 32 * kScanWarps, 0, st>>>(a, cu, init, fin, err, B, T); break;
+  float* states = reinterpret_cast<float*>(w + l.states);
+  float* decays = reinterpret_cast<float*>(w + l.decays);
+  const long long ntok = packed ? (long long)T : (long long)B * T;
+  if ((long long)p.slots * (a.Hv / p.hpc) > 0x7fffffffLL) return cudaErrorInvalidValue;
+  CUtensorMap tx = {}, tb = {}, tc_ = {};
+  if (ntok > 0 && (!token_map(&tx, a.x, a.xs, (long long)a.Hv * a.dv, ntok) ||
+                   !token_map(&tb, a.Bm, a.bs, (long long)a.Hk * dk, ntok) ||
+                   !token_map(&tc_, a.Cm, a.cs, (long long)a.Hk * dk, ntok)))
+    return cudaErrorInvalidValue;
+  ssm::Segs g;
+  g.cu = cu;
+  g.order = nullptr;
+  g.B = B;
+  g.T = T;
+  g.len = p.len;
+  g.slots = p.slots;
+  auto run = [&](int phase) {
+    switch (dk) {
+      case 32: return ssm::launch_dk<32>(tx, tb, tc_, a, g, states, decays, init, fin, err, p.hpc, phase, st);
+      case 64: return ssm::launch_dk<64>(tx, tb, tc_, a, g, states, decays, init, fin, err, p.hpc, phase, st);
+      default: return ssm::launch_dk<128>(tx, tb, tc_, a, g, states, decays, init, fin, err, p.hpc, phase, st);
+    }
+  };
+  cudaError_t e;
+  if (p.len != 0) {
+    if ((e = run(0)) != cudaSuccess) return e;
+    const int nstate = a.dv * dk;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(B * a.Hv), (unsigned)((nstate / 4 + kJoinThreads - 1) / kJoinThreads));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, gdn_ssm_join_kernel, (const ssm::Segs)g, init, states, (const float*)decays, a.Hv, nstate);
+    if (e != cudaSuccess) return e;
+  } else if (packed && B > 1) {  // whole sequences of different lengths: the longest start first
+    int32_t* off = reinterpret_cast<int32_t*>(w + 256);
+    if ((e = launch_chunk_table(cu, B, T, off, off + B + 1, err, st)) != cudaSuccess) return e;
+    g.order = off + B + 1;
   }
-  return cudaGetLastError();
+  return run(1);
 }
 
 }  // namespace gdn
