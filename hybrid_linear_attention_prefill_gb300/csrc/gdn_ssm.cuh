@@ -21,15 +21,16 @@ struct SsmArgs {
   int softplus, dt_f32;
 };
 
-// The step of (token, head): softplus(dt + bias), or dt + bias.
-__device__ __forceinline__ float ssm_dt(const SsmArgs& a, long long t, int h) {
+// The step of (token, head), softplus(dt + bias) or dt + bias, in two parts, so that the load can go ahead.
+__device__ __forceinline__ uint32_t ssm_load_dt(const SsmArgs& a, long long t, int h) {  // as it is in memory
   const long long at = t * a.dts + h;
-  float d = a.dt_f32 ? static_cast<const float*>(a.dt)[at]
-                     : __bfloat162float(static_cast<const __nv_bfloat16*>(a.dt)[at]);
-  if (a.dt_bias != nullptr) d += a.dt_bias[h];
-  if (a.softplus) d = d > 20.f ? d : log1pf(expf(d));  // beyond 20 they agree to fp32
-  return d;
+  return a.dt_f32 ? static_cast<const uint32_t*>(a.dt)[at] : (uint32_t) static_cast<const uint16_t*>(a.dt)[at];
 }
+__device__ __forceinline__ float ssm_step_of(const SsmArgs& a, uint32_t dt, float bias) {
+  const float d = __uint_as_float(a.dt_f32 ? dt : dt << 16) + bias;
+  return a.softplus && d <= 20.f ? log1pf(expf(d)) : d;  // beyond 20 they agree to fp32
+}
+__device__ __forceinline__ float ssm_bias(const SsmArgs& a, int h) { return a.dt_bias != nullptr ? a.dt_bias[h] : 0.f; }
 
 // A decay by e^l, l <= 0, as keep S + (more S + what is added).  Above a half that is S + (e^l - 1) S:
 // e^l itself, rounded near 1, is off the same way for every token or chunk of a slowly decaying state,
@@ -46,7 +47,19 @@ __device__ __forceinline__ float ssm_decayed(const SsmDecay& d, float s, float a
   return fmaf(d.keep, s, fmaf(d.more, s, add));
 }
 
-__device__ __forceinline__ float ssm_silu(float v) { return v / (1.f + __expf(-v)); }
+// 1 / x and 2^x to a few units in the last place.
+__device__ __forceinline__ float ssm_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float ssm_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float ssm_silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
 
 // E (1, 2 or 4) consecutive fp32 of a state row.
 template <int E>

@@ -11,14 +11,13 @@
 // chunks, and only by an elementwise update, so the products of a chunk need nothing but the state.
 // A CTA carries the state of 128 rows (one head of dv = 128, or two heads of one key head, 64 rows
 // reserved for each) through a run of chunks (a segment: the whole sequence when there are enough
-// sequences and heads to fill the device).  All sixteen warps do the elementwise work of each step
-// between two block barriers a chunk while one thread issues MMAs that run behind it:
+// sequences and heads to fill the device).  Sixteen worker warps do the elementwise work, one thread
+// issues the MMAs and the tile copies, one warp makes the decay tables a chunk ahead; they meet on
+// mbarriers only, so that warps drift apart and one's arithmetic covers another's wait:
 //
-//   S (fp32 registers) -> bf16 operand; w x of tokens 0..63    | barrier
-//   MMA: C S_0^T, (w x)^T B of tokens 0..63                    | meanwhile M from the scores, the chunk
-//                                                              | before's outputs to memory, e^{L_i} (C S_0^T)
-//   w x of tokens 64..127                                      | barrier
-//   MMA: + M x, (w x)^T B of tokens 64..127, the next scores   | meanwhile outputs, then S
+//   workers: S (fp32 registers) -> bf16 operand; w x of tokens 0..63      | MMA: C S_0^T, (w x)^T B
+//            M from the scores; y = e^{L_i} (C S_0^T); w x of 64..127     | MMA: y += M x, (w x)^T B,
+//            outputs, then S                                              |      the next scores
 //
 // Operands.  x, B and C are used as they come (bf16).  The state and M are rounded to bf16 as operands
 // (2^-9 of each term, the size of the outputs' own rounding).  The state itself stays fp32: w x is
@@ -34,8 +33,9 @@ namespace gdn {
 namespace ssm {
 
 constexpr int kQ = 128;        // tokens a chunk
-constexpr int kThreads = 512;  // 16 warps: warp w reads TMEM lanes 32 (w % 4) .. + 31
-constexpr uint32_t kMaxPolls = 1u << 24;
+constexpr int kWorkers = 16;   // worker warps: warp w reads TMEM lanes 32 (w % 4) .. + 31
+constexpr int kThreads = 32 * (kWorkers + 2);  // and a warp that issues, a warp that makes tables
+constexpr int kIssueWarp = kWorkers, kTableWarp = kWorkers + 1;
 constexpr uint32_t kTmemCols = 512;
 // TMEM columns: the scores and, in their place, M in bf16; y; the state's sum; w x in three terms
 constexpr uint32_t kColSc = 0, kColY = 128, kColDs = 256, kColXw = 384;
@@ -117,24 +117,71 @@ struct Cfg {
   static constexpr int kXB = kRows / 64;            // 64-wide blocks of x
   static constexpr int kSC = DK / 4;                // state columns a thread holds
   static constexpr int kYC = kRows / 4;             // output columns a thread works on
-  // shared memory: two stages of [B][x], one C, the state operand, tables, barriers
+  // shared memory: two stages of [B][x], one C, the state operand (the gate's tile takes its place once
+  // C S^T is done), tables, barriers
   static constexpr int kOffB = 0, kOffX = kNB * 16384, kStage = (kNB + kXB) * 16384;
   static constexpr int kOffC = 2 * kStage;
   static constexpr int kOffS = kOffC + kNB * 16384;
-  static constexpr int kOffTab = kOffS + kNB * kRows * 128;
-  static constexpr int kTab = HPC * 3 * kQ * 4;     // L, s and w of a chunk
-  static constexpr int kOffBar = kOffTab + 2 * kTab;
+  static constexpr int kSBytes = kNB * kRows * 128 > kXB * 16384 ? kNB * kRows * 128 : kXB * 16384;
+  static constexpr int kOffTab = kOffS + kSBytes;
+  static constexpr int kTab = HPC * 3 * kQ * 4;     // L, K and w of a chunk
+  static constexpr int kOffBar = kOffTab + kTab;  // mbarriers, TMEM base, abort flag, decays
   static constexpr int kSmemBytes = kOffBar + 256 + 1024;  // + slack for 1024-byte alignment
   static_assert(PB == 64 || (PB == 128 && HPC == 1), "128 rows at most");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+// A wait that gives up when another thread has (or after 2^24 polls), and says so to the others.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t par, volatile int* abort_flag, int* err, int bit) {
+  for (int i = 0; i < 1 << 14; ++i) {
+    if (tc::mbar_wait(bar, par, 1u << 10)) return true;
+    if (*abort_flag) return false;
+  }
+  *abort_flag = 1;
+  atomicOr(err, bit);
+  return false;
 }
 
+__device__ __forceinline__ void tma_prefetch_l2_2d(const void* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// silu of two values: v / (1 + e^-v).
+__device__ __forceinline__ float2 silu2(float2 v) {
+  const float2 t = mul2(v, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+  const float2 d = fma2(make_float2(ssm_ex2(t.x), ssm_ex2(t.y)), make_float2(1.f, 1.f), make_float2(1.f, 1.f));
+  return mul2(v, make_float2(ssm_rcp(d.x), ssm_rcp(d.y)));
+}
+
+// Sixteen lanes (from taddr's) of eight columns: register 2 j + i of thread l holds lane l / 4 + 8 i,
+// column 4 j + l % 4 -- the layout of transposed ldmatrix fragments.
+__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t a, const uint32_t (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st8_nowait(uint32_t a, const uint32_t (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -158,16 +205,22 @@ __device__ __forceinline__ void tmem_load(uint32_t a, float (&v)[N]) {
   else tc::tmem_ld32(a, v);
 }
 
-// The steps of chunk tokens 4 lane .. + 3 of head h (0 past the chunk's n tokens).
-__device__ __forceinline__ void load_steps(const SsmArgs& a, long long t, int n, int h, int lane, float (&d)[4]) {
+// dt of chunk tokens 4 lane .. + 3 of head h, loaded a chunk ahead (the last token's past the chunk's n), and
+// the steps it stands for (0 past n).
+__device__ __forceinline__ void load_dt(const SsmArgs& a, long long t, int n, int h, int lane, uint32_t (&d)[4]) {
 #pragma unroll
-  for (int u = 0; u < 4; ++u) d[u] = 4 * lane + u < n ? ssm_dt(a, t + 4 * lane + u, h) : 0.f;
+  for (int u = 0; u < 4; ++u) d[u] = ssm_load_dt(a, t + min(4 * lane + u, n - 1), h);
+}
+__device__ __forceinline__ void to_steps(const SsmArgs& a, int n, float bias, int lane, const uint32_t (&r)[4],
+                                         float (&d)[4]) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) d[u] = 4 * lane + u < n ? ssm_step_of(a, r[u], bias) : 0.f;
 }
 
 // One warp: the tables of a chunk from its steps.  L in units of log2, inclusive of each token's own
 // decay; returns L of the last token in every lane.  The weights' exponents are sums over the tokens after
 // each, from the end: as differences of L they would carry the rounding of a strong decay's large L.
-// tab: L, s, w (kQ each), or w alone when STATES_ONLY.
+// tab: L, K = L - log2 s, w (kQ each), or w alone when STATES_ONLY.
 template <bool STATES_ONLY>
 __device__ __forceinline__ float make_tables(float* tab, const float (&d)[4], float a_log2, int lane) {
   const float e0 = d[0] * a_log2, e1 = d[1] * a_log2, e2 = d[2] * a_log2, e3 = d[3] * a_log2;
@@ -188,59 +241,60 @@ __device__ __forceinline__ float make_tables(float* tab, const float (&d)[4], fl
   if (STATES_ONLY) {
     reinterpret_cast<float4*>(tab)[lane] = w;
   } else {
-    reinterpret_cast<float4*>(tab)[lane] =
-        make_float4(before + e0, before + (e0 + e1), before + ((e0 + e1) + e2), before + own);
-    reinterpret_cast<float4*>(tab + kQ)[lane] = make_float4(d[0], d[1], d[2], d[3]);
+    const float4 l = make_float4(before + e0, before + (e0 + e1), before + ((e0 + e1) + e2), before + own);
+    reinterpret_cast<float4*>(tab)[lane] = l;
+    reinterpret_cast<float4*>(tab + kQ)[lane] =
+        make_float4(l.x - log2f(d[0]), l.y - log2f(d[1]), l.z - log2f(d[2]), l.w - log2f(d[3]));
     reinterpret_cast<float4*>(tab + 2 * kQ)[lane] = w;
   }
   return end;
 }
 
-// w x of sixteen tokens t .. t + 15 of state row `row` as three bf16 terms into columns col, col + 32
-// and col + 64 (two tokens a column): the A operand of the state's product, 24 bits in all.
-__device__ __forceinline__ void split_xw(const unsigned char* xt, const float* w, int row, int t, uint32_t col) {
-  uint32_t hi[8], mid[8], lo[8];
-  const unsigned char* blk = xt + (row >> 6) * 16384 + (row & 7) * 2;
-  const uint32_t ch = (uint32_t)(row & 63) >> 3;
+// w x of sixteen tokens t .. t + 15 of state rows row0 .. + 31 as three bf16 terms into columns col,
+// col + 32 and col + 64 (two tokens a column) of the warp's lanes: the A operand of the state's product.
+// The terms take fp32's 24 bits eight at a time, so nothing is lost.
+__device__ __forceinline__ void split_xw(const unsigned char* xt, const float* w, int row0, int t, uint32_t col) {
+  const int lane = threadIdx.x & 31;
+  const float2 w0 = *reinterpret_cast<const float2*>(w + t + 2 * (lane & 3));
+  const float2 w1 = *reinterpret_cast<const float2*>(w + t + 8 + 2 * (lane & 3));
+  const uint32_t tok = (uint32_t)(t + ((lane >> 4) << 3) + (lane & 7));  // this lane's row of the four 8 x 8 tiles
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 w4 = *reinterpret_cast<const float4*>(w + t + 4 * i);
-    const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
-    float v[4];
+  for (int rh = 0; rh < 2; ++rh) {
+    const int r = row0 + 16 * rh + (lane & 8);
+    uint32_t x[4], hi[4], mid[4], lo[4];
+    ldsm_x4_t(x, xt + (r >> 6) * 16384 + tc::sw128(tok, (uint32_t)(r & 63) >> 3));
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t raw = *reinterpret_cast<const uint16_t*>(blk + tc::sw128((uint32_t)(t + 4 * i + u), ch));
-      v[u] = __uint_as_float(raw << 16) * wv[u];
+    for (int i = 0; i < 4; ++i) {  // tiles (tokens 0..7, 8..15) x (rows 0..7, 8..15), rows innermost
+      const float2 v =
+          mul2(make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)), i < 2 ? w0 : w1);
+      const uint32_t a = __float_as_uint(v.x), b = __float_as_uint(v.y);
+      hi[i] = __byte_perm(a, b, 0x7632);
+      const float2 m = fma2(make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)),
+                            make_float2(-1.f, -1.f), v);
+      const uint32_t c = __float_as_uint(m.x), d = __float_as_uint(m.y);
+      mid[i] = __byte_perm(c, d, 0x7632);
+      const float2 l = fma2(make_float2(__uint_as_float(c & 0xffff0000u), __uint_as_float(d & 0xffff0000u)),
+                            make_float2(-1.f, -1.f), m);
+      lo[i] = __byte_perm(__float_as_uint(l.x), __float_as_uint(l.y), 0x7632);
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int k = 2 * i + u;
-      float a = v[2 * u], b = v[2 * u + 1];
-      hi[k] = pack_bf16(a, b);
-      a -= __uint_as_float(hi[k] << 16);
-      b -= __uint_as_float(hi[k] & 0xffff0000u);
-      mid[k] = pack_bf16(a, b);
-      a -= __uint_as_float(mid[k] << 16);
-      b -= __uint_as_float(mid[k] & 0xffff0000u);
-      lo[k] = pack_bf16(a, b);
-    }
+    const uint32_t at = col + ((uint32_t)(16 * rh) << 16);
+    tmem_st_16x128b_x2(at, hi);
+    tmem_st_16x128b_x2(at + 32, mid);
+    tmem_st_16x128b_x2(at + 64, lo);
   }
-  tmem_st8_nowait(col, hi);
-  tmem_st8_nowait(col + 32, mid);
-  tmem_st8_nowait(col + 64, lo);
 }
 
-// Issue (w x)^T B of 64 tokens (half `hf` of the tile at shared address bt): the small terms first, so
-// that the accumulator truncates the large sum's steps only.
+// Issue (w x)^T B of 64 tokens (half `hf` of the tile at shared address bt) into columns `sum`: the small
+// terms first, so that the accumulator truncates the large sum's steps only.
 template <int DK>
-__device__ __forceinline__ void issue_state(uint32_t tmem, uint32_t xw, uint32_t bt, int hf, bool start) {
+__device__ __forceinline__ void issue_state(uint32_t sum, uint32_t xw, uint32_t bt, int hf, bool start) {
   constexpr uint32_t kId = tc::idesc_bf16(128, DK, 0, 1);
   const uint64_t bd = tc::sdesc(bt, 16384, 1024, tc::kSw128) + (uint64_t)((hf * 8192) >> 4);
 #pragma unroll
   for (int term = 2; term >= 0; --term)
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks)
-      tc::mma_f16_ta(tmem + kColDs, xw + 32 * term + 8 * ks, bd + (uint64_t)((ks * 2048) >> 4), kId,
+      tc::mma_f16_ta(sum, xw + 32 * term + 8 * ks, bd + (uint64_t)((ks * 2048) >> 4), kId,
                      !(start && term == 2 && ks == 0));
 }
 

@@ -17,8 +17,8 @@ cudaError_t launch_chunk_table(const int32_t*, int, int, int32_t*, int32_t*, int
 
 namespace ssm {
 template <int DK>
-cudaError_t launch_dk(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const SsmArgs&, const Segs&, float*,
-                      float*, const float*, float*, int*, int, int, cudaStream_t);
+cudaError_t launch_dk(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const SsmArgs&,
+                      const Segs&, float*, float*, const float*, float*, int*, int, int, cudaStream_t);
 }
 
 namespace {
@@ -176,10 +176,11 @@ cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* in
   float* decays = reinterpret_cast<float*>(w + l.decays);
   const long long ntok = packed ? (long long)T : (long long)B * T;
   if ((long long)p.slots * (a.Hv / p.hpc) > 0x7fffffffLL) return cudaErrorInvalidValue;
-  CUtensorMap tx = {}, tb = {}, tc_ = {};
+  CUtensorMap tx = {}, tb = {}, tc_ = {}, tz = {};
   if (ntok > 0 && (!token_map(&tx, a.x, a.xs, (long long)a.Hv * a.dv, ntok) ||
                    !token_map(&tb, a.Bm, a.bs, (long long)a.Hk * dk, ntok) ||
-                   !token_map(&tc_, a.Cm, a.cs, (long long)a.Hk * dk, ntok)))
+                   !token_map(&tc_, a.Cm, a.cs, (long long)a.Hk * dk, ntok) ||
+                   (a.z != nullptr && !token_map(&tz, a.z, a.zs, (long long)a.Hv * a.dv, ntok))))
     return cudaErrorInvalidValue;
   ssm::Segs g;
   g.cu = cu;
@@ -190,9 +191,9 @@ cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* in
   g.slots = p.slots;
   auto run = [&](int phase) {
     switch (dk) {
-      case 32: return ssm::launch_dk<32>(tx, tb, tc_, a, g, states, decays, init, fin, err, p.hpc, phase, st);
-      case 64: return ssm::launch_dk<64>(tx, tb, tc_, a, g, states, decays, init, fin, err, p.hpc, phase, st);
-      default: return ssm::launch_dk<128>(tx, tb, tc_, a, g, states, decays, init, fin, err, p.hpc, phase, st);
+      case 32: return ssm::launch_dk<32>(tx, tb, tc_, tz, a, g, states, decays, init, fin, err, p.hpc, phase, st);
+      case 64: return ssm::launch_dk<64>(tx, tb, tc_, tz, a, g, states, decays, init, fin, err, p.hpc, phase, st);
+      default: return ssm::launch_dk<128>(tx, tb, tc_, tz, a, g, states, decays, init, fin, err, p.hpc, phase, st);
     }
   };
   cudaError_t e;

@@ -24,7 +24,7 @@ gdn_ssm_step_kernel(const SsmArgs a, float* __restrict__ state) {
   const int b = blockIdx.x / a.Hv, h = blockIdx.x - b * a.Hv;
   const int hk = h / (a.Hv / a.Hk);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float step = ssm_dt(a, b, h);
+  const float step = ssm_step_of(a, ssm_load_dt(a, b, h), ssm_bias(a, h));
   const SsmDecay decay = ssm_decay(step * a.A[h]);
   const float skip = a.D != nullptr ? a.D[h] : 0.f;
   float bv[E], cv[E];
