@@ -13,11 +13,13 @@
 // reserved for each) through a run of chunks (a segment: the whole sequence when there are enough
 // sequences and heads to fill the device).  Sixteen worker warps do the elementwise work, one thread
 // issues the MMAs and the tile copies, one warp makes the decay tables a chunk ahead; they meet on
-// mbarriers only, so that warps drift apart and one's arithmetic covers another's wait:
+// mbarriers only, so that warps drift apart and one's arithmetic covers another's wait.  A chunk's
+// outputs are worked on after the next chunk's first operands are out, beside its first products:
 //
-//   workers: S (fp32 registers) -> bf16 operand; w x of tokens 0..63      | MMA: C S_0^T, (w x)^T B
-//            M from the scores; y = e^{L_i} (C S_0^T); w x of 64..127     | MMA: y += M x, (w x)^T B,
-//            outputs, then S                                              |      the next scores
+//   workers: M from the scores; y = e^{L_i} (C S_0^T); w x of 64..127  | MMA: C S_0^T
+//            silu(z)                                                  | MMA: (w x)^T B of 64..127, y += M x
+//            S; the next chunk's S -> bf16 and w x of tokens 0..63    | MMA: the next scores
+//            outputs                                                  | MMA: the next (w x)^T B of 0..63
 //
 // Operands.  x, B and C are used as they come (bf16).  The state and M are rounded to bf16 as operands
 // (2^-9 of each term, the size of the outputs' own rounding).  The state itself stays fp32: w x is
@@ -108,6 +110,11 @@ __device__ __forceinline__ bool find_seg(const Segs& g, int i, Seg& s) {
   return true;
 }
 
+// Tensor maps of a call: boxes of 128 tokens x 64 columns, 128-byte swizzle (out: 32 tokens).
+struct Maps {
+  CUtensorMap x, b, c, z, out;
+};
+
 // PB: state rows reserved for a head (64 or 128; a head of dv = 32 leaves the upper half unused);
 // HPC: heads of the CTA.
 template <int DK, int PB, int HPC>
@@ -125,22 +132,39 @@ struct Cfg {
   static constexpr int kSBytes = kNB * kRows * 128 > kXB * 16384 ? kNB * kRows * 128 : kXB * 16384;
   static constexpr int kOffTab = kOffS + kSBytes;
   static constexpr int kTab = HPC * 3 * kQ * 4;     // L, K and w of a chunk
-  static constexpr int kOffBar = kOffTab + kTab;  // mbarriers, TMEM base, abort flag, decays
+  static constexpr int kOffBar = kOffTab + 2 * kTab;  // mbarriers, TMEM base, abort flag, decays
   static constexpr int kSmemBytes = kOffBar + 256 + 1024;  // + slack for 1024-byte alignment
   static_assert(PB == 64 || (PB == 128 && HPC == 1), "128 rows at most");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 };
 
-// A wait that gives up when another thread has (or after 2^24 polls), and says so to the others.
+// A wait that gives up when another thread has (or after 2^26 polls), and says so to the others.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t par, volatile int* abort_flag, int* err, int bit) {
-  for (int i = 0; i < 1 << 14; ++i) {
-    if (tc::mbar_wait(bar, par, 1u << 10)) return true;
-    if (*abort_flag) return false;
+  const uint32_t addr = smem_u32(bar);
+  for (uint32_t i = 0; i < 1u << 26; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(addr), "r"(par)
+        : "memory");
+    if (done) return true;
+    if ((i & 1023u) == 1023u && *abort_flag) return false;
   }
   *abort_flag = 1;
   atomicOr(err, bit);
   return false;
 }
+
+// A box of a tile from shared memory to global memory, in the thread's next bulk group.
+__device__ __forceinline__ void tma_store_2d(const void* map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(map), "r"(x),
+               "r"(y), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;\n" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
 
 __device__ __forceinline__ void tma_prefetch_l2_2d(const void* map, int x, int y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(map), "r"(x), "r"(y) : "memory");
@@ -168,11 +192,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
-// silu of two values: v / (1 + e^-v).
+// silu of two values, v / (1 + e^-v), with one reciprocal: 1 / a = b / (a b).  The exponents stop at 2^62, so
+// that the product stays finite: below -43 a value v gives v 2^-62 where less would be exact.
 __device__ __forceinline__ float2 silu2(float2 v) {
   const float2 t = mul2(v, make_float2(-1.4426950408889634f, -1.4426950408889634f));
-  const float2 d = fma2(make_float2(ssm_ex2(t.x), ssm_ex2(t.y)), make_float2(1.f, 1.f), make_float2(1.f, 1.f));
-  return mul2(v, make_float2(ssm_rcp(d.x), ssm_rcp(d.y)));
+  const float2 d = fma2(make_float2(ssm_ex2(fminf(t.x, 62.f)), ssm_ex2(fminf(t.y, 62.f))), make_float2(1.f, 1.f),
+                        make_float2(1.f, 1.f));
+  const float r = ssm_rcp(d.x * d.y);
+  return mul2(v, mul2(make_float2(r, r), make_float2(d.y, d.x)));
 }
 
 // Sixteen lanes (from taddr's) of eight columns: register 2 j + i of thread l holds lane l / 4 + 8 i,

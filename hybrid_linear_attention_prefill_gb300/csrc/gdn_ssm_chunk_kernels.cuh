@@ -7,6 +7,8 @@
 namespace gdn {
 namespace ssm {
 
+constexpr int kBars = 14;
+
 // What both kernels set up: shared memory from a 1024-byte boundary, TMEM, barriers.
 struct Frame {
   unsigned char* sm;
@@ -24,7 +26,7 @@ __device__ __forceinline__ Frame make_frame(unsigned char* raw) {
   f.sm = raw + pad;
   f.sb = r + pad;
   f.bars = reinterpret_cast<uint64_t*>(f.sm + C::kOffBar);
-  f.tmem_slot = reinterpret_cast<uint32_t*>(f.bars + 13);
+  f.tmem_slot = reinterpret_cast<uint32_t*>(f.bars + kBars);
   f.abort_flag = reinterpret_cast<volatile int*>(f.tmem_slot + 1);
   f.lend = reinterpret_cast<SsmDecay*>(f.tmem_slot + 2);
   f.tabs = reinterpret_cast<float*>(f.sm + C::kOffTab);
@@ -50,17 +52,18 @@ template <int DK, int PB, int HPC>
 __global__ void __launch_bounds__(kThreads, 1)
 gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_z,
-                     const SsmArgs a, const Segs g,
+                     const __grid_constant__ CUtensorMap tm_o, const SsmArgs a, const Segs g,
                      const float* seg_state, const float* init, float* fin, int* __restrict__ err) {
   using C = Cfg<DK, PB, HPC>;
   extern __shared__ unsigned char smem_raw[];
   const Frame f = make_frame<C>(smem_raw);
-  // Completed by the MMAs, once a chunk each: scores, C S^T, state half 0, y, state half 1.  By copies: the two
-  // stages, C, the gate's tile.  By the worker warps: the first operands of a chunk (the state, w x), the second
-  // (M, y, w x), the gate read.  By the table warp: a chunk's tables, its stage loaded.
-  uint64_t *b_sc = f.bars, *b_in = f.bars + 1, *b_d0 = f.bars + 2, *b_y = f.bars + 3, *b_d1 = f.bars + 4,
-           *b_st = f.bars + 5, *b_c = f.bars + 7, *b_z = f.bars + 8, *w_a = f.bars + 9, *w_b = f.bars + 10,
-           *w_z = f.bars + 11, *b_tab = f.bars + 12;
+  // Completed by the MMAs, once a chunk each: scores, (w x)^T B of half 0 and C S^T, (w x)^T B of half 1, y.  By
+  // copies: the two stages, C, the gate's tile.  By the worker warps: the first operands of a chunk (the state,
+  // w x), the second (M, y, w x), the gate read, y read, the outputs out of the x tile.  By the table warp: a
+  // chunk's tables, its stage loaded.
+  uint64_t *b_sc = f.bars, *b_in = f.bars + 1, *b_d1 = f.bars + 2, *b_y = f.bars + 3, *b_st = f.bars + 4,
+           *b_c = f.bars + 6, *b_z = f.bars + 7, *w_a = f.bars + 8, *w_b = f.bars + 9, *w_z = f.bars + 10,
+           *w_y = f.bars + 11, *w_s = f.bars + 12, *b_tab = f.bars + 13;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == kIssueWarp) {
@@ -74,7 +77,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     }
   }
   if (tid == 0) {
-    for (int i = 0; i < 13; ++i) tc::mbar_init(&f.bars[i], i >= 9 && i < 12 ? kWorkers : 1);
+    for (int i = 0; i < kBars; ++i) tc::mbar_init(&f.bars[i], i >= 8 && i < 13 ? kWorkers : 1);
     tc::fence_mbar_init();
     *f.abort_flag = 0;
   }
@@ -145,8 +148,11 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
         const uint32_t stage = f.sb + (c & 1) * C::kStage;
         if (!(ok = wait1(w_a, par, 1))) break;
         tc::fence_after();
-        // the chunk before's stage is free: its outputs are written, its products done
-        if (c > 0 && c + 1 < nc) load(c + 1);
+        issue_state<DK>(tmem + kColDs, tmem + kColXw, stage + C::kOffB, 0, true);
+        if (c > 0) {  // the chunk before's y has been read
+          if (!(ok = wait1(w_y, par ^ 1u, 1))) break;
+          tc::fence_after();
+        }
         {
           constexpr uint32_t kId = tc::idesc_bf16(128, C::kRows, 0, 0);
           const uint64_t bd = tc::sdesc(f.sb + C::kOffS, 16, 1024, tc::kSw128);
@@ -156,15 +162,19 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                          bd + (uint64_t)(((ks >> 2) * (C::kRows * 128) + (ks & 3) * 32) >> 4), kId, ks > 0);
           tc::commit(b_in);
         }
-        issue_state<DK>(tmem + kColDs, tmem + kColXw, stage + C::kOffB, 0, true);
-        tc::commit(b_d0);
         if (c + 1 < nc || a.z != nullptr) {
           if (!(ok = wait1(b_in, par, 1))) break;
           if (a.z != nullptr) load_z(c);  // over the state operand
           if (c + 1 < nc) load_c(c + 1);
+          if (c > 0 && c + 1 < nc) {  // the stage of the chunk before
+            if (!(ok = wait1(w_s, par ^ 1u, 1))) break;
+            load(c + 1);
+          }
         }
         if (!(ok = wait1(w_b, par, 1))) break;
         tc::fence_after();
+        issue_state<DK>(tmem + kColDs, tmem + kColXw, stage + C::kOffB, 1, false);
+        tc::commit(b_d1);
         {
           constexpr uint32_t kId = tc::idesc_bf16(128, PB, 0, 1);
 #pragma unroll
@@ -177,8 +187,6 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
           }
           tc::commit(b_y);
         }
-        issue_state<DK>(tmem + kColDs, tmem + kColXw, stage + C::kOffB, 1, false);
-        tc::commit(b_d1);
         if (c + 1 < nc) {  // the next scores take M's place, once M x is done
           if (!(ok = wait1(b_y, par, 1))) break;
           ok = scores(c + 1);
@@ -197,22 +205,30 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       if (nc > 0) load_dt(a, tok0, ntok, h0 + hh, lane, raw[hh]);
     }
     for (int c = 0; c < nc; ++c) {
-      // The tables of the chunk before are read up to its second operands.
-      if (c > 0 && !wait(w_b, (uint32_t)((c - 1) & 1), 1)) break;
+      // The tables of chunk c - 2 were read up to its second operands.  Every phase is waited for in turn: a
+      // parity names the last phase that ended, whichever that is.
+      if (c > 1 && !wait(w_b, (uint32_t)(c & 1), 1)) break;
 #pragma unroll
       for (int hh = 0; hh < HPC; ++hh) {
         float d[4];
         to_steps(a, ntok - c * kQ, bias[hh], lane, raw[hh], d);
         if (c + 1 < nc) load_dt(a, tok0 + (long long)(c + 1) * kQ, ntok - (c + 1) * kQ, h0 + hh, lane, raw[hh]);
-        const float end = make_tables<false>(f.tabs + hh * 3 * kQ, d, a_log2[hh], lane);
+        const float end = make_tables<false>(f.tabs + (c & 1) * (C::kTab / 4) + hh * 3 * kQ, d, a_log2[hh], lane);
         if (lane == 0) f.lend[(c & 1) * HPC + hh] = ssm_decay(end * 0.6931471805599453f);
       }
       if (!wait(&b_st[c & 1], (uint32_t)((c >> 1) & 1), 2)) break;
       if (lane == 0) arrive(b_tab);
-      if (lane == 0 && a.z != nullptr) {  // the chunk's gate tile into L2: its place is free only late in the chunk
+      if (lane == 0) {  // into L2, where their places in shared memory are free only late: this chunk's gate, the next x and B
+        const int t = (int)(tok0 + (long long)c * kQ);
 #pragma unroll
-        for (int i = 0; i < C::kXB; ++i)
-          tma_prefetch_l2_2d(&tm_z, PB == 64 ? (h0 + i) * a.dv : h0 * a.dv + 64 * i, (int)(tok0 + (long long)c * kQ));
+        for (int i = 0; i < C::kXB; ++i) {
+          const int col = PB == 64 ? (h0 + i) * a.dv : h0 * a.dv + 64 * i;
+          if (a.z != nullptr) tma_prefetch_l2_2d(&tm_z, col, t);
+          if (c > 0 && c + 1 < nc) tma_prefetch_l2_2d(&tm_x, col, t + kQ);
+        }
+        if (c > 0 && c + 1 < nc)
+#pragma unroll
+          for (int i = 0; i < C::kNB; ++i) tma_prefetch_l2_2d(&tm_b, hk * DK + 64 * i, t + kQ);
       }
       __syncwarp();
     }
@@ -244,19 +260,16 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     const bool my_cols = yp < a.dv;
     const float skip = a.D != nullptr && my_cols ? a.D[h0 + yh] : 0.f;
     const int mt = 32 * q4 + lane / kP, mp = lane % kP;  // memory order: token mt + (32 / kP) i, piece mp
+    const int quad = 2 + 4 * (yc >> 6) + q4;  // named barrier of the warps that share 32 tokens of a 64-wide block
     const uint32_t yoff = (uint32_t)(yc >> 6) * 16384, ych = (uint32_t)(yc & 63) >> 3;
-    const float* tab = f.tabs;
     const bool gate = a.z != nullptr;
 
     bool ok = true;
-    for (int c = 0; c < nc; ++c) {
-      const uint32_t par = (uint32_t)(c & 1);
+    // The first operands of chunk c: the state, and w x of its first 64 tokens.
+    auto first_operands = [&](int c) {
       unsigned char* stage = f.sm + (c & 1) * C::kStage;
-      unsigned char* xt = stage + C::kOffX;
-      unsigned char* yt = xt + yoff;
       const int n = min(kQ, ntok - c * kQ);
-
-      if (!(ok = wait(b_tab, par, 1))) break;
+      if (!wait(b_tab, (uint32_t)(c & 1), 1)) return false;
       if (n < kQ) {  // rows of the sequence after this one: zeros, so that no value of theirs meets a zero weight
         const int rows = kQ - n;
         for (int e = tid; e < rows * 8 * (C::kNB + C::kXB); e += 32 * kWorkers)
@@ -264,9 +277,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
               make_uint4(0, 0, 0, 0);
         asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kWorkers) : "memory");
       }
-
-      // ---- the state as an operand; w x of the first 64 tokens ----------------------------------
-      if (gate && c > 0 && !(ok = wait(w_z, par ^ 1u, 1))) break;  // every warp has read the gate's tile there
+      if (gate && c > 0 && !wait(w_z, (uint32_t)((c - 1) & 1), 1)) return false;  // every warp has read the gate there
       if (row < C::kRows) {
 #pragma unroll
         for (int i = 0; i < C::kSC; i += 8) {
@@ -277,12 +288,23 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                          pack_bf16(st[i + 6], st[i + 7]));
         }
       }
-      if (32 * q4 < C::kRows) split_xw(xt, tab + hr * 3 * kQ + 2 * kQ, 32 * q4, 16 * cg, tq + kColXw + 8 * cg);
+      const float* tab = f.tabs + (c & 1) * (C::kTab / 4);
+      if (32 * q4 < C::kRows)
+        split_xw(stage + C::kOffX, tab + hr * 3 * kQ + 2 * kQ, 32 * q4, 16 * cg, tq + kColXw + 8 * cg);
       tmem_st_wait();
       tc::fence_proxy_async();
       tc::fence_before();
       __syncwarp();
       if (lane == 0) arrive(w_a);
+      return true;
+    };
+    if (nc > 0) ok = first_operands(0);
+    for (int c = 0; ok && c < nc; ++c) {
+      const uint32_t par = (uint32_t)(c & 1);
+      unsigned char* xt = f.sm + (c & 1) * C::kStage + C::kOffX;
+      unsigned char* yt = xt + yoff;
+      const float* tab = f.tabs + (c & 1) * (C::kTab / 4);
+      const int n = min(kQ, ntok - c * kQ);
 
       // ---- M from the scores, in their place: eight columns a head of each 16 ------------------------
       if (!(ok = wait(b_sc, par, 1))) break;
@@ -323,8 +345,13 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
           for (int hh = 0; hh < HPC; ++hh) tmem_st8_nowait(col + 8 * hh, m);
         }
       }
+      if (c > 0) {  // the chunk before's outputs have left its x tile
+        bulk_wait_read();
+        __syncwarp();
+        if (lane == 0) arrive(w_s);
+      }
       // ---- y = e^{L_i} (C S^T), in place; w x of the other 64 tokens ----------------------------------
-      if (!(ok = wait(b_d0, par, 1))) break;  // and C S^T before it
+      if (!(ok = wait(b_in, par, 1))) break;  // and (w x)^T B of the first 64 before it
       tc::fence_after();
       {
         float y[C::kYC];
@@ -347,7 +374,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       __syncwarp();
       if (lane == 0) arrive(w_b);
 
-      // ---- outputs, by way of the warp's own part of the x tile -----------------------------------------
+      // ---- the gate -------------------------------------------------------------------------------------
       // Of this thread's row of the gate, half goes through silu while M x runs; the rest waits as it is (all of
       // it would not fit the registers).
       uint4 zr[kP];
@@ -368,38 +395,6 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
 #pragma unroll
           for (int u = 0; u < 4; ++u) gv[4 * i + u] = gates(i, u);
       }
-      if (!(ok = wait(b_y, par, 1))) break;
-      tc::fence_after();
-      {
-#pragma unroll
-        for (int i = 0; i < kP; ++i) {  // eight columns of this thread's own row at a time
-          uint4* at = reinterpret_cast<uint4*>(yt + tc::sw128((uint32_t)row, ych + i));
-          float y[8];
-          tc::tmem_ld8(tq + kColY + yc + 8 * i, y);
-          const uint4 xr = *at;
-          const uint32_t x4[4] = {xr.x, xr.y, xr.z, xr.w};
-          float2 v[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            v[u] = fma2(make_float2(__uint_as_float(x4[u] << 16), __uint_as_float(x4[u] & 0xffff0000u)),
-                        make_float2(skip, skip), make_float2(y[2 * u], y[2 * u + 1]));
-            if (gate) v[u] = mul2(v[u], i < kP / 2 ? gv[4 * (i % (kP / 2)) + u] : gates(i, u));
-          }
-          *at = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y),
-                           pack_bf16(v[3].x, v[3].y));
-        }
-        __syncwarp();
-        if (my_cols) {
-          __nv_bfloat16* o = a.out + ((size_t)(tok0 + (long long)c * kQ) * a.Hv + h0 + yh) * a.dv + yp + 8 * mp;
-#pragma unroll
-          for (int i = 0; i < kP; ++i) {
-            const int t = mt + (32 / kP) * i;
-            if (t < n)
-              *reinterpret_cast<uint4*>(o + (size_t)t * a.Hv * a.dv) =
-                  *reinterpret_cast<const uint4*>(yt + tc::sw128((uint32_t)t, ych + mp));
-          }
-        }
-      }
       // ---- S = e^{L_last} S + the chunk's sum ---------------------------------------------------------
       if (!(ok = wait(b_d1, par, 1))) break;
       tc::fence_after();
@@ -416,6 +411,64 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
           st[i + 1] = r.y;
         }
       }
+      if (c + 1 < nc && !(ok = first_operands(c + 1))) break;
+      // ---- outputs, by way of the warp's own part of the x tile -----------------------------------------
+      if (!(ok = wait(b_y, par, 1))) break;
+      tc::fence_after();
+      {
+        for (int i0 = 0; i0 < kP; i0 += 2) {  // sixteen columns of this thread's own row at a time
+          float y[16];
+          tc::tmem_ld16(tq + kColY + yc + 8 * i0, y);
+          if (i0 + 2 == kP) {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(w_y);
+          }
+          uint4 x[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const uint4*>(yt + tc::sw128((uint32_t)row, ych + i0 + i));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t x4[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            float2 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              v[u] = fma2(make_float2(__uint_as_float(x4[u] << 16), __uint_as_float(x4[u] & 0xffff0000u)),
+                          make_float2(skip, skip), make_float2(y[8 * i + 2 * u], y[8 * i + 2 * u + 1]));
+              if (gate) v[u] = mul2(v[u], i0 + i < kP / 2 ? gv[4 * ((i0 + i) % (kP / 2)) + u] : gates(i0 + i, u));
+            }
+            *reinterpret_cast<uint4*>(yt + tc::sw128((uint32_t)row, ych + i0 + i)) = make_uint4(
+                pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
+          }
+        }
+        if (a.dv >= 64 && 32 * q4 + 32 <= n) {  // 32 whole tokens of 64 columns: one copy by the first of their warps
+          tc::fence_proxy_async();
+          asm volatile("bar.sync %0, %1;\n" ::"r"(quad), "n"(32 * (64 / C::kYC)) : "memory");
+          if ((yc & 63) == 0 && lane == 0) {
+            tma_store_2d(&tm_o, smem_u32(yt) + 32 * q4 * 128, (h0 + yh) * a.dv + yp, (int)(tok0 + (long long)c * kQ) + 32 * q4);
+            bulk_commit();
+          }
+          __syncwarp();
+        } else {
+          __syncwarp();
+          if (my_cols) {
+            __nv_bfloat16* o = a.out + ((size_t)(tok0 + (long long)c * kQ) * a.Hv + h0 + yh) * a.dv + yp + 8 * mp;
+#pragma unroll
+            for (int i = 0; i < kP; ++i) {
+              const int t = mt + (32 / kP) * i;
+              if (t < n)
+                *reinterpret_cast<uint4*>(o + (size_t)t * a.Hv * a.dv) =
+                    *reinterpret_cast<const uint4*>(yt + tc::sw128((uint32_t)t, ych + mp));
+            }
+          }
+          tc::fence_proxy_async();
+        }
+      }
+    }
+    bulk_wait_read();
+    if (!ok) {  // another warp may have passed the wait that this one gave up, and stand at a barrier between warps
+      asm volatile("bar.arrive 1, %0;\n" ::"n"(32 * kWorkers) : "memory");
+      asm volatile("bar.arrive %0, %1;\n" ::"r"(quad), "n"(32 * (64 / C::kYC)) : "memory");
     }
     if (ok && fin != nullptr && s.last && my_row) {
       float* dst = fin + (((size_t)s.b * a.Hv + h0 + hr) * a.dv + p) * DK + C::kSC * cg;
@@ -427,7 +480,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
   tc::fence_before();
   __syncthreads();
   if (*f.abort_flag && warp == kIssueWarp && lane == 0) {  // let what is in flight land, bounded again
-    for (int i = 0; i < 9; ++i)
+    for (int i = 0; i < 8; ++i)
       for (uint32_t par = 0; par < 2; ++par) (void)tc::mbar_wait(&f.bars[i], par, 1u << 14);
   }
   __syncwarp();
@@ -444,7 +497,7 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
   using C = Cfg<DK, PB, HPC>;
   extern __shared__ unsigned char smem_raw[];
   const Frame f = make_frame<C>(smem_raw);
-  uint64_t *b_d = f.bars, *b_st = f.bars + 1, *w_a = f.bars + 9, *b_tab = f.bars + 12;
+  uint64_t *b_d = f.bars, *b_st = f.bars + 1, *w_a = f.bars + 8, *b_tab = f.bars + 13;
   const int nhb = a.Hv / HPC, seg = blockIdx.x / nhb;
   Seg s;
   if (!find_seg(g, seg, s) || s.last) return;  // a last segment's sum is nobody's start
@@ -454,7 +507,7 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
     tc::tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < 13; ++i) tc::mbar_init(&f.bars[i], i == 9 ? kWorkers : 1);
+    for (int i = 0; i < kBars; ++i) tc::mbar_init(&f.bars[i], i == 8 ? kWorkers : 1);
     tc::fence_mbar_init();
     *f.abort_flag = 0;
   }
@@ -581,8 +634,7 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
 }
 
 template <int DK, int PB, int HPC>
-cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tb, const CUtensorMap& tcm, const CUtensorMap& tz,
-                   const SsmArgs& a,
+cudaError_t launch(const Maps& m, const SsmArgs& a,
                    const Segs& g, float* seg_state, float* seg_decay, const float* init, float* fin, int* err,
                    int phase, cudaStream_t st) {
   using C = Cfg<DK, PB, HPC>;
@@ -590,7 +642,7 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tb, const CUtensorM
   if (phase == 0) {
     const cudaError_t e = set_smem_limit_once<gdn_ssm_segment_kernel<DK, PB, HPC>>(C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    gdn_ssm_segment_kernel<DK, PB, HPC><<<grid, kThreads, C::kSmemBytes, st>>>(tx, tb, a, g, seg_state, seg_decay, err);
+    gdn_ssm_segment_kernel<DK, PB, HPC><<<grid, kThreads, C::kSmemBytes, st>>>(m.x, m.b, a, g, seg_state, seg_decay, err);
     return cudaGetLastError();
   }
   cudaError_t e = set_smem_limit_once<gdn_ssm_chunk_kernel<DK, PB, HPC>>(C::kSmemBytes);
@@ -605,20 +657,19 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tb, const CUtensorM
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = g.len != 0 ? 1 : 0;  // behind the combine kernel of the same call
-  e = cudaLaunchKernelEx(&cfg, gdn_ssm_chunk_kernel<DK, PB, HPC>, tx, tb, tcm, tz, a, g, (const float*)seg_state, init, fin,
+  e = cudaLaunchKernelEx(&cfg, gdn_ssm_chunk_kernel<DK, PB, HPC>, m.x, m.b, m.c, m.z, m.out, a, g, (const float*)seg_state, init, fin,
                          err);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
 template <int DK>
-cudaError_t launch_dk(const CUtensorMap& tx, const CUtensorMap& tb, const CUtensorMap& tcm, const CUtensorMap& tz,
-                      const SsmArgs& a,
+cudaError_t launch_dk(const Maps& m, const SsmArgs& a,
                       const Segs& g, float* seg_state, float* seg_decay, const float* init, float* fin, int* err,
                       int hpc, int phase, cudaStream_t st) {
-  if (a.dv == 128) return launch<DK, 128, 1>(tx, tb, tcm, tz, a, g, seg_state, seg_decay, init, fin, err, phase, st);
-  if (hpc == 2) return launch<DK, 64, 2>(tx, tb, tcm, tz, a, g, seg_state, seg_decay, init, fin, err, phase, st);
-  return launch<DK, 64, 1>(tx, tb, tcm, tz, a, g, seg_state, seg_decay, init, fin, err, phase, st);
+  if (a.dv == 128) return launch<DK, 128, 1>(m, a, g, seg_state, seg_decay, init, fin, err, phase, st);
+  if (hpc == 2) return launch<DK, 64, 2>(m, a, g, seg_state, seg_decay, init, fin, err, phase, st);
+  return launch<DK, 64, 1>(m, a, g, seg_state, seg_decay, init, fin, err, phase, st);
 }
 
 }  // namespace ssm

@@ -17,8 +17,8 @@ cudaError_t launch_chunk_table(const int32_t*, int, int, int32_t*, int32_t*, int
 
 namespace ssm {
 template <int DK>
-cudaError_t launch_dk(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const SsmArgs&,
-                      const Segs&, float*, float*, const float*, float*, int*, int, int, cudaStream_t);
+cudaError_t launch_dk(const Maps&, const SsmArgs&, const Segs&, float*, float*, const float*, float*, int*, int, int,
+                      cudaStream_t);
 }
 
 namespace {
@@ -147,10 +147,11 @@ Layout layout(const Plan& p, int B, int Hv, int dk, int dv, bool packed) {
   return l;
 }
 
-bool token_map(CUtensorMap* m, const void* base, long long stride, long long width, long long tokens) {
+bool token_map(CUtensorMap* m, const void* base, long long stride, long long width, long long tokens,
+               cuuint32_t box_tokens = ssm::kQ) {
   const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)tokens};
   const cuuint64_t strides[1] = {(cuuint64_t)(tokens > 1 ? stride : (width + 7) / 8 * 8) * 2};
-  const cuuint32_t box[2] = {64, ssm::kQ};
+  const cuuint32_t box[2] = {64, box_tokens};
   return make_map16(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
@@ -176,11 +177,12 @@ cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* in
   float* decays = reinterpret_cast<float*>(w + l.decays);
   const long long ntok = packed ? (long long)T : (long long)B * T;
   if ((long long)p.slots * (a.Hv / p.hpc) > 0x7fffffffLL) return cudaErrorInvalidValue;
-  CUtensorMap tx = {}, tb = {}, tc_ = {}, tz = {};
-  if (ntok > 0 && (!token_map(&tx, a.x, a.xs, (long long)a.Hv * a.dv, ntok) ||
-                   !token_map(&tb, a.Bm, a.bs, (long long)a.Hk * dk, ntok) ||
-                   !token_map(&tc_, a.Cm, a.cs, (long long)a.Hk * dk, ntok) ||
-                   (a.z != nullptr && !token_map(&tz, a.z, a.zs, (long long)a.Hv * a.dv, ntok))))
+  ssm::Maps m = {};
+  const long long wv = (long long)a.Hv * a.dv, wk = (long long)a.Hk * dk;
+  if (ntok > 0 &&
+      (!token_map(&m.x, a.x, a.xs, wv, ntok) || !token_map(&m.b, a.Bm, a.bs, wk, ntok) ||
+       !token_map(&m.c, a.Cm, a.cs, wk, ntok) || (a.z != nullptr && !token_map(&m.z, a.z, a.zs, wv, ntok)) ||
+       !token_map(&m.out, a.out, wv, wv, ntok, 32)))
     return cudaErrorInvalidValue;
   ssm::Segs g;
   g.cu = cu;
@@ -191,9 +193,9 @@ cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* in
   g.slots = p.slots;
   auto run = [&](int phase) {
     switch (dk) {
-      case 32: return ssm::launch_dk<32>(tx, tb, tc_, tz, a, g, states, decays, init, fin, err, p.hpc, phase, st);
-      case 64: return ssm::launch_dk<64>(tx, tb, tc_, tz, a, g, states, decays, init, fin, err, p.hpc, phase, st);
-      default: return ssm::launch_dk<128>(tx, tb, tc_, tz, a, g, states, decays, init, fin, err, p.hpc, phase, st);
+      case 32: return ssm::launch_dk<32>(m, a, g, states, decays, init, fin, err, p.hpc, phase, st);
+      case 64: return ssm::launch_dk<64>(m, a, g, states, decays, init, fin, err, p.hpc, phase, st);
+      default: return ssm::launch_dk<128>(m, a, g, states, decays, init, fin, err, p.hpc, phase, st);
     }
   };
   cudaError_t e;
