@@ -32,8 +32,8 @@ struct Plan {
 };
 
 // Heads a CTA and the segments' length, from the sizes alone (a packed batch's lengths are on the device:
-// taken as equal).  In units of an output pass's chunk step, a segmented call costs its waves times the
-// segment's chunks, 0.4 of that again for the sums, and about two steps for the join.
+// taken as equal).  In units of an output pass's chunk step: a CTA costs its chunks and about one more to start
+// and drain, 0.4 of a step a chunk and one in the pass of the sums, and the join about one.
 Plan make_plan(int B, int T, int Hk, int Hv, int dv, bool packed, int sms) {
   Plan p;
   p.hpc = dv < 128 && (Hv / Hk) % 2 == 0 ? 2 : 1;
@@ -43,12 +43,12 @@ Plan make_plan(int B, int T, int Hk, int Hv, int dv, bool packed, int sms) {
   const int nc = packed ? std::max(1, (int)(((long long)T + B - 1) / B + ssm::kQ - 1) / ssm::kQ)
                         : (T + ssm::kQ - 1) / ssm::kQ;
   auto waves = [&](long long ctas) { return (ctas + sms - 1) / sms; };
-  double best = (double)waves(hb * B) * nc;
+  double best = (double)waves(hb * B) * (nc + 1);
   for (int n = 2; n <= nc; ++n) {  // segments a sequence
     const int len = (nc + n - 1) / n;
     if (n > 2 && (nc + n - 2) / (n - 1) == len) continue;  // the same length as with fewer
     const long long segs = (nc + len - 1) / len;
-    const double cost = (double)len * (waves(hb * B * segs) + 0.4 * waves(hb * B * (segs - 1))) + 2.0;
+    const double cost = waves(hb * B * segs) * (len + 1.0) + waves(hb * B * (segs - 1)) * (0.4 * len + 1.0) + 1.0;
     if (cost < best) {
       best = cost;
       p.len = len;
