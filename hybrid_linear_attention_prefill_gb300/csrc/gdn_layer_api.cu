@@ -93,10 +93,10 @@ gdn::SsmArgs ssm_args(const void* x, long long xs, const void* dt, long long dts
 
 extern "C" {
 
-int gdn_conv(const void* x, long long x_stride, const void* weight, const void* bias, const int32_t* cu_seqlens,
-             const void* init_state, void* out, void* final_state, int B, int T, int C, int K, unsigned flags,
-             void* stream) {
+int gdn_conv(const gdn_conv_args* args) {
   gdn::clear_cuda_error();
+  if (args == nullptr) return GDN_ERR_ARG;
+  const auto& [x, x_stride, weight, bias, cu_seqlens, init_state, out, final_state, B, T, C, K, flags, stream] = *args;
   if (!conv_sizes_ok(B, T, C, K, flags)) return GDN_ERR_ARG;
   if (B == 0) return GDN_OK;
   const long long ntok = cu_seqlens != nullptr ? (long long)T : (long long)B * T;
@@ -117,9 +117,10 @@ int gdn_conv(const void* x, long long x_stride, const void* weight, const void* 
                                K, (flags & GDN_CONV_SILU) != 0, static_cast<cudaStream_t>(stream)));
 }
 
-int gdn_conv_step(const void* x, long long x_stride, const void* weight, const void* bias, void* state, void* out,
-                  int B, int C, int K, unsigned flags, void* stream) {
+int gdn_conv_step(const gdn_conv_step_args* args) {
   gdn::clear_cuda_error();
+  if (args == nullptr) return GDN_ERR_ARG;
+  const auto& [x, x_stride, weight, bias, state, out, B, C, K, flags, stream] = *args;
   if (!conv_sizes_ok(B, 1, C, K, flags)) return GDN_ERR_ARG;
   if (B == 0) return GDN_OK;
   if (weight == nullptr || state == nullptr || out == nullptr) return GDN_ERR_ARG;
@@ -136,12 +137,10 @@ size_t gdn_ssm_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv, int
   return gdn::ssm_scan_workspace(B, T, Hk, Hv, dk, dv, packed);
 }
 
-int gdn_ssm_scan(const void* x, long long x_stride, const void* dt, long long dt_stride, const float* A,
-                 const void* Bm, long long b_stride, const void* Cm, long long c_stride, const float* D,
-                 const void* z, long long z_stride, const float* dt_bias, const int32_t* cu_seqlens,
-                 const float* init_state, void* out, float* final_state, int B, int T, int Hk, int Hv, int dk,
-                 int dv, unsigned flags, void* workspace, size_t workspace_bytes, void* stream) {
+int gdn_ssm_scan(const gdn_ssm_scan_args* args) {
   gdn::clear_cuda_error();
+  if (args == nullptr) return GDN_ERR_ARG;
+  const auto& [x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, D, z, z_stride, dt_bias, cu_seqlens, init_state, out, final_state, B, T, Hk, Hv, dk, dv, flags, workspace_given, workspace_bytes, stream] = *args;
   if (!ssm_sizes_ok(B, T, Hk, Hv, dk, dv) || (flags & ~(GDN_SSM_SOFTPLUS | GDN_SSM_DT_F32)) != 0) return GDN_ERR_ARG;
   if (B == 0) return GDN_OK;
   const long long ntok = cu_seqlens != nullptr ? (long long)T : (long long)B * T;
@@ -156,6 +155,7 @@ int gdn_ssm_scan(const void* x, long long x_stride, const void* dt, long long dt
   if (ntok == 0 && final_state == nullptr) return GDN_OK;
   if (ntok == 0 && A == nullptr) return GDN_ERR_ARG;
   const size_t need = gdn::ssm_scan_workspace(B, T, Hk, Hv, dk, dv, cu_seqlens != nullptr);
+  void* workspace = workspace_given;
   if (workspace == nullptr) {
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
@@ -170,11 +170,10 @@ int gdn_ssm_scan(const void* x, long long x_stride, const void* dt, long long dt
                                    static_cast<cudaStream_t>(stream)));
 }
 
-int gdn_ssm_step(const void* x, long long x_stride, const void* dt, long long dt_stride, const float* A,
-                 const void* Bm, long long b_stride, const void* Cm, long long c_stride, const float* D,
-                 const void* z, long long z_stride, const float* dt_bias, float* state, void* out, int B, int Hk,
-                 int Hv, int dk, int dv, unsigned flags, void* stream) {
+int gdn_ssm_step(const gdn_ssm_step_args* args) {
   gdn::clear_cuda_error();
+  if (args == nullptr) return GDN_ERR_ARG;
+  const auto& [x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, D, z, z_stride, dt_bias, state, out, B, Hk, Hv, dk, dv, flags, stream] = *args;
   if (!ssm_sizes_ok(B, 1, Hk, Hv, dk, dv) || (flags & ~(GDN_SSM_SOFTPLUS | GDN_SSM_DT_F32)) != 0) return GDN_ERR_ARG;
   if (B == 0) return GDN_OK;
   if ((long long)B * Hv > 0x7fffffffLL || state == nullptr) return GDN_ERR_ARG;
@@ -186,9 +185,10 @@ int gdn_ssm_step(const void* x, long long x_stride, const void* dt, long long dt
   return done(gdn::launch_ssm_step(a, state, B, dk, static_cast<cudaStream_t>(stream)));
 }
 
-int gdn_add_norm(const void* x, long long x_stride, const void* residual, const void* weight, void* residual_out,
-                 void* out, float* scales, int rows, int D, int group, float eps, unsigned flags, void* stream) {
+int gdn_add_norm(const gdn_add_norm_args* args) {
   gdn::clear_cuda_error();
+  if (args == nullptr) return GDN_ERR_ARG;
+  const auto& [x, x_stride, residual, weight, residual_out, out, scales, rows, D, group, eps, flags, stream] = *args;
   const bool e4m3 = (flags & GDN_NORM_E4M3) != 0;
   if (rows < 0 || D <= 0 || D % 8 != 0 || D > 32768 || (flags & ~GDN_NORM_E4M3) != 0) return GDN_ERR_ARG;
   if (group != 0 && (!e4m3 || (group != 32 && group != 64 && group != 128))) return GDN_ERR_ARG;

@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -78,6 +79,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = False):
     """Load libgdn.so (optionally building it first) and declare the signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -122,20 +125,11 @@ def load(build_if_missing: bool = False):
         lib.gdn_selftest_static_wait_timeout.restype = i
         lib.gdn_debug_fail_allocations.argtypes = [i]
         lib.gdn_debug_fail_allocations.restype = i
-        ll, u = ctypes.c_longlong, ctypes.c_uint
-        lib.gdn_conv.argtypes = [vp, ll, vp, vp, ip, vp, vp, vp, i, i, i, i, u, vp]
-        lib.gdn_conv.restype = i
-        lib.gdn_conv_step.argtypes = [vp, ll, vp, vp, vp, vp, i, i, i, u, vp]
-        lib.gdn_conv_step.restype = i
-        ssm = [vp, ll, vp, ll, fp, vp, ll, vp, ll, fp, vp, ll, fp]
-        lib.gdn_ssm_scan.argtypes = ssm + [ip, fp, vp, fp, i, i, i, i, i, i, u, vp, ctypes.c_size_t, vp]
-        lib.gdn_ssm_scan.restype = i
         lib.gdn_ssm_workspace_bytes.argtypes = [i] * 7
         lib.gdn_ssm_workspace_bytes.restype = ctypes.c_size_t
-        lib.gdn_ssm_step.argtypes = ssm + [fp, vp, i, i, i, i, i, u, vp]
-        lib.gdn_ssm_step.restype = i
-        lib.gdn_add_norm.argtypes = [vp, ll, vp, vp, vp, vp, fp, i, i, i, ctypes.c_float, u, vp]
-        lib.gdn_add_norm.restype = i
+        for name in ("gdn_conv", "gdn_conv_step", "gdn_ssm_scan", "gdn_ssm_step", "gdn_add_norm"):
+            getattr(lib, name).argtypes = [ctypes.c_char_p]  # the packed argument struct
+            getattr(lib, name).restype = i
         lib.gdn_release_workspace.argtypes = []
         lib.gdn_release_workspace.restype = None
         _lib = lib
@@ -300,30 +294,61 @@ def prefill(q, k, v, g, beta, cu_seqlens=None, init_state=None, *, B=None, want_
 
 
 # ---- the operators around the recurrence -----------------------------------------------------
+#
+# Their C entries take a struct: packed here in the C layout (native alignment; P pointer, q long long,
+# i int, I unsigned, N size_t, f float).  A call costs about as much as its launch, so the checks are
+# written for speed.
+
+_CONV = struct.Struct("@PqPPPPPPiiiiIP")
+_CONV_STEP = struct.Struct("@PqPPPPiiiIP")
+_SSM_SCAN = struct.Struct("@PqPqPPqPqPPqPPPPPiiiiiiIPNP")
+_SSM_STEP = struct.Struct("@PqPqPPqPqPPqPPPiiiiiIP")
+_NORM = struct.Struct("@PqPPPPPiiifIP")
+
+
+def _addr(x) -> int:
+    """Address of a tensor, array or integer; 0 for None."""
+    if x is None:
+        return 0
+    if isinstance(x, int):
+        return x
+    if hasattr(x, "data_ptr"):
+        return x.data_ptr()
+    return _ptr(x)
+
+
+def _raw_stream(stream, device_index) -> int:
+    if device_index < 0:
+        raise ValueError("CUDA tensors are wanted")
+    if stream is None:
+        import torch
+
+        return torch._C._cuda_getCurrentRawStream(device_index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def gdn_conv(x, x_stride, weight, bias, cu_seqlens, init_state, out, final_state, B, T, C, K, flags,
              stream=None) -> int:
     """Short causal convolution of a prompt; returns the status."""
-    return load().gdn_conv(_ptr(x), int(x_stride), _ptr(weight), _ptr(bias), _ptr(cu_seqlens), _ptr(init_state),
-                           _ptr(out), _ptr(final_state), int(B), int(T), int(C), int(K), int(flags), _stream(stream))
+    return load().gdn_conv(_CONV.pack(_addr(x), x_stride, _addr(weight), _addr(bias), _addr(cu_seqlens),
+                                      _addr(init_state), _addr(out), _addr(final_state), B, T, C, K, flags,
+                                      _stream(stream)))
 
 
 def gdn_conv_step(x, x_stride, weight, bias, state, out, B, C, K, flags, stream=None) -> int:
     """One token per sequence of the convolution, state updated in place; returns the status."""
-    return load().gdn_conv_step(_ptr(x), int(x_stride), _ptr(weight), _ptr(bias), _ptr(state), _ptr(out), int(B),
-                                int(C), int(K), int(flags), _stream(stream))
+    return load().gdn_conv_step(_CONV_STEP.pack(_addr(x), x_stride, _addr(weight), _addr(bias), _addr(state),
+                                                _addr(out), B, C, K, flags, _stream(stream)))
 
 
 def gdn_ssm_scan(x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, D, z, z_stride, dt_bias, cu_seqlens,
                  init_state, out, final_state, B, T, Hk, Hv, dk, dv, flags, workspace=None, workspace_bytes=0,
                  stream=None) -> int:
     """Selective state space scan of a prompt; returns the status."""
-    return load().gdn_ssm_scan(_ptr(x), int(x_stride), _ptr(dt), int(dt_stride), _ptr(A), _ptr(Bm), int(b_stride),
-                               _ptr(Cm), int(c_stride), _ptr(D), _ptr(z), int(z_stride), _ptr(dt_bias),
-                               _ptr(cu_seqlens), _ptr(init_state), _ptr(out), _ptr(final_state), int(B), int(T),
-                               int(Hk), int(Hv), int(dk), int(dv), int(flags), _ptr(workspace),
-                               int(workspace_bytes), _stream(stream))
+    return load().gdn_ssm_scan(_SSM_SCAN.pack(
+        _addr(x), x_stride, _addr(dt), dt_stride, _addr(A), _addr(Bm), b_stride, _addr(Cm), c_stride, _addr(D),
+        _addr(z), z_stride, _addr(dt_bias), _addr(cu_seqlens), _addr(init_state), _addr(out), _addr(final_state), B,
+        T, Hk, Hv, dk, dv, flags, _addr(workspace), workspace_bytes, _stream(stream)))
 
 
 def gdn_ssm_workspace_bytes(B, T, Hk, Hv, dk, dv, packed) -> int:
@@ -333,16 +358,16 @@ def gdn_ssm_workspace_bytes(B, T, Hk, Hv, dk, dv, packed) -> int:
 def gdn_ssm_step(x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, D, z, z_stride, dt_bias, state, out, B,
                  Hk, Hv, dk, dv, flags, stream=None) -> int:
     """One token per sequence of the scan, state updated in place; returns the status."""
-    return load().gdn_ssm_step(_ptr(x), int(x_stride), _ptr(dt), int(dt_stride), _ptr(A), _ptr(Bm), int(b_stride),
-                               _ptr(Cm), int(c_stride), _ptr(D), _ptr(z), int(z_stride), _ptr(dt_bias), _ptr(state),
-                               _ptr(out), int(B), int(Hk), int(Hv), int(dk), int(dv), int(flags), _stream(stream))
+    return load().gdn_ssm_step(_SSM_STEP.pack(
+        _addr(x), x_stride, _addr(dt), dt_stride, _addr(A), _addr(Bm), b_stride, _addr(Cm), c_stride, _addr(D),
+        _addr(z), z_stride, _addr(dt_bias), _addr(state), _addr(out), B, Hk, Hv, dk, dv, flags, _stream(stream)))
 
 
 def gdn_add_norm(x, x_stride, residual, weight, residual_out, out, scales, rows, D, group, eps, flags,
                  stream=None) -> int:
     """Root-mean-square norm with the residual's addition; returns the status."""
-    return load().gdn_add_norm(_ptr(x), int(x_stride), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(out),
-                               _ptr(scales), int(rows), int(D), int(group), float(eps), int(flags), _stream(stream))
+    return load().gdn_add_norm(_NORM.pack(_addr(x), x_stride, _addr(residual), _addr(weight), _addr(residual_out),
+                                          _addr(out), _addr(scales), rows, D, group, eps, flags, _stream(stream)))
 
 
 def _want(cond, what) -> None:
@@ -350,38 +375,45 @@ def _want(cond, what) -> None:
         raise ValueError(what)
 
 
-def _plain(t, name, dtype, shape, like) -> None:
-    """A contiguous tensor of this type and shape on `like`'s device."""
-    if t.dtype is not dtype or tuple(t.shape) != shape or t.device != like.device or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {shape} on {like.device} is wanted, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _plain(t, name, dtype, shape, dev) -> int:
+    """The address of a contiguous tensor of this type and shape on device `dev`; 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {shape} on the device of x is wanted, "
+                         f"got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    return t.data_ptr()
 
 
-def _rows(t, name, dtypes, shape, like) -> int:
+def _rows(t, name, dtype, shape, dev) -> int:
     """Row stride of a tensor of this shape whose rows are contiguous (a slice of a wider one may be)."""
-    if t.dtype not in dtypes or tuple(t.shape) != shape or t.device != like.device:
-        raise ValueError(f"{name}: a {' or '.join(map(str, dtypes))} tensor of shape {shape} on {like.device} is "
-                         f"wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    st, width = t.stride(), 1
-    for n, s in zip(shape[:0:-1], st[:0:-1]):
-        if n != 1 and s != width:
-            raise ValueError(f"{name}: the elements of a row have to be contiguous (strides {st})")
-        width *= n
-    return st[0] if shape[0] > 1 else width
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name}: a {dtype} tensor of shape {shape} on the device of x is wanted, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    st = t.stride()
+    if len(shape) == 3:
+        n, h, d = shape
+        width = h * d
+        ok = (st[2] == 1 or d == 1) and (st[1] == d or h == 1)
+    else:
+        n, width = shape
+        ok = st[1] == 1 or width == 1
+    if not ok:
+        raise ValueError(f"{name}: the elements of a row have to be contiguous (strides {st})")
+    return st[0] if n > 1 else width
 
 
-def _batch(x, cu_seqlens, B):
-    """(sequences, tokens per sequence or in all) of a dense or packed batch of x's rows."""
-    import torch
-
-    n = x.shape[0]
+def _batch(n, cu_seqlens, B, dev):
+    """(sequences, tokens per sequence or in all, boundaries' address) of a dense or packed batch of n rows."""
     if cu_seqlens is None:
         B = 1 if B is None else int(B)
         _want(B >= 0 and (n % B == 0 if B else n == 0), "the tokens have to divide into B sequences")
-        return B, n // B if B else 0
+        return B, n // B if B else 0, 0
+    import torch
+
     _want(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 1, "cu_seqlens: B + 1 boundaries")
-    _plain(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), x)
-    return cu_seqlens.numel() - 1, n
+    b1 = cu_seqlens.numel()
+    return b1 - 1, n, _plain(cu_seqlens, "cu_seqlens", torch.int32, (b1,), dev)
 
 
 def causal_conv(x, weight, bias=None, cu_seqlens=None, init_state=None, *, B=None, silu=True, out=None,
@@ -396,24 +428,18 @@ def causal_conv(x, weight, bias=None, cu_seqlens=None, init_state=None, *, B=Non
 
     bf16 = torch.bfloat16
     _want(x.dim() == 2 and weight.dim() == 2, "x: [Ttot, C], weight: [C, K]")
-    C, K = weight.shape
-    xs = _rows(x, "x", (bf16,), (x.shape[0], C), x)
-    B, T = _batch(x, cu_seqlens, B)
-    _plain(weight, "weight", bf16, (C, K), x)
-    if bias is not None:
-        _plain(bias, "bias", bf16, (C,), x)
-    if init_state is not None:
-        _plain(init_state, "init_state", bf16, (B, K - 1, C), x)
+    (n, _), (C, K), dev = x.shape, weight.shape, x.get_device()
+    xs = _rows(x, "x", bf16, (n, C), dev)
+    B, T, cu = _batch(n, cu_seqlens, B, dev)
     if out is None:
-        out = torch.empty((x.shape[0], C), dtype=bf16, device=x.device)
-    else:
-        _plain(out, "out", bf16, (x.shape[0], C), x)
-    if final_state is not None:
-        _plain(final_state, "final_state", bf16, (B, K - 1, C), x)
-    elif want_final:
+        out = torch.empty((n, C), dtype=bf16, device=x.device)
+    if final_state is None and want_final:
         final_state = torch.empty((B, K - 1, C), dtype=bf16, device=x.device)
-    check(gdn_conv(x, xs, weight, bias, cu_seqlens, init_state, out, final_state, B, T, C, K,
-                   GDN_CONV_SILU if silu else 0, stream))
+    check(load().gdn_conv(_CONV.pack(
+        x.data_ptr(), xs, _plain(weight, "weight", bf16, (C, K), dev), _plain(bias, "bias", bf16, (C,), dev), cu,
+        _plain(init_state, "init_state", bf16, (B, K - 1, C), dev), _plain(out, "out", bf16, (n, C), dev),
+        _plain(final_state, "final_state", bf16, (B, K - 1, C), dev), B, T, C, K, GDN_CONV_SILU if silu else 0,
+        _raw_stream(stream, dev))))
     return out, final_state
 
 
@@ -423,42 +449,38 @@ def causal_conv_step(x, weight, state, bias=None, *, silu=True, out=None, stream
 
     bf16 = torch.bfloat16
     _want(x.dim() == 2 and weight.dim() == 2, "x: [B, C], weight: [C, K]")
-    C, K = weight.shape
-    B = x.shape[0]
-    xs = _rows(x, "x", (bf16,), (B, C), x)
-    _plain(weight, "weight", bf16, (C, K), x)
-    _plain(state, "state", bf16, (B, K - 1, C), x)
-    if bias is not None:
-        _plain(bias, "bias", bf16, (C,), x)
+    (B, _), (C, K), dev = x.shape, weight.shape, x.get_device()
+    xs = _rows(x, "x", bf16, (B, C), dev)
     if out is None:
         out = torch.empty((B, C), dtype=bf16, device=x.device)
-    else:
-        _plain(out, "out", bf16, (B, C), x)
-    check(gdn_conv_step(x, xs, weight, bias, state, out, B, C, K, GDN_CONV_SILU if silu else 0, stream))
+    check(load().gdn_conv_step(_CONV_STEP.pack(
+        x.data_ptr(), xs, _plain(weight, "weight", bf16, (C, K), dev), _plain(bias, "bias", bf16, (C,), dev),
+        _plain(state, "state", bf16, (B, K - 1, C), dev), _plain(out, "out", bf16, (B, C), dev), B, C, K,
+        GDN_CONV_SILU if silu else 0, _raw_stream(stream, dev))))
     return out
 
 
-def _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out):
-    """Shapes, row strides and `out` of the scan and its step."""
+def _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus):
+    """Of the scan and its step: (device, sizes, the struct's fields up to dt_bias, out, flags)."""
     import torch
 
     bf16, f32 = torch.bfloat16, torch.float32
     _want(x.dim() == 3 and Bm.dim() == 3, "x: [Ttot, Hv, dv], Bm and Cm: [Ttot, Hk, dk]")
-    n, Hv, dv = x.shape
-    Hk, dk = Bm.shape[1:]
-    strides = (_rows(x, "x", (bf16,), (n, Hv, dv), x), _rows(dt, "dt", (bf16, f32), (n, Hv), x),
-               _rows(Bm, "Bm", (bf16,), (n, Hk, dk), x), _rows(Cm, "Cm", (bf16,), (n, Hk, dk), x),
-               0 if z is None else _rows(z, "z", (bf16,), (n, Hv, dv), x))
-    _plain(A, "A", f32, (Hv,), x)
-    if D is not None:
-        _plain(D, "D", f32, (Hv,), x)
-    if dt_bias is not None:
-        _plain(dt_bias, "dt_bias", f32, (Hv,), x)
+    n, Hv, dv = shape = x.shape
+    _, Hk, dk = Bm.shape
+    dev = x.get_device()
+    kshape = (n, Hk, dk)
+    dt32 = dt.dtype is f32
+    fields = (x.data_ptr(), _rows(x, "x", bf16, shape, dev), dt.data_ptr(),
+              _rows(dt, "dt", f32 if dt32 else bf16, (n, Hv), dev), _plain(A, "A", f32, (Hv,), dev), Bm.data_ptr(),
+              _rows(Bm, "Bm", bf16, kshape, dev), Cm.data_ptr(), _rows(Cm, "Cm", bf16, kshape, dev),
+              _plain(D, "D", f32, (Hv,), dev), 0 if z is None else z.data_ptr(),
+              0 if z is None else _rows(z, "z", bf16, shape, dev), _plain(dt_bias, "dt_bias", f32, (Hv,), dev))
     if out is None:
         out = torch.empty((n, Hv, dv), dtype=bf16, device=x.device)
     else:
-        _plain(out, "out", bf16, (n, Hv, dv), x)
-    return (Hk, Hv, dk, dv), strides, out, GDN_SSM_DT_F32 if dt.dtype is f32 else 0
+        _plain(out, "out", bf16, shape, dev)
+    return dev, (n, Hk, Hv, dk, dv), fields, out, (GDN_SSM_DT_F32 if dt32 else 0) | (GDN_SSM_SOFTPLUS if softplus else 0)
 
 
 def ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, cu_seqlens=None, init_state=None, *, B=None,
@@ -472,17 +494,16 @@ def ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, cu_seqlens=None, in
     """
     import torch
 
-    dims, (xs, ds, bs, cs, zs), out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out)
-    Hk, Hv, dk, dv = dims
-    B, T = _batch(x, cu_seqlens, B)
-    for name, t in (("init_state", init_state), ("final_state", final_state)):
-        if t is not None:
-            _plain(t, name, torch.float32, (B, Hv, dv, dk), x)
+    dev, (n, Hk, Hv, dk, dv), fields, out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus)
+    B, T, cu = _batch(n, cu_seqlens, B, dev)
+    shape = (B, Hv, dv, dk)
     if final_state is None and want_final:
-        final_state = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=x.device)
-    check(gdn_ssm_scan(x, xs, dt, ds, A, Bm, bs, Cm, cs, D, z, zs, dt_bias, cu_seqlens, init_state, out, final_state,
-                       B, T, Hk, Hv, dk, dv, flags | (GDN_SSM_SOFTPLUS if softplus else 0), workspace,
-                       0 if workspace is None else workspace.numel() * workspace.element_size(), stream))
+        final_state = torch.empty(shape, dtype=torch.float32, device=x.device)
+    check(load().gdn_ssm_scan(_SSM_SCAN.pack(
+        *fields, cu, _plain(init_state, "init_state", torch.float32, shape, dev), out.data_ptr(),
+        _plain(final_state, "final_state", torch.float32, shape, dev), B, T, Hk, Hv, dk, dv, flags,
+        0 if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))))
     return out, final_state
 
 
@@ -490,11 +511,10 @@ def ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softplus=
     """One token of each of B sequences of the scan: state fp32 [B, Hv, dv, dk], updated in place."""
     import torch
 
-    dims, (xs, ds, bs, cs, zs), out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out)
-    Hk, Hv, dk, dv = dims
-    _plain(state, "state", torch.float32, (x.shape[0], Hv, dv, dk), x)
-    check(gdn_ssm_step(x, xs, dt, ds, A, Bm, bs, Cm, cs, D, z, zs, dt_bias, state, out, x.shape[0], Hk, Hv, dk, dv,
-                       flags | (GDN_SSM_SOFTPLUS if softplus else 0), stream))
+    dev, (n, Hk, Hv, dk, dv), fields, out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus)
+    check(load().gdn_ssm_step(_SSM_STEP.pack(
+        *fields, _plain(state, "state", torch.float32, (n, Hv, dv, dk), dev), out.data_ptr(), n, Hk, Hv, dk, dv, flags,
+        _raw_stream(stream, dev))))
     return out
 
 
@@ -509,30 +529,24 @@ def add_norm(x, weight, residual=None, *, eps=1e-6, group=0, e4m3=False, out=Non
     """
     import torch
 
-    bf16, f32, f8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+    bf16, f8 = torch.bfloat16, torch.float8_e4m3fn
     _want(x.dim() == 2, "x: [rows, D]")
-    rows, D = x.shape
-    xs = _rows(x, "x", (bf16,), (rows, D), x)
-    _plain(weight, "weight", bf16, (D,), x)
+    rows, D = shape = x.shape
+    dev = x.get_device()
+    xs = _rows(x, "x", bf16, shape, dev)
     if out is None:
-        out = torch.empty((rows, D), dtype=f8 if e4m3 else bf16, device=x.device)
+        out = torch.empty(shape, dtype=f8 if e4m3 else bf16, device=x.device)
     else:
         e4m3 = out.dtype is f8
-        _plain(out, "out", f8 if e4m3 else bf16, (rows, D), x)
-    if e4m3:
-        shape = (rows, -(-D // group) if group else 1)
-        if scales is None:
-            scales = torch.empty(shape, dtype=f32, device=x.device)
-        else:
-            _plain(scales, "scales", f32, shape, x)
-    else:
+    if not e4m3:
         scales = None
-    if residual is not None:
-        _plain(residual, "residual", bf16, (rows, D), x)
-        if residual_out is None:
-            residual_out = torch.empty((rows, D), dtype=bf16, device=x.device)
-    if residual_out is not None:
-        _plain(residual_out, "residual_out", bf16, (rows, D), x)
-    check(gdn_add_norm(x, xs, residual, weight, residual_out, out, scales, rows, D, group, eps,
-                       GDN_NORM_E4M3 if e4m3 else 0, stream))
+    elif scales is None:
+        scales = torch.empty((rows, -(-D // group) if group else 1), dtype=torch.float32, device=x.device)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty(shape, dtype=bf16, device=x.device)
+    check(load().gdn_add_norm(_NORM.pack(
+        x.data_ptr(), xs, _plain(residual, "residual", bf16, shape, dev), _plain(weight, "weight", bf16, (D,), dev),
+        _plain(residual_out, "residual_out", bf16, shape, dev), _plain(out, "out", f8 if e4m3 else bf16, shape, dev),
+        _plain(scales, "scales", torch.float32, (rows, -(-D // group) if group else 1), dev), rows, D, group, eps,
+        GDN_NORM_E4M3 if e4m3 else 0, _raw_stream(stream, dev))))
     return out, scales, residual_out

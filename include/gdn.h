@@ -345,7 +345,8 @@ void gdn_release_workspace(void);
  * be a slice of a wider projection or convolution output; within a token the elements are
  * contiguous.  bf16 activations start on 16 bytes and, with more than one token, their
  * strides are multiples of 8 elements (GDN_ERR_ALIGN otherwise); dt has no such rule.
- * Outputs are contiguous and must not overlap the inputs unless stated.
+ * Outputs are contiguous and must not overlap the inputs unless stated.  Each call takes its
+ * arguments in a struct, read before it returns.
  * ------------------------------------------------------------------------------------- */
 
 /* Flags of gdn_conv and gdn_conv_step. */
@@ -369,16 +370,33 @@ void gdn_release_workspace(void);
  *
  * K is 2, 3 or 4, C a multiple of 8.  Sums in fp32, one rounding to bf16.
  */
-int gdn_conv(const void *x, long long x_stride, const void *weight, const void *bias,
-             const int32_t *cu_seqlens, const void *init_state, void *out, void *final_state,
-             int B, int T, int C, int K, unsigned flags, void *stream);
+typedef struct gdn_conv_args {
+  const void *x;
+  long long x_stride;
+  const void *weight, *bias;
+  const int32_t *cu_seqlens;
+  const void *init_state;
+  void *out, *final_state;
+  int B, T, C, K;
+  unsigned flags;
+  void *stream;
+} gdn_conv_args;
+int gdn_conv(const gdn_conv_args *args);
 
 /*
  * gdn_conv_step -- gdn_conv for one token per sequence: x and out [B, C], state bf16
  * [B, K - 1, C] read and overwritten with the last K - 1 inputs.
  */
-int gdn_conv_step(const void *x, long long x_stride, const void *weight, const void *bias, void *state,
-                  void *out, int B, int C, int K, unsigned flags, void *stream);
+typedef struct gdn_conv_step_args {
+  const void *x;
+  long long x_stride;
+  const void *weight, *bias;
+  void *state, *out;
+  int B, C, K;
+  unsigned flags;
+  void *stream;
+} gdn_conv_step_args;
+int gdn_conv_step(const gdn_conv_step_args *args);
 
 /* Flags of gdn_ssm_scan and gdn_ssm_step. */
 #define GDN_SSM_SOFTPLUS 1u /* the step is softplus(dt + dt_bias), else dt + dt_bias */
@@ -417,11 +435,31 @@ int gdn_conv_step(const void *x, long long x_stride, const void *weight, const v
  * small.  Its first word collects status bits; gdn_device_status reports those of the
  * library's own.
  */
-int gdn_ssm_scan(const void *x, long long x_stride, const void *dt, long long dt_stride, const float *A,
-                 const void *Bm, long long b_stride, const void *Cm, long long c_stride, const float *D,
-                 const void *z, long long z_stride, const float *dt_bias, const int32_t *cu_seqlens,
-                 const float *init_state, void *out, float *final_state, int B, int T, int Hk, int Hv,
-                 int dk, int dv, unsigned flags, void *workspace, size_t workspace_bytes, void *stream);
+typedef struct gdn_ssm_scan_args {
+  const void *x;
+  long long x_stride;
+  const void *dt;
+  long long dt_stride;
+  const float *A;
+  const void *Bm;
+  long long b_stride;
+  const void *Cm;
+  long long c_stride;
+  const float *D;
+  const void *z;
+  long long z_stride;
+  const float *dt_bias;
+  const int32_t *cu_seqlens;
+  const float *init_state;
+  void *out;
+  float *final_state;
+  int B, T, Hk, Hv, dk, dv;
+  unsigned flags;
+  void *workspace;
+  size_t workspace_bytes;
+  void *stream;
+} gdn_ssm_scan_args;
+int gdn_ssm_scan(const gdn_ssm_scan_args *args);
 
 /* Bytes of workspace gdn_ssm_scan needs for these sizes on the current device (0 on bad arguments). */
 size_t gdn_ssm_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv, int packed);
@@ -430,10 +468,27 @@ size_t gdn_ssm_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv, int
  * gdn_ssm_step -- gdn_ssm_scan for one token per sequence (x, z, out [B, Hv, dv], dt [B, Hv],
  * Bm, Cm [B, Hk, dk]); state fp32 [B, Hv, dv, dk], 16-byte aligned, updated in place.
  */
-int gdn_ssm_step(const void *x, long long x_stride, const void *dt, long long dt_stride, const float *A,
-                 const void *Bm, long long b_stride, const void *Cm, long long c_stride, const float *D,
-                 const void *z, long long z_stride, const float *dt_bias, float *state, void *out, int B,
-                 int Hk, int Hv, int dk, int dv, unsigned flags, void *stream);
+typedef struct gdn_ssm_step_args {
+  const void *x;
+  long long x_stride;
+  const void *dt;
+  long long dt_stride;
+  const float *A;
+  const void *Bm;
+  long long b_stride;
+  const void *Cm;
+  long long c_stride;
+  const float *D;
+  const void *z;
+  long long z_stride;
+  const float *dt_bias;
+  float *state;
+  void *out;
+  int B, Hk, Hv, dk, dv;
+  unsigned flags;
+  void *stream;
+} gdn_ssm_step_args;
+int gdn_ssm_step(const gdn_ssm_step_args *args);
 
 /* Flags of gdn_add_norm. */
 #define GDN_NORM_E4M3 1u /* out is e4m3 with scales, else bf16 */
@@ -453,8 +508,18 @@ int gdn_ssm_step(const void *x, long long x_stride, const void *dt, long long dt
  * D is a multiple of 8 up to 32,768.  y is computed from the unrounded sum and rounded once.  A NaN
  * in a group makes its scale NaN.
  */
-int gdn_add_norm(const void *x, long long x_stride, const void *residual, const void *weight, void *residual_out,
-                 void *out, float *scales, int rows, int D, int group, float eps, unsigned flags, void *stream);
+typedef struct gdn_add_norm_args {
+  const void *x;
+  long long x_stride;
+  const void *residual, *weight;
+  void *residual_out, *out;
+  float *scales;
+  int rows, D, group;
+  float eps;
+  unsigned flags;
+  void *stream;
+} gdn_add_norm_args;
+int gdn_add_norm(const gdn_add_norm_args *args);
 
 #ifdef __cplusplus
 }

@@ -118,3 +118,14 @@ def test_wrappers_refuse_wrong_tensors():
         gdn.ssm_scan(**s, init_state=z(1, 4, 32, 64))
     with pytest.raises(ValueError):
         gdn.ssm_step(**s, state=z(8, 4, 64, 64))
+
+
+def test_wrappers_refuse_host_tensors():
+    bf, z = torch.bfloat16, torch.zeros
+    x, w = z(8, 64, dtype=bf), z(64, 4, dtype=bf)
+    s = dict(x=z(8, 4, 64, dtype=bf), dt=z(8, 4), A=z(4), Bm=z(8, 2, 32, dtype=bf), Cm=z(8, 2, 32, dtype=bf))
+    for call in (lambda: gdn.causal_conv(x, w), lambda: gdn.causal_conv_step(x, w, z(8, 3, 64, dtype=bf)),
+                 lambda: gdn.add_norm(x, z(64, dtype=bf)), lambda: gdn.ssm_scan(**s),
+                 lambda: gdn.ssm_step(**s, state=z(8, 4, 64, 32))):
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            call()
