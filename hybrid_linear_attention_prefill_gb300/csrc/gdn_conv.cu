@@ -7,65 +7,50 @@
 // and written once (4 bytes) for 2 K + ~6 operations, so HBM bandwidth bounds it.  A thread owns
 // eight consecutive channels (one 16-byte access a token) and walks a run of tokens with the last
 // K - 1 inputs in registers, so that only a run's first K - 1 inputs are read twice.
-#include "gdn_common.cuh"
+#include "gdn_vec.cuh"
 
 namespace gdn {
 
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kConvRun = 16;  // tokens a thread walks
+constexpr int kConvBatch = 4;  // tokens whose loads a thread has in flight
 
-
-__device__ __forceinline__ void widen8(const uint4& r, float (&f)[8]) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-__device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
-  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-}
-
-__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
-
-// A thread's eight channels' weights w[k][i] and biases.
+// A thread's eight channels' weights and biases, in pairs.
 template <int K>
 struct Taps {
-  float w[K][8], b[8];
+  float2 w[K][4], b[4];
   __device__ __forceinline__ void load(const __nv_bfloat16* weight, const __nv_bfloat16* bias, int c) {
     uint4 raw[K];
 #pragma unroll
     for (int j = 0; j < K; ++j) raw[j] = *reinterpret_cast<const uint4*>(weight + (size_t)c * K + 8 * j);
+    float f[8 * K];  // [channel][tap]
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      float f[8];
-      widen8(raw[j], f);
+      float2 t[4];
+      widen8(raw[j], t);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[(8 * j + i) % K][(8 * j + i) / K] = f[i];  // [channel][tap] order
+      for (int i = 0; i < 4; ++i) f[8 * j + 2 * i] = t[i].x, f[8 * j + 2 * i + 1] = t[i].y;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = 0.f;
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[k][i] = make_float2(f[2 * i * K + k], f[(2 * i + 1) * K + k]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = make_float2(0.f, 0.f);
     if (bias != nullptr) widen8(*reinterpret_cast<const uint4*>(bias + c), b);
   }
   // The output of the token with input `cur` after `past` (oldest first).
   template <bool SILU>
-  __device__ __forceinline__ uint4 apply(const uint4 (&past)[K - 1], const uint4& cur) const {
-    float acc[8], f[8];
+  __device__ __forceinline__ uint4 apply(const float2 (&past)[K - 1][4], const float2 (&cur)[4]) const {
+    float2 acc[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = b[i];
+    for (int i = 0; i < 4; ++i) {
+      acc[i] = fma2(w[0][i], past[0][i], b[i]);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      widen8(k < K - 1 ? past[k < K - 1 ? k : 0] : cur, f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[k][i], f[i], acc[i]);
-    }
-    if (SILU) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = silu(acc[i]);
+      for (int k = 1; k < K - 1; ++k) acc[i] = fma2(w[k][i], past[k][i], acc[i]);
+      acc[i] = fma2(w[K - 1][i], cur[i], acc[i]);
+      if (SILU) acc[i] = silu2(acc[i]);
     }
     return narrow8(acc);
   }
@@ -84,14 +69,14 @@ __device__ __forceinline__ int find_seq(const int32_t* __restrict__ cu, int B, i
 
 }  // namespace
 
-// grid: (ceil(Ttot / run) + B when the final states are wanted, channel blocks).  The first blocks
-// compute outputs; block ceil(Ttot / run) + b copies sequence b's final state.
+// grid: (runs + B when the final states are wanted, channel blocks).  The first blocks compute outputs, `run`
+// tokens each; block runs + b copies sequence b's final state.
 template <int K, bool SILU>
 __global__ void __launch_bounds__(kConvThreads)
 gdn_conv_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __nv_bfloat16* __restrict__ weight,
                 const __nv_bfloat16* __restrict__ bias, const int32_t* __restrict__ cu,
                 const __nv_bfloat16* __restrict__ init, __nv_bfloat16* __restrict__ out,
-                __nv_bfloat16* __restrict__ fin, int B, int T, int Ttot, int C, int runs) {
+                __nv_bfloat16* __restrict__ fin, int B, int T, int Ttot, int C, int runs, int run) {
   const int c = (blockIdx.y * kConvThreads + threadIdx.x) * 8;
   if (c >= C) return;
   const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -108,7 +93,7 @@ gdn_conv_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __nv_bf
     }
     return;
   }
-  const int t0 = blockIdx.x * kConvRun, t1 = min(t0 + kConvRun, Ttot);
+  const int t0 = blockIdx.x * run, t1 = min(t0 + run, Ttot);
   Taps<K> taps;
   taps.load(weight, bias, c);
   int b, start, end;  // the sequence of token t and its bounds
@@ -121,42 +106,57 @@ gdn_conv_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __nv_bf
     start = max(0, min(cu[b], t0));
     end = b + 1 < B ? cu[b + 1] : Ttot;
   }
-  uint4 past[K - 1];
+  float2 past[K - 1][4];
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) {
     const int t = t0 - (K - 1) + j;
-    past[j] = zero;
-    if (t >= start) past[j] = *reinterpret_cast<const uint4*>(x + (long long)t * xs + c);
+    uint4 v = zero;
+    if (t >= start) v = *reinterpret_cast<const uint4*>(x + (long long)t * xs + c);
     else if (init != nullptr)
-      past[j] = *reinterpret_cast<const uint4*>(init + ((size_t)b * (K - 1) + K - 1 + (t - start)) * C + c);
+      v = *reinterpret_cast<const uint4*>(init + ((size_t)b * (K - 1) + K - 1 + (t - start)) * C + c);
+    widen8(v, past[j]);
   }
-  auto step = [&](int t, const uint4& cur) {
-    if (t >= end) {  // the next sequence that has tokens begins here
-      if (cu == nullptr) {
-        ++b;
-        end += T;
-      } else {
-        b = find_seq(cu, B, t);
-        end = b + 1 < B ? cu[b + 1] : Ttot;
-      }
+  const __nv_bfloat16* xp = x + (long long)t0 * xs + c;
+  __nv_bfloat16* op = out + (size_t)t0 * C + c;
+  uint4 next[kConvBatch];
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j)
-        past[j] = init != nullptr ? *reinterpret_cast<const uint4*>(init + ((size_t)b * (K - 1) + j) * C + c) : zero;
+  for (int u = 0; u < kConvBatch; ++u) next[u] = t0 + u < t1 ? *reinterpret_cast<const uint4*>(xp + u * xs) : zero;
+  for (int t = t0; t < t1; t += kConvBatch) {
+    uint4 cur[kConvBatch];
+    xp += kConvBatch * xs;
+#pragma unroll
+    for (int u = 0; u < kConvBatch; ++u) {
+      cur[u] = next[u];
+      if (t + kConvBatch + u < t1) next[u] = *reinterpret_cast<const uint4*>(xp + u * xs);
     }
-    *reinterpret_cast<uint4*>(out + (size_t)t * C + c) = taps.template apply<SILU>(past, cur);
 #pragma unroll
-    for (int j = 0; j + 1 < K - 1; ++j) past[j] = past[j + 1];
-    past[K - 2] = cur;
-  };
-  int t = t0;
-  for (; t + 4 <= t1; t += 4) {  // four tokens' loads in flight
-    uint4 cur[4];
+    for (int u = 0; u < kConvBatch; ++u) {
+      if (t + u >= t1) break;
+      if (t + u >= end) {  // the next sequence that has tokens begins here
+        if (cu == nullptr) {
+          ++b;
+          end += T;
+        } else {
+          b = find_seq(cu, B, t + u);
+          end = b + 1 < B ? cu[b + 1] : Ttot;
+        }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) cur[u] = *reinterpret_cast<const uint4*>(x + (long long)(t + u) * xs + c);
+        for (int j = 0; j < K - 1; ++j)
+          widen8(init != nullptr ? *reinterpret_cast<const uint4*>(init + ((size_t)b * (K - 1) + j) * C + c) : zero,
+                 past[j]);
+      }
+      float2 f[4];
+      widen8(cur[u], f);
+      *reinterpret_cast<uint4*>(op) = taps.template apply<SILU>(past, f);
+      op += C;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) step(t + u, cur[u]);
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j + 1 < K - 1; ++j) past[j][i] = past[j + 1][i];
+        past[K - 2][i] = f[i];
+      }
+    }
   }
-  for (; t < t1; ++t) step(t, *reinterpret_cast<const uint4*>(x + (long long)t * xs + c));
 }
 
 // One thread per (sequence, eight channels).
@@ -174,7 +174,11 @@ gdn_conv_step_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __
   const uint4 cur = *reinterpret_cast<const uint4*>(x + b * xs + c);
   Taps<K> taps;
   taps.load(weight, bias, c);
-  *reinterpret_cast<uint4*>(out + (size_t)b * C + c) = taps.template apply<SILU>(past, cur);
+  float2 pf[K - 1][4], cf[4];
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) widen8(past[j], pf[j]);
+  widen8(cur, cf);
+  *reinterpret_cast<uint4*>(out + (size_t)b * C + c) = taps.template apply<SILU>(pf, cf);
 #pragma unroll
   for (int j = 0; j + 1 < K - 1; ++j) *reinterpret_cast<uint4*>(sp + (size_t)j * C) = past[j + 1];
   *reinterpret_cast<uint4*>(sp + (size_t)(K - 2) * C) = cur;
@@ -184,11 +188,15 @@ template <int K, bool SILU>
 cudaError_t conv_k(const void* x, long long xs, const void* weight, const void* bias, const int32_t* cu,
                    const void* init, void* out, void* fin, int B, int T, int Ttot, int C, cudaStream_t st) {
   using bf = __nv_bfloat16;
-  const int runs = (Ttot + kConvRun - 1) / kConvRun;
+  // Runs of 32 tokens read a tenth of the inputs twice; shorter ones while they leave SMs idle.
+  const int cb = (C / 8 + kConvThreads - 1) / kConvThreads;
+  int run = 32;
+  while (run > kConvBatch && (long long)(Ttot / run) * cb < 8 * 152) run >>= 1;
+  const int runs = (Ttot + run - 1) / run;
   const unsigned gx = (unsigned)runs + (fin != nullptr ? (unsigned)B : 0u);
-  gdn_conv_kernel<K, SILU><<<dim3(gx, (C / 8 + kConvThreads - 1) / kConvThreads), kConvThreads, 0, st>>>(
+  gdn_conv_kernel<K, SILU><<<dim3(gx, cb), kConvThreads, 0, st>>>(
       static_cast<const bf*>(x), xs, static_cast<const bf*>(weight), static_cast<const bf*>(bias), cu,
-      static_cast<const bf*>(init), static_cast<bf*>(out), static_cast<bf*>(fin), B, T, Ttot, C, runs);
+      static_cast<const bf*>(init), static_cast<bf*>(out), static_cast<bf*>(fin), B, T, Ttot, C, runs, run);
   return cudaGetLastError();
 }
 

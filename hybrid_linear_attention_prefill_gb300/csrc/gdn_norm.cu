@@ -8,24 +8,11 @@
 // between its two reductions.
 #include <cuda_fp8.h>
 
-#include "gdn_common.cuh"
+#include "gdn_vec.cuh"
 
 namespace gdn {
 
 namespace {
-
-__device__ __forceinline__ void widen8(const uint4& r, float (&f)[8]) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-__device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
-  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-}
 
 constexpr int kNormMinThreads = 128;
 
@@ -48,30 +35,33 @@ gdn_add_norm_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __n
   const long long row = (long long)blockIdx.x * (blockDim.x / tpr) + rib;
   const bool live = row < rows;
 
-  float r[VPT][8];
-  float ss = 0.f;
+  float2 r[VPT][4];
+  float2 sq = make_float2(0.f, 0.f);
+  uint4 xr[VPT], rr[VPT];  // every load of the row before any use
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = tid + j * tpr;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[j][i] = 0.f;
+    xr[j] = rr[j] = make_uint4(0, 0, 0, 0);
     if (live && v < nv) {
-      widen8(*reinterpret_cast<const uint4*>(x + row * xs + 8 * v), r[j]);
-      if (residual != nullptr) {
-        float f[8];
-        widen8(*reinterpret_cast<const uint4*>(residual + row * D + 8 * v), f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[j][i] += f[i];
-      }
+      xr[j] = *reinterpret_cast<const uint4*>(x + row * xs + 8 * v);
+      if (residual != nullptr) rr[j] = *reinterpret_cast<const uint4*>(residual + row * D + 8 * v);
     }
   }
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = tid + j * tpr;
+    widen8(xr[j], r[j]);
+    if (residual != nullptr) {
+      float2 f[4];
+      widen8(rr[j], f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[j][i] = make_float2(r[j][i].x + f[i].x, r[j][i].y + f[i].y);
+    }
     if (residual_out != nullptr && live && v < nv) *reinterpret_cast<uint4*>(residual_out + row * D + 8 * v) = narrow8(r[j]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(r[j][i], r[j][i], ss);
+    for (int i = 0; i < 4; ++i) sq = fma2(r[j][i], r[j][i], sq);
   }
+  float ss = sq.x + sq.y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   if (wpr > 1) {
@@ -90,12 +80,13 @@ gdn_add_norm_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __n
     const int v = tid + j * tpr;
     mx[j] = 0;
     if (live && v < nv) {
-      float w[8];
+      float2 w[4];
       widen8(*reinterpret_cast<const uint4*>(weight + 8 * v), w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        r[j][i] = r[j][i] * rstd * w[i];
-        mx[j] = max(mx[j], __float_as_uint(r[j][i]) & 0x7fffffffu);
+      for (int i = 0; i < 4; ++i) {
+        r[j][i] = mul2(mul2(r[j][i], make_float2(rstd, rstd)), w[i]);
+        if (E4M3)
+          mx[j] = max(mx[j], max(__float_as_uint(r[j][i].x) & 0x7fffffffu, __float_as_uint(r[j][i].y) & 0x7fffffffu));
       }
     }
   }
@@ -134,9 +125,9 @@ gdn_add_norm_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __n
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const __nv_fp8x2_storage_t a =
-            __nv_cvt_float2_to_fp8x2(make_float2(r[j][4 * i] * inv, r[j][4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(
-            make_float2(r[j][4 * i + 2] * inv, r[j][4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+            __nv_cvt_float2_to_fp8x2(mul2(r[j][2 * i], make_float2(inv, inv)), __NV_SATFINITE, __NV_E4M3);
+        const __nv_fp8x2_storage_t b =
+            __nv_cvt_float2_to_fp8x2(mul2(r[j][2 * i + 1], make_float2(inv, inv)), __NV_SATFINITE, __NV_E4M3);
         q[i] = (uint32_t)a | ((uint32_t)b << 16);
       }
       *reinterpret_cast<uint2*>(static_cast<unsigned char*>(out) + row * D + 8 * v) = make_uint2(q[0], q[1]);

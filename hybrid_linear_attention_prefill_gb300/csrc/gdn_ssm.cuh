@@ -1,7 +1,7 @@
 // What the selective state space scan and its single-token step share.
 #pragma once
 
-#include "gdn_common.cuh"
+#include "gdn_vec.cuh"
 
 namespace gdn {
 
@@ -46,20 +46,6 @@ __device__ __forceinline__ SsmDecay ssm_decay(float l) {
 __device__ __forceinline__ float ssm_decayed(const SsmDecay& d, float s, float add) {
   return fmaf(d.keep, s, fmaf(d.more, s, add));
 }
-
-// 1 / x and 2^x to a few units in the last place.
-__device__ __forceinline__ float ssm_rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float ssm_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float ssm_silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
 
 // E (1, 2 or 4) consecutive fp32 of a state row.
 template <int E>

@@ -174,34 +174,6 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Two fp32 operations an instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
-      "mov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-
-// silu of two values, v / (1 + e^-v), with one reciprocal: 1 / a = b / (a b).  The exponents stop at 2^62, so
-// that the product stays finite: below -43 a value v gives v 2^-62 where less would be exact.
-__device__ __forceinline__ float2 silu2(float2 v) {
-  const float2 t = mul2(v, make_float2(-1.4426950408889634f, -1.4426950408889634f));
-  const float2 d = fma2(make_float2(ssm_ex2(fminf(t.x, 62.f)), ssm_ex2(fminf(t.y, 62.f))), make_float2(1.f, 1.f),
-                        make_float2(1.f, 1.f));
-  const float r = ssm_rcp(d.x * d.y);
-  return mul2(v, mul2(make_float2(r, r), make_float2(d.y, d.x)));
-}
-
 // Sixteen lanes (from taddr's) of eight columns: register 2 j + i of thread l holds lane l / 4 + 8 i,
 // column 4 j + l % 4 -- the layout of transposed ldmatrix fragments.
 __device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t a, const uint32_t (&v)[4]) {

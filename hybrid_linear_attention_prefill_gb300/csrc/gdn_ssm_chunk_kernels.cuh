@@ -325,8 +325,8 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
               const float4 k4 = *reinterpret_cast<const float4*>(th + kQ + 32 * cg + j0 + j);
               const float2 minus = make_float2(-1.f, -1.f), l2 = make_float2(li, li);
               const float2 e0 = fma2(make_float2(k4.x, k4.y), minus, l2), e1 = fma2(make_float2(k4.z, k4.w), minus, l2);
-              float2 u = mul2(make_float2(sc[j], sc[j + 1]), make_float2(ssm_ex2(e0.x), ssm_ex2(e0.y)));
-              float2 v = mul2(make_float2(sc[j + 2], sc[j + 3]), make_float2(ssm_ex2(e1.x), ssm_ex2(e1.y)));
+              float2 u = mul2(make_float2(sc[j], sc[j + 1]), make_float2(ex2_approx(e0.x), ex2_approx(e0.y)));
+              float2 v = mul2(make_float2(sc[j + 2], sc[j + 3]), make_float2(ex2_approx(e1.x), ex2_approx(e1.y)));
               if (cg == q4) {
                 u.x = j0 + j <= lane ? u.x : 0.f;
                 u.y = j0 + j + 1 <= lane ? u.y : 0.f;

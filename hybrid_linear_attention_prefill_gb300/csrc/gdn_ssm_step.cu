@@ -36,36 +36,48 @@ gdn_ssm_step_kernel(const SsmArgs a, float* __restrict__ state) {
     cv[e] = __bfloat162float(cr[e]);
   }
   const int rows = a.dv / kStepWarps;  // 4, 8 or 16 a warp
-  for (int j = 0; j < rows; j += R) {
-    const int row = warp * rows + j;
-    float* p = state + ((size_t)blockIdx.x * a.dv + row) * DK + lane * E;
-    float s[R][E], y[R];
+  float* p0 = state + ((size_t)blockIdx.x * a.dv + warp * rows) * DK + lane * E;
+  // this lane's x and gate value of the warp's rows
+  const __nv_bfloat16* xr = a.x + b * a.xs + h * a.dv + warp * rows;
+  const float xv = lane < rows ? __bfloat162float(xr[lane]) : 0.f;
+  float zv = 0.f;
+  if (a.z != nullptr && lane < rows) zv = __bfloat162float(a.z[b * a.zs + h * a.dv + warp * rows + lane]);
+  float s[R][E], next[R][E];
 #pragma unroll
-    for (int r = 0; r < R; ++r) ssm_load_row<E>(p + r * DK, s[r]);
+  for (int r = 0; r < R; ++r) ssm_load_row<E>(p0 + r * DK, s[r]);
+  for (int j = 0; j < rows; j += R) {
+    if (j + R < rows) {  // the next rows' loads before this batch's arithmetic
+#pragma unroll
+      for (int r = 0; r < R; ++r) ssm_load_row<E>(p0 + (j + R + r) * DK, next[r]);
+    }
+    float y[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float xr = __bfloat162float(a.x[b * a.xs + h * a.dv + row + r]);
-      const float u = step * xr;
+      const float u = step * __shfl_sync(0xffffffffu, xv, j + r);
       y[r] = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         s[r][e] = ssm_decayed(decay, s[r][e], u * bv[e]);
         y[r] = fmaf(s[r][e], cv[e], y[r]);
       }
-      ssm_store_row<E>(p + r * DK, s[r]);
+      ssm_store_row<E>(p0 + (j + r) * DK, s[r]);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
       for (int r = 0; r < R; ++r) y[r] += __shfl_xor_sync(0xffffffffu, y[r], o);
-    if (lane < R) {
+    if (lane >= j && lane < j + R) {
       float v = y[0];
 #pragma unroll
-      for (int r = 1; r < R; ++r) v = lane == r ? y[r] : v;
-      v = fmaf(skip, __bfloat162float(a.x[b * a.xs + h * a.dv + row + lane]), v);
-      if (a.z != nullptr) v *= ssm_silu(__bfloat162float(a.z[b * a.zs + h * a.dv + row + lane]));
-      a.out[(size_t)blockIdx.x * a.dv + row + lane] = __float2bfloat16_rn(v);
+      for (int r = 1; r < R; ++r) v = lane == j + r ? y[r] : v;
+      v = fmaf(skip, xv, v);
+      if (a.z != nullptr) v *= silu2(make_float2(zv, zv)).x;
+      a.out[(size_t)blockIdx.x * a.dv + warp * rows + lane] = __float2bfloat16_rn(v);
     }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[r][e] = next[r][e];
   }
 }
 

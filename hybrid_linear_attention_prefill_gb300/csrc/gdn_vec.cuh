@@ -1,0 +1,63 @@
+// Arithmetic on a few values at a time that the elementwise kernels share.
+#pragma once
+
+#include "gdn_common.cuh"
+
+namespace gdn {
+
+// 1 / x and 2^x to a few units in the last place.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// silu of two values, v / (1 + e^-v), with one reciprocal: 1 / a = b / (a b).  The exponents stop at 2^62, so
+// that the product stays finite: below -43 a value v gives v 2^-62 where less would be exact.
+__device__ __forceinline__ float2 silu2(float2 v) {
+  const float2 t = mul2(v, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+  const float2 d = fma2(make_float2(ex2_approx(fminf(t.x, 62.f)), ex2_approx(fminf(t.y, 62.f))), make_float2(1.f, 1.f),
+                        make_float2(1.f, 1.f));
+  const float r = rcp_approx(d.x * d.y);
+  return mul2(v, mul2(make_float2(r, r), make_float2(d.y, d.x)));
+}
+
+// Eight bf16 as four pairs of fp32, and back.
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ void widen8(const uint4& r, float2 (&f)[4]) {
+  f[0] = widen2(r.x);
+  f[1] = widen2(r.y);
+  f[2] = widen2(r.z);
+  f[3] = widen2(r.w);
+}
+__device__ __forceinline__ uint4 narrow8(const float2 (&f)[4]) {
+  return make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y), pack_bf16(f[2].x, f[2].y),
+                    pack_bf16(f[3].x, f[3].y));
+}
+
+}  // namespace gdn
