@@ -397,6 +397,24 @@ bool take_injected_alloc_failure() {
   return n > 0;
 }
 
+int device_sms() {
+  static std::atomic<int> known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return 0;
+    }
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 int ensure_ssm_workspace(int dev, size_t need, void** ws) {
   if (dev < 0 || dev >= kMaxDevices) return GDN_ERR_ARG;
   std::lock_guard<std::mutex> lock(g_mu);

@@ -23,6 +23,9 @@ void* static_scratch_address(int dev);
 // is to fail (and counts it down).
 bool take_injected_alloc_failure();
 
+// SMs of the current device (0 without one).
+int device_sms();
+
 // gdn_ssm_scan's library-owned workspace on device `dev`, grown to at least `need` bytes (its first
 // 256 bytes are status words, zero when new): GDN_OK or the error code to return.
 int ensure_ssm_workspace(int dev, size_t need, void** ws);

@@ -114,24 +114,6 @@ gdn_ssm_join_kernel(const ssm::Segs g, const float* __restrict__ init, float* __
   }
 }
 
-int device_sms() {
-  static std::atomic<int> known[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return 0;
-  }
-  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return 0;
-    }
-    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Workspace: [256 B status words][packed: chunk table and dispatch order][segment states][segment decays]

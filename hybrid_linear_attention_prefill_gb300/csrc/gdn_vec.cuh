@@ -45,7 +45,7 @@ __device__ __forceinline__ float2 silu2(float2 v) {
   return mul2(v, mul2(make_float2(r, r), make_float2(d.y, d.x)));
 }
 
-// Eight bf16 as four pairs of fp32, and back.
+// Four or eight bf16 as pairs of fp32, and back.
 __device__ __forceinline__ float2 widen2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
@@ -58,6 +58,14 @@ __device__ __forceinline__ void widen8(const uint4& r, float2 (&f)[4]) {
 __device__ __forceinline__ uint4 narrow8(const float2 (&f)[4]) {
   return make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y), pack_bf16(f[2].x, f[2].y),
                     pack_bf16(f[3].x, f[3].y));
+}
+
+__device__ __forceinline__ void widen4(const uint2& r, float2 (&f)[2]) {
+  f[0] = widen2(r.x);
+  f[1] = widen2(r.y);
+}
+__device__ __forceinline__ uint2 narrow4(const float2 (&f)[2]) {
+  return make_uint2(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y));
 }
 
 }  // namespace gdn

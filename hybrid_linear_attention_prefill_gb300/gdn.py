@@ -62,6 +62,7 @@ EXPORTED = ("gdn_abi_version", "gdn_strerror", "gdn_last_cuda_error", "gdn_prefi
 
 _lock = threading.Lock()
 _lib = None
+_fast = None  # the gdn_torch module: the tensor wrappers' common case in C++
 
 
 class GdnError(RuntimeError):
@@ -78,7 +79,7 @@ def library_path() -> str:
 
 def load(build_if_missing: bool = False):
     """Load libgdn.so (optionally building it first) and declare the signatures."""
-    global _lib
+    global _lib, _fast
     if _lib is not None:
         return _lib
     with _lock:
@@ -132,8 +133,23 @@ def load(build_if_missing: bool = False):
             getattr(lib, name).restype = i
         lib.gdn_release_workspace.argtypes = []
         lib.gdn_release_workspace.restype = None
+        _fast = _load_fast()
         _lib = lib
         return lib
+
+
+def _load_fast():
+    """The gdn_torch module next to the library, or None where it was not built."""
+    if not os.path.exists(_build.TORCH_LIB):
+        return None
+    import importlib.util
+
+    import torch  # noqa: F401  (its libraries have to be there first)
+
+    spec = importlib.util.spec_from_file_location("gdn_torch", _build.TORCH_LIB)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
 
 
 def _ptr(x):
@@ -424,6 +440,13 @@ def causal_conv(x, weight, bias=None, cu_seqlens=None, init_state=None, *, B=Non
     init_state: bf16 [B, K-1, C], the inputs before each sequence, oldest first.  Returns (out bf16
     [Ttot, C], final_state bf16 [B, K-1, C] or None), in `out` and `final_state` where given.
     """
+    load()
+    if _fast is not None and out is not None and (final_state is not None or not want_final):
+        rc = _fast.causal_conv(x, weight, bias, cu_seqlens, init_state, B, silu, out, final_state, stream)
+        if rc is not None:
+            if rc:
+                check(rc)
+            return out, final_state
     import torch
 
     bf16 = torch.bfloat16
@@ -445,6 +468,13 @@ def causal_conv(x, weight, bias=None, cu_seqlens=None, init_state=None, *, B=Non
 
 def causal_conv_step(x, weight, state, bias=None, *, silu=True, out=None, stream=None):
     """One token of each of B sequences: x bf16 [B, C]; state bf16 [B, K-1, C], updated in place."""
+    load()
+    if _fast is not None and out is not None:
+        rc = _fast.causal_conv_step(x, weight, state, bias, silu, out, stream)
+        if rc is not None:
+            if rc:
+                check(rc)
+            return out
     import torch
 
     bf16 = torch.bfloat16
@@ -492,6 +522,14 @@ def ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, cu_seqlens=None, in
     `workspace`: a byte tensor of gdn_ssm_workspace_bytes(...), for calls that overlap or are captured.
     Returns (out bf16 [Ttot, Hv, dv], final_state fp32 [B, Hv, dv, dk] or None).
     """
+    load()
+    if _fast is not None and out is not None and (final_state is not None or not want_final):
+        rc = _fast.ssm_scan(x, dt, A, Bm, Cm, D, z, dt_bias, cu_seqlens, init_state, B, softplus, out, final_state,
+                            workspace, stream)
+        if rc is not None:
+            if rc:
+                check(rc)
+            return out, final_state
     import torch
 
     dev, (n, Hk, Hv, dk, dv), fields, out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus)
@@ -509,6 +547,13 @@ def ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, cu_seqlens=None, in
 
 def ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softplus=True, out=None, stream=None):
     """One token of each of B sequences of the scan: state fp32 [B, Hv, dv, dk], updated in place."""
+    load()
+    if _fast is not None and out is not None:
+        rc = _fast.ssm_step(x, dt, A, Bm, Cm, state, D, z, dt_bias, softplus, out, stream)
+        if rc is not None:
+            if rc:
+                check(rc)
+            return out
     import torch
 
     dev, (n, Hk, Hv, dk, dv), fields, out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus)
@@ -527,6 +572,13 @@ def add_norm(x, weight, residual=None, *, eps=1e-6, group=0, e4m3=False, out=Non
     `e4m3` follows from `out` where that is given.  Returns (out, scales or None, residual_out or None);
     residual_out may be `residual` itself.
     """
+    load()
+    if _fast is not None and out is not None and (residual is None or residual_out is not None):
+        rc = _fast.add_norm(x, weight, residual, eps, group, out, scales, residual_out, stream)
+        if rc is not None:
+            if rc:
+                check(rc)
+            return out, scales, residual_out
     import torch
 
     bf16, f8 = torch.bfloat16, torch.float8_e4m3fn
