@@ -8,6 +8,7 @@
 // between its two reductions.
 #include <cuda_fp8.h>
 
+#include "gdn_internal.h"
 #include "gdn_vec.cuh"
 
 namespace gdn {
@@ -37,14 +38,15 @@ gdn_add_norm_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __n
 
   float2 r[VPT][4];
   float2 sq = make_float2(0.f, 0.f);
-  uint4 xr[VPT], rr[VPT];  // every load of the row before any use
+  uint4 xr[VPT], rr[VPT], wr[VPT];  // every load of the row before any use
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = tid + j * tpr;
-    xr[j] = rr[j] = make_uint4(0, 0, 0, 0);
+    xr[j] = rr[j] = wr[j] = make_uint4(0, 0, 0, 0);
     if (live && v < nv) {
       xr[j] = *reinterpret_cast<const uint4*>(x + row * xs + 8 * v);
       if (residual != nullptr) rr[j] = *reinterpret_cast<const uint4*>(residual + row * D + 8 * v);
+      wr[j] = *reinterpret_cast<const uint4*>(weight + 8 * v);
     }
   }
 #pragma unroll
@@ -81,7 +83,7 @@ gdn_add_norm_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __n
     mx[j] = 0;
     if (live && v < nv) {
       float2 w[4];
-      widen8(*reinterpret_cast<const uint4*>(weight + 8 * v), w);
+      widen8(wr[j], w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         r[j][i] = mul2(mul2(r[j][i], make_float2(rstd, rstd)), w[i]);
@@ -163,8 +165,11 @@ cudaError_t launch_add_norm(const void* x, long long xs, const void* residual, c
                             void* out, float* scales, int rows, int D, int group, float eps, bool e4m3,
                             cudaStream_t st) {
   const int nv = D / 8;
-  int tpr = 32;  // two vectors a thread up to 1024 threads a row
-  while (tpr < 1024 && 2 * tpr < nv) tpr <<= 1;
+  // Four vectors a thread; with few rows one, for the latency of a row (4,096 columns: 4,096 rows 26.0 us with four,
+  // 27.1 with two, 30.5 with one).
+  const int want = rows < 2 * device_sms() ? 1 : 4;
+  int tpr = 32;
+  while (tpr < 1024 && want * tpr < nv) tpr <<= 1;
   const int vpt = (nv + tpr - 1) / tpr;
   if (vpt <= 1) return add_norm_v<1>(x, xs, residual, weight, residual_out, out, scales, rows, D, tpr, group, eps, e4m3, st);
   if (vpt <= 2) return add_norm_v<2>(x, xs, residual, weight, residual_out, out, scales, rows, D, tpr, group, eps, e4m3, st);

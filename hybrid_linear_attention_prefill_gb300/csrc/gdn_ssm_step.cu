@@ -6,7 +6,7 @@
 // (8 bytes an element) for five operations an element, so HBM bandwidth bounds it.  A warp holds
 // whole state rows, dk / 32 consecutive elements a lane, a batch of rows in flight; the row sums
 // S C go by warp shuffles.
-#include "gdn_common.cuh"
+#include "gdn_internal.h"
 #include "gdn_ssm.cuh"
 
 namespace gdn {
@@ -16,35 +16,42 @@ constexpr int kStepWarps = 8;
 constexpr int kStepRows = 4;  // rows a warp has in flight together
 }  // namespace
 
-// One CTA per (sequence, value head).
+// grid: ((sequence, value head), dv / (8 rows)); `rows` state rows a warp, 4, 8 or 16.
 template <int DK>
 __global__ void __launch_bounds__(32 * kStepWarps)
-gdn_ssm_step_kernel(const SsmArgs a, float* __restrict__ state) {
+gdn_ssm_step_kernel(const SsmArgs a, float* __restrict__ state, int rows) {
   constexpr int E = DK / 32, R = kStepRows;
   const int b = blockIdx.x / a.Hv, h = blockIdx.x - b * a.Hv;
   const int hk = h / (a.Hv / a.Hk);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float step = ssm_step_of(a, ssm_load_dt(a, b, h), ssm_bias(a, h));
-  const SsmDecay decay = ssm_decay(step * a.A[h]);
+  const int row0 = (blockIdx.y * kStepWarps + warp) * rows;
+  // every load before the first use of one
+  float* p0 = state + ((size_t)blockIdx.x * a.dv + row0) * DK + lane * E;
+  float s[R][E], next[R][E];
+#pragma unroll
+  for (int r = 0; r < R; ++r) ssm_load_row<E>(p0 + r * DK, s[r]);
+  const uint32_t raw_dt = ssm_load_dt(a, b, h);
+  const float bias = ssm_bias(a, h), rate = a.A[h];
   const float skip = a.D != nullptr ? a.D[h] : 0.f;
+  __nv_bfloat16 br[E], cr[E], xr = __float2bfloat16_rn(0.f), zr = xr;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    br[e] = a.Bm[b * a.bs + hk * DK + lane * E + e];
+    cr[e] = a.Cm[b * a.cs + hk * DK + lane * E + e];
+  }
+  if (lane < rows) {  // this lane's x and gate value of the warp's rows
+    xr = a.x[b * a.xs + h * a.dv + row0 + lane];
+    if (a.z != nullptr) zr = a.z[b * a.zs + h * a.dv + row0 + lane];
+  }
+  const float xv = __bfloat162float(xr), zv = __bfloat162float(zr);
   float bv[E], cv[E];
-  const __nv_bfloat16* br = a.Bm + b * a.bs + hk * DK + lane * E;
-  const __nv_bfloat16* cr = a.Cm + b * a.cs + hk * DK + lane * E;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     bv[e] = __bfloat162float(br[e]);
     cv[e] = __bfloat162float(cr[e]);
   }
-  const int rows = a.dv / kStepWarps;  // 4, 8 or 16 a warp
-  float* p0 = state + ((size_t)blockIdx.x * a.dv + warp * rows) * DK + lane * E;
-  // this lane's x and gate value of the warp's rows
-  const __nv_bfloat16* xr = a.x + b * a.xs + h * a.dv + warp * rows;
-  const float xv = lane < rows ? __bfloat162float(xr[lane]) : 0.f;
-  float zv = 0.f;
-  if (a.z != nullptr && lane < rows) zv = __bfloat162float(a.z[b * a.zs + h * a.dv + warp * rows + lane]);
-  float s[R][E], next[R][E];
-#pragma unroll
-  for (int r = 0; r < R; ++r) ssm_load_row<E>(p0 + r * DK, s[r]);
+  const float step = ssm_step_of(a, raw_dt, bias);
+  const SsmDecay decay = ssm_decay(step * rate);
   for (int j = 0; j < rows; j += R) {
     if (j + R < rows) {  // the next rows' loads before this batch's arithmetic
 #pragma unroll
@@ -72,7 +79,7 @@ gdn_ssm_step_kernel(const SsmArgs a, float* __restrict__ state) {
       for (int r = 1; r < R; ++r) v = lane == j + r ? y[r] : v;
       v = fmaf(skip, xv, v);
       if (a.z != nullptr) v *= silu2(make_float2(zv, zv)).x;
-      a.out[(size_t)blockIdx.x * a.dv + warp * rows + lane] = __float2bfloat16_rn(v);
+      a.out[(size_t)blockIdx.x * a.dv + row0 + lane] = __float2bfloat16_rn(v);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -82,11 +89,16 @@ gdn_ssm_step_kernel(const SsmArgs a, float* __restrict__ state) {
 }
 
 cudaError_t launch_ssm_step(const SsmArgs& a, float* state, int B, int dk, cudaStream_t st) {
-  const unsigned grid = (unsigned)(B * a.Hv);
+  // A warp streams up to 16 rows, the next four's loads in flight; with too few heads to fill the device four each,
+  // so that more SMs share the state.
+  const unsigned heads = (unsigned)(B * a.Hv);
+  int rows = a.dv / kStepWarps;
+  while (rows > kStepRows && heads * (a.dv / (kStepWarps * rows)) < 2u * (unsigned)device_sms()) rows >>= 1;
+  const dim3 grid(heads, a.dv / (kStepWarps * rows));
   switch (dk) {
-    case 32: gdn_ssm_step_kernel<32><<<grid, 32 * kStepWarps, 0, st>>>(a, state); break;
-    case 64: gdn_ssm_step_kernel<64><<<grid, 32 * kStepWarps, 0, st>>>(a, state); break;
-    default: gdn_ssm_step_kernel<128><<<grid, 32 * kStepWarps, 0, st>>>(a, state); break;
+    case 32: gdn_ssm_step_kernel<32><<<grid, 32 * kStepWarps, 0, st>>>(a, state, rows); break;
+    case 64: gdn_ssm_step_kernel<64><<<grid, 32 * kStepWarps, 0, st>>>(a, state, rows); break;
+    default: gdn_ssm_step_kernel<128><<<grid, 32 * kStepWarps, 0, st>>>(a, state, rows); break;
   }
   return cudaGetLastError();
 }
