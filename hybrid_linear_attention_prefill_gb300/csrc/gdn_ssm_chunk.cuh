@@ -21,6 +21,9 @@
 //            S; the next chunk's S -> bf16 and w x of tokens 0..63    | MMA: the next scores
 //            outputs                                                  | MMA: the next (w x)^T B of 0..63
 //
+// (With the warps split into a group that carries the state and a group that makes outputs, each chain
+// has half the warps to hide its latencies with: 783 us against 648 on 32 ragged prompts of 32 heads.)
+//
 // Operands.  x, B and C are used as they come (bf16).  The state and M are rounded to bf16 as operands
 // (2^-9 of each term, the size of the outputs' own rounding).  The state itself stays fp32: w x is
 // split into three bf16 terms (24 bits together) and each chunk's sum, 128 tokens long, is added to S
@@ -35,9 +38,11 @@ namespace gdn {
 namespace ssm {
 
 constexpr int kQ = 128;        // tokens a chunk
-constexpr int kWorkers = 16;   // worker warps: warp w reads TMEM lanes 32 (w % 4) .. + 31
-constexpr int kThreads = 32 * (kWorkers + 2);  // and a warp that issues, a warp that makes tables
+constexpr int kWorkers = 16;  // worker warp w reads TMEM lanes 32 (w % 4) .. + 31
+// A warp that issues and two that make tables (the output pass uses one).  Nineteen warps put five on three of the
+// SM's sub-partitions, which caps a thread at 96 registers.
 constexpr int kIssueWarp = kWorkers, kTableWarp = kWorkers + 1;
+constexpr int kThreads = 32 * (kWorkers + 3);
 constexpr uint32_t kTmemCols = 512;
 // TMEM columns: the scores and, in their place, M in bf16; y; the state's sum; w x in three terms
 constexpr uint32_t kColSc = 0, kColY = 128, kColDs = 256, kColXw = 384;
@@ -50,10 +55,12 @@ struct Segs {
   int B, T;
   int len;     // chunks a segment (0: whole sequences)
   int slots;   // segments of the grid
+  int joined;  // the stored states are start states (else the segments' sums)
 };
 
 struct Seg {
   int b;            // sequence
+  int p;            // the segment's place in it
   long long bos;    // its first token
   int t0, t1;       // the segment's tokens within it
   int slot;         // index of the segment's stored state
@@ -100,6 +107,7 @@ __device__ __forceinline__ bool find_seg(const Segs& g, int i, Seg& s) {
     if (s.b < 0) return false;
   }
   const SeqChunk q = seq_bounds(g.cu, s.b, g.T);
+  s.p = p;
   s.bos = q.bos;
   s.slot = i;
   const int per = g.len == 0 ? q.len : g.len * kQ;
@@ -124,16 +132,19 @@ struct Cfg {
   static constexpr int kXB = kRows / 64;            // 64-wide blocks of x
   static constexpr int kSC = DK / 4;                // state columns a thread holds
   static constexpr int kYC = kRows / 4;             // output columns a thread works on
-  // shared memory: two stages of [B][x], one C, the state operand (the gate's tile takes its place once
-  // C S^T is done), tables, barriers
+  // shared memory: two stages of [B][x], one C, the state operand, the gate's tile (in the place of the state
+  // operand, once C S^T is done, where there is no room for its own), tables, barriers
   static constexpr int kOffB = 0, kOffX = kNB * 16384, kStage = (kNB + kXB) * 16384;
   static constexpr int kOffC = 2 * kStage;
   static constexpr int kOffS = kOffC + kNB * 16384;
   static constexpr int kSBytes = kNB * kRows * 128 > kXB * 16384 ? kNB * kRows * 128 : kXB * 16384;
-  static constexpr int kOffTab = kOffS + kSBytes;
-  static constexpr int kTab = HPC * 3 * kQ * 4;     // L, K and w of a chunk
-  static constexpr int kOffBar = kOffTab + 2 * kTab;  // mbarriers, TMEM base, abort flag, decays
-  static constexpr int kSmemBytes = kOffBar + 256 + 1024;  // + slack for 1024-byte alignment
+  static constexpr int kTabBytes = HPC * 4 * kQ * 4;  // L and K of a chunk; w of two
+  static constexpr int kBarBytes = 256;               // mbarriers, TMEM base, abort flag, decays
+  static constexpr bool kOwnGate = kOffS + kSBytes + kXB * 16384 + kTabBytes + kBarBytes <= 227 * 1024;
+  static constexpr int kOffZ = kOwnGate ? kOffS + kSBytes : kOffS;
+  static constexpr int kOffTab = kOwnGate ? kOffZ + kXB * 16384 : kOffS + kSBytes;
+  static constexpr int kOffBar = kOffTab + kTabBytes;
+  static constexpr int kSmemBytes = kOffBar + kBarBytes;
   static_assert(PB == 64 || (PB == 128 && HPC == 1), "128 rows at most");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 };
@@ -216,12 +227,14 @@ __device__ __forceinline__ void to_steps(const SsmArgs& a, int n, float bias, in
   for (int u = 0; u < 4; ++u) d[u] = 4 * lane + u < n ? ssm_step_of(a, r[u], bias) : 0.f;
 }
 
-// One warp: the tables of a chunk from its steps.  L in units of log2, inclusive of each token's own
-// decay; returns L of the last token in every lane.  The weights' exponents are sums over the tokens after
-// each, from the end: as differences of L they would carry the rounding of a strong decay's large L.
-// tab: L, K = L - log2 s, w (kQ each), or w alone when STATES_ONLY.
-template <bool STATES_ONLY>
-__device__ __forceinline__ float make_tables(float* tab, const float (&d)[4], float a_log2, int lane) {
+// One warp: the tables of a chunk from its steps, tokens 4 lane .. + 3 in each lane: L in units of log2, inclusive
+// of each token's own decay; K = L - log2 s; w.  The weights' exponents are sums over the tokens after each, from
+// the end: as differences of L they would carry the rounding of a strong decay's large L.
+struct Tables {
+  float4 L, K, w;
+  float end;  // L of the last token, in every lane
+};
+__device__ __forceinline__ Tables make_tables(const float (&d)[4], float a_log2, int lane) {
   const float e0 = d[0] * a_log2, e1 = d[1] * a_log2, e2 = d[2] * a_log2, e3 = d[3] * a_log2;
   const float own = (e0 + e1) + (e2 + e3);
   float from = own, upto = own;  // sums over the lanes from and up to this one
@@ -231,22 +244,16 @@ __device__ __forceinline__ float make_tables(float* tab, const float (&d)[4], fl
     if (lane >= o) upto += y;
     if (lane + o < 32) from += z;
   }
-  const float end = __shfl_sync(0xffffffffu, upto, 31);
+  Tables t;
+  t.end = __shfl_sync(0xffffffffu, upto, 31);
   float before = __shfl_up_sync(0xffffffffu, upto, 1), after = __shfl_down_sync(0xffffffffu, from, 1);
   if (lane == 0) before = 0.f;
   if (lane == 31) after = 0.f;
-  const float4 w = make_float4(exp2f(after + ((e3 + e2) + e1)) * d[0], exp2f(after + (e3 + e2)) * d[1],
-                               exp2f(after + e3) * d[2], exp2f(after) * d[3]);
-  if (STATES_ONLY) {
-    reinterpret_cast<float4*>(tab)[lane] = w;
-  } else {
-    const float4 l = make_float4(before + e0, before + (e0 + e1), before + ((e0 + e1) + e2), before + own);
-    reinterpret_cast<float4*>(tab)[lane] = l;
-    reinterpret_cast<float4*>(tab + kQ)[lane] =
-        make_float4(l.x - log2f(d[0]), l.y - log2f(d[1]), l.z - log2f(d[2]), l.w - log2f(d[3]));
-    reinterpret_cast<float4*>(tab + 2 * kQ)[lane] = w;
-  }
-  return end;
+  t.w = make_float4(exp2f(after + ((e3 + e2) + e1)) * d[0], exp2f(after + (e3 + e2)) * d[1], exp2f(after + e3) * d[2],
+                    exp2f(after) * d[3]);
+  t.L = make_float4(before + e0, before + (e0 + e1), before + ((e0 + e1) + e2), before + own);
+  t.K = make_float4(t.L.x - log2f(d[0]), t.L.y - log2f(d[1]), t.L.z - log2f(d[2]), t.L.w - log2f(d[3]));
+  return t;
 }
 
 // w x of sixteen tokens t .. t + 15 of state rows row0 .. + 31 as three bf16 terms into columns col,

@@ -7,24 +7,23 @@
 namespace gdn {
 namespace ssm {
 
-constexpr int kBars = 14;
+constexpr int kBars = 15;
 
-// What both kernels set up: shared memory from a 1024-byte boundary, TMEM, barriers.
+// What both kernels set up: shared memory (from a 1024-byte boundary, as the swizzled tiles want), TMEM, barriers.
 struct Frame {
   unsigned char* sm;
   uint32_t sb;  // shared-window address of sm
   uint64_t* bars;
   uint32_t* tmem_slot;
   volatile int* abort_flag;
-  SsmDecay* lend;  // [2 buffers][heads]: e^{L_last}
+  SsmDecay* lend;  // [4 buffers][heads]: e^{L_last}
   float* tabs;
 };
 template <class C>
 __device__ __forceinline__ Frame make_frame(unsigned char* raw) {
-  const uint32_t r = smem_u32(raw), pad = ((r + 1023u) & ~1023u) - r;
   Frame f;
-  f.sm = raw + pad;
-  f.sb = r + pad;
+  f.sm = raw;
+  f.sb = smem_u32(raw);
   f.bars = reinterpret_cast<uint64_t*>(f.sm + C::kOffBar);
   f.tmem_slot = reinterpret_cast<uint32_t*>(f.bars + kBars);
   f.abort_flag = reinterpret_cast<volatile int*>(f.tmem_slot + 1);
@@ -46,6 +45,57 @@ __device__ __forceinline__ void load_stage(const Frame& f, int stage, const CUte
     tc::tma_load_2d(dst + C::kOffX + i * 16384, tm_x, PB == 64 ? (h0 + i) * dv : h0 * dv + 64 * i, t, bar);
 }
 
+// A segment's sum in the workspace is laid out by threads, kSC values of each of the 512 workers, float4 by float4,
+// so that a warp's access is one run of 512 bytes.
+template <class C>
+__device__ __forceinline__ size_t seg_at(int slot, int nhb, int hb, int tid) {
+  return (((size_t)slot * nhb + hb) * (C::kSC / 4) * (32 * kWorkers) + tid) * 4;
+}
+
+// The state of the CTA's heads between memory (rows of DK values, the heads one after the other) and the workers'
+// registers, by way of shared memory (the state operand's place), 64 columns at a time: a row's 16-byte pieces are
+// XORed with its number, so that both orders are free of bank conflicts.  All workers call it together.
+template <int DK, int PB, int HPC, bool kStore>
+__device__ __forceinline__ void move_state(unsigned char* buf, float* mem, int dv, int tid, float (&st)[DK / 4]) {
+  constexpr int kHalf = DK < 64 ? DK : 64, kPieces = kHalf / 4, kSC = DK / 4;
+  const int row = 32 * ((tid >> 5) & 3) + (tid & 31), cg = tid >> 7;
+  const int rows = HPC * dv;
+  const int hr = HPC == 2 ? row >> 6 : 0, p = PB == 64 ? row & 63 : row;
+  const bool mine = row < PB * HPC && p < dv;
+  const int my = hr * dv + p;  // the row in memory
+#pragma unroll
+  for (int hf = 0; hf < DK / kHalf; ++hf) {
+    const bool here = mine && cg / (kHalf / kSC) == hf;
+    const int c0 = (cg % (kHalf / kSC)) * (kSC / 4);
+    if (kStore && here) {
+#pragma unroll
+      for (int i = 0; i < kSC / 4; ++i)
+        *reinterpret_cast<float4*>(buf + (my * kPieces + ((c0 + i) ^ (my & (kPieces - 1)))) * 16) =
+            make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
+    }
+    if (kStore) asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kWorkers) : "memory");
+    for (int e = tid; e < rows * kPieces; e += 32 * kWorkers) {
+      const int r = e / kPieces, c = e % kPieces;
+      float4* s = reinterpret_cast<float4*>(buf + (r * kPieces + (c ^ (r & (kPieces - 1)))) * 16);
+      float4* m = reinterpret_cast<float4*>(mem + (size_t)r * DK + hf * kHalf + 4 * c);
+      if (kStore) *m = *s;
+      else *s = *m;
+    }
+    asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kWorkers) : "memory");
+    if (!kStore) {
+      if (here) {
+#pragma unroll
+        for (int i = 0; i < kSC / 4; ++i) {
+          const float4 v =
+              *reinterpret_cast<const float4*>(buf + (my * kPieces + ((c0 + i) ^ (my & (kPieces - 1)))) * 16);
+          st[4 * i] = v.x; st[4 * i + 1] = v.y; st[4 * i + 2] = v.z; st[4 * i + 3] = v.w;
+        }
+      }
+      asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kWorkers) : "memory");
+    }
+  }
+}
+
 // Outputs (and the final state of a sequence's last segment) of one segment and head block.
 // grid: segments x head blocks, the head blocks of a segment side by side (they read the same B and C).
 template <int DK, int PB, int HPC>
@@ -53,17 +103,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_z,
                      const __grid_constant__ CUtensorMap tm_o, const SsmArgs a, const Segs g,
-                     const float* seg_state, const float* init, float* fin, int* __restrict__ err) {
+                     const float* seg_state, const float* seg_decay, const float* init, float* fin,
+                     int* __restrict__ err) {
   using C = Cfg<DK, PB, HPC>;
-  extern __shared__ unsigned char smem_raw[];
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
   const Frame f = make_frame<C>(smem_raw);
   // Completed by the MMAs, once a chunk each: scores, (w x)^T B of half 0 and C S^T, (w x)^T B of half 1, y.  By
   // copies: the two stages, C, the gate's tile.  By the worker warps: the first operands of a chunk (the state,
-  // w x), the second (M, y, w x), the gate read, y read, the outputs out of the x tile.  By the table warp: a
-  // chunk's tables, its stage loaded.
+  // w x), the second (M, y, w x), the gate read, y (and the gate) read, the outputs out of the x tile, and once their last chunk.  By the
+  // table warp: a chunk's tables, its stage loaded.  Every waiter waits for every phase in turn, and no phase after it can
+  // end before it has looked (a parity only names the last phase that ended): what leads to the next one waits for
+  // the waiter.
   uint64_t *b_sc = f.bars, *b_in = f.bars + 1, *b_d1 = f.bars + 2, *b_y = f.bars + 3, *b_st = f.bars + 4,
            *b_c = f.bars + 6, *b_z = f.bars + 7, *w_a = f.bars + 8, *w_b = f.bars + 9, *w_z = f.bars + 10,
-           *w_y = f.bars + 11, *w_s = f.bars + 12, *b_tab = f.bars + 13;
+           *w_y = f.bars + 11, *w_s = f.bars + 12, *b_tab = f.bars + 13, *w_e = f.bars + 14;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == kIssueWarp) {
@@ -77,18 +130,16 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     }
   }
   if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) tc::mbar_init(&f.bars[i], i >= 8 && i < 13 ? kWorkers : 1);
+    for (int i = 0; i < kBars; ++i) tc::mbar_init(&f.bars[i], i >= 8 && i != 13 ? kWorkers : 1);
     tc::fence_mbar_init();
     *f.abort_flag = 0;
   }
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the segments' start states
-
   const int nhb = a.Hv / HPC, seg = blockIdx.x / nhb;
   const int h0 = (blockIdx.x - seg * nhb) * HPC;
   const int hk = h0 / (a.Hv / a.Hk);
   Seg s;
   const bool live = find_seg(g, seg, s);
-  if (!live) s.t0 = s.t1 = 0, s.b = 0, s.bos = 0, s.slot = 0, s.first = s.last = false;
+  if (!live) s.t0 = s.t1 = 0, s.b = 0, s.p = 0, s.bos = 0, s.slot = 0, s.first = s.last = false;
   const int ntok = s.t1 - s.t0, nc = (ntok + kQ - 1) / kQ;
   const long long tok0 = s.bos + s.t0;
   if (g.cu != nullptr && h0 == 0 && live && s.first && tid == 0) {
@@ -99,6 +150,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *f.tmem_slot;
+  const bool gate = a.z != nullptr;
   auto wait1 = [&](uint64_t* bar, uint32_t par, int bit) { return wait_for(bar, par, f.abort_flag, err, bit); };
   auto wait = [&](uint64_t* bar, uint32_t par, int bit) {  // a whole warp
     const bool done = wait1(bar, par, bit);
@@ -122,7 +174,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       tc::mbar_arrive_expect_tx(b_z, C::kXB * 16384);
 #pragma unroll
       for (int i = 0; i < C::kXB; ++i)
-        tc::tma_load_2d(f.sm + C::kOffS + i * 16384, &tm_z, PB == 64 ? (h0 + i) * a.dv : h0 * a.dv + 64 * i, t, b_z);
+        tc::tma_load_2d(f.sm + C::kOffZ + i * 16384, &tm_z, PB == 64 ? (h0 + i) * a.dv : h0 * a.dv + 64 * i, t, b_z);
     };
     const uint64_t c_kmajor = tc::sdesc(f.sb + C::kOffC, 16, 1024, tc::kSw128);
     // scores of chunk c: C_i . B_j over the chunk's tokens, once both tiles are in
@@ -153,6 +205,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
           if (!(ok = wait1(w_y, par ^ 1u, 1))) break;
           tc::fence_after();
         }
+        if (C::kOwnGate && gate) load_z(c);
         {
           constexpr uint32_t kId = tc::idesc_bf16(128, C::kRows, 0, 0);
           const uint64_t bd = tc::sdesc(f.sb + C::kOffS, 16, 1024, tc::kSw128);
@@ -162,9 +215,9 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                          bd + (uint64_t)(((ks >> 2) * (C::kRows * 128) + (ks & 3) * 32) >> 4), kId, ks > 0);
           tc::commit(b_in);
         }
-        if (c + 1 < nc || a.z != nullptr) {
+        if (c + 1 < nc || (!C::kOwnGate && gate)) {
           if (!(ok = wait1(b_in, par, 1))) break;
-          if (a.z != nullptr) load_z(c);  // over the state operand
+          if (!C::kOwnGate && gate) load_z(c);  // over the state operand
           if (c + 1 < nc) load_c(c + 1);
           if (c > 0 && c + 1 < nc) {  // the stage of the chunk before
             if (!(ok = wait1(w_s, par ^ 1u, 1))) break;
@@ -205,16 +258,23 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       if (nc > 0) load_dt(a, tok0, ntok, h0 + hh, lane, raw[hh]);
     }
     for (int c = 0; c < nc; ++c) {
-      // The tables of chunk c - 2 were read up to its second operands.  Every phase is waited for in turn: a
-      // parity names the last phase that ended, whichever that is.
-      if (c > 1 && !wait(w_b, (uint32_t)(c & 1), 1)) break;
+      Tables t[HPC];
 #pragma unroll
       for (int hh = 0; hh < HPC; ++hh) {
         float d[4];
         to_steps(a, ntok - c * kQ, bias[hh], lane, raw[hh], d);
         if (c + 1 < nc) load_dt(a, tok0 + (long long)(c + 1) * kQ, ntok - (c + 1) * kQ, h0 + hh, lane, raw[hh]);
-        const float end = make_tables<false>(f.tabs + (c & 1) * (C::kTab / 4) + hh * 3 * kQ, d, a_log2[hh], lane);
-        if (lane == 0) f.lend[(c & 1) * HPC + hh] = ssm_decay(end * 0.6931471805599453f);
+        t[hh] = make_tables(d, a_log2[hh], lane);
+      }
+      // the tables of chunk c - 1 were read up to its second operands (the decays, used after them, have four places)
+      if (c > 0 && !wait(w_b, (uint32_t)((c - 1) & 1), 1)) break;
+#pragma unroll
+      for (int hh = 0; hh < HPC; ++hh) {
+        float4* tab = reinterpret_cast<float4*>(f.tabs + hh * 3 * kQ);
+        tab[lane] = t[hh].L;
+        tab[32 + lane] = t[hh].K;
+        tab[64 + lane] = t[hh].w;
+        if (lane == 0) f.lend[(c & 3) * HPC + hh] = ssm_decay(t[hh].end * 0.6931471805599453f);
       }
       if (!wait(&b_st[c & 1], (uint32_t)((c >> 1) & 1), 2)) break;
       if (lane == 0) arrive(b_tab);
@@ -223,7 +283,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
 #pragma unroll
         for (int i = 0; i < C::kXB; ++i) {
           const int col = PB == 64 ? (h0 + i) * a.dv : h0 * a.dv + 64 * i;
-          if (a.z != nullptr) tma_prefetch_l2_2d(&tm_z, col, t);
+          if (gate) tma_prefetch_l2_2d(&tm_z, col, t);
           if (c > 0 && c + 1 < nc) tma_prefetch_l2_2d(&tm_x, col, t + kQ);
         }
         if (c > 0 && c + 1 < nc)
@@ -232,7 +292,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       }
       __syncwarp();
     }
-  } else {
+  } else if (warp < kWorkers) {
     // ================= workers =================
     const int q4 = warp & 3, cg = warp >> 2;
     const int row = 32 * q4 + lane;  // state row, or token of the chunk
@@ -241,15 +301,24 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     const int hr = HPC == 2 ? row >> 6 : 0, p = PB == 64 ? row & 63 : row;
     const bool my_row = live && row < C::kRows && p < a.dv;
     float st[C::kSC];
-    {
-      const float* src = g.len != 0 ? seg_state + (size_t)s.slot * a.Hv * a.dv * DK
-                                    : init != nullptr ? init + (size_t)s.b * a.Hv * a.dv * DK : nullptr;
 #pragma unroll
-      for (int i = 0; i < C::kSC; i += 4) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (my_row && src != nullptr)
-          v = *reinterpret_cast<const float4*>(src + ((size_t)(h0 + hr) * a.dv + p) * DK + C::kSC * cg + i);
-        st[i] = v.x; st[i + 1] = v.y; st[i + 2] = v.z; st[i + 3] = v.w;
+    for (int i = 0; i < C::kSC; ++i) st[i] = 0.f;
+    const size_t st_at = ((size_t)s.b * a.Hv + h0) * a.dv * DK;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the segments' sums; the final state may replace init
+    if (live && init != nullptr)
+      move_state<DK, PB, HPC, false>(f.sm + C::kOffS, const_cast<float*>(init) + st_at, a.dv, tid, st);
+    // the sums of the segments before: one by one where they are few, or joined into one
+    for (int i = g.joined ? s.slot : s.slot - s.p; i < s.slot + (g.joined && s.p > 0 ? 1 : 0); ++i) {
+      if (!my_row) break;
+      const float4* e = reinterpret_cast<const float4*>(seg_state + seg_at<C>(i, nhb, h0 / HPC, tid));
+      const SsmDecay d = ssm_decay(seg_decay[(size_t)i * a.Hv + h0 + hr] * 0.6931471805599453f);
+#pragma unroll
+      for (int u = 0; u < C::kSC / 4; ++u) {
+        const float4 v = e[u * 32 * kWorkers];
+        st[4 * u] = ssm_decayed(d, st[4 * u], v.x);
+        st[4 * u + 1] = ssm_decayed(d, st[4 * u + 1], v.y);
+        st[4 * u + 2] = ssm_decayed(d, st[4 * u + 2], v.z);
+        st[4 * u + 3] = ssm_decayed(d, st[4 * u + 3], v.w);
       }
     }
     // this warp's outputs: tokens 32 q4 .. + 31, columns kYC cg .., worked on by rows in the warp's own part of the
@@ -262,8 +331,6 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     const int mt = 32 * q4 + lane / kP, mp = lane % kP;  // memory order: token mt + (32 / kP) i, piece mp
     const int quad = 2 + 4 * (yc >> 6) + q4;  // named barrier of the warps that share 32 tokens of a 64-wide block
     const uint32_t yoff = (uint32_t)(yc >> 6) * 16384, ych = (uint32_t)(yc & 63) >> 3;
-    const bool gate = a.z != nullptr;
-
     bool ok = true;
     // The first operands of chunk c: the state, and w x of its first 64 tokens.
     auto first_operands = [&](int c) {
@@ -277,7 +344,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
               make_uint4(0, 0, 0, 0);
         asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kWorkers) : "memory");
       }
-      if (gate && c > 0 && !wait(w_z, (uint32_t)((c - 1) & 1), 1)) return false;  // every warp has read the gate there
+      if (!C::kOwnGate && gate && c > 0 && !wait(w_z, (uint32_t)((c - 1) & 1), 1)) return false;  // the gate there is read
       if (row < C::kRows) {
 #pragma unroll
         for (int i = 0; i < C::kSC; i += 8) {
@@ -288,7 +355,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                          pack_bf16(st[i + 6], st[i + 7]));
         }
       }
-      const float* tab = f.tabs + (c & 1) * (C::kTab / 4);
+      const float* tab = f.tabs;
       if (32 * q4 < C::kRows)
         split_xw(stage + C::kOffX, tab + hr * 3 * kQ + 2 * kQ, 32 * q4, 16 * cg, tq + kColXw + 8 * cg);
       tmem_st_wait();
@@ -303,46 +370,48 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       const uint32_t par = (uint32_t)(c & 1);
       unsigned char* xt = f.sm + (c & 1) * C::kStage + C::kOffX;
       unsigned char* yt = xt + yoff;
-      const float* tab = f.tabs + (c & 1) * (C::kTab / 4);
+      const float* tab = f.tabs;
       const int n = min(kQ, ntok - c * kQ);
 
       // ---- M from the scores, in their place: eight columns a head of each 16 ------------------------
       if (!(ok = wait(b_sc, par, 1))) break;
       tc::fence_after();
-#pragma unroll
-      for (int j0 = 0; j0 < 32; j0 += 16) {
-        const uint32_t col = tq + kColSc + 32 * cg + j0;
+      {
+        const uint32_t col = tq + kColSc + 32 * cg;
         uint32_t m[8];
         if (cg <= q4) {
-          float sc[16];
-          tc::tmem_ld16(col, sc);
+          float sc[32];
+          tc::tmem_ld32(col, sc);
 #pragma unroll
           for (int hh = 0; hh < HPC; ++hh) {
             const float* th = tab + hh * 3 * kQ;
             const float li = th[row];
+            const float2 minus = make_float2(-1.f, -1.f), l2 = make_float2(li, li);
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 k4 = *reinterpret_cast<const float4*>(th + kQ + 32 * cg + j0 + j);
-              const float2 minus = make_float2(-1.f, -1.f), l2 = make_float2(li, li);
+            for (int j = 0; j < 32; j += 4) {
+              const float4 k4 = *reinterpret_cast<const float4*>(th + kQ + 32 * cg + j);
               const float2 e0 = fma2(make_float2(k4.x, k4.y), minus, l2), e1 = fma2(make_float2(k4.z, k4.w), minus, l2);
               float2 u = mul2(make_float2(sc[j], sc[j + 1]), make_float2(ex2_approx(e0.x), ex2_approx(e0.y)));
               float2 v = mul2(make_float2(sc[j + 2], sc[j + 3]), make_float2(ex2_approx(e1.x), ex2_approx(e1.y)));
               if (cg == q4) {
-                u.x = j0 + j <= lane ? u.x : 0.f;
-                u.y = j0 + j + 1 <= lane ? u.y : 0.f;
-                v.x = j0 + j + 2 <= lane ? v.x : 0.f;
-                v.y = j0 + j + 3 <= lane ? v.y : 0.f;
+                u.x = j <= lane ? u.x : 0.f;
+                u.y = j + 1 <= lane ? u.y : 0.f;
+                v.x = j + 2 <= lane ? v.x : 0.f;
+                v.y = j + 3 <= lane ? v.y : 0.f;
               }
-              m[j / 2] = pack_bf16(u.x, u.y);
-              m[j / 2 + 1] = pack_bf16(v.x, v.y);
+              m[(j & 15) / 2] = pack_bf16(u.x, u.y);
+              m[(j & 15) / 2 + 1] = pack_bf16(v.x, v.y);
+              if ((j & 15) == 12) tmem_st8_nowait(col + (j & 16) + 8 * hh, m);
             }
-            tmem_st8_nowait(col + 8 * hh, m);
           }
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) m[j] = 0u;
 #pragma unroll
-          for (int hh = 0; hh < HPC; ++hh) tmem_st8_nowait(col + 8 * hh, m);
+          for (int hh = 0; hh < HPC; ++hh) {
+            tmem_st8_nowait(col + 8 * hh, m);
+            tmem_st8_nowait(col + 16 + 8 * hh, m);
+          }
         }
       }
       if (c > 0) {  // the chunk before's outputs have left its x tile
@@ -375,25 +444,29 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       if (lane == 0) arrive(w_b);
 
       // ---- the gate -------------------------------------------------------------------------------------
-      // Of this thread's row of the gate, half goes through silu while M x runs; the rest waits as it is (all of
-      // it would not fit the registers).
-      uint4 zr[kP];
-      float2 gv[2 * kP];
-      auto gates = [&](int i, int u) {
-        const uint32_t w = u == 0 ? zr[i].x : u == 1 ? zr[i].y : u == 2 ? zr[i].z : zr[i].w;
-        return silu2(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
-      };
+      // Of this thread's row of the gate, half goes through silu while M x runs; the rest waits (all of it would not
+      // fit the registers).
+      const unsigned char* zt = f.sm + C::kOffZ + yoff;
+      uint4 zr[C::kOwnGate ? 1 : kP / 2];
+      float2 gv[4 * kP];
+      auto gates = [](const uint4& z, int u) { return silu2(widen2(u == 0 ? z.x : u == 1 ? z.y : u == 2 ? z.z : z.w)); };
+      auto z_piece = [&](int i) { return *reinterpret_cast<const uint4*>(zt + tc::sw128((uint32_t)row, ych + i)); };
       if (gate) {
         if (!(ok = wait(b_z, par, 2))) break;
-        const unsigned char* zt = f.sm + C::kOffS + yoff;
+        if (!C::kOwnGate) {
 #pragma unroll
-        for (int i = 0; i < kP; ++i) zr[i] = *reinterpret_cast<const uint4*>(zt + tc::sw128((uint32_t)row, ych + i));
-        __syncwarp();
-        if (lane == 0) arrive(w_z);
+          for (int i = kP / 2; i < kP; ++i) zr[C::kOwnGate ? 0 : i - kP / 2] = z_piece(i);
+        }
 #pragma unroll
-        for (int i = 0; i < kP / 2; ++i)
+        for (int i = 0; i < kP / 2; ++i) {
+          const uint4 z = z_piece(i);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) gv[4 * i + u] = gates(i, u);
+          for (int u = 0; u < 4; ++u) gv[4 * i + u] = gates(z, u);
+        }
+        if (!C::kOwnGate) {
+          __syncwarp();
+          if (lane == 0) arrive(w_z);
+        }
       }
       // ---- S = e^{L_last} S + the chunk's sum ---------------------------------------------------------
       if (!(ok = wait(b_d1, par, 1))) break;
@@ -401,7 +474,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       {
         float ds[C::kSC];
         tmem_load<C::kSC>(tq + kColDs + C::kSC * cg, ds);
-        const SsmDecay decay = f.lend[(c & 1) * HPC + hr];
+        const SsmDecay decay = f.lend[(c & 3) * HPC + hr];
 #pragma unroll
         for (int i = 0; i < C::kSC; i += 2) {
           const float2 v = make_float2(st[i], st[i + 1]);
@@ -419,26 +492,30 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
         for (int i0 = 0; i0 < kP; i0 += 2) {  // sixteen columns of this thread's own row at a time
           float y[16];
           tc::tmem_ld16(tq + kColY + yc + 8 * i0, y);
+#pragma unroll
+          for (int i = i0; i < i0 + 2; ++i) {
+            if (gate && i >= kP / 2) {
+              const uint4 z = C::kOwnGate ? z_piece(i) : zr[C::kOwnGate ? 0 : i - kP / 2];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) gv[4 * i + u] = gates(z, u);
+            }
+          }
           if (i0 + 2 == kP) {
             tc::fence_before();
             __syncwarp();
             if (lane == 0) arrive(w_y);
           }
-          uint4 x[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const uint4*>(yt + tc::sw128((uint32_t)row, ych + i0 + i));
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t x4[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint4* at = reinterpret_cast<uint4*>(yt + tc::sw128((uint32_t)row, ych + i0 + i));
             float2 v[4];
+            widen8(*at, v);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              v[u] = fma2(make_float2(__uint_as_float(x4[u] << 16), __uint_as_float(x4[u] & 0xffff0000u)),
-                          make_float2(skip, skip), make_float2(y[8 * i + 2 * u], y[8 * i + 2 * u + 1]));
-              if (gate) v[u] = mul2(v[u], i0 + i < kP / 2 ? gv[4 * ((i0 + i) % (kP / 2)) + u] : gates(i0 + i, u));
+              v[u] = fma2(v[u], make_float2(skip, skip), make_float2(y[8 * i + 2 * u], y[8 * i + 2 * u + 1]));
+              if (gate) v[u] = mul2(v[u], gv[4 * (i0 + i) + u]);
             }
-            *reinterpret_cast<uint4*>(yt + tc::sw128((uint32_t)row, ych + i0 + i)) = make_uint4(
-                pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
+            *at = narrow8(v);
           }
         }
         if (a.dv >= 64 && 32 * q4 + 32 <= n) {  // 32 whole tokens of 64 columns: one copy by the first of their warps
@@ -470,11 +547,11 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       asm volatile("bar.arrive 1, %0;\n" ::"n"(32 * kWorkers) : "memory");
       asm volatile("bar.arrive %0, %1;\n" ::"r"(quad), "n"(32 * (64 / C::kYC)) : "memory");
     }
-    if (ok && fin != nullptr && s.last && my_row) {
-      float* dst = fin + (((size_t)s.b * a.Hv + h0 + hr) * a.dv + p) * DK + C::kSC * cg;
-#pragma unroll
-      for (int i = 0; i < C::kSC; i += 4)
-        *reinterpret_cast<float4*>(dst + i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
+    if (ok && fin != nullptr && live && s.last) {
+      __syncwarp();
+      if (lane == 0) arrive(w_e);
+      if (wait(w_e, 0, 1))  // every warp has come this far
+        move_state<DK, PB, HPC, true>(f.sm + C::kOffS, fin + st_at, a.dv, tid, st);
     }
   }
   tc::fence_before();
@@ -495,9 +572,11 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
                        const SsmArgs a, const Segs g, float* __restrict__ seg_state, float* __restrict__ seg_decay,
                        int* __restrict__ err) {
   using C = Cfg<DK, PB, HPC>;
-  extern __shared__ unsigned char smem_raw[];
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
   const Frame f = make_frame<C>(smem_raw);
-  uint64_t *b_d = f.bars, *b_st = f.bars + 1, *w_a = f.bars + 8, *b_tab = f.bars + 13;
+  constexpr int kSC = C::kSC;
+  uint64_t *b_d = f.bars, *b_st = f.bars + 1, *w_a = f.bars + 3, *b_tab = f.bars + 5;  // w_a, b_tab: even and odd chunks
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // what follows starts up beside this pass
   const int nhb = a.Hv / HPC, seg = blockIdx.x / nhb;
   Seg s;
   if (!find_seg(g, seg, s) || s.last) return;  // a last segment's sum is nobody's start
@@ -507,7 +586,7 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
     tc::tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) tc::mbar_init(&f.bars[i], i == 8 ? kWorkers : 1);
+    for (int i = 0; i < kBars; ++i) tc::mbar_init(&f.bars[i], i == 3 || i == 4 ? kWorkers : 1);
     tc::fence_mbar_init();
     *f.abort_flag = 0;
   }
@@ -537,7 +616,7 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
       load(0);
       if (nc > 1) load(1);
       for (int c = 0; c < nc; ++c) {
-        if (!wait1(w_a, (uint32_t)(c & 1), 1)) break;  // w x of chunk c written, the sum of c - 1 read
+        if (!wait1(&w_a[c & 1], (uint32_t)((c >> 1) & 1), 1)) break;  // w x of chunk c written, the sum of c - 1 read
         tc::fence_after();
         if (c > 0 && c + 1 < nc) load(c + 1);
 #pragma unroll
@@ -547,7 +626,9 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
       }
     }
     __syncwarp();
-  } else if (warp == kTableWarp) {
+  } else if (warp >= kWorkers) {
+    // even and odd chunks' tables
+    const int odd = warp == (kTableWarp + 1);
     float a_log2[HPC], bias[HPC], total[HPC];
     uint32_t raw[HPC][4];
 #pragma unroll
@@ -555,43 +636,45 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
       a_log2[hh] = a.A[h0 + hh] * 1.4426950408889634f;
       bias[hh] = ssm_bias(a, h0 + hh);
       total[hh] = 0.f;
-      load_dt(a, tok0, kQ, h0 + hh, lane, raw[hh]);
+      if (odd < nc) load_dt(a, tok0 + odd * kQ, kQ, h0 + hh, lane, raw[hh]);
     }
-    for (int c = 0; c < nc; ++c) {
-      if (c > 0 && !wait(w_a, (uint32_t)((c - 1) & 1), 1)) break;
+    for (int c = odd; c < nc; c += 2) {
+      // the tables of chunk c - 2 were read before its operands were announced
+      if (c > 1 && !wait(&w_a[odd], (uint32_t)(((c - 2) >> 1) & 1), 1)) break;
 #pragma unroll
       for (int hh = 0; hh < HPC; ++hh) {
         float d[4];
         to_steps(a, kQ, bias[hh], lane, raw[hh], d);
-        if (c + 1 < nc) load_dt(a, tok0 + (long long)(c + 1) * kQ, kQ, h0 + hh, lane, raw[hh]);
-        const float end = make_tables<true>(f.tabs + ((c & 1) * HPC + hh) * kQ, d, a_log2[hh], lane);
-        total[hh] += end;
-        if (lane == 0) f.lend[(c & 1) * HPC + hh] = ssm_decay(end * 0.6931471805599453f);
+        if (c + 2 < nc) load_dt(a, tok0 + (long long)(c + 2) * kQ, kQ, h0 + hh, lane, raw[hh]);
+        const Tables t = make_tables(d, a_log2[hh], lane);
+        reinterpret_cast<float4*>(f.tabs + (odd * HPC + hh) * kQ)[lane] = t.w;
+        total[hh] += t.end;
+        if (lane == 0) f.lend[odd * HPC + hh] = ssm_decay(t.end * 0.6931471805599453f);
       }
       __syncwarp();
-      if (lane == 0) arrive(b_tab);
+      if (lane == 0) arrive(&b_tab[odd]);
     }
     if (lane == 0) {
 #pragma unroll
-      for (int hh = 0; hh < HPC; ++hh) seg_decay[(size_t)s.slot * a.Hv + h0 + hh] = total[hh];
+      for (int hh = 0; hh < HPC; ++hh) f.tabs[(2 + odd) * HPC * kQ + hh] = total[hh];  // past both buffers
     }
   } else {
     const int q4 = warp & 3, cg = warp >> 2;
     const int row = 32 * q4 + lane;
     const uint32_t tq = tmem + ((uint32_t)(32 * q4) << 16);
     const int hr = HPC == 2 ? row >> 6 : 0, p = PB == 64 ? row & 63 : row;
-    float st[C::kSC];
+    float st[kSC];
 #pragma unroll
-    for (int i = 0; i < C::kSC; ++i) st[i] = 0.f;
+    for (int i = 0; i < kSC; ++i) st[i] = 0.f;
     bool ok = true;
     SsmDecay decay = {1.f, 0.f};  // of the chunk whose sum comes next
     auto update = [&](int c) {    // S after chunk c
       if (!(ok = wait(b_d, (uint32_t)(c & 1), 1))) return;
       tc::fence_after();
-      float ds[C::kSC];
-      tmem_load<C::kSC>(tq + kSum + C::kSC * cg, ds);
+      float ds[kSC];
+      tmem_load<kSC>(tq + kSum + kSC * cg, ds);
 #pragma unroll
-      for (int i = 0; i < C::kSC; i += 2) {
+      for (int i = 0; i < kSC; i += 2) {
         const float2 v = make_float2(st[i], st[i + 1]);
         const float2 r = fma2(make_float2(decay.keep, decay.keep), v,
                               fma2(make_float2(decay.more, decay.more), v, make_float2(ds[i], ds[i + 1])));
@@ -602,7 +685,7 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
     for (int c = 0; c < nc; ++c) {
       const float* w = f.tabs + ((c & 1) * HPC + hr) * kQ;
       const unsigned char* xt = f.sm + (c & 1) * C::kStage + C::kOffX;
-      if (!(ok = wait(&b_st[c & 1], (uint32_t)((c >> 1) & 1), 2) && wait(b_tab, (uint32_t)(c & 1), 1))) break;
+      if (!(ok = wait(&b_st[c & 1], (uint32_t)((c >> 1) & 1), 2) && wait(&b_tab[c & 1], (uint32_t)((c >> 1) & 1), 1))) break;
       if (32 * q4 < C::kRows) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) split_xw(xt, w, 32 * q4, 64 * hf + 16 * cg, tq + xw_col(c, hf) + 8 * cg);
@@ -613,18 +696,20 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
       tmem_st_wait();
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) arrive(w_a);
+      if (lane == 0) arrive(&w_a[c & 1]);
     }
     if (ok) update(nc - 1);
     if (ok && row < C::kRows && p < a.dv) {
-      float* dst = seg_state + (((size_t)s.slot * a.Hv + h0 + hr) * a.dv + p) * DK + C::kSC * cg;
+      float4* dst = reinterpret_cast<float4*>(seg_state + seg_at<C>(s.slot, nhb, h0 / HPC, tid));
 #pragma unroll
-      for (int i = 0; i < C::kSC; i += 4)
-        *reinterpret_cast<float4*>(dst + i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
+      for (int u = 0; u < kSC / 4; ++u)
+        dst[u * 32 * kWorkers] = make_float4(st[4 * u], st[4 * u + 1], st[4 * u + 2], st[4 * u + 3]);
     }
   }
   tc::fence_before();
   __syncthreads();
+  if (!*f.abort_flag && tid < HPC)
+    seg_decay[(size_t)s.slot * a.Hv + h0 + tid] = f.tabs[2 * HPC * kQ + tid] + f.tabs[3 * HPC * kQ + tid];
   if (*f.abort_flag && warp == kIssueWarp && lane == 0) {
     for (int i = 0; i < 3; ++i)
       for (uint32_t par = 0; par < 2; ++par) (void)tc::mbar_wait(&f.bars[i], par, 1u << 14);
@@ -657,7 +742,8 @@ cudaError_t launch(const Maps& m, const SsmArgs& a,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = g.len != 0 ? 1 : 0;  // behind the combine kernel of the same call
-  e = cudaLaunchKernelEx(&cfg, gdn_ssm_chunk_kernel<DK, PB, HPC>, m.x, m.b, m.c, m.z, m.out, a, g, (const float*)seg_state, init, fin,
+  e = cudaLaunchKernelEx(&cfg, gdn_ssm_chunk_kernel<DK, PB, HPC>, m.x, m.b, m.c, m.z, m.out, a, g, (const float*)seg_state,
+                         (const float*)seg_decay, init, fin,
                          err);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

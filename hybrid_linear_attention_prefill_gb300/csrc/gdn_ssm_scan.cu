@@ -3,8 +3,9 @@
 //
 // A CTA carries the state of its heads through a segment's chunks one after the other.  Where sequences
 // and heads are too few to fill the device, sequences are cut into segments: one pass sums every segment
-// from a zero state (x, B and dt only, about 0.4 of a chunk's time), gdn_ssm_join_kernel turns the sums
-// into start states, and the output pass runs every segment from its own.
+// from a zero state (x, B and dt only, about 0.4 of a chunk's time), and the output pass runs every segment
+// from the sums before it (with many segments gdn_ssm_join_kernel makes start states of them first).  The
+// later kernels are programmatic dependents: they set up beside the one before.
 #include <algorithm>
 
 #include "../../include/gdn.h"
@@ -23,7 +24,7 @@ cudaError_t launch_dk(const Maps&, const SsmArgs&, const Segs&, float*, float*, 
 
 namespace {
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;
 
 struct Plan {
   int hpc = 1;    // heads a CTA
@@ -62,15 +63,18 @@ Plan make_plan(int B, int T, int Hk, int Hv, int dv, bool packed, int sms) {
   return p;
 }
 
-// Segment start states from the segments' sums E and decays, in place: S_start(0) = the initial state,
-// S_start(k + 1) = decay_k S_start(k) + E_k.  One thread per four state elements of a (sequence, head).
-// grid: (B * Hv, blocks over dv * dk / 4)
+// The segments' sums E_k joined, in place: the state before segment k but for the initial state, and the log of that
+// state's decay up to it.  One thread per four values of a (sequence, head block), in the workspace's layout by
+// worker threads (`pb` rows reserved for each of `hpc` heads).  grid: (B * head blocks, blocks over dk * 32)
 __global__ void __launch_bounds__(kJoinThreads)
-gdn_ssm_join_kernel(const ssm::Segs g, const float* __restrict__ init, float* __restrict__ seg_state,
-                    const float* __restrict__ seg_decay, int Hv, int nstate) {
+gdn_ssm_join_kernel(const ssm::Segs g, float* __restrict__ seg_state, const float* __restrict__ seg_decay,
+                    float* __restrict__ seg_total, int Hv, int dk, int dv, int pb, int hpc) {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int b = blockIdx.x / Hv, h = blockIdx.x - b * Hv;
+  const int nhb = Hv / hpc, b = blockIdx.x / nhb, hb = blockIdx.x - b * nhb;
   const int e = blockIdx.y * kJoinThreads + threadIdx.x;
+  const int worker = e % (32 * ssm::kWorkers), row = 32 * ((worker >> 5) & 3) + (worker & 31);
+  const int hr = hpc == 2 ? row >> 6 : 0, p = pb == 64 ? row & 63 : row;
   int slot0 = 0, n;
   if (g.cu == nullptr) {
     n = ssm::seg_count(g, g.T);
@@ -78,37 +82,41 @@ gdn_ssm_join_kernel(const ssm::Segs g, const float* __restrict__ init, float* __
   } else {
     n = ssm::seg_count(g, seq_bounds(g.cu, b, g.T).len);
     const int lane = threadIdx.x & 31;  // segments of the sequences before: every warp sums them
-    int sum = 0;
+    long long sum = 0;
     for (int i = lane; i < b; i += 32) sum += ssm::seg_count(g, seq_bounds(g.cu, i, g.T).len);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    slot0 = sum;
-    if (slot0 > g.slots) slot0 = g.slots;
-    if (n > g.slots - slot0) n = g.slots - slot0;  // malformed boundaries
+    slot0 = sum < g.slots ? (int)sum : g.slots;  // malformed boundaries may claim more than there are
+    n = n < g.slots - slot0 ? n : g.slots - slot0;
   }
-  if (4 * e >= nstate) return;
+  if (e >= dk * 32 || row >= pb * hpc || p >= dv) return;
+  const int h = hb * hpc + hr;
+  const bool teller = p == 0 && worker < 32 * 4 && e == worker;  // one thread a head
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (init != nullptr) s = *reinterpret_cast<const float4*>(init + ((size_t)b * Hv + h) * nstate + 4 * e);
-  constexpr int kAhead = 4;
+  float total = 0.f;
+  constexpr int kAhead = 8;
   float4 v[kAhead];
-  SsmDecay m[kAhead];
-  auto at = [&](int k) { return seg_state + ((size_t)(slot0 + k) * Hv + h) * nstate + 4 * e; };
+  float l[kAhead];
+  auto at = [&](int k) { return reinterpret_cast<float4*>(seg_state) + ((size_t)(slot0 + k) * nhb + hb) * dk * 32 + e; };
   for (int k0 = 0; k0 < n; k0 += kAhead) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
       if (k0 + u + 1 < n) {
-        v[u] = *reinterpret_cast<const float4*>(at(k0 + u));
-        m[u] = ssm_decay(seg_decay[(size_t)(slot0 + k0 + u) * Hv + h] * 0.6931471805599453f);
+        v[u] = *at(k0 + u);
+        l[u] = seg_decay[(size_t)(slot0 + k0 + u) * Hv + h];
       }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (k0 + u >= n) break;
-      *reinterpret_cast<float4*>(at(k0 + u)) = s;
+      if (k0 + u > 0) *at(k0 + u) = s;
+      if (teller) seg_total[(size_t)(slot0 + k0 + u) * Hv + h] = total;
       if (k0 + u + 1 < n) {
-        s.x = ssm_decayed(m[u], s.x, v[u].x);
-        s.y = ssm_decayed(m[u], s.y, v[u].y);
-        s.z = ssm_decayed(m[u], s.z, v[u].z);
-        s.w = ssm_decayed(m[u], s.w, v[u].w);
+        const SsmDecay m = ssm_decay(l[u] * 0.6931471805599453f);
+        total += l[u];
+        s.x = ssm_decayed(m, s.x, v[u].x);
+        s.y = ssm_decayed(m, s.y, v[u].y);
+        s.z = ssm_decayed(m, s.z, v[u].z);
+        s.w = ssm_decayed(m, s.w, v[u].w);
       }
     }
   }
@@ -116,16 +124,18 @@ gdn_ssm_join_kernel(const ssm::Segs g, const float* __restrict__ init, float* __
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Workspace: [256 B status words][packed: chunk table and dispatch order][segment states][segment decays]
+// Workspace: [256 B status words][packed: chunk table and dispatch order][segment states, 128 rows a head block]
+//            [segment decays][joined decays]
 struct Layout {
-  size_t states, decays, total;
+  size_t states, decays, totals, total;
 };
-Layout layout(const Plan& p, int B, int Hv, int dk, int dv, bool packed) {
+Layout layout(const Plan& p, int B, int Hv, int dk, bool packed) {
   Layout l;
   l.states = 256 + (packed ? chunk_table_bytes(B) : 0);
-  const size_t n = p.len != 0 ? (size_t)p.slots * Hv : 0;
-  l.decays = l.states + align256(n * dv * dk * 4);
-  l.total = l.decays + align256(n * 4);
+  const size_t n = p.len != 0 ? (size_t)p.slots : 0;
+  l.decays = l.states + align256(n * (Hv / p.hpc) * dk * 128 * 4);
+  l.totals = l.decays + align256(n * Hv * 4);
+  l.total = l.totals + align256(n * Hv * 4);
   return l;
 }
 
@@ -143,7 +153,7 @@ size_t ssm_scan_workspace(int B, int T, int Hk, int Hv, int dk, int dv, int pack
   const int sms = device_sms();
   // without a device: enough for any (a segment of one chunk for every chunk)
   Plan p = make_plan(B, T, Hk, Hv, dv, packed != 0, sms > 0 ? sms : 1 << 20);
-  return layout(p, B, Hv, dk, dv, packed != 0).total;
+  return layout(p, B, Hv, dk, packed != 0).total;
 }
 
 cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* init, float* fin, void* ws, int B, int T,
@@ -152,11 +162,12 @@ cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* in
   if (sms == 0) return cudaErrorNoDevice;
   const bool packed = cu != nullptr;
   const Plan p = make_plan(B, T, a.Hk, a.Hv, a.dv, packed, sms);
-  const Layout l = layout(p, B, a.Hv, dk, a.dv, packed);
+  const Layout l = layout(p, B, a.Hv, dk, packed);
   unsigned char* w = static_cast<unsigned char*>(ws);
   int* err = static_cast<int*>(ws);
   float* states = reinterpret_cast<float*>(w + l.states);
   float* decays = reinterpret_cast<float*>(w + l.decays);
+  float* totals = reinterpret_cast<float*>(w + l.totals);
   const long long ntok = packed ? (long long)T : (long long)B * T;
   if ((long long)p.slots * (a.Hv / p.hpc) > 0x7fffffffLL) return cudaErrorInvalidValue;
   ssm::Maps m = {};
@@ -173,19 +184,25 @@ cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* in
   g.T = T;
   g.len = p.len;
   g.slots = p.slots;
+  // With few segments a sequence the output pass goes through the sums before its own by itself (a load of the state
+  // each, hidden behind its first tiles); more are joined by a kernel (about 5 us).
+  const int per = p.len * ssm::kQ;
+  g.joined = p.len != 0 && (T + per - 1) / per > 8;
   auto run = [&](int phase) {
+    float* dec = phase == 1 && g.joined ? totals : decays;
     switch (dk) {
-      case 32: return ssm::launch_dk<32>(m, a, g, states, decays, init, fin, err, p.hpc, phase, st);
-      case 64: return ssm::launch_dk<64>(m, a, g, states, decays, init, fin, err, p.hpc, phase, st);
-      default: return ssm::launch_dk<128>(m, a, g, states, decays, init, fin, err, p.hpc, phase, st);
+      case 32: return ssm::launch_dk<32>(m, a, g, states, dec, init, fin, err, p.hpc, phase, st);
+      case 64: return ssm::launch_dk<64>(m, a, g, states, dec, init, fin, err, p.hpc, phase, st);
+      default: return ssm::launch_dk<128>(m, a, g, states, dec, init, fin, err, p.hpc, phase, st);
     }
   };
   cudaError_t e;
   if (p.len != 0) {
     if ((e = run(0)) != cudaSuccess) return e;
-    const int nstate = a.dv * dk;
+  }
+  if (g.joined) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(B * a.Hv), (unsigned)((nstate / 4 + kJoinThreads - 1) / kJoinThreads));
+    cfg.gridDim = dim3((unsigned)(B * (a.Hv / p.hpc)), (unsigned)(dk * 32 / kJoinThreads));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -193,9 +210,10 @@ cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* in
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, gdn_ssm_join_kernel, (const ssm::Segs)g, init, states, (const float*)decays, a.Hv, nstate);
+    e = cudaLaunchKernelEx(&cfg, gdn_ssm_join_kernel, (const ssm::Segs)g, states, (const float*)decays, totals, a.Hv, dk,
+                           a.dv, a.dv == 128 ? 128 : 64, p.hpc);
     if (e != cudaSuccess) return e;
-  } else if (packed && B > 1) {  // whole sequences of different lengths: the longest start first
+  } else if (p.len == 0 && packed && B > 1) {  // whole sequences of different lengths: the longest start first
     int32_t* off = reinterpret_cast<int32_t*>(w + 256);
     if ((e = launch_chunk_table(cu, B, T, off, off + B + 1, err, st)) != cudaSuccess) return e;
     g.order = off + B + 1;
