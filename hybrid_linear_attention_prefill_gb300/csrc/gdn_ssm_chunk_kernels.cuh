@@ -489,6 +489,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       if (!(ok = wait(b_y, par, 1))) break;
       tc::fence_after();
       {
+#pragma unroll
         for (int i0 = 0; i0 < kP; i0 += 2) {  // sixteen columns of this thread's own row at a time
           float y[16];
           tc::tmem_ld16(tq + kColY + yc + 8 * i0, y);
