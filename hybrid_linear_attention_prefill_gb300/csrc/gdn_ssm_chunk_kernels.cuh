@@ -8,6 +8,7 @@ namespace gdn {
 namespace ssm {
 
 constexpr int kBars = 15;
+constexpr int kSegStages = 3;  // of the pass of the sums
 
 // What both kernels set up: shared memory (from a 1024-byte boundary, as the swizzled tiles want), TMEM, barriers.
 struct Frame {
@@ -565,7 +566,8 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
   if (warp == kIssueWarp) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-// The sums of the segments before a sequence's last (from a zero state) and their decays in log2.
+// The sums of the segments before a sequence's last (from a zero state) and their decays in log2.  Three stages of B
+// and x: with two, a chunk's load (about 2,000 cycles) stood in the way of every chunk.
 // grid: segments x head blocks.
 template <int DK, int PB, int HPC>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -576,7 +578,9 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const Frame f = make_frame<C>(smem_raw);
   constexpr int kSC = C::kSC;
-  uint64_t *b_d = f.bars, *b_st = f.bars + 1, *w_a = f.bars + 3, *b_tab = f.bars + 5;  // w_a, b_tab: even and odd chunks
+  static_assert(kSegStages * C::kStage <= C::kOffTab, "stages");
+  // the sum; the stages loaded; w x written and tables made, for even and odd chunks
+  uint64_t *b_d = f.bars, *b_st = f.bars + 1, *w_a = f.bars + 4, *b_tab = f.bars + 6;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // what follows starts up beside this pass
   const int nhb = a.Hv / HPC, seg = blockIdx.x / nhb;
   Seg s;
@@ -585,9 +589,13 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
   if (warp == kIssueWarp) {
     tc::tmem_alloc(f.tmem_slot, kTmemCols);
     tc::tmem_relinquish();
+    if (lane == 0) {
+      tc::prefetch_tensormap(&tm_x);
+      tc::prefetch_tensormap(&tm_b);
+    }
   }
   if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) tc::mbar_init(&f.bars[i], i == 3 || i == 4 ? kWorkers : 1);
+    for (int i = 0; i < kBars; ++i) tc::mbar_init(&f.bars[i], i == 4 || i == 5 ? kWorkers : 1);
     tc::fence_mbar_init();
     *f.abort_flag = 0;
   }
@@ -611,18 +619,18 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
 
   if (warp == kIssueWarp) {
     auto load = [&](int c) {
-      load_stage<DK, PB, C>(f, c & 1, &tm_b, &tm_x, hk, h0, a.dv, (int)(tok0 + (long long)c * kQ), &b_st[c & 1]);
+      load_stage<DK, PB, C>(f, c % kSegStages, &tm_b, &tm_x, hk, h0, a.dv, (int)(tok0 + (long long)c * kQ),
+                            &b_st[c % kSegStages]);
     };
     if (lane == 0) {
-      load(0);
-      if (nc > 1) load(1);
+      for (int c = 0; c < kSegStages && c < nc; ++c) load(c);
       for (int c = 0; c < nc; ++c) {
         if (!wait1(&w_a[c & 1], (uint32_t)((c >> 1) & 1), 1)) break;  // w x of chunk c written, the sum of c - 1 read
         tc::fence_after();
-        if (c > 0 && c + 1 < nc) load(c + 1);
+        if (c > 0 && c + kSegStages - 1 < nc) load(c + kSegStages - 1);  // the stage of chunk c - 1
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
-          issue_state<DK>(tmem + kSum, tmem + xw_col(c, hf), f.sb + (c & 1) * C::kStage + C::kOffB, hf, hf == 0);
+          issue_state<DK>(tmem + kSum, tmem + xw_col(c, hf), f.sb + (c % kSegStages) * C::kStage + C::kOffB, hf, hf == 0);
         tc::commit(b_d);
       }
     }
@@ -685,8 +693,8 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
     };
     for (int c = 0; c < nc; ++c) {
       const float* w = f.tabs + ((c & 1) * HPC + hr) * kQ;
-      const unsigned char* xt = f.sm + (c & 1) * C::kStage + C::kOffX;
-      if (!(ok = wait(&b_st[c & 1], (uint32_t)((c >> 1) & 1), 2) && wait(&b_tab[c & 1], (uint32_t)((c >> 1) & 1), 1))) break;
+      const unsigned char* xt = f.sm + (c % kSegStages) * C::kStage + C::kOffX;
+      if (!(ok = wait(&b_st[c % kSegStages], (uint32_t)((c / kSegStages) & 1), 2) && wait(&b_tab[c & 1], (uint32_t)((c >> 1) & 1), 1))) break;
       if (32 * q4 < C::kRows) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) split_xw(xt, w, 32 * q4, 64 * hf + 16 * cg, tq + xw_col(c, hf) + 8 * cg);
@@ -712,7 +720,7 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
   if (!*f.abort_flag && tid < HPC)
     seg_decay[(size_t)s.slot * a.Hv + h0 + tid] = f.tabs[2 * HPC * kQ + tid] + f.tabs[3 * HPC * kQ + tid];
   if (*f.abort_flag && warp == kIssueWarp && lane == 0) {
-    for (int i = 0; i < 3; ++i)
+    for (int i = 0; i < 1 + kSegStages; ++i)
       for (uint32_t par = 0; par < 2; ++par) (void)tc::mbar_wait(&f.bars[i], par, 1u << 14);
   }
   __syncwarp();
