@@ -149,10 +149,10 @@ struct Cfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 };
 
-// A wait that gives up when another thread has (or after 2^26 polls), and says so to the others.
+// A wait that gives up when another thread has (or after 2^24 polls, about half a second), and says so to the others.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t par, volatile int* abort_flag, int* err, int bit) {
   const uint32_t addr = smem_u32(bar);
-  for (uint32_t i = 0; i < 1u << 26; ++i) {
+  for (uint32_t i = 0; i < 1u << 24; ++i) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"

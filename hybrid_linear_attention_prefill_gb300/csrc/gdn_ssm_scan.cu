@@ -3,7 +3,7 @@
 //
 // A CTA carries the state of its heads through a segment's chunks one after the other.  Where sequences
 // and heads are too few to fill the device, sequences are cut into segments: one pass sums every segment
-// from a zero state (x, B and dt only, about 0.4 of a chunk's time), and the output pass runs every segment
+// from a zero state (x, B and dt only, about a quarter of a chunk's time), and the output pass runs every segment
 // from the sums before it (with many segments gdn_ssm_join_kernel makes start states of them first).  The
 // later kernels are programmatic dependents: they set up beside the one before.
 #include <algorithm>
@@ -25,6 +25,7 @@ cudaError_t launch_dk(const Maps&, const SsmArgs&, const Segs&, float*, float*, 
 namespace {
 
 constexpr int kJoinThreads = 128;
+constexpr int kAloneSegs = 8;  // segments a sequence that the output pass goes through by itself
 
 struct Plan {
   int hpc = 1;    // heads a CTA
@@ -34,7 +35,7 @@ struct Plan {
 
 // Heads a CTA and the segments' length, from the sizes alone (a packed batch's lengths are on the device:
 // taken as equal).  In units of an output pass's chunk step: a CTA costs its chunks and about one more to start
-// and drain, 0.4 of a step a chunk and one in the pass of the sums, and the join about one.
+// and drain, a quarter of a step a chunk and 0.8 in the pass of the sums, and the join about one.
 Plan make_plan(int B, int T, int Hk, int Hv, int dv, bool packed, int sms) {
   Plan p;
   p.hpc = dv < 128 && (Hv / Hk) % 2 == 0 ? 2 : 1;
@@ -49,7 +50,8 @@ Plan make_plan(int B, int T, int Hk, int Hv, int dv, bool packed, int sms) {
     const int len = (nc + n - 1) / n;
     if (n > 2 && (nc + n - 2) / (n - 1) == len) continue;  // the same length as with fewer
     const long long segs = (nc + len - 1) / len;
-    const double cost = waves(hb * B * segs) * (len + 1.0) + waves(hb * B * (segs - 1)) * (0.4 * len + 1.0) + 1.0;
+    const double cost = waves(hb * B * segs) * (len + 1.0) +
+                        waves(hb * B * (segs - 1)) * (0.25 * len + 0.8) + (segs > kAloneSegs ? 1.0 : 0.15 * (segs - 1));
     if (cost < best) {
       best = cost;
       p.len = len;
@@ -184,10 +186,10 @@ cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* in
   g.T = T;
   g.len = p.len;
   g.slots = p.slots;
-  // With few segments a sequence the output pass goes through the sums before its own by itself (a load of the state
-  // each, hidden behind its first tiles); more are joined by a kernel (about 5 us).
+  // With few segments a sequence the output pass goes through the sums before its own by itself (about 0.8 us each,
+  // beside its first tiles' load); more are joined by a kernel (about 5 us).
   const int per = p.len * ssm::kQ;
-  g.joined = p.len != 0 && (T + per - 1) / per > 8;
+  g.joined = p.len != 0 && (T + per - 1) / per > kAloneSegs;
   auto run = [&](int phase) {
     float* dec = phase == 1 && g.joined ? totals : decays;
     switch (dk) {
