@@ -41,7 +41,7 @@ constexpr int kQ = 128;        // tokens a chunk
 constexpr int kWorkers = 16;  // worker warp w reads TMEM lanes 32 (w % 4) .. + 31
 // A warp that issues and two that make tables (the output pass uses one).  Nineteen warps put five on three of the
 // SM's sub-partitions, which caps a thread at 96 registers.
-constexpr int kIssueWarp = kWorkers, kTableWarp = kWorkers + 1;
+constexpr int kIssueWarp = kWorkers, kTableWarp = kWorkers + 1, kAllocWarp = kWorkers + 2;
 constexpr int kThreads = 32 * (kWorkers + 3);
 constexpr uint32_t kTmemCols = 512;
 // TMEM columns: the scores and, in their place, M in bf16; y; the state's sum; w x in three terms

@@ -120,20 +120,9 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
            *w_y = f.bars + 11, *w_s = f.bars + 12, *b_tab = f.bars + 13, *w_e = f.bars + 14;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (warp == kIssueWarp) {
+  if (warp == kAllocWarp) {
     tc::tmem_alloc(f.tmem_slot, kTmemCols);
     tc::tmem_relinquish();
-    if (lane == 0 && g.T > 0) {
-      tc::prefetch_tensormap(&tm_x);
-      tc::prefetch_tensormap(&tm_b);
-      tc::prefetch_tensormap(&tm_c);
-      if (a.z != nullptr) tc::prefetch_tensormap(&tm_z);
-    }
-  }
-  if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) tc::mbar_init(&f.bars[i], i >= 8 && i != 13 ? kWorkers : 1);
-    tc::fence_mbar_init();
-    *f.abort_flag = 0;
   }
   const int nhb = a.Hv / HPC, seg = blockIdx.x / nhb;
   const int h0 = (blockIdx.x - seg * nhb) * HPC;
@@ -143,9 +132,28 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
   if (!live) s.t0 = s.t1 = 0, s.b = 0, s.p = 0, s.bos = 0, s.slot = 0, s.first = s.last = false;
   const int ntok = s.t1 - s.t0, nc = (ntok + kQ - 1) / kQ;
   const long long tok0 = s.bos + s.t0;
-  if (g.cu != nullptr && h0 == 0 && live && s.first && tid == 0) {
-    const int lo = g.cu[s.b], hi = g.cu[s.b + 1];
-    if (lo < 0 || hi < lo || hi > g.T || (s.b == 0 && lo != 0) || (s.b == g.B - 1 && hi != g.T)) atomicOr(err, 8);
+  auto load = [&](int c) {
+    load_stage<DK, PB, C>(f, c & 1, &tm_b, &tm_x, hk, h0, a.dv, (int)(tok0 + (long long)c * kQ), &b_st[c & 1]);
+  };
+  auto load_c = [&](int c) {
+    const int t = (int)(tok0 + (long long)c * kQ);
+    tc::mbar_arrive_expect_tx(b_c, C::kNB * 16384);
+#pragma unroll
+    for (int i = 0; i < C::kNB; ++i) tc::tma_load_2d(f.sm + C::kOffC + i * 16384, &tm_c, hk * DK + 64 * i, t, b_c);
+  };
+  if (warp == kIssueWarp && lane == 0) {  // the inputs are there whatever runs before: the first tiles at once
+    for (int i = 0; i < kBars; ++i) tc::mbar_init(&f.bars[i], i >= 8 && i != 13 ? kWorkers : 1);
+    tc::fence_mbar_init();
+    *f.abort_flag = 0;
+    if (nc > 0) {
+      load(0);
+      load_c(0);
+      if (nc > 1) load(1);
+    }
+    if (g.cu != nullptr && h0 == 0 && live && s.first) {
+      const int lo = g.cu[s.b], hi = g.cu[s.b + 1];
+      if (lo < 0 || hi < lo || hi > g.T || (s.b == 0 && lo != 0) || (s.b == g.B - 1 && hi != g.T)) atomicOr(err, 8);
+    }
   }
   tc::fence_before();
   __syncthreads();
@@ -161,15 +169,6 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
 
   if (warp == kIssueWarp) {
     // ================= copies and MMAs: one thread =================
-    auto load = [&](int c) {
-      load_stage<DK, PB, C>(f, c & 1, &tm_b, &tm_x, hk, h0, a.dv, (int)(tok0 + (long long)c * kQ), &b_st[c & 1]);
-    };
-    auto load_c = [&](int c) {
-      const int t = (int)(tok0 + (long long)c * kQ);
-      tc::mbar_arrive_expect_tx(b_c, C::kNB * 16384);
-#pragma unroll
-      for (int i = 0; i < C::kNB; ++i) tc::tma_load_2d(f.sm + C::kOffC + i * 16384, &tm_c, hk * DK + 64 * i, t, b_c);
-    };
     auto load_z = [&](int c) {
       const int t = (int)(tok0 + (long long)c * kQ);
       tc::mbar_arrive_expect_tx(b_z, C::kXB * 16384);
@@ -192,9 +191,6 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       return true;
     };
     if (lane == 0 && nc > 0) {
-      load(0);
-      load_c(0);
-      if (nc > 1) load(1);
       bool ok = scores(0);
       for (int c = 0; ok && c < nc; ++c) {
         const uint32_t par = (uint32_t)(c & 1);
@@ -309,17 +305,35 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     if (live && init != nullptr)
       move_state<DK, PB, HPC, false>(f.sm + C::kOffS, const_cast<float*>(init) + st_at, a.dv, tid, st);
     // the sums of the segments before: one by one where they are few, or joined into one
-    for (int i = g.joined ? s.slot : s.slot - s.p; i < s.slot + (g.joined && s.p > 0 ? 1 : 0); ++i) {
-      if (!my_row) break;
-      const float4* e = reinterpret_cast<const float4*>(seg_state + seg_at<C>(i, nhb, h0 / HPC, tid));
-      const SsmDecay d = ssm_decay(seg_decay[(size_t)i * a.Hv + h0 + hr] * 0.6931471805599453f);
+    const int i0 = g.joined ? s.slot : s.slot - s.p, i1 = s.slot + (g.joined && s.p > 0 ? 1 : 0);
+    if (my_row && i0 < i1) {  // half of a sum's values are on their way while the other half is added
+      constexpr int kH = C::kSC / 8;
+      auto fetch = [&](int i, int hf, float4 (&v)[kH]) {
+        const float4* e = reinterpret_cast<const float4*>(seg_state + seg_at<C>(i, nhb, h0 / HPC, tid));
 #pragma unroll
-      for (int u = 0; u < C::kSC / 4; ++u) {
-        const float4 v = e[u * 32 * kWorkers];
-        st[4 * u] = ssm_decayed(d, st[4 * u], v.x);
-        st[4 * u + 1] = ssm_decayed(d, st[4 * u + 1], v.y);
-        st[4 * u + 2] = ssm_decayed(d, st[4 * u + 2], v.z);
-        st[4 * u + 3] = ssm_decayed(d, st[4 * u + 3], v.w);
+        for (int u = 0; u < kH; ++u) v[u] = e[(hf * kH + u) * 32 * kWorkers];
+      };
+      auto add = [&](const SsmDecay& d, int hf, const float4 (&v)[kH]) {
+#pragma unroll
+        for (int u = 0; u < kH; ++u) {
+          float* q = st + 4 * (hf * kH + u);
+          q[0] = ssm_decayed(d, q[0], v[u].x);
+          q[1] = ssm_decayed(d, q[1], v[u].y);
+          q[2] = ssm_decayed(d, q[2], v[u].z);
+          q[3] = ssm_decayed(d, q[3], v[u].w);
+        }
+      };
+      const float* dec = seg_decay + h0 + hr;
+      float4 lo[kH], hi[kH];
+      float l = dec[(size_t)i0 * a.Hv];
+      fetch(i0, 0, lo);
+      for (int i = i0; i < i1; ++i) {
+        fetch(i, 1, hi);
+        const SsmDecay d = ssm_decay(l * 0.6931471805599453f);
+        if (i + 1 < i1) l = dec[(size_t)(i + 1) * a.Hv];
+        add(d, 0, lo);
+        if (i + 1 < i1) fetch(i + 1, 0, lo);
+        add(d, 1, hi);
       }
     }
     // this warp's outputs: tokens 32 q4 .. + 31, columns kYC cg .., worked on by rows in the warp's own part of the
@@ -542,12 +556,14 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
   }
   tc::fence_before();
   __syncthreads();
-  if (*f.abort_flag && warp == kIssueWarp && lane == 0) {  // let what is in flight land, bounded again
-    for (int i = 0; i < 8; ++i)
-      for (uint32_t par = 0; par < 2; ++par) (void)tc::mbar_wait(&f.bars[i], par, 1u << 14);
+  if (*f.abort_flag) {  // let what is in flight land, bounded again
+    if (tid == 0) {
+      for (int i = 0; i < 8; ++i)
+        for (uint32_t par = 0; par < 2; ++par) (void)tc::mbar_wait(&f.bars[i], par, 1u << 14);
+    }
+    __syncthreads();
   }
-  __syncwarp();
-  if (warp == kIssueWarp) tc::tmem_dealloc(tmem, kTmemCols);
+  if (warp == kAllocWarp) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
 // The sums of the segments before a sequence's last (from a zero state) and their decays in log2.  Three stages of B
@@ -570,23 +586,24 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
   Seg s;
   if (!find_seg(g, seg, s) || s.last) return;  // a last segment's sum is nobody's start
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (warp == kIssueWarp) {
+  if (warp == kAllocWarp) {
     tc::tmem_alloc(f.tmem_slot, kTmemCols);
     tc::tmem_relinquish();
-    if (lane == 0) {
-      tc::prefetch_tensormap(&tm_x);
-      tc::prefetch_tensormap(&tm_b);
-    }
-  }
-  if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) tc::mbar_init(&f.bars[i], i == 4 || i == 5 ? kWorkers : 1);
-    tc::fence_mbar_init();
-    *f.abort_flag = 0;
   }
   const int h0 = (blockIdx.x - seg * nhb) * HPC;
   const int hk = h0 / (a.Hv / a.Hk);
   const int nc = (s.t1 - s.t0) / kQ;  // whole chunks: only a last segment is ragged
   const long long tok0 = s.bos + s.t0;
+  auto load = [&](int c) {
+    load_stage<DK, PB, C>(f, c % kSegStages, &tm_b, &tm_x, hk, h0, a.dv, (int)(tok0 + (long long)c * kQ),
+                          &b_st[c % kSegStages]);
+  };
+  if (warp == kIssueWarp && lane == 0) {
+    for (int i = 0; i < kBars; ++i) tc::mbar_init(&f.bars[i], i == 4 || i == 5 ? kWorkers : 1);
+    tc::fence_mbar_init();
+    *f.abort_flag = 0;
+    for (int c = 0; c < kSegStages && c < nc; ++c) load(c);
+  }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -602,12 +619,7 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
   auto xw_col = [](int c, int hf) { return (uint32_t)((c & 1) ? (hf ? 416 : 192) : (hf ? 96 : 0)); };
 
   if (warp == kIssueWarp) {
-    auto load = [&](int c) {
-      load_stage<DK, PB, C>(f, c % kSegStages, &tm_b, &tm_x, hk, h0, a.dv, (int)(tok0 + (long long)c * kQ),
-                            &b_st[c % kSegStages]);
-    };
     if (lane == 0) {
-      for (int c = 0; c < kSegStages && c < nc; ++c) load(c);
       for (int c = 0; c < nc; ++c) {
         if (!wait1(&w_a[c & 1], (uint32_t)((c >> 1) & 1), 1)) break;  // w x of chunk c written, the sum of c - 1 read
         tc::fence_after();
@@ -703,12 +715,14 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
   __syncthreads();
   if (!*f.abort_flag && tid < HPC)
     seg_decay[(size_t)s.slot * a.Hv + h0 + tid] = f.tabs[2 * HPC * kQ + tid] + f.tabs[3 * HPC * kQ + tid];
-  if (*f.abort_flag && warp == kIssueWarp && lane == 0) {
-    for (int i = 0; i < 1 + kSegStages; ++i)
-      for (uint32_t par = 0; par < 2; ++par) (void)tc::mbar_wait(&f.bars[i], par, 1u << 14);
+  if (*f.abort_flag) {
+    if (tid == 0) {
+      for (int i = 0; i < 1 + kSegStages; ++i)
+        for (uint32_t par = 0; par < 2; ++par) (void)tc::mbar_wait(&f.bars[i], par, 1u << 14);
+    }
+    __syncthreads();
   }
-  __syncwarp();
-  if (warp == kIssueWarp) tc::tmem_dealloc(tmem, kTmemCols);
+  if (warp == kAllocWarp) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
 template <int DK, int PB, int HPC>

@@ -96,7 +96,7 @@ gdn_ssm_join_kernel(const ssm::Segs g, float* __restrict__ seg_state, const floa
   const bool teller = p == 0 && worker < 32 * 4 && e == worker;  // one thread a head
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   float total = 0.f;
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 16;
   float4 v[kAhead];
   float l[kAhead];
   auto at = [&](int k) { return reinterpret_cast<float4*>(seg_state) + ((size_t)(slot0 + k) * nhb + hb) * dk * 32 + e; };
