@@ -98,7 +98,7 @@ gdn_conv_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __nv_bf
     }
     return;
   }
-  const int t0 = blockIdx.x * run, t1 = min(t0 + run, Ttot);
+  const int t0 = blockIdx.x * run, t1 = t0 + min(run, Ttot - t0);
   Taps<K> taps;
   taps.load(weight, bias, c);
   int b, start, end;  // the sequence of token t and its bounds
@@ -125,22 +125,22 @@ gdn_conv_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __nv_bf
   __nv_bfloat16* op = out + (size_t)t0 * C + c;
   uint2 next[kConvBatch];
 #pragma unroll
-  for (int u = 0; u < kConvBatch; ++u) next[u] = t0 + u < t1 ? *reinterpret_cast<const uint2*>(xp + u * xs) : zero;
-  for (int t = t0; t < t1; t += kConvBatch) {
+  for (int u = 0; u < kConvBatch; ++u) next[u] = u < t1 - t0 ? *reinterpret_cast<const uint2*>(xp + u * xs) : zero;
+  for (int t = t0;; t += kConvBatch) {
     uint2 cur[kConvBatch];
     xp += kConvBatch * xs;
 #pragma unroll
     for (int u = 0; u < kConvBatch; ++u) {
       cur[u] = next[u];
-      if (t + kConvBatch + u < t1) next[u] = *reinterpret_cast<const uint2*>(xp + u * xs);
+      if (kConvBatch + u < t1 - t) next[u] = *reinterpret_cast<const uint2*>(xp + u * xs);
     }
 #pragma unroll
     for (int u = 0; u < kConvBatch; ++u) {
-      if (t + u >= t1) break;
+      if (u >= t1 - t) break;
       if (t + u >= end) {  // the next sequence that has tokens begins here
         if (cu == nullptr) {
           ++b;
-          end += T;
+          end = b + 1 < B ? end + T : Ttot;
         } else {
           b = find_seq(cu, B, t + u);
           end = b + 1 < B ? cu[b + 1] : Ttot;
@@ -161,6 +161,7 @@ gdn_conv_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __nv_bf
         past[K - 2][i] = f[i];
       }
     }
+    if (t1 - t <= kConvBatch) break;
   }
 }
 

@@ -140,7 +140,9 @@ size_t gdn_ssm_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv, int
 int gdn_ssm_scan(const gdn_ssm_scan_args* args) {
   gdn::clear_cuda_error();
   if (args == nullptr) return GDN_ERR_ARG;
-  const auto& [x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, D, z, z_stride, dt_bias, cu_seqlens, init_state, out, final_state, B, T, Hk, Hv, dk, dv, flags, workspace_given, workspace_bytes, stream] = *args;
+  const auto& [x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, D, z, z_stride, dt_bias, cu_seqlens,
+               init_state, out, final_state, B, T, Hk, Hv, dk, dv, flags, workspace_given, workspace_bytes, stream] =
+      *args;
   if (!ssm_sizes_ok(B, T, Hk, Hv, dk, dv) || (flags & ~(GDN_SSM_SOFTPLUS | GDN_SSM_DT_F32)) != 0) return GDN_ERR_ARG;
   if (B == 0) return GDN_OK;
   const long long ntok = cu_seqlens != nullptr ? (long long)T : (long long)B * T;
@@ -173,7 +175,8 @@ int gdn_ssm_scan(const gdn_ssm_scan_args* args) {
 int gdn_ssm_step(const gdn_ssm_step_args* args) {
   gdn::clear_cuda_error();
   if (args == nullptr) return GDN_ERR_ARG;
-  const auto& [x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, D, z, z_stride, dt_bias, state, out, B, Hk, Hv, dk, dv, flags, stream] = *args;
+  const auto& [x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, D, z, z_stride, dt_bias, state, out, B, Hk,
+               Hv, dk, dv, flags, stream] = *args;
   if (!ssm_sizes_ok(B, 1, Hk, Hv, dk, dv) || (flags & ~(GDN_SSM_SOFTPLUS | GDN_SSM_DT_F32)) != 0) return GDN_ERR_ARG;
   if (B == 0) return GDN_OK;
   if ((long long)B * Hv > 0x7fffffffLL || state == nullptr) return GDN_ERR_ARG;

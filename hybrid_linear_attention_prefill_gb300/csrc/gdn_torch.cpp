@@ -91,7 +91,8 @@ bool batch(Call& c, int64_t n, int cu_at, int b_at, const int32_t*& cu, int& B, 
   cu = nullptr;
   if (c.argv[cu_at] != Py_None) {
     const Tensor* t = c.tensor(cu_at);
-    if (t == nullptr || t->scalar_type() != at::ScalarType::Int || t->dim() != 1 || t->numel() < 1 || !t->is_contiguous())
+    if (t == nullptr || t->scalar_type() != at::ScalarType::Int || t->dim() != 1 || t->numel() < 1 ||
+        !t->is_contiguous())
       return false;
     cu = static_cast<const int32_t*>(t->data_ptr());
     B = (int)(t->numel() - 1);
@@ -244,7 +245,8 @@ PyObject* norm(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   });
 }
 
-#define GDN_METHOD(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
+#define GDN_METHOD(name, f) \
+  {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {GDN_METHOD("causal_conv", conv), GDN_METHOD("causal_conv_step", conv_step),
                          GDN_METHOD("ssm_scan", scan),    GDN_METHOD("ssm_step", step),
                          GDN_METHOD("add_norm", norm),    {nullptr, nullptr, 0, nullptr}};
