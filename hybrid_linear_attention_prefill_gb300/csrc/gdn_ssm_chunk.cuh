@@ -138,13 +138,15 @@ struct Cfg {
   static constexpr int kOffC = 2 * kStage;
   static constexpr int kOffS = kOffC + kNB * 16384;
   static constexpr int kSBytes = kNB * kRows * 128 > kXB * 16384 ? kNB * kRows * 128 : kXB * 16384;
-  static constexpr int kTabBytes = HPC * 4 * kQ * 4;  // L and K of a chunk; w of two
+  static constexpr int kTabBytes = HPC * 4 * kQ * 4;  // L, K and w of a chunk (the pass of the sums: w of two, decays)
   static constexpr int kBarBytes = 256;               // mbarriers, TMEM base, abort flag, decays
   static constexpr bool kOwnGate = kOffS + kSBytes + kXB * 16384 + kTabBytes + kBarBytes <= 227 * 1024;
   static constexpr int kOffZ = kOwnGate ? kOffS + kSBytes : kOffS;
   static constexpr int kOffTab = kOwnGate ? kOffZ + kXB * 16384 : kOffS + kSBytes;
   static constexpr int kOffBar = kOffTab + kTabBytes;
-  static constexpr int kSmemBytes = kOffBar + kBarBytes;
+  // More than half an SM's, so that two CTAs never share one: each takes all of its TMEM, and one of the output pass
+  // that had it would wait for the pass of the sums, which would wait for the TMEM.
+  static constexpr int kSmemBytes = kOffBar + kBarBytes > 116 * 1024 ? kOffBar + kBarBytes : 116 * 1024;
   static_assert(PB == 64 || (PB == 128 && HPC == 1), "128 rows at most");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 };
@@ -178,7 +180,8 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
 
 __device__ __forceinline__ void tma_prefetch_l2_2d(const void* map, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(map), "r"(x), "r"(y) : "memory");
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(map), "r"(x), "r"(y)
+               : "memory");
 }
 
 __device__ __forceinline__ void arrive(uint64_t* bar) {

@@ -3,7 +3,7 @@
 
 namespace gdn {
 namespace ssm {
-template cudaError_t launch_dk<64>(const Maps&, const SsmArgs&, const Segs&, float*, float*, const float*, float*, int*,
-                                    int, int, cudaStream_t);
+template cudaError_t launch_dk<64>(const Maps&, const SsmArgs&, const Segs&, float*, float*, const float*, float*,
+                                    float*, int*, int, int, cudaStream_t);
 }  // namespace ssm
 }  // namespace gdn

@@ -104,17 +104,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_z,
                      const __grid_constant__ CUtensorMap tm_o, const SsmArgs a, const Segs g,
-                     const float* seg_state, const float* seg_decay, const float* init, float* fin,
+                     const float* seg_state, const float* seg_decay, const float* init, const float* kept, float* fin,
                      int* __restrict__ err) {
   using C = Cfg<DK, PB, HPC>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const Frame f = make_frame<C>(smem_raw);
-  // Completed by the MMAs, once a chunk each: scores, (w x)^T B of half 0 and C S^T, (w x)^T B of half 1, y.  By
-  // copies: the two stages, C, the gate's tile.  By the worker warps: the first operands of a chunk (the state,
-  // w x), the second (M, y, w x), the gate read, y (and the gate) read, the outputs out of the x tile, and once their last chunk.  By the
-  // table warp: a chunk's tables, its stage loaded.  Every waiter waits for every phase in turn, and no phase after it can
-  // end before it has looked (a parity only names the last phase that ended): what leads to the next one waits for
-  // the waiter.
+  // Completed by the MMAs, once a chunk each: scores; (w x)^T B of half 0 and C S^T; (w x)^T B of half 1; y.  By
+  // copies: the two stages, C, the gate's tile.  By the worker warps: the first operands of a chunk (the state, w x),
+  // the second (M, y, w x), the gate read, y read, the outputs out of the x tile, and once, their last chunk.  By the
+  // table warp: a chunk's tables made and its stage loaded.  Every waiter waits for every phase in turn, and no phase
+  // after it can end before it has looked (a parity only names the last phase that ended): what leads to the next one
+  // waits for the waiter.
   uint64_t *b_sc = f.bars, *b_in = f.bars + 1, *b_d1 = f.bars + 2, *b_y = f.bars + 3, *b_st = f.bars + 4,
            *b_c = f.bars + 6, *b_z = f.bars + 7, *w_a = f.bars + 8, *w_b = f.bars + 9, *w_z = f.bars + 10,
            *w_y = f.bars + 11, *w_s = f.bars + 12, *b_tab = f.bars + 13, *w_e = f.bars + 14;
@@ -275,7 +275,8 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       }
       if (!wait(&b_st[c & 1], (uint32_t)((c >> 1) & 1), 2)) break;
       if (lane == 0) arrive(b_tab);
-      if (lane == 0) {  // into L2, where their places in shared memory are free only late: this chunk's gate, the next x and B
+      // into L2, since their places in shared memory are free only late: this chunk's gate, the next x and B
+      if (lane == 0) {
         const int t = (int)(tok0 + (long long)c * kQ);
 #pragma unroll
         for (int i = 0; i < C::kXB; ++i) {
@@ -301,9 +302,11 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
 #pragma unroll
     for (int i = 0; i < C::kSC; ++i) st[i] = 0.f;
     const size_t st_at = ((size_t)s.b * a.Hv + h0) * a.dv * DK;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the segments' sums; the final state may replace init
-    if (live && init != nullptr)
-      move_state<DK, PB, HPC, false>(f.sm + C::kOffS, const_cast<float*>(init) + st_at, a.dv, tid, st);
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the segments' sums
+    if (live && init != nullptr) {  // where the final state replaces it, the later segments' copy of it
+      const float* from = kept != nullptr && !(s.first && s.last) ? kept : init;
+      move_state<DK, PB, HPC, false>(f.sm + C::kOffS, const_cast<float*>(from) + st_at, a.dv, tid, st);
+    }
     // the sums of the segments before: one by one where they are few, or joined into one
     const int i0 = g.joined ? s.slot : s.slot - s.p, i1 = s.slot + (g.joined && s.p > 0 ? 1 : 0);
     if (my_row && i0 < i1) {  // half of a sum's values are on their way while the other half is added
@@ -359,7 +362,9 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
               make_uint4(0, 0, 0, 0);
         asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kWorkers) : "memory");
       }
-      if (!C::kOwnGate && gate && c > 0 && !wait(w_z, (uint32_t)((c - 1) & 1), 1)) return false;  // the gate there is read
+      if (!C::kOwnGate && gate && c > 0) {  // the gate there is read
+        if (!wait(w_z, (uint32_t)((c - 1) & 1), 1)) return false;
+      }
       if (row < C::kRows) {
 #pragma unroll
         for (int i = 0; i < C::kSC; i += 8) {
@@ -522,7 +527,8 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
           tc::fence_proxy_async();
           asm volatile("bar.sync %0, %1;\n" ::"r"(quad), "n"(32 * (64 / C::kYC)) : "memory");
           if ((yc & 63) == 0 && lane == 0) {
-            tma_store_2d(&tm_o, smem_u32(yt) + 32 * q4 * 128, (h0 + yh) * a.dv + yp, (int)(tok0 + (long long)c * kQ) + 32 * q4);
+            tma_store_2d(&tm_o, smem_u32(yt) + 32 * q4 * 128, (h0 + yh) * a.dv + yp,
+                         (int)(tok0 + (long long)c * kQ) + 32 * q4);
             bulk_commit();
           }
           __syncwarp();
@@ -566,14 +572,14 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
   if (warp == kAllocWarp) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-// The sums of the segments before a sequence's last (from a zero state) and their decays in log2.  Three stages of B
-// and x: with two, a chunk's load (about 2,000 cycles) stood in the way of every chunk.
-// grid: segments x head blocks.
+// The sums of the segments before a sequence's last (from a zero state) and their decays in log2, and, where the final
+// states will replace the initial ones, a copy of these.  Three stages of B and x: with two, a chunk's load (about
+// 2,000 cycles) stood in the way of every chunk.  grid: segments x head blocks.
 template <int DK, int PB, int HPC>
 __global__ void __launch_bounds__(kThreads, 1)
 gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
                        const SsmArgs a, const Segs g, float* __restrict__ seg_state, float* __restrict__ seg_decay,
-                       int* __restrict__ err) {
+                       const float* __restrict__ init, float* __restrict__ kept, int* __restrict__ err) {
   using C = Cfg<DK, PB, HPC>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const Frame f = make_frame<C>(smem_raw);
@@ -626,7 +632,8 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
         if (c > 0 && c + kSegStages - 1 < nc) load(c + kSegStages - 1);  // the stage of chunk c - 1
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
-          issue_state<DK>(tmem + kSum, tmem + xw_col(c, hf), f.sb + (c % kSegStages) * C::kStage + C::kOffB, hf, hf == 0);
+          issue_state<DK>(tmem + kSum, tmem + xw_col(c, hf), f.sb + (c % kSegStages) * C::kStage + C::kOffB, hf,
+                          hf == 0);
         tc::commit(b_d);
       }
     }
@@ -672,6 +679,11 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
 #pragma unroll
     for (int i = 0; i < kSC; ++i) st[i] = 0.f;
     bool ok = true;
+    if (kept != nullptr && s.first) {
+      const size_t at = ((size_t)s.b * a.Hv + h0) * a.dv * DK;
+      for (int e = 4 * tid; e < HPC * a.dv * DK; e += 4 * 32 * kWorkers)
+        *reinterpret_cast<float4*>(kept + at + e) = *reinterpret_cast<const float4*>(init + at + e);
+    }
     SsmDecay decay = {1.f, 0.f};  // of the chunk whose sum comes next
     auto update = [&](int c) {    // S after chunk c
       if (!(ok = wait(b_d, (uint32_t)(c & 1), 1))) return;
@@ -690,7 +702,9 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
     for (int c = 0; c < nc; ++c) {
       const float* w = f.tabs + ((c & 1) * HPC + hr) * kQ;
       const unsigned char* xt = f.sm + (c % kSegStages) * C::kStage + C::kOffX;
-      if (!(ok = wait(&b_st[c % kSegStages], (uint32_t)((c / kSegStages) & 1), 2) && wait(&b_tab[c & 1], (uint32_t)((c >> 1) & 1), 1))) break;
+      ok = wait(&b_st[c % kSegStages], (uint32_t)((c / kSegStages) & 1), 2) &&
+           wait(&b_tab[c & 1], (uint32_t)((c >> 1) & 1), 1);
+      if (!ok) break;
       if (32 * q4 < C::kRows) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) split_xw(xt, w, 32 * q4, 64 * hf + 16 * cg, tq + xw_col(c, hf) + 8 * cg);
@@ -726,15 +740,15 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
 }
 
 template <int DK, int PB, int HPC>
-cudaError_t launch(const Maps& m, const SsmArgs& a,
-                   const Segs& g, float* seg_state, float* seg_decay, const float* init, float* fin, int* err,
-                   int phase, cudaStream_t st) {
+cudaError_t launch(const Maps& m, const SsmArgs& a, const Segs& g, float* seg_state, float* seg_decay,
+                   const float* init, float* kept, float* fin, int* err, int phase, cudaStream_t st) {
   using C = Cfg<DK, PB, HPC>;
   const unsigned grid = (unsigned)(a.Hv / HPC) * (unsigned)g.slots;
   if (phase == 0) {
     const cudaError_t e = set_smem_limit_once<gdn_ssm_segment_kernel<DK, PB, HPC>>(C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    gdn_ssm_segment_kernel<DK, PB, HPC><<<grid, kThreads, C::kSmemBytes, st>>>(m.x, m.b, a, g, seg_state, seg_decay, err);
+    gdn_ssm_segment_kernel<DK, PB, HPC>
+        <<<grid, kThreads, C::kSmemBytes, st>>>(m.x, m.b, a, g, seg_state, seg_decay, init, kept, err);
     return cudaGetLastError();
   }
   cudaError_t e = set_smem_limit_once<gdn_ssm_chunk_kernel<DK, PB, HPC>>(C::kSmemBytes);
@@ -748,21 +762,19 @@ cudaError_t launch(const Maps& m, const SsmArgs& a,
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = g.len != 0 ? 1 : 0;  // behind the combine kernel of the same call
-  e = cudaLaunchKernelEx(&cfg, gdn_ssm_chunk_kernel<DK, PB, HPC>, m.x, m.b, m.c, m.z, m.out, a, g, (const float*)seg_state,
-                         (const float*)seg_decay, init, fin,
-                         err);
+  cfg.numAttrs = g.len != 0 ? 1 : 0;  // behind the passes before it in the same call
+  e = cudaLaunchKernelEx(&cfg, gdn_ssm_chunk_kernel<DK, PB, HPC>, m.x, m.b, m.c, m.z, m.out, a, g,
+                         (const float*)seg_state, (const float*)seg_decay, init, (const float*)kept, fin, err);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
 template <int DK>
-cudaError_t launch_dk(const Maps& m, const SsmArgs& a,
-                      const Segs& g, float* seg_state, float* seg_decay, const float* init, float* fin, int* err,
-                      int hpc, int phase, cudaStream_t st) {
-  if (a.dv == 128) return launch<DK, 128, 1>(m, a, g, seg_state, seg_decay, init, fin, err, phase, st);
-  if (hpc == 2) return launch<DK, 64, 2>(m, a, g, seg_state, seg_decay, init, fin, err, phase, st);
-  return launch<DK, 64, 1>(m, a, g, seg_state, seg_decay, init, fin, err, phase, st);
+cudaError_t launch_dk(const Maps& m, const SsmArgs& a, const Segs& g, float* seg_state, float* seg_decay,
+                      const float* init, float* kept, float* fin, int* err, int hpc, int phase, cudaStream_t st) {
+  if (a.dv == 128) return launch<DK, 128, 1>(m, a, g, seg_state, seg_decay, init, kept, fin, err, phase, st);
+  if (hpc == 2) return launch<DK, 64, 2>(m, a, g, seg_state, seg_decay, init, kept, fin, err, phase, st);
+  return launch<DK, 64, 1>(m, a, g, seg_state, seg_decay, init, kept, fin, err, phase, st);
 }
 
 }  // namespace ssm

@@ -18,8 +18,8 @@ cudaError_t launch_chunk_table(const int32_t*, int, int, int32_t*, int32_t*, int
 
 namespace ssm {
 template <int DK>
-cudaError_t launch_dk(const Maps&, const SsmArgs&, const Segs&, float*, float*, const float*, float*, int*, int, int,
-                      cudaStream_t);
+cudaError_t launch_dk(const Maps&, const SsmArgs&, const Segs&, float*, float*, const float*, float*, float*, int*, int,
+                      int, cudaStream_t);
 }
 
 namespace {
@@ -42,8 +42,7 @@ Plan make_plan(int B, int T, int Hk, int Hv, int dv, bool packed, int sms) {
   const long long hb = Hv / p.hpc;
   p.slots = B;
   if (B == 0 || T == 0) return p;
-  const int nc = packed ? std::max(1, (int)(((long long)T + B - 1) / B + ssm::kQ - 1) / ssm::kQ)
-                        : (T + ssm::kQ - 1) / ssm::kQ;
+  const int nc = (int)(((packed ? ((long long)T + B - 1) / B : (long long)T) + ssm::kQ - 1) / ssm::kQ);
   auto waves = [&](long long ctas) { return (ctas + sms - 1) / sms; };
   double best = (double)waves(hb * B) * (nc + 1);
   for (int n = 2; n <= nc; ++n) {  // segments a sequence
@@ -60,7 +59,7 @@ Plan make_plan(int B, int T, int Hk, int Hv, int dv, bool packed, int sms) {
   }
   if (p.len != 0) {
     const int per = p.len * ssm::kQ;
-    p.slots = packed ? T / per + B : B * ((T + per - 1) / per);
+    p.slots = packed ? T / per + B : B * ((T - 1) / per + 1);
   }
   return p;
 }
@@ -99,7 +98,9 @@ gdn_ssm_join_kernel(const ssm::Segs g, float* __restrict__ seg_state, const floa
   constexpr int kAhead = 16;
   float4 v[kAhead];
   float l[kAhead];
-  auto at = [&](int k) { return reinterpret_cast<float4*>(seg_state) + ((size_t)(slot0 + k) * nhb + hb) * dk * 32 + e; };
+  auto at = [&](int k) {
+    return reinterpret_cast<float4*>(seg_state) + ((size_t)(slot0 + k) * nhb + hb) * dk * 32 + e;
+  };
   for (int k0 = 0; k0 < n; k0 += kAhead) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
@@ -127,17 +128,18 @@ gdn_ssm_join_kernel(const ssm::Segs g, float* __restrict__ seg_state, const floa
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Workspace: [256 B status words][packed: chunk table and dispatch order][segment states, 128 rows a head block]
-//            [segment decays][joined decays]
+//            [segment decays][joined decays][copy of the initial states]
 struct Layout {
-  size_t states, decays, totals, total;
+  size_t states, decays, totals, kept, total;
 };
-Layout layout(const Plan& p, int B, int Hv, int dk, bool packed) {
+Layout layout(const Plan& p, int B, int Hv, int dk, int dv, bool packed) {
   Layout l;
   l.states = 256 + (packed ? chunk_table_bytes(B) : 0);
   const size_t n = p.len != 0 ? (size_t)p.slots : 0;
   l.decays = l.states + align256(n * (Hv / p.hpc) * dk * 128 * 4);
   l.totals = l.decays + align256(n * Hv * 4);
-  l.total = l.totals + align256(n * Hv * 4);
+  l.kept = l.totals + align256(n * Hv * 4);
+  l.total = l.kept + (p.len != 0 ? align256((size_t)B * Hv * dv * dk * 4) : 0);
   return l;
 }
 
@@ -155,7 +157,7 @@ size_t ssm_scan_workspace(int B, int T, int Hk, int Hv, int dk, int dv, int pack
   const int sms = device_sms();
   // without a device: enough for any (a segment of one chunk for every chunk)
   Plan p = make_plan(B, T, Hk, Hv, dv, packed != 0, sms > 0 ? sms : 1 << 20);
-  return layout(p, B, Hv, dk, packed != 0).total;
+  return layout(p, B, Hv, dk, dv, packed != 0).total;
 }
 
 cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* init, float* fin, void* ws, int B, int T,
@@ -164,12 +166,14 @@ cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* in
   if (sms == 0) return cudaErrorNoDevice;
   const bool packed = cu != nullptr;
   const Plan p = make_plan(B, T, a.Hk, a.Hv, a.dv, packed, sms);
-  const Layout l = layout(p, B, a.Hv, dk, packed);
+  const Layout l = layout(p, B, a.Hv, dk, a.dv, packed);
   unsigned char* w = static_cast<unsigned char*>(ws);
   int* err = static_cast<int*>(ws);
   float* states = reinterpret_cast<float*>(w + l.states);
   float* decays = reinterpret_cast<float*>(w + l.decays);
   float* totals = reinterpret_cast<float*>(w + l.totals);
+  // In place, a sequence's last segment may end before an earlier one has read the initial state.
+  float* kept = p.len != 0 && init != nullptr && init == fin ? reinterpret_cast<float*>(w + l.kept) : nullptr;
   const long long ntok = packed ? (long long)T : (long long)B * T;
   if ((long long)p.slots * (a.Hv / p.hpc) > 0x7fffffffLL) return cudaErrorInvalidValue;
   ssm::Maps m = {};
@@ -189,13 +193,13 @@ cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* in
   // With few segments a sequence the output pass goes through the sums before its own by itself (about 0.8 us each,
   // beside its first tiles' load); more are joined by a kernel (about 5 us).
   const int per = p.len * ssm::kQ;
-  g.joined = p.len != 0 && (T + per - 1) / per > kAloneSegs;
+  g.joined = p.len != 0 && (T - 1) / per + 1 > kAloneSegs;
   auto run = [&](int phase) {
     float* dec = phase == 1 && g.joined ? totals : decays;
     switch (dk) {
-      case 32: return ssm::launch_dk<32>(m, a, g, states, dec, init, fin, err, p.hpc, phase, st);
-      case 64: return ssm::launch_dk<64>(m, a, g, states, dec, init, fin, err, p.hpc, phase, st);
-      default: return ssm::launch_dk<128>(m, a, g, states, dec, init, fin, err, p.hpc, phase, st);
+      case 32: return ssm::launch_dk<32>(m, a, g, states, dec, init, kept, fin, err, p.hpc, phase, st);
+      case 64: return ssm::launch_dk<64>(m, a, g, states, dec, init, kept, fin, err, p.hpc, phase, st);
+      default: return ssm::launch_dk<128>(m, a, g, states, dec, init, kept, fin, err, p.hpc, phase, st);
     }
   };
   cudaError_t e;
@@ -212,8 +216,8 @@ cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* in
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, gdn_ssm_join_kernel, (const ssm::Segs)g, states, (const float*)decays, totals, a.Hv, dk,
-                           a.dv, a.dv == 128 ? 128 : 64, p.hpc);
+    e = cudaLaunchKernelEx(&cfg, gdn_ssm_join_kernel, (const ssm::Segs)g, states, (const float*)decays, totals, a.Hv,
+                           dk, a.dv, a.dv == 128 ? 128 : 64, p.hpc);
     if (e != cudaSuccess) return e;
   } else if (p.len == 0 && packed && B > 1) {  // whole sequences of different lengths: the longest start first
     int32_t* off = reinterpret_cast<int32_t*>(w + 256);

@@ -289,9 +289,9 @@ int gdn_prefill_static(const void *q, const void *k, const void *v,
 
 /*
  * gdn_device_status -- synchronise the current device, return the status bits
- * accumulated since the last call (in *status: the OR of the library workspace's
- * word and, once gdn_prefill_static has run on the device, the fixed array's) and
- * clear them.  Returns GDN_OK or GDN_ERR_LAUNCH.
+ * accumulated since the last call (in *status: the OR of the words of the library's
+ * workspaces, gdn_prefill's and gdn_ssm_scan's, and, once gdn_prefill_static has run
+ * on the device, the fixed array's) and clear them.  Returns GDN_OK or GDN_ERR_LAUNCH.
  */
 int gdn_device_status(int *status);
 

@@ -356,6 +356,36 @@ def test_scan_offsets_past_32_bits(gdn):
         assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
 
 
+def test_scan_in_place_over_many_segments(gdn):
+    # enough segments for several waves: the first ones' start must not be the final state of the last
+    s = scan_inputs(gen(36), 40000, 1, 1, 4, 64, 128, init=True)
+    out, fin = gdn.ssm_scan(**s)
+    packed = cu_of([30000, 0, 100, 9900])
+    s4 = {**s, "init_state": s["init_state"].repeat(4, 1, 1, 1)}
+    out4, fin4 = gdn.ssm_scan(**s4, cu_seqlens=packed)
+    for _ in range(5):
+        st, st4 = s["init_state"].clone(), s4["init_state"].clone()
+        o, _ = gdn.ssm_scan(**{**s, "init_state": st}, final_state=st)
+        assert torch.equal(o, out) and torch.equal(st, fin)
+        o, _ = gdn.ssm_scan(**{**s4, "init_state": st4}, cu_seqlens=packed, final_state=st4)
+        assert torch.equal(o, out4) and torch.equal(st4, fin4)
+
+
+def test_scan_without_memory_for_its_workspace(gdn):
+    s = scan_inputs(gen(37), 2000, 1, 1, 2, 32, 64)
+    ref = gdn.ssm_scan(**s)
+    gdn.gdn_release_workspace()
+    assert gdn.gdn_debug_fail_allocations(1) == 0
+    try:
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.ssm_scan(**s)
+        assert e.value.status == gdn.GDN_ERR_ALLOC
+    finally:
+        gdn.gdn_debug_fail_allocations(0)
+    again = gdn.ssm_scan(**s)
+    assert torch.equal(again[0], ref[0]) and torch.equal(again[1], ref[1])
+
+
 # ---- norm -----------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("rows,D", [(1, 8), (1, 4096), (3, 64), (5, 264), (33, 520), (2, 1000), (7, 2056), (3, 8192),
@@ -423,3 +453,49 @@ def test_norm_offsets_past_32_bits(gdn):
     v = big.as_strided((3, 512), (2 ** 30 + 8, 1))
     v.copy_(x)
     assert torch.equal(gdn.add_norm(v, w)[0], gdn.add_norm(x, w)[0])
+
+
+# ---- both ways to a call --------------------------------------------------------------------------
+
+def test_calls_with_outputs_given_are_the_same_calls(gdn, monkeypatch):
+    """With every output given a call may take a shorter way through the binding: the same results and refusals."""
+    g = gen(50)
+    x, w, b, st = rnd(g, 40, 72), rnd(g, 72, 4), rnd(g, 72), rnd(g, 2, 3, 72)
+    s = scan_inputs(gen(51), 40, 2, 1, 2, 32, 64, init=True)
+    one = {k: (v[:2] if k in ("x", "dt", "Bm", "Cm", "z") else v) for k, v in s.items() if k != "init_state"}
+    r, nw = rnd(g, 40, 72), rnd(g, 72)
+
+    def calls():
+        o, f = torch.empty_like(x), torch.empty_like(st)
+        yield gdn.causal_conv(x, w, b, cu_of([15, 25]), st, out=o, final_state=f)
+        o, st1 = torch.empty_like(x[:2]), st.clone()
+        yield gdn.causal_conv_step(x[:2], w, st1, b, out=o), st1
+        o, f = torch.empty_like(s["x"]), torch.empty_like(s["init_state"])
+        yield gdn.ssm_scan(**s, B=2, out=o, final_state=f)
+        o, f = torch.empty_like(one["x"]), s["init_state"].clone()
+        yield gdn.ssm_step(**one, state=f, out=o), f
+        o, rr = torch.empty_like(x), r.clone()
+        yield gdn.add_norm(x, nw, rr, out=o, residual_out=rr)[0], rr
+        q, sc = torch.empty(40, 72, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(40, 3, device="cuda")
+        q, sc, _ = gdn.add_norm(x, nw, group=32, e4m3=True, out=q, scales=sc)
+        yield q.view(torch.uint8), sc
+
+    def refusals():
+        o = torch.empty_like(x)
+        yield lambda: gdn.causal_conv(x, w.float(), b, want_final=False, out=o)
+        yield lambda: gdn.causal_conv(x, w[:, :1], b, want_final=False, out=o)
+        yield lambda: gdn.causal_conv_step(x[:2], w, st, b, out=o)
+        yield lambda: gdn.ssm_scan(**s, B=2, want_final=False, out=torch.empty_like(s["x"])[:39])
+        yield lambda: gdn.ssm_step(**one, state=s["init_state"].double(), out=torch.empty_like(one["x"]))
+        yield lambda: gdn.add_norm(x, nw[:64], out=o)
+
+    short = [(a.clone(), c.clone()) for a, c in calls()]
+    for f in refusals():
+        with pytest.raises((ValueError, gdn.GdnError)):
+            f()
+    monkeypatch.setattr(gdn, "_fast", None)
+    for (a, c), (a2, c2) in zip(short, calls()):
+        assert torch.equal(a, a2) and torch.equal(c, c2)
+    for f in refusals():
+        with pytest.raises((ValueError, gdn.GdnError)):
+            f()
