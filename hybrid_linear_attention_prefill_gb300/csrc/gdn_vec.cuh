@@ -35,14 +35,22 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
-// silu of two values, v / (1 + e^-v), with one reciprocal: 1 / a = b / (a b).  The exponents stop at 2^62, so
-// that the product stays finite: below -43 a value v gives v 2^-62 where less would be exact.
+// The larger of x and lo, or NaN for a NaN.
+__device__ __forceinline__ float max_nan(float x, float lo) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(lo));
+  return y;
+}
+
+// silu of two values, v / (1 + e^-v), with one reciprocal: 1 / a = b / (a b).  Values stop at -43.5, so that the
+// product stays finite: any below gives that one's silu, -6e-18, for its own between that and 0.  A NaN stays out of
+// the product (fminf drops it), and so out of the other value's result.
 __device__ __forceinline__ float2 silu2(float2 v) {
   const float2 t = mul2(v, make_float2(-1.4426950408889634f, -1.4426950408889634f));
-  const float2 d = fma2(make_float2(ex2_approx(fminf(t.x, 62.f)), ex2_approx(fminf(t.y, 62.f))), make_float2(1.f, 1.f),
-                        make_float2(1.f, 1.f));
+  const float2 d = fma2(make_float2(ex2_approx(fminf(t.x, 62.757f)), ex2_approx(fminf(t.y, 62.757f))),
+                        make_float2(1.f, 1.f), make_float2(1.f, 1.f));
   const float r = rcp_approx(d.x * d.y);
-  return mul2(v, mul2(make_float2(r, r), make_float2(d.y, d.x)));
+  return mul2(make_float2(max_nan(v.x, -43.5f), max_nan(v.y, -43.5f)), mul2(make_float2(r, r), make_float2(d.y, d.x)));
 }
 
 // Four or eight bf16 as pairs of fp32, and back.

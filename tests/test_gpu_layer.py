@@ -293,6 +293,32 @@ def test_scan_reads_nothing_beside_its_slices(gdn):
     assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
 
 
+def test_silu_far_below_zero(gdn):
+    # silu goes to zero there; a neighbour's value and a NaN keep their own results
+    far = torch.tensor([-50.0, -100.0, -1e10, -3e38, float("-inf")], device="cuda").bfloat16()
+    s = scan_inputs(gen(38), 10, 1, 1, 1, 32, 32)
+    ref = gdn.ssm_scan(**s)[0]
+    row = {k: (v[:2] if k in ("x", "dt", "Bm", "Cm", "z") else v) for k, v in s.items() if k != "init_state"}
+    st = torch.zeros(2, 1, 32, 32, device="cuda")
+    ref1 = gdn.ssm_step(**row, state=st.clone())
+    for i, v in enumerate(far):
+        z = s["z"].clone()
+        z[0::2, 0, 2 * i + 1] = v
+        z[0, 0, 20] = float("nan")
+        for out, want in ((gdn.ssm_scan(**{**s, "z": z})[0], ref), (gdn.ssm_step(**{**row, "z": z[:2]},
+                                                                                 state=st.clone()), ref1)):
+            assert bool((out[0::2, 0, 2 * i + 1].abs() < 1e-15).all()) and bool(out[0, 0, 20].isnan())
+            same = torch.ones_like(out, dtype=torch.bool)
+            same[0::2, 0, 2 * i + 1] = False
+            same[0, 0, 20] = False
+            assert torch.equal(out[same], want[same])
+    x, w = torch.zeros(4, 16, dtype=torch.bfloat16, device="cuda"), torch.zeros(16, 2, device="cuda").bfloat16()
+    x[1, :4], w[:, 1] = far[:4], 1.0
+    x[2, 5] = float("nan")
+    out, _ = gdn.causal_conv(x, w)
+    assert bool((out[1].abs() < 1e-15).all()) and bool(out[2, 5].isnan())
+
+
 def test_scan_infinite_step_and_zero_rows(gdn):
     # a head whose inputs are all zero returns zeros whatever its decay
     s = scan_inputs(gen(31), 100, 1, 1, 2, 64, 64, gate=False)
