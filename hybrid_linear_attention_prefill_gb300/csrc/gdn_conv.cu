@@ -17,7 +17,7 @@ namespace {
 
 constexpr int kConvThreads = 128;
 // Blocks an SM: 72 registers a thread.  More blocks spill, fewer have too few loads in flight (72,102 tokens of
-// 8,192 channels: 386 us with 7, 450 with 6, 478 with 8).
+// 8,192 channels: 372 us with 7, 385 with 6, 448 with 8).
 constexpr int kConvBlocks = 7;
 constexpr int kConvBatch = 8;  // tokens whose loads a thread has in flight
 
@@ -126,39 +126,45 @@ gdn_conv_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __nv_bf
   uint2 next[kConvBatch];
 #pragma unroll
   for (int u = 0; u < kConvBatch; ++u) next[u] = u < t1 - t0 ? *reinterpret_cast<const uint2*>(xp + u * xs) : zero;
-  for (int t = t0;; t += kConvBatch) {
-    uint2 cur[kConvBatch];
-    xp += kConvBatch * xs;
+  auto token = [&](const uint2& in) {
+    float2 f[2];
+    widen4(in, f);
+    *reinterpret_cast<uint2*>(op) = taps.template apply<SILU>(past, f);
+    op += C;
 #pragma unroll
-    for (int u = 0; u < kConvBatch; ++u) {
-      cur[u] = next[u];
-      if (kConvBatch + u < t1 - t) next[u] = *reinterpret_cast<const uint2*>(xp + u * xs);
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int j = 0; j + 1 < K - 1; ++j) past[j][i] = past[j + 1][i];
+      past[K - 2][i] = f[i];
     }
+  };
+  for (int t = t0;; t += kConvBatch) {
+    xp += kConvBatch * xs;
+    if (min(end, t1) - t >= kConvBatch) {  // all of the batch in the run and in the sequence
 #pragma unroll
-    for (int u = 0; u < kConvBatch; ++u) {
-      if (u >= t1 - t) break;
-      if (t + u >= end) {  // the next sequence that has tokens begins here
-        if (cu == nullptr) {
-          ++b;
-          end = b + 1 < B ? end + T : Ttot;
-        } else {
-          b = find_seq(cu, B, t + u);
-          end = b + 1 < B ? cu[b + 1] : Ttot;
-        }
-#pragma unroll
-        for (int j = 0; j < K - 1; ++j)
-          widen4(init != nullptr ? *reinterpret_cast<const uint2*>(init + ((size_t)b * (K - 1) + j) * C + c) : zero,
-                 past[j]);
+      for (int u = 0; u < kConvBatch; ++u) {
+        token(next[u]);
+        if (kConvBatch + u < t1 - t) next[u] = *reinterpret_cast<const uint2*>(xp + u * xs);
       }
-      float2 f[2];
-      widen4(cur[u], f);
-      *reinterpret_cast<uint2*>(op) = taps.template apply<SILU>(past, f);
-      op += C;
+    } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int u = 0; u < kConvBatch; ++u) {
+        if (u >= t1 - t) break;
+        if (t + u >= end) {  // the next sequence that has tokens begins here
+          if (cu == nullptr) {
+            ++b;
+            end = b + 1 < B ? end + T : Ttot;
+          } else {
+            b = find_seq(cu, B, t + u);
+            end = b + 1 < B ? cu[b + 1] : Ttot;
+          }
 #pragma unroll
-        for (int j = 0; j + 1 < K - 1; ++j) past[j][i] = past[j + 1][i];
-        past[K - 2][i] = f[i];
+          for (int j = 0; j < K - 1; ++j)
+            widen4(init != nullptr ? *reinterpret_cast<const uint2*>(init + ((size_t)b * (K - 1) + j) * C + c) : zero,
+                   past[j]);
+        }
+        token(next[u]);
+        if (kConvBatch + u < t1 - t) next[u] = *reinterpret_cast<const uint2*>(xp + u * xs);
       }
     }
     if (t1 - t <= kConvBatch) break;
@@ -195,8 +201,8 @@ cudaError_t conv_k(const void* x, long long xs, const void* weight, const void* 
                    const void* init, void* out, void* fin, int B, int T, int Ttot, int C, cudaStream_t st) {
   using bf = __nv_bfloat16;
   // Runs of 64 tokens read a twentieth of the inputs twice; shorter ones where they would not give every SM its
-  // blocks half over again (T = 4,096, C = 8,192: 29.7 us with 32, 29.9 with 64, 31.3 with 16; 72,102 tokens: 375 us
-  // with 64, 386 with 32).
+  // blocks half over again (T = 4,096, C = 8,192: 27.2 us with 32, a few tenths more with 64, 1.6 with 16; 72,102
+  // tokens: 369 us with 64, 380 with 32).
   const int cb = (C / 4 + kConvThreads - 1) / kConvThreads;
   int run = 64;
   while (run > kConvBatch && 2LL * (Ttot / run) * cb < 3LL * kConvBlocks * device_sms()) run >>= 1;

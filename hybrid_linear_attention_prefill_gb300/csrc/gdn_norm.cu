@@ -18,6 +18,14 @@ namespace gdn {
 namespace {
 
 constexpr int kNormMinThreads = 128;
+constexpr int kRowShift = 12;  // groups are 2^gshift vectors of eight columns; this one holds the longest row
+
+// The largest magnitude of three, or NaN.
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 
 }  // namespace
 
@@ -28,7 +36,8 @@ template <int VPT, bool E4M3>
 __global__ void __launch_bounds__(1024)
 gdn_add_norm_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __nv_bfloat16* residual,
                     const __nv_bfloat16* __restrict__ weight, __nv_bfloat16* residual_out, void* __restrict__ out,
-                    float* __restrict__ scales, int rows, int D, int tpr, int group, int ngroups, float eps) {
+                    float* __restrict__ scales, int rows, int D, int tpr, int gshift, int ngroups, float inv_d,
+                    float eps) {
   __shared__ float part[32];
   __shared__ uint32_t part_max[32];
   const int nv = D / 8;
@@ -59,7 +68,7 @@ gdn_add_norm_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __n
       float2 f[4];
       widen8(rr[j], f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[j][i] = make_float2(r[j][i].x + f[i].x, r[j][i].y + f[i].y);
+      for (int i = 0; i < 4; ++i) r[j][i] = fma2(r[j][i], make_float2(1.f, 1.f), f[i]);
     }
     if (residual_out != nullptr && live && v < nv)
       *reinterpret_cast<uint4*>(residual_out + row * D + 8 * v) = narrow8(r[j]);
@@ -76,24 +85,24 @@ gdn_add_norm_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __n
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   }
-  const float rstd = 1.f / sqrtf(ss / (float)D + eps);
+  const float rstd = rsqrtf(fmaf(ss, inv_d, eps));
 
   // y in place; its largest magnitude as bits (a NaN's are above every number's, so it stays)
   uint32_t mx[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = tid + j * tpr;
-    mx[j] = 0;
+    float big = 0.f;
     if (live && v < nv) {
       float2 w[4];
       widen8(wr[j], w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         r[j][i] = mul2(mul2(r[j][i], make_float2(rstd, rstd)), w[i]);
-        if (E4M3)
-          mx[j] = max(mx[j], max(__float_as_uint(r[j][i].x) & 0x7fffffffu, __float_as_uint(r[j][i].y) & 0x7fffffffu));
+        if (E4M3) big = max3_abs_nan(big, r[j][i].x, r[j][i].y);
       }
     }
+    mx[j] = __float_as_uint(big);
   }
   if constexpr (!E4M3) {
 #pragma unroll
@@ -103,7 +112,7 @@ gdn_add_norm_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __n
         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + row * D + 8 * v) = narrow8(r[j]);
     }
   } else {
-    if (group == 0) {  // one scale a row
+    if (gshift == kRowShift) {  // one scale a row
 #pragma unroll
       for (int j = 1; j < VPT; ++j) mx[0] = max(mx[0], mx[j]);
       mx[0] = __reduce_max_sync(0xffffffffu, mx[0]);
@@ -115,7 +124,7 @@ gdn_add_norm_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __n
 #pragma unroll
       for (int j = 1; j < VPT; ++j) mx[j] = mx[0];
     } else {
-      for (int o = 1; o < group / 8; o <<= 1)
+      for (int o = 1; o < 1 << gshift; o <<= 1)
 #pragma unroll
         for (int j = 0; j < VPT; ++j) mx[j] = max(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], o));
     }
@@ -124,8 +133,8 @@ gdn_add_norm_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __n
       const int v = tid + j * tpr;
       if (!live || v >= nv) continue;
       // 2^-96 keeps scale and 1 / scale normal numbers; NaN bits compare above it
-      const float scale = __uint_as_float(max(mx[j], __float_as_uint(0x1p-96f))) / 448.f;
-      const float inv = 1.f / scale;
+      const float scale = __uint_as_float(max(mx[j], __float_as_uint(0x1p-96f))) * (1.f / 448.f);
+      const float inv = rcp_approx(scale);
       uint32_t q[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -136,11 +145,7 @@ gdn_add_norm_kernel(const __nv_bfloat16* __restrict__ x, long long xs, const __n
         q[i] = (uint32_t)a | ((uint32_t)b << 16);
       }
       *reinterpret_cast<uint2*>(static_cast<unsigned char*>(out) + row * D + 8 * v) = make_uint2(q[0], q[1]);
-      if (group == 0) {
-        if (v == 0) scales[row] = scale;
-      } else if (v % (group / 8) == 0) {
-        scales[row * ngroups + v / (group / 8)] = scale;
-      }
+      if ((v & ((1 << gshift) - 1)) == 0) scales[row * ngroups + (v >> gshift)] = scale;
     }
   }
 }
@@ -153,14 +158,16 @@ static cudaError_t add_norm_v(const void* x, long long xs, const void* residual,
   const int threads = tpr < kNormMinThreads ? kNormMinThreads : tpr;
   const unsigned grid = (unsigned)((rows + threads / tpr - 1) / (threads / tpr));
   const int ngroups = group ? (D + group - 1) / group : 1;
+  const int gshift = group == 32 ? 2 : group == 64 ? 3 : group == 128 ? 4 : kRowShift;
+  const float inv_d = 1.f / (float)D;
   if (e4m3)
     gdn_add_norm_kernel<VPT, true><<<grid, threads, 0, st>>>(
         static_cast<const bf*>(x), xs, static_cast<const bf*>(residual), static_cast<const bf*>(weight),
-        static_cast<bf*>(residual_out), out, scales, rows, D, tpr, group, ngroups, eps);
+        static_cast<bf*>(residual_out), out, scales, rows, D, tpr, gshift, ngroups, inv_d, eps);
   else
     gdn_add_norm_kernel<VPT, false><<<grid, threads, 0, st>>>(
         static_cast<const bf*>(x), xs, static_cast<const bf*>(residual), static_cast<const bf*>(weight),
-        static_cast<bf*>(residual_out), out, scales, rows, D, tpr, group, ngroups, eps);
+        static_cast<bf*>(residual_out), out, scales, rows, D, tpr, gshift, ngroups, inv_d, eps);
   return cudaGetLastError();
 }
 
@@ -168,9 +175,9 @@ cudaError_t launch_add_norm(const void* x, long long xs, const void* residual, c
                             void* out, float* scales, int rows, int D, int group, float eps, bool e4m3,
                             cudaStream_t st) {
   const int nv = D / 8;
-  // Four vectors a thread; with few rows one, for the latency of a row (4,096 columns: 4,096 rows 26.0 us with four,
-  // 27.1 with two, 30.5 with one).
-  const int want = rows < 2 * device_sms() ? 1 : 4;
+  // Two vectors a thread; with few rows one, for the latency of a row (4,096 columns: 16,384 rows 79.7 us with two,
+  // 80.9 with four; 4,096 rows 22.6 and 22.9, with one 26).
+  const int want = rows < 2 * device_sms() ? 1 : 2;
   int tpr = 32;
   while (tpr < 1024 && want * tpr < nv) tpr <<= 1;
   const int vpt = (nv + tpr - 1) / tpr;

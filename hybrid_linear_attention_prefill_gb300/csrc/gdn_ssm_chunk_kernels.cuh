@@ -471,9 +471,11 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
         if (!(ok = wait(b_z, par, 2))) break;
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
-          widen8(*reinterpret_cast<const uint4*>(f.sm + C::kOffZ + yoff + tc::sw128((uint32_t)row, ych + i)), gv[i]);
+          widen8(above_minus_inf(*reinterpret_cast<const uint4*>(f.sm + C::kOffZ + yoff +
+                                                                 tc::sw128((uint32_t)row, ych + i))),
+                 gv[i]);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) gv[i][u] = silu2(gv[i][u]);
+          for (int u = 0; u < 4; ++u) gv[i][u] = silu2_above(gv[i][u]);
         }
         if (!C::kOwnGate) {
           __syncwarp();
