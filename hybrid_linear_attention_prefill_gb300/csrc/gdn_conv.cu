@@ -201,8 +201,8 @@ cudaError_t conv_k(const void* x, long long xs, const void* weight, const void* 
                    const void* init, void* out, void* fin, int B, int T, int Ttot, int C, cudaStream_t st) {
   using bf = __nv_bfloat16;
   // Runs of 64 tokens read a twentieth of the inputs twice; shorter ones where they would not give every SM its
-  // blocks half over again (T = 4,096, C = 8,192: 27.2 us with 32, a few tenths more with 64, 1.6 with 16; 72,102
-  // tokens: 369 us with 64, 380 with 32).
+  // blocks half over again (72,102 tokens of 8,192 channels: 373 us with 64, 379 with 32, 412 with 16; 4,096 tokens
+  // take 32: 27.5 us, with 16 29.1).
   const int cb = (C / 4 + kConvThreads - 1) / kConvThreads;
   int run = 64;
   while (run > kConvBatch && 2LL * (Ttot / run) * cb < 3LL * kConvBlocks * device_sms()) run >>= 1;

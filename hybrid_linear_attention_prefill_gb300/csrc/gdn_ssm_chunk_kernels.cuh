@@ -161,10 +161,8 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
   const uint32_t tmem = *f.tmem_slot;
   const bool gate = a.z != nullptr;
   auto wait1 = [&](uint64_t* bar, uint32_t par, int bit) { return wait_for(bar, par, f.abort_flag, err, bit); };
-  auto wait = [&](uint64_t* bar, uint32_t par, int bit) {  // a whole warp
-    const bool done = wait1(bar, par, bit);
-    __syncwarp();
-    return done;
+  auto wait = [&](uint64_t* bar, uint32_t par, int bit) {  // a whole warp, together and of one mind after it
+    return __all_sync(0xffffffffu, wait1(bar, par, bit)) != 0;
   };
 
   if (warp == kIssueWarp) {
@@ -360,6 +358,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
         for (int e = tid; e < rows * 8 * (C::kNB + C::kXB); e += 32 * kWorkers)
           *reinterpret_cast<uint4*>(stage + (e / (rows * 8)) * 16384 + (n * 8 + e % (rows * 8)) * 16) =
               make_uint4(0, 0, 0, 0);
+        __syncwarp();
         asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kWorkers) : "memory");
       }
       if (!C::kOwnGate && gate && c > 0) {  // the gate there is read
@@ -571,7 +570,10 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     }
     __syncthreads();
   }
-  if (warp == kAllocWarp) tc::tmem_dealloc(tmem, kTmemCols);
+  if (warp == kAllocWarp) {
+    __syncwarp();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
 // The sums of the segments before a sequence's last (from a zero state) and their decays in log2, and, where the final
@@ -617,10 +619,8 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
   tc::fence_after();
   const uint32_t tmem = *f.tmem_slot;
   auto wait1 = [&](uint64_t* bar, uint32_t par, int bit) { return wait_for(bar, par, f.abort_flag, err, bit); };
-  auto wait = [&](uint64_t* bar, uint32_t par, int bit) {  // a whole warp
-    const bool done = wait1(bar, par, bit);
-    __syncwarp();
-    return done;
+  auto wait = [&](uint64_t* bar, uint32_t par, int bit) {  // a whole warp, together and of one mind after it
+    return __all_sync(0xffffffffu, wait1(bar, par, bit)) != 0;
   };
   // TMEM: w x of a chunk (two halves of 96 columns) in two buffers, the sum between them
   constexpr uint32_t kSum = 288;
@@ -672,6 +672,7 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
 #pragma unroll
       for (int hh = 0; hh < HPC; ++hh) f.tabs[(2 + odd) * HPC * kQ + hh] = total[hh];  // past both buffers
     }
+    __syncwarp();
   } else {
     const int q4 = warp & 3, cg = warp >> 2;
     const int row = 32 * q4 + lane;
@@ -738,7 +739,10 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
     }
     __syncthreads();
   }
-  if (warp == kAllocWarp) tc::tmem_dealloc(tmem, kTmemCols);
+  if (warp == kAllocWarp) {
+    __syncwarp();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
 template <int DK, int PB, int HPC>
