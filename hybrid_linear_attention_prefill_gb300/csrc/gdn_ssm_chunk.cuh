@@ -151,23 +151,17 @@ struct Cfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 };
 
-// A wait that gives up when another thread has (or after 2^24 polls, about half a second), and says so to the others.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t par, volatile int* abort_flag, int* err, int bit) {
-  const uint32_t addr = smem_u32(bar);
-  for (uint32_t i = 0; i < 1u << 24; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(done)
-        : "r"(addr), "r"(par)
-        : "memory");
-    if (done) return true;
-    if ((i & 1023u) == 1023u && *abort_flag) return false;
-  }
-  *abort_flag = 1;
-  atomicOr(err, bit);
-  return false;
+constexpr uint32_t kMaxPolls = 1u << 22;  // of a wait; then it gives up
+
+// Whether a phase has ended, asked some time before it matters: the answer takes about 200 cycles.
+__device__ __forceinline__ uint32_t peek(uint64_t* bar, uint32_t par) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(par));
+  return done;
 }
 
 // A box of a tile from shared memory to global memory, in the thread's next bulk group.
@@ -267,7 +261,7 @@ __device__ __forceinline__ void split_xw(const unsigned char* xt, const float* w
   const float2 w0 = *reinterpret_cast<const float2*>(w + t + 2 * (lane & 3));
   const float2 w1 = *reinterpret_cast<const float2*>(w + t + 8 + 2 * (lane & 3));
   const uint32_t tok = (uint32_t)(t + ((lane >> 4) << 3) + (lane & 7));  // this lane's row of the four 8 x 8 tiles
-#pragma unroll
+#pragma unroll 1  // (the kernels are long already)
   for (int rh = 0; rh < 2; ++rh) {
     const int r = row0 + 16 * rh + (lane & 8);
     uint32_t x[4], hi[4], mid[4], lo[4];

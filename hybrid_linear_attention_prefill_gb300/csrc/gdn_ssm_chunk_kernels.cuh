@@ -160,9 +160,23 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
   tc::fence_after();
   const uint32_t tmem = *f.tmem_slot;
   const bool gate = a.z != nullptr;
-  auto wait1 = [&](uint64_t* bar, uint32_t par, int bit) { return wait_for(bar, par, f.abort_flag, err, bit); };
+  int gave_up = 0;  // the status bit of the wait that this warp gave up
+  auto wait1 = [&](uint64_t* bar, uint32_t par, int bit) {
+    const bool done = tc::mbar_wait(bar, par, kMaxPolls);
+    if (!done) gave_up = bit;
+    return done;
+  };
   auto wait = [&](uint64_t* bar, uint32_t par, int bit) {  // a whole warp, together and of one mind after it
-    return __all_sync(0xffffffffu, wait1(bar, par, bit)) != 0;
+    const bool done = __all_sync(0xffffffffu, tc::mbar_wait(bar, par, kMaxPolls)) != 0;
+    if (!done) gave_up = bit;
+    return done;
+  };
+
+  // The same, where the phase was looked at before.
+  auto settle = [&](uint32_t seen, uint64_t* bar, uint32_t par, int bit) {
+    const bool done = __all_sync(0xffffffffu, seen) != 0;
+    asm volatile("" ::: "memory");
+    return done || wait(bar, par, bit);
   };
 
   if (warp == kIssueWarp) {
@@ -349,10 +363,10 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     const uint32_t yoff = (uint32_t)(yc >> 6) * 16384, ych = (uint32_t)(yc & 63) >> 3;
     bool ok = true;
     // The first operands of chunk c: the state, and w x of its first 64 tokens.
-    auto first_operands = [&](int c) {
+    auto first_operands = [&](int c, uint32_t seen) {
       unsigned char* stage = f.sm + (c & 1) * C::kStage;
       const int n = min(kQ, ntok - c * kQ);
-      if (!wait(b_tab, (uint32_t)(c & 1), 1)) return false;
+      if (!settle(seen, b_tab, (uint32_t)(c & 1), 1)) return false;
       if (n < kQ) {  // rows of the sequence after this one: zeros, so that no value of theirs meets a zero weight
         const int rows = kQ - n;
         for (int e = tid; e < rows * 8 * (C::kNB + C::kXB); e += 32 * kWorkers)
@@ -384,7 +398,8 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       if (lane == 0) arrive(w_a);
       return true;
     };
-    if (nc > 0) ok = first_operands(0);
+    if (nc > 0) ok = first_operands(0, 0);
+    uint32_t seen_sc = 0;
     for (int c = 0; ok && c < nc; ++c) {
       const uint32_t par = (uint32_t)(c & 1);
       unsigned char* xt = f.sm + (c & 1) * C::kStage + C::kOffX;
@@ -393,34 +408,37 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       const int n = min(kQ, ntok - c * kQ);
 
       // ---- M from the scores, in their place: eight columns a head of each 16 ------------------------
-      if (!(ok = wait(b_sc, par, 1))) break;
+      if (!(ok = settle(seen_sc, b_sc, par, 1))) break;
       tc::fence_after();
       {
         const uint32_t col = tq + kColSc + 32 * cg;
         uint32_t m[8];
         if (cg <= q4) {
-          float sc[32];
-          tc::tmem_ld32(col, sc);
+#pragma unroll 1
+          for (int j0 = 0; j0 < 32; j0 += 16) {
+            float sc[16];
+            tc::tmem_ld16(col + j0, sc);
+            const int upto = cg == q4 ? lane - j0 : 32;  // this token's last column
 #pragma unroll
-          for (int hh = 0; hh < HPC; ++hh) {
-            const float* th = tab + hh * 3 * kQ;
-            const float li = th[row];
-            const float2 minus = make_float2(-1.f, -1.f), l2 = make_float2(li, li);
+            for (int hh = 0; hh < HPC; ++hh) {
+              const float* th = tab + hh * 3 * kQ;
+              const float li = th[row];
+              const float2 minus = make_float2(-1.f, -1.f), l2 = make_float2(li, li);
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 k4 = *reinterpret_cast<const float4*>(th + kQ + 32 * cg + j);
-              const float2 e0 = fma2(make_float2(k4.x, k4.y), minus, l2), e1 = fma2(make_float2(k4.z, k4.w), minus, l2);
-              float2 u = mul2(make_float2(sc[j], sc[j + 1]), make_float2(ex2_approx(e0.x), ex2_approx(e0.y)));
-              float2 v = mul2(make_float2(sc[j + 2], sc[j + 3]), make_float2(ex2_approx(e1.x), ex2_approx(e1.y)));
-              if (cg == q4) {
-                u.x = j <= lane ? u.x : 0.f;
-                u.y = j + 1 <= lane ? u.y : 0.f;
-                v.x = j + 2 <= lane ? v.x : 0.f;
-                v.y = j + 3 <= lane ? v.y : 0.f;
+              for (int j = 0; j < 16; j += 4) {
+                const float4 k4 = *reinterpret_cast<const float4*>(th + kQ + 32 * cg + j0 + j);
+                const float2 e0 = fma2(make_float2(k4.x, k4.y), minus, l2);
+                const float2 e1 = fma2(make_float2(k4.z, k4.w), minus, l2);
+                float2 u = mul2(make_float2(sc[j], sc[j + 1]), make_float2(ex2_approx(e0.x), ex2_approx(e0.y)));
+                float2 v = mul2(make_float2(sc[j + 2], sc[j + 3]), make_float2(ex2_approx(e1.x), ex2_approx(e1.y)));
+                u.x = j <= upto ? u.x : 0.f;
+                u.y = j + 1 <= upto ? u.y : 0.f;
+                v.x = j + 2 <= upto ? v.x : 0.f;
+                v.y = j + 3 <= upto ? v.y : 0.f;
+                m[j / 2] = pack_bf16(u.x, u.y);
+                m[j / 2 + 1] = pack_bf16(v.x, v.y);
               }
-              m[(j & 15) / 2] = pack_bf16(u.x, u.y);
-              m[(j & 15) / 2 + 1] = pack_bf16(v.x, v.y);
-              if ((j & 15) == 12) tmem_st8_nowait(col + (j & 16) + 8 * hh, m);
+              tmem_st8_nowait(col + j0 + 8 * hh, m);
             }
           }
         } else {
@@ -433,29 +451,32 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
           }
         }
       }
+      const uint32_t seen_in = peek(b_in, par);
       if (c > 0) {  // the chunk before's outputs have left its x tile
         bulk_wait_read();
         __syncwarp();
         if (lane == 0) arrive(w_s);
       }
       // ---- y = e^{L_i} (C S^T), in place; w x of the other 64 tokens ----------------------------------
-      if (!(ok = wait(b_in, par, 1))) break;  // and (w x)^T B of the first 64 before it
+      if (!(ok = settle(seen_in, b_in, par, 1))) break;  // and (w x)^T B of the first 64 before it
       tc::fence_after();
       {
-        float y[C::kYC];
-        tmem_load<C::kYC>(tq + kColY + yc, y);
         const float e = exp2f(tab[yh * 3 * kQ + row]);
-        uint32_t u[C::kYC];
 #pragma unroll
-        for (int i = 0; i < C::kYC; i += 2) {
-          const float2 v = mul2(make_float2(y[i], y[i + 1]), make_float2(e, e));
-          u[i] = __float_as_uint(v.x);
-          u[i + 1] = __float_as_uint(v.y);
+        for (int i0 = 0; i0 < C::kYC; i0 += 16) {
+          float y[16];
+          tc::tmem_ld16(tq + kColY + yc + i0, y);
+          uint32_t u[16];
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float2 v = mul2(make_float2(y[i], y[i + 1]), make_float2(e, e));
+            u[i] = __float_as_uint(v.x);
+            u[i + 1] = __float_as_uint(v.y);
+          }
+          tmem_st16_nowait(tq + kColY + yc + i0, u);
         }
-#pragma unroll
-        for (int i = 0; i < C::kYC; i += 16)
-          tmem_st16_nowait(tq + kColY + yc + i, reinterpret_cast<const uint32_t(&)[16]>(u[i]));
       }
+      const uint32_t seen_z = gate ? peek(b_z, par) : 0;
       if (32 * q4 < C::kRows) split_xw(xt, tab + hr * 3 * kQ + 2 * kQ, 32 * q4, 64 + 16 * cg, tq + kColXw + 8 * cg);
       tmem_st_wait();
       tc::fence_before();
@@ -467,7 +488,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       // registers but is slower: 668 us against 652 on 32 ragged prompts of 32 heads).
       float2 gv[kP][4];
       if (gate) {
-        if (!(ok = wait(b_z, par, 2))) break;
+        if (!(ok = settle(seen_z, b_z, par, 2))) break;
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
           widen8(above_minus_inf(*reinterpret_cast<const uint4*>(f.sm + C::kOffZ + yoff +
@@ -482,10 +503,11 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
         }
       }
       // ---- S = e^{L_last} S + the chunk's sum ---------------------------------------------------------
+      const uint32_t seen_tab = peek(b_tab, par ^ 1u);
       if (!(ok = wait(b_d1, par, 1))) break;
       tc::fence_after();
       {
-        float ds[C::kSC];
+        float ds[C::kSC];  // (in two halves it spares spills and still costs 2% more, for a second wait)
         tmem_load<C::kSC>(tq + kColDs + C::kSC * cg, ds);
         const SsmDecay decay = f.lend[(c & 3) * HPC + hr];
 #pragma unroll
@@ -497,7 +519,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
           st[i + 1] = r.y;
         }
       }
-      if (c + 1 < nc && !(ok = first_operands(c + 1))) break;
+      if (c + 1 < nc && !(ok = first_operands(c + 1, seen_tab))) break;
       // ---- outputs, by way of the warp's own part of the x tile -----------------------------------------
       if (!(ok = wait(b_y, par, 1))) break;
       tc::fence_after();
@@ -507,6 +529,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
           float y[16];
           tc::tmem_ld16(tq + kColY + yc + 8 * i0, y);
           if (i0 + 2 == kP) {
+            seen_sc = peek(b_sc, par ^ 1u);
             tc::fence_before();
             __syncwarp();
             if (lane == 0) arrive(w_y);
@@ -560,6 +583,10 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       if (wait(w_e, 0, 1))  // every warp has come this far
         move_state<DK, PB, HPC, true>(f.sm + C::kOffS, fin + st_at, a.dv, tid, st);
     }
+  }
+  if (gave_up != 0 && lane == 0) {
+    *f.abort_flag = 1;
+    atomicOr(err, gave_up);
   }
   tc::fence_before();
   __syncthreads();
@@ -618,9 +645,16 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *f.tmem_slot;
-  auto wait1 = [&](uint64_t* bar, uint32_t par, int bit) { return wait_for(bar, par, f.abort_flag, err, bit); };
+  int gave_up = 0;  // the status bit of the wait that this warp gave up
+  auto wait1 = [&](uint64_t* bar, uint32_t par, int bit) {
+    const bool done = tc::mbar_wait(bar, par, kMaxPolls);
+    if (!done) gave_up = bit;
+    return done;
+  };
   auto wait = [&](uint64_t* bar, uint32_t par, int bit) {  // a whole warp, together and of one mind after it
-    return __all_sync(0xffffffffu, wait1(bar, par, bit)) != 0;
+    const bool done = __all_sync(0xffffffffu, tc::mbar_wait(bar, par, kMaxPolls)) != 0;
+    if (!done) gave_up = bit;
+    return done;
   };
   // TMEM: w x of a chunk (two halves of 96 columns) in two buffers, the sum between them
   constexpr uint32_t kSum = 288;
@@ -728,6 +762,11 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
         dst[u * 32 * kWorkers] = make_float4(st[4 * u], st[4 * u + 1], st[4 * u + 2], st[4 * u + 3]);
     }
   }
+  if (gave_up != 0 && lane == 0) {
+    *f.abort_flag = 1;
+    atomicOr(err, gave_up);
+  }
+  __syncwarp();
   tc::fence_before();
   __syncthreads();
   if (!*f.abort_flag && tid < HPC)
