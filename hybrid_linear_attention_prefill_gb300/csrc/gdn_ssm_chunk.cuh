@@ -16,13 +16,18 @@
 // mbarriers only, so that warps drift apart and one's arithmetic covers another's wait.  A chunk's
 // outputs are worked on after the next chunk's first operands are out, beside its first products:
 //
-//   workers: M from the scores; y = e^{L_i} (C S_0^T); w x of 64..127  | MMA: C S_0^T
-//            silu(z)                                                  | MMA: (w x)^T B of 64..127, y += M x
-//            S; the next chunk's S -> bf16 and w x of tokens 0..63    | MMA: the next scores
-//            outputs                                                  | MMA: the next (w x)^T B of 0..63
+//   workers: y = e^{L_i} (C S_0^T); w x of tokens 64..127            | MMA: -
+//            M from the scores                                       | MMA: (w x)^T B of 64..127
+//            S; the next chunk's S -> bf16 and w x of tokens 0..63   | MMA: y += M x, the next scores
+//            silu(z), outputs                                        | MMA: the next (w x)^T B of 0..63 and C S_0^T
 //
-// (With the warps split into a group that carries the state and a group that makes outputs, each chain
-// has half the warps to hide its latencies with: 783 us against 648 on 32 ragged prompts of 32 heads.)
+// What bounds a step (about 9,200 cycles at 128 x 128) is the workers' own path: its instructions, and the latency of
+// what they meet: a barrier's state (200 cycles beside running MMAs, hence `peek`), TMEM, spilled registers, which come
+// back from L2 (so nothing is kept that can be worked out anew, and the gate is taken through silu only where it is
+// used).  The MMAs take 3,840 cycles of it, the tiles' bytes about 5,600 at the device's bandwidth.  32 ragged prompts of
+// 32 heads, 72,102 tokens: 598 us, 4.07 TB/s.  (Warps split into a group that carries the state and one that makes
+// outputs, each with half the warps to hide its latencies: 20% slower.  The gate through silu beside the state's
+// product, kept in registers until the outputs: 4% slower.)
 //
 // Operands.  x, B and C are used as they come (bf16).  The state and M are rounded to bf16 as operands
 // (2^-9 of each term, the size of the outputs' own rounding).  The state itself stays fp32: w x is
@@ -153,6 +158,17 @@ struct Cfg {
 
 constexpr uint32_t kMaxPolls = 1u << 22;  // of a wait; then it gives up
 
+// A worker thread's place, worked out anew where it is used: kept from one use to the next it would not fit the
+// registers, and with so little of the SM's memory left as L1 a spilled value comes back from L2.
+struct Worker {
+  int lane, q4, cg, row;  // q4: TMEM lanes 32 q4 .. + 31; cg: its quarter of the columns; row: state row, or token
+};
+__device__ __forceinline__ Worker worker() {
+  int t;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+  return {t & 31, (t >> 5) & 3, t >> 7, t & 127};
+}
+
 // Whether a phase has ended, asked some time before it matters: the answer takes about 200 cycles.
 __device__ __forceinline__ uint32_t peek(uint64_t* bar, uint32_t par) {
   uint32_t done;
@@ -256,8 +272,8 @@ __device__ __forceinline__ Tables make_tables(const float (&d)[4], float a_log2,
 // w x of sixteen tokens t .. t + 15 of state rows row0 .. + 31 as three bf16 terms into columns col,
 // col + 32 and col + 64 (two tokens a column) of the warp's lanes: the A operand of the state's product.
 // The terms take fp32's 24 bits eight at a time, so nothing is lost.
-__device__ __forceinline__ void split_xw(const unsigned char* xt, const float* w, int row0, int t, uint32_t col) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void split_xw(const unsigned char* xt, const float* w, int lane, int row0, int t,
+                                         uint32_t col) {
   const float2 w0 = *reinterpret_cast<const float2*>(w + t + 2 * (lane & 3));
   const float2 w1 = *reinterpret_cast<const float2*>(w + t + 8 + 2 * (lane & 3));
   const uint32_t tok = (uint32_t)(t + ((lane >> 4) << 3) + (lane & 7));  // this lane's row of the four 8 x 8 tiles

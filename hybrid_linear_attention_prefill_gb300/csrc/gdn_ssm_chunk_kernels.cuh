@@ -7,7 +7,7 @@
 namespace gdn {
 namespace ssm {
 
-constexpr int kBars = 15;
+constexpr int kBars = 16;
 constexpr int kSegStages = 3;  // of the pass of the sums
 
 // What both kernels set up: shared memory (from a 1024-byte boundary, as the swizzled tiles want), TMEM, barriers.
@@ -111,13 +111,13 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
   const Frame f = make_frame<C>(smem_raw);
   // Completed by the MMAs, once a chunk each: scores; (w x)^T B of half 0 and C S^T; (w x)^T B of half 1; y.  By
   // copies: the two stages, C, the gate's tile.  By the worker warps: the first operands of a chunk (the state, w x),
-  // the second (M, y, w x), the gate read, y read, the outputs out of the x tile, and once, their last chunk.  By the
+  // the second (y, w x), the gate read, y read, the outputs out of the x tile, M, and once, their last chunk.  By the
   // table warp: a chunk's tables made and its stage loaded.  Every waiter waits for every phase in turn, and no phase
   // after it can end before it has looked (a parity only names the last phase that ended): what leads to the next one
   // waits for the waiter.
   uint64_t *b_sc = f.bars, *b_in = f.bars + 1, *b_d1 = f.bars + 2, *b_y = f.bars + 3, *b_st = f.bars + 4,
            *b_c = f.bars + 6, *b_z = f.bars + 7, *w_a = f.bars + 8, *w_b = f.bars + 9, *w_z = f.bars + 10,
-           *w_y = f.bars + 11, *w_s = f.bars + 12, *b_tab = f.bars + 13, *w_e = f.bars + 14;
+           *w_y = f.bars + 11, *w_s = f.bars + 12, *b_tab = f.bars + 13, *w_m = f.bars + 14, *w_e = f.bars + 15;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == kAllocWarp) {
@@ -214,7 +214,6 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
           if (!(ok = wait1(w_y, par ^ 1u, 1))) break;
           tc::fence_after();
         }
-        if (C::kOwnGate && gate) load_z(c);
         {
           constexpr uint32_t kId = tc::idesc_bf16(128, C::kRows, 0, 0);
           const uint64_t bd = tc::sdesc(f.sb + C::kOffS, 16, 1024, tc::kSw128);
@@ -223,6 +222,10 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
             tc::mma_bf16(tmem + kColY, c_kmajor + (uint64_t)(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
                          bd + (uint64_t)(((ks >> 2) * (C::kRows * 128) + (ks & 3) * 32) >> 4), kId, ks > 0);
           tc::commit(b_in);
+        }
+        if (C::kOwnGate && gate) {
+          if (c > 0 && !(ok = wait1(w_z, par ^ 1u, 1))) break;
+          load_z(c);
         }
         if (c + 1 < nc || (!C::kOwnGate && gate)) {
           if (!(ok = wait1(b_in, par, 1))) break;
@@ -237,6 +240,8 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
         tc::fence_after();
         issue_state<DK>(tmem + kColDs, tmem + kColXw, stage + C::kOffB, 1, false);
         tc::commit(b_d1);
+        if (!(ok = wait1(w_m, par, 1))) break;
+        tc::fence_after();
         {
           constexpr uint32_t kId = tc::idesc_bf16(128, PB, 0, 1);
 #pragma unroll
@@ -275,8 +280,9 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
         if (c + 1 < nc) load_dt(a, tok0 + (long long)(c + 1) * kQ, ntok - (c + 1) * kQ, h0 + hh, lane, raw[hh]);
         t[hh] = make_tables(d, a_log2[hh], lane);
       }
-      // the tables of chunk c - 1 were read up to its second operands (the decays, used after them, have four places)
-      if (c > 0 && !wait(w_b, (uint32_t)((c - 1) & 1), 1)) break;
+      if (!wait(&b_st[c & 1], (uint32_t)((c >> 1) & 1), 2)) break;
+      // the tables of chunk c - 1 were read up to its M (the decays, used after it, have four places)
+      if (c > 0 && !wait(w_m, (uint32_t)((c - 1) & 1), 1)) break;
 #pragma unroll
       for (int hh = 0; hh < HPC; ++hh) {
         float4* tab = reinterpret_cast<float4*>(f.tabs + hh * 3 * kQ);
@@ -285,7 +291,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
         tab[64 + lane] = t[hh].w;
         if (lane == 0) f.lend[(c & 3) * HPC + hh] = ssm_decay(t[hh].end * 0.6931471805599453f);
       }
-      if (!wait(&b_st[c & 1], (uint32_t)((c >> 1) & 1), 2)) break;
+      __syncwarp();
       if (lane == 0) arrive(b_tab);
       // into L2, since their places in shared memory are free only late: this chunk's gate, the next x and B
       if (lane == 0) {
@@ -304,13 +310,9 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     }
   } else if (warp < kWorkers) {
     // ================= workers =================
-    const int q4 = warp & 3, cg = warp >> 2;
-    const int row = 32 * q4 + lane;  // state row, or token of the chunk
-    const uint32_t tq = tmem + ((uint32_t)(32 * q4) << 16);
-    // this thread's state: row (head, p), columns kSC cg ..
-    const int hr = HPC == 2 ? row >> 6 : 0, p = PB == 64 ? row & 63 : row;
-    const bool my_row = live && row < C::kRows && p < a.dv;
-    float st[C::kSC];
+    auto lanes_of = [&](const Worker& me) { return tmem + ((uint32_t)(32 * me.q4) << 16); };  // its TMEM lanes
+    auto head_of = [](int row) { return HPC == 2 ? row >> 6 : 0; };                            // a state row's head
+    float st[C::kSC];  // this thread's state: its row (head, p), columns kSC cg ..
 #pragma unroll
     for (int i = 0; i < C::kSC; ++i) st[i] = 0.f;
     const size_t st_at = ((size_t)s.b * a.Hv + h0) * a.dv * DK;
@@ -321,7 +323,9 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     }
     // the sums of the segments before: one by one where they are few, or joined into one
     const int i0 = g.joined ? s.slot : s.slot - s.p, i1 = s.slot + (g.joined && s.p > 0 ? 1 : 0);
-    if (my_row && i0 < i1) {  // half of a sum's values are on their way while the other half is added
+    const int my_p = PB == 64 ? tid & 63 : tid & 127;
+    // half of a sum's values are on their way while the other half is added
+    if (live && (tid & 127) < C::kRows && my_p < a.dv && i0 < i1) {
       constexpr int kH = C::kSC / 8;
       auto fetch = [&](int i, int hf, float4 (&v)[kH]) {
         const float4* e = reinterpret_cast<const float4*>(seg_state + seg_at<C>(i, nhb, h0 / HPC, tid));
@@ -338,7 +342,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
           q[3] = ssm_decayed(d, q[3], v[u].w);
         }
       };
-      const float* dec = seg_decay + h0 + hr;
+      const float* dec = seg_decay + h0 + head_of(tid & 127);
       float4 lo[kH], hi[kH];
       float l = dec[(size_t)i0 * a.Hv];
       fetch(i0, 0, lo);
@@ -351,25 +355,34 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
         add(d, 1, hi);
       }
     }
-    // this warp's outputs: tokens 32 q4 .. + 31, columns kYC cg .., worked on by rows in the warp's own part of the
-    // x tile and stored from there in memory order (kP 16-byte pieces a token)
+    // a warp's outputs: tokens 32 q4 .. + 31, columns kYC cg .., worked on by rows in the warp's own part of the x tile
+    // and stored from there in memory order (kP 16-byte pieces a token)
     constexpr int kP = C::kYC / 8;
-    const int yc = C::kYC * cg;
-    const int yh = HPC == 2 ? yc >> 6 : 0, yp = PB == 64 ? yc & 63 : yc;
-    const bool my_cols = yp < a.dv;
-    const float skip = a.D != nullptr && my_cols ? a.D[h0 + yh] : 0.f;
-    const int mt = 32 * q4 + lane / kP, mp = lane % kP;  // memory order: token mt + (32 / kP) i, piece mp
-    const int quad = 2 + 4 * (yc >> 6) + q4;  // named barrier of the warps that share 32 tokens of a 64-wide block
-    const uint32_t yoff = (uint32_t)(yc >> 6) * 16384, ych = (uint32_t)(yc & 63) >> 3;
+    struct Cols {
+      int h, p;             // head and its first column
+      uint32_t off, piece;  // offset of the tile's 64-wide block, first 16-byte piece in its rows
+      int quad;             // named barrier of the warps that share 32 tokens of the block
+    };
+    auto cols_of = [](const Worker& me) {
+      const int yc = C::kYC * me.cg;
+      return Cols{HPC == 2 ? yc >> 6 : 0, PB == 64 ? yc & 63 : yc, (uint32_t)(yc >> 6) * 16384,
+                  (uint32_t)(yc & 63) >> 3, 2 + 4 * (yc >> 6) + me.q4};
+    };
+    float skip = 0.f;
+    {
+      const Cols y = cols_of(worker());
+      if (a.D != nullptr && y.p < a.dv) skip = a.D[h0 + y.h];
+    }
     bool ok = true;
     // The first operands of chunk c: the state, and w x of its first 64 tokens.
     auto first_operands = [&](int c, uint32_t seen) {
+      const Worker me = worker();
       unsigned char* stage = f.sm + (c & 1) * C::kStage;
       const int n = min(kQ, ntok - c * kQ);
       if (!settle(seen, b_tab, (uint32_t)(c & 1), 1)) return false;
       if (n < kQ) {  // rows of the sequence after this one: zeros, so that no value of theirs meets a zero weight
         const int rows = kQ - n;
-        for (int e = tid; e < rows * 8 * (C::kNB + C::kXB); e += 32 * kWorkers)
+        for (int e = 128 * me.cg + me.row; e < rows * 8 * (C::kNB + C::kXB); e += 32 * kWorkers)
           *reinterpret_cast<uint4*>(stage + (e / (rows * 8)) * 16384 + (n * 8 + e % (rows * 8)) * 16) =
               make_uint4(0, 0, 0, 0);
         __syncwarp();
@@ -378,55 +391,87 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       if (!C::kOwnGate && gate && c > 0) {  // the gate there is read
         if (!wait(w_z, (uint32_t)((c - 1) & 1), 1)) return false;
       }
-      if (row < C::kRows) {
+      if (me.row < C::kRows) {
 #pragma unroll
         for (int i = 0; i < C::kSC; i += 8) {
-          const int col = C::kSC * cg + i;
+          const int col = C::kSC * me.cg + i;
           *reinterpret_cast<uint4*>(f.sm + C::kOffS + (col >> 6) * (C::kRows * 128) +
-                                    tc::sw128((uint32_t)row, (uint32_t)(col & 63) >> 3)) =
+                                    tc::sw128((uint32_t)me.row, (uint32_t)(col & 63) >> 3)) =
               make_uint4(pack_bf16(st[i], st[i + 1]), pack_bf16(st[i + 2], st[i + 3]), pack_bf16(st[i + 4], st[i + 5]),
                          pack_bf16(st[i + 6], st[i + 7]));
         }
       }
-      const float* tab = f.tabs;
-      if (32 * q4 < C::kRows)
-        split_xw(stage + C::kOffX, tab + hr * 3 * kQ + 2 * kQ, 32 * q4, 16 * cg, tq + kColXw + 8 * cg);
+      if (32 * me.q4 < C::kRows)
+        split_xw(stage + C::kOffX, f.tabs + head_of(me.row) * 3 * kQ + 2 * kQ, me.lane, 32 * me.q4, 16 * me.cg,
+                 lanes_of(me) + kColXw + 8 * me.cg);
       tmem_st_wait();
       tc::fence_proxy_async();
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) arrive(w_a);
+      if (me.lane == 0) arrive(w_a);
       return true;
     };
     if (nc > 0) ok = first_operands(0, 0);
-    uint32_t seen_sc = 0;
+    uint32_t seen_in = 0;
     for (int c = 0; ok && c < nc; ++c) {
       const uint32_t par = (uint32_t)(c & 1);
       unsigned char* xt = f.sm + (c & 1) * C::kStage + C::kOffX;
-      unsigned char* yt = xt + yoff;
-      const float* tab = f.tabs;
-      const int n = min(kQ, ntok - c * kQ);
+
+      // ---- y = e^{L_i} (C S^T), in place; w x of the other 64 tokens ----------------------------------
+      if (!(ok = settle(seen_in, b_in, par, 1))) break;  // and (w x)^T B of the first 64 before it
+      tc::fence_after();
+      const uint32_t seen_sc = peek(b_sc, par);
+      {
+        const Worker me = worker();
+        const uint32_t at = lanes_of(me) + kColY + C::kYC * me.cg;
+        const float e = exp2f(f.tabs[cols_of(me).h * 3 * kQ + me.row]);
+#pragma unroll
+        for (int i0 = 0; i0 < C::kYC; i0 += 16) {
+          float y[16];
+          tc::tmem_ld16(at + i0, y);
+          uint32_t u[16];
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float2 v = mul2(make_float2(y[i], y[i + 1]), make_float2(e, e));
+            u[i] = __float_as_uint(v.x);
+            u[i + 1] = __float_as_uint(v.y);
+          }
+          tmem_st16_nowait(at + i0, u);
+        }
+        if (32 * me.q4 < C::kRows)
+          split_xw(xt, f.tabs + head_of(me.row) * 3 * kQ + 2 * kQ, me.lane, 32 * me.q4, 64 + 16 * me.cg,
+                   lanes_of(me) + kColXw + 8 * me.cg);
+        tmem_st_wait();
+        tc::fence_before();
+        bulk_wait_read();  // the chunk before's outputs have left its x tile
+        __syncwarp();
+        if (me.lane == 0) {
+          arrive(w_b);
+          if (c > 0) arrive(w_s);
+        }
+      }
 
       // ---- M from the scores, in their place: eight columns a head of each 16 ------------------------
       if (!(ok = settle(seen_sc, b_sc, par, 1))) break;
       tc::fence_after();
       {
-        const uint32_t col = tq + kColSc + 32 * cg;
+        const Worker me = worker();
+        const uint32_t col = lanes_of(me) + kColSc + 32 * me.cg;
         uint32_t m[8];
-        if (cg <= q4) {
+        if (me.cg <= me.q4) {
 #pragma unroll 1
           for (int j0 = 0; j0 < 32; j0 += 16) {
             float sc[16];
             tc::tmem_ld16(col + j0, sc);
-            const int upto = cg == q4 ? lane - j0 : 32;  // this token's last column
+            const int upto = me.cg == me.q4 ? me.lane - j0 : 32;  // this token's last column
 #pragma unroll
             for (int hh = 0; hh < HPC; ++hh) {
-              const float* th = tab + hh * 3 * kQ;
-              const float li = th[row];
+              const float* th = f.tabs + hh * 3 * kQ;
+              const float li = th[me.row];
               const float2 minus = make_float2(-1.f, -1.f), l2 = make_float2(li, li);
 #pragma unroll
               for (int j = 0; j < 16; j += 4) {
-                const float4 k4 = *reinterpret_cast<const float4*>(th + kQ + 32 * cg + j0 + j);
+                const float4 k4 = *reinterpret_cast<const float4*>(th + kQ + 32 * me.cg + j0 + j);
                 const float2 e0 = fma2(make_float2(k4.x, k4.y), minus, l2);
                 const float2 e1 = fma2(make_float2(k4.z, k4.w), minus, l2);
                 float2 u = mul2(make_float2(sc[j], sc[j + 1]), make_float2(ex2_approx(e0.x), ex2_approx(e0.y)));
@@ -451,56 +496,21 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
           }
         }
       }
-      const uint32_t seen_in = peek(b_in, par);
-      if (c > 0) {  // the chunk before's outputs have left its x tile
-        bulk_wait_read();
-        __syncwarp();
-        if (lane == 0) arrive(w_s);
-      }
-      // ---- y = e^{L_i} (C S^T), in place; w x of the other 64 tokens ----------------------------------
-      if (!(ok = settle(seen_in, b_in, par, 1))) break;  // and (w x)^T B of the first 64 before it
-      tc::fence_after();
-      {
-        const float e = exp2f(tab[yh * 3 * kQ + row]);
-#pragma unroll
-        for (int i0 = 0; i0 < C::kYC; i0 += 16) {
-          float y[16];
-          tc::tmem_ld16(tq + kColY + yc + i0, y);
-          uint32_t u[16];
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float2 v = mul2(make_float2(y[i], y[i + 1]), make_float2(e, e));
-            u[i] = __float_as_uint(v.x);
-            u[i + 1] = __float_as_uint(v.y);
-          }
-          tmem_st16_nowait(tq + kColY + yc + i0, u);
-        }
-      }
-      const uint32_t seen_z = gate ? peek(b_z, par) : 0;
-      if (32 * q4 < C::kRows) split_xw(xt, tab + hr * 3 * kQ + 2 * kQ, 32 * q4, 64 + 16 * cg, tq + kColXw + 8 * cg);
       tmem_st_wait();
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) arrive(w_b);
-
-      // ---- the gate -------------------------------------------------------------------------------------
-      // This thread's row of the gate goes through silu while M x runs (half of it now and half with the outputs spares
-      // registers but is slower: 668 us against 652 on 32 ragged prompts of 32 heads).
-      float2 gv[kP][4];
-      if (gate) {
-        if (!(ok = settle(seen_z, b_z, par, 2))) break;
+      if (lane == 0) arrive(w_m);
+      uint4 zr[kP];
+      if (!C::kOwnGate && gate) {  // the gate, before the next state takes its place
+        if (!(ok = wait(b_z, par, 2))) break;
+        const Worker me = worker();
+        const Cols cols = cols_of(me);
 #pragma unroll
-        for (int i = 0; i < kP; ++i) {
-          widen8(above_minus_inf(*reinterpret_cast<const uint4*>(f.sm + C::kOffZ + yoff +
-                                                                 tc::sw128((uint32_t)row, ych + i))),
-                 gv[i]);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) gv[i][u] = silu2_above(gv[i][u]);
-        }
-        if (!C::kOwnGate) {
-          __syncwarp();
-          if (lane == 0) arrive(w_z);
-        }
+        for (int i = 0; i < kP; ++i)
+          zr[i] = *reinterpret_cast<const uint4*>(f.sm + C::kOffZ + cols.off +
+                                                  tc::sw128((uint32_t)me.row, cols.piece + i));
+        __syncwarp();
+        if (me.lane == 0) arrive(w_z);
       }
       // ---- S = e^{L_last} S + the chunk's sum ---------------------------------------------------------
       const uint32_t seen_tab = peek(b_tab, par ^ 1u);
@@ -508,8 +518,9 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       tc::fence_after();
       {
         float ds[C::kSC];  // (in two halves it spares spills and still costs 2% more, for a second wait)
-        tmem_load<C::kSC>(tq + kColDs + C::kSC * cg, ds);
-        const SsmDecay decay = f.lend[(c & 3) * HPC + hr];
+        const Worker me = worker();
+        tmem_load<C::kSC>(lanes_of(me) + kColDs + C::kSC * me.cg, ds);
+        const SsmDecay decay = f.lend[(c & 3) * HPC + head_of(me.row)];
 #pragma unroll
         for (int i = 0; i < C::kSC; i += 2) {
           const float2 v = make_float2(st[i], st[i + 1]);
@@ -521,51 +532,64 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       }
       if (c + 1 < nc && !(ok = first_operands(c + 1, seen_tab))) break;
       // ---- outputs, by way of the warp's own part of the x tile -----------------------------------------
+      const uint32_t seen_z = C::kOwnGate && gate ? peek(b_z, par) : 0;
       if (!(ok = wait(b_y, par, 1))) break;
       tc::fence_after();
       {
+        const Worker me = worker();
+        const Cols cols = cols_of(me);
+        unsigned char* yt = xt + cols.off;
+        const int n = min(kQ, ntok - c * kQ);
+        float y[C::kYC];
+        tmem_load<C::kYC>(lanes_of(me) + kColY + C::kYC * me.cg, y);
+        tc::fence_before();
+        __syncwarp();
+        if (me.lane == 0) arrive(w_y);
+        if (C::kOwnGate && gate && !(ok = settle(seen_z, b_z, par, 2))) break;
 #pragma unroll
-        for (int i0 = 0; i0 < kP; i0 += 2) {  // sixteen columns of this thread's own row at a time
-          float y[16];
-          tc::tmem_ld16(tq + kColY + yc + 8 * i0, y);
-          if (i0 + 2 == kP) {
-            seen_sc = peek(b_sc, par ^ 1u);
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) arrive(w_y);
+        for (int i = 0; i < kP; ++i) {  // eight columns of this thread's own row at a time
+          const uint32_t piece = tc::sw128((uint32_t)me.row, cols.piece + i);
+          uint4* at = reinterpret_cast<uint4*>(yt + piece);
+          float2 v[4], g4[4];
+          widen8(*at, v);
+          if (gate) {
+            if (C::kOwnGate) zr[i] = *reinterpret_cast<const uint4*>(f.sm + C::kOffZ + cols.off + piece);
+            widen8(above_minus_inf(zr[i]), g4);
           }
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint4* at = reinterpret_cast<uint4*>(yt + tc::sw128((uint32_t)row, ych + i0 + i));
-            float2 v[4];
-            widen8(*at, v);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              v[u] = fma2(v[u], make_float2(skip, skip), make_float2(y[8 * i + 2 * u], y[8 * i + 2 * u + 1]));
-              if (gate) v[u] = mul2(v[u], gv[i0 + i][u]);
-            }
-            *at = narrow8(v);
+          for (int u = 0; u < 4; ++u) {
+            v[u] = fma2(v[u], make_float2(skip, skip), make_float2(y[8 * i + 2 * u], y[8 * i + 2 * u + 1]));
+            if (gate) v[u] = mul2(v[u], silu2_above(g4[u]));
           }
+          *at = narrow8(v);
         }
-        if (a.dv >= 64 && 32 * q4 + 32 <= n) {  // 32 whole tokens of 64 columns: one copy by the first of their warps
+        if (C::kOwnGate && gate) {
+          __syncwarp();
+          if (me.lane == 0) arrive(w_z);
+        }
+        seen_in = peek(b_in, par ^ 1u);
+        // 32 whole tokens of 64 columns: one copy by the first of their warps
+        if (a.dv >= 64 && 32 * me.q4 + 32 <= n) {
           tc::fence_proxy_async();
-          asm volatile("bar.sync %0, %1;\n" ::"r"(quad), "n"(32 * (64 / C::kYC)) : "memory");
-          if ((yc & 63) == 0 && lane == 0) {
-            tma_store_2d(&tm_o, smem_u32(yt) + 32 * q4 * 128, (h0 + yh) * a.dv + yp,
-                         (int)(tok0 + (long long)c * kQ) + 32 * q4);
+          asm volatile("bar.sync %0, %1;\n" ::"r"(cols.quad), "n"(32 * (64 / C::kYC)) : "memory");
+          if (cols.piece == 0 && me.lane == 0) {
+            tma_store_2d(&tm_o, smem_u32(yt) + 32 * me.q4 * 128, (h0 + cols.h) * a.dv + cols.p,
+                         (int)(tok0 + (long long)c * kQ) + 32 * me.q4);
             bulk_commit();
           }
           __syncwarp();
         } else {
           __syncwarp();
-          if (my_cols) {
-            __nv_bfloat16* o = a.out + ((size_t)(tok0 + (long long)c * kQ) * a.Hv + h0 + yh) * a.dv + yp + 8 * mp;
+          if (cols.p < a.dv) {
+            const int mt = 32 * me.q4 + me.lane / kP, mp = me.lane % kP;  // token mt + (32 / kP) i, piece mp
+            __nv_bfloat16* o =
+                a.out + ((size_t)(tok0 + (long long)c * kQ) * a.Hv + h0 + cols.h) * a.dv + cols.p + 8 * mp;
 #pragma unroll
             for (int i = 0; i < kP; ++i) {
               const int t = mt + (32 / kP) * i;
               if (t < n)
                 *reinterpret_cast<uint4*>(o + (size_t)t * a.Hv * a.dv) =
-                    *reinterpret_cast<const uint4*>(yt + tc::sw128((uint32_t)t, ych + mp));
+                    *reinterpret_cast<const uint4*>(yt + tc::sw128((uint32_t)t, cols.piece + mp));
             }
           }
           tc::fence_proxy_async();
@@ -575,7 +599,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     bulk_wait_read();
     if (!ok) {  // another warp may have passed the wait that this one gave up, and stand at a barrier between warps
       asm volatile("bar.arrive 1, %0;\n" ::"n"(32 * kWorkers) : "memory");
-      asm volatile("bar.arrive %0, %1;\n" ::"r"(quad), "n"(32 * (64 / C::kYC)) : "memory");
+      asm volatile("bar.arrive %0, %1;\n" ::"r"(cols_of(worker()).quad), "n"(32 * (64 / C::kYC)) : "memory");
     }
     if (ok && fin != nullptr && live && s.last) {
       __syncwarp();
@@ -744,7 +768,7 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
       if (!ok) break;
       if (32 * q4 < C::kRows) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) split_xw(xt, w, 32 * q4, 64 * hf + 16 * cg, tq + xw_col(c, hf) + 8 * cg);
+        for (int hf = 0; hf < 2; ++hf) split_xw(xt, w, lane, 32 * q4, 64 * hf + 16 * cg, tq + xw_col(c, hf) + 8 * cg);
       }
       if (c > 0) update(c - 1);
       if (!ok) break;
