@@ -293,13 +293,14 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       }
       __syncwarp();
       if (lane == 0) arrive(b_tab);
-      // into L2, since their places in shared memory are free only late: this chunk's gate, the next x and B
+      // into L2, since their places in shared memory are free only late: the next gate, x and B
       if (lane == 0) {
         const int t = (int)(tok0 + (long long)c * kQ);
 #pragma unroll
         for (int i = 0; i < C::kXB; ++i) {
           const int col = PB == 64 ? (h0 + i) * a.dv : h0 * a.dv + 64 * i;
-          if (gate) tma_prefetch_l2_2d(&tm_z, col, t);
+          if (gate && c == 0) tma_prefetch_l2_2d(&tm_z, col, t);
+          if (gate && c + 1 < nc) tma_prefetch_l2_2d(&tm_z, col, t + kQ);
           if (c > 0 && c + 1 < nc) tma_prefetch_l2_2d(&tm_x, col, t + kQ);
         }
         if (c > 0 && c + 1 < nc)
@@ -417,10 +418,25 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       const uint32_t par = (uint32_t)(c & 1);
       unsigned char* xt = f.sm + (c & 1) * C::kStage + C::kOffX;
 
-      // ---- y = e^{L_i} (C S^T), in place; w x of the other 64 tokens ----------------------------------
-      if (!(ok = settle(seen_in, b_in, par, 1))) break;  // and (w x)^T B of the first 64 before it
+      // ---- w x of the other 64 tokens ------------------------------------------------------------------
+      if (!(ok = settle(seen_in, b_in, par, 1))) break;  // (w x)^T B of the first 64 and C S^T
       tc::fence_after();
       const uint32_t seen_sc = peek(b_sc, par);
+      {
+        const Worker me = worker();
+        if (32 * me.q4 < C::kRows)
+          split_xw(xt, f.tabs + head_of(me.row) * 3 * kQ + 2 * kQ, me.lane, 32 * me.q4, 64 + 16 * me.cg,
+                   lanes_of(me) + kColXw + 8 * me.cg);
+        tmem_st_wait();
+        tc::fence_before();
+        bulk_wait_read();  // the chunk before's outputs have left its x tile
+        __syncwarp();
+        if (me.lane == 0) {
+          arrive(w_b);
+          if (c > 0) arrive(w_s);
+        }
+      }
+      // ---- y = e^{L_i} (C S^T), in place ---------------------------------------------------------------
       {
         const Worker me = worker();
         const uint32_t at = lanes_of(me) + kColY + C::kYC * me.cg;
@@ -438,19 +454,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
           }
           tmem_st16_nowait(at + i0, u);
         }
-        if (32 * me.q4 < C::kRows)
-          split_xw(xt, f.tabs + head_of(me.row) * 3 * kQ + 2 * kQ, me.lane, 32 * me.q4, 64 + 16 * me.cg,
-                   lanes_of(me) + kColXw + 8 * me.cg);
-        tmem_st_wait();
-        tc::fence_before();
-        bulk_wait_read();  // the chunk before's outputs have left its x tile
-        __syncwarp();
-        if (me.lane == 0) {
-          arrive(w_b);
-          if (c > 0) arrive(w_s);
-        }
       }
-
       // ---- M from the scores, in their place: eight columns a head of each 16 ------------------------
       if (!(ok = settle(seen_sc, b_sc, par, 1))) break;
       tc::fence_after();
