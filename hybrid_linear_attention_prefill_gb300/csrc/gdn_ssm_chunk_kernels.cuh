@@ -622,25 +622,27 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     }
     if (ok && fin != nullptr && live && s.last) {
       __syncwarp();
-      if (lane == 0) arrive(w_e);
+      const Worker me = worker();
+      if (me.lane == 0) arrive(w_e);
       if (wait(w_e, 0, 1))  // every warp has come this far
-        move_state<DK, PB, HPC, true>(f.sm + C::kOffS, fin + st_at, a.dv, tid, st);
+        move_state<DK, PB, HPC, true>(f.sm + C::kOffS, fin + st_at, a.dv, 128 * me.cg + me.row, st);
     }
   }
-  if (gave_up != 0 && lane == 0) {
+  const Worker at_end = worker();
+  if (gave_up != 0 && at_end.lane == 0) {
     *f.abort_flag = 1;
     atomicOr(err, gave_up);
   }
   tc::fence_before();
   __syncthreads();
   if (*f.abort_flag) {  // let what is in flight land, bounded again
-    if (tid == 0) {
+    if (at_end.row == 0 && at_end.cg == 0) {
       for (int i = 0; i < 8; ++i)
         for (uint32_t par = 0; par < 2; ++par) (void)tc::mbar_wait(&f.bars[i], par, 1u << 14);
     }
     __syncthreads();
   }
-  if (warp == kAllocWarp) {
+  if (4 * at_end.cg + at_end.q4 == kAllocWarp) {
     __syncwarp();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
