@@ -16,18 +16,18 @@
 // mbarriers only, so that warps drift apart and one's arithmetic covers another's wait.  A chunk's
 // outputs are worked on after the next chunk's first operands are out, beside its first products:
 //
-//   workers: y = e^{L_i} (C S_0^T); w x of tokens 64..127            | MMA: -
-//            M from the scores                                       | MMA: (w x)^T B of 64..127
-//            S; the next chunk's S -> bf16 and w x of tokens 0..63   | MMA: y += M x, the next scores
-//            silu(z), outputs                                        | MMA: the next (w x)^T B of 0..63 and C S_0^T
+//   workers: w x of tokens 64..127                                   | MMA: -
+//            y = e^{L_i} (C S_0^T); M from the scores; some of silu(z) | MMA: (w x)^T B of 64..127
+//            S; the next chunk's S -> bf16 and w x of tokens 0..63     | MMA: y += M x, the next scores
+//            the rest of silu(z), outputs                              | MMA: the next (w x)^T B of 0..63 and C S_0^T
 //
-// What bounds a step (about 9,200 cycles at 128 x 128) is the workers' own path: its instructions, and the latency of
-// what they meet: a barrier's state (200 cycles beside running MMAs, hence `peek`), TMEM, spilled registers, which come
-// back from L2 (so nothing is kept that can be worked out anew, and the gate is taken through silu only where it is
-// used).  The MMAs take 3,840 cycles of it, the tiles' bytes about 5,600 at the device's bandwidth.  32 ragged prompts of
-// 32 heads, 72,102 tokens: 598 us, 4.07 TB/s.  (Warps split into a group that carries the state and one that makes
-// outputs, each with half the warps to hide its latencies: 20% slower.  The gate through silu beside the state's
-// product, kept in registers until the outputs: 4% slower.)
+// What bounds a step (about 8,000 cycles at 128 x 128) is the workers' own path: its instructions (the SM issues in 57%
+// of the cycles) and the latency of what they meet: a barrier's state (200 cycles beside running MMAs, hence `peek`),
+// TMEM, spilled registers, which come back from L2 (so that little is kept that can be worked out anew, and the gate
+// goes through silu only where it is used).  The MMAs take 3,840 cycles of it, the tiles' bytes about 5,600 at the
+// device's bandwidth.  32 ragged prompts of 32 heads, 72,102 tokens: 549 us, 4.43 TB/s of needed bytes.  (Warps split
+// into a group that carries the state and one that makes outputs, each with half the warps to hide its latencies: 20%
+// slower.  All of the gate through silu beside the state's product, kept in registers until the outputs: 8% slower.)
 //
 // Operands.  x, B and C are used as they come (bf16).  The state and M are rounded to bf16 as operands
 // (2^-9 of each term, the size of the outputs' own rounding).  The state itself stays fp32: w x is

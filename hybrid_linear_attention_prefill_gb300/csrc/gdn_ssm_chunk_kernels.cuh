@@ -7,7 +7,7 @@
 namespace gdn {
 namespace ssm {
 
-constexpr int kBars = 16;
+constexpr int kBars = 15;
 constexpr int kSegStages = 3;  // of the pass of the sums
 
 // What both kernels set up: shared memory (from a 1024-byte boundary, as the swizzled tiles want), TMEM, barriers.
@@ -54,46 +54,50 @@ __device__ __forceinline__ size_t seg_at(int slot, int nhb, int hb, int tid) {
 }
 
 // The state of the CTA's heads between memory (rows of DK values, the heads one after the other) and the workers'
-// registers, by way of shared memory (the state operand's place), 64 columns at a time: a row's 16-byte pieces are
-// XORed with its number, so that both orders are free of bank conflicts.  All workers call it together.
+// registers, by way of a piece of shared memory of each warp's own (in the state operand's place): its 32 rows, up to 16
+// columns at a time, 16-byte pieces XORed with the row so that both orders are free of bank conflicts.
 template <int DK, int PB, int HPC, bool kStore>
-__device__ __forceinline__ void move_state(unsigned char* buf, float* mem, int dv, int tid, float (&st)[DK / 4]) {
-  constexpr int kHalf = DK < 64 ? DK : 64, kPieces = kHalf / 4, kSC = DK / 4;
-  const int row = 32 * ((tid >> 5) & 3) + (tid & 31), cg = tid >> 7;
-  const int rows = HPC * dv;
-  const int hr = HPC == 2 ? row >> 6 : 0, p = PB == 64 ? row & 63 : row;
-  const bool mine = row < PB * HPC && p < dv;
-  const int my = hr * dv + p;  // the row in memory
+__device__ __forceinline__ void move_state(unsigned char* place, float* mem, int dv, const Worker& me,
+                                           float (&st)[DK / 4]) {
+  constexpr int kSC = DK / 4, kPart = kSC < 16 ? kSC : 16, kPc = kPart / 4, kParts = kSC / kPart;
+  const int row0 = 32 * me.q4, p0 = PB == 64 ? row0 & 63 : row0;
+  if (row0 >= PB * HPC || p0 >= dv) return;
+  unsigned char* buf = place + (me.cg * (PB * HPC / 32) + me.q4) * (32 * kPart * 4);
+  auto at = [&](int row, int piece) {
+    return reinterpret_cast<float4*>(buf + (row * kPc + (piece ^ ((row / (8 / kPc)) & (kPc - 1)))) * 16);
+  };
+  float4* m = reinterpret_cast<float4*>(mem + (size_t)((HPC == 2 ? row0 >> 6 : 0) * dv + p0) * DK + kSC * me.cg);
+  auto out_at = [&](int part, int i) {  // memory order: lane's piece i of a part
+    const int e = me.lane + 32 * i;
+    return m + (e / kPc) * (DK / 4) + part * kPc + e % kPc;
+  };
+  float4 v[kParts][kPc];
+  if (!kStore) {
 #pragma unroll
-  for (int hf = 0; hf < DK / kHalf; ++hf) {
-    const bool here = mine && cg / (kHalf / kSC) == hf;
-    const int c0 = (cg % (kHalf / kSC)) * (kSC / 4);
-    if (kStore && here) {
+    for (int h = 0; h < kParts; ++h)
 #pragma unroll
-      for (int i = 0; i < kSC / 4; ++i)
-        *reinterpret_cast<float4*>(buf + (my * kPieces + ((c0 + i) ^ (my & (kPieces - 1)))) * 16) =
-            make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
+      for (int i = 0; i < kPc; ++i) v[h][i] = *out_at(h, i);
+  }
+#pragma unroll
+  for (int h = 0; h < kParts; ++h) {
+#pragma unroll
+    for (int i = 0; i < kPc; ++i) {
+      const float* q = st + h * kPart + 4 * i;
+      if (kStore) *at(me.lane, i) = make_float4(q[0], q[1], q[2], q[3]);
+      else *at((me.lane + 32 * i) / kPc, (me.lane + 32 * i) % kPc) = v[h][i];
     }
-    if (kStore) asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kWorkers) : "memory");
-    for (int e = tid; e < rows * kPieces; e += 32 * kWorkers) {
-      const int r = e / kPieces, c = e % kPieces;
-      float4* s = reinterpret_cast<float4*>(buf + (r * kPieces + (c ^ (r & (kPieces - 1)))) * 16);
-      float4* m = reinterpret_cast<float4*>(mem + (size_t)r * DK + hf * kHalf + 4 * c);
-      if (kStore) *m = *s;
-      else *s = *m;
-    }
-    asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kWorkers) : "memory");
-    if (!kStore) {
-      if (here) {
+    __syncwarp();
 #pragma unroll
-        for (int i = 0; i < kSC / 4; ++i) {
-          const float4 v =
-              *reinterpret_cast<const float4*>(buf + (my * kPieces + ((c0 + i) ^ (my & (kPieces - 1)))) * 16);
-          st[4 * i] = v.x; st[4 * i + 1] = v.y; st[4 * i + 2] = v.z; st[4 * i + 3] = v.w;
-        }
+    for (int i = 0; i < kPc; ++i) {
+      if (kStore) {
+        *out_at(h, i) = *at((me.lane + 32 * i) / kPc, (me.lane + 32 * i) % kPc);
+      } else {
+        const float4 t = *at(me.lane, i);
+        float* q = st + h * kPart + 4 * i;
+        q[0] = t.x; q[1] = t.y; q[2] = t.z; q[3] = t.w;
       }
-      asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kWorkers) : "memory");
     }
+    __syncwarp();
   }
 }
 
@@ -111,13 +115,12 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
   const Frame f = make_frame<C>(smem_raw);
   // Completed by the MMAs, once a chunk each: scores; (w x)^T B of half 0 and C S^T; (w x)^T B of half 1; y.  By
   // copies: the two stages, C, the gate's tile.  By the worker warps: the first operands of a chunk (the state, w x),
-  // the second (y, w x), the gate read, y read, the outputs out of the x tile, M, and once, their last chunk.  By the
-  // table warp: a chunk's tables made and its stage loaded.  Every waiter waits for every phase in turn, and no phase
-  // after it can end before it has looked (a parity only names the last phase that ended): what leads to the next one
-  // waits for the waiter.
+  // the second (w x), the gate read, y read, the outputs out of the x tile, y scaled and M.  By the table warp: a chunk's
+  // tables made and its stage loaded.  Every waiter waits for every phase in turn, and no phase after it can end before
+  // it has looked (a parity only names the last phase that ended): what leads to the next one waits for the waiter.
   uint64_t *b_sc = f.bars, *b_in = f.bars + 1, *b_d1 = f.bars + 2, *b_y = f.bars + 3, *b_st = f.bars + 4,
            *b_c = f.bars + 6, *b_z = f.bars + 7, *w_a = f.bars + 8, *w_b = f.bars + 9, *w_z = f.bars + 10,
-           *w_y = f.bars + 11, *w_s = f.bars + 12, *b_tab = f.bars + 13, *w_m = f.bars + 14, *w_e = f.bars + 15;
+           *w_y = f.bars + 11, *w_s = f.bars + 12, *b_tab = f.bars + 13, *w_m = f.bars + 14;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == kAllocWarp) {
@@ -320,7 +323,8 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the segments' sums
     if (live && init != nullptr) {  // where the final state replaces it, the later segments' copy of it
       const float* from = kept != nullptr && !(s.first && s.last) ? kept : init;
-      move_state<DK, PB, HPC, false>(f.sm + C::kOffS, const_cast<float*>(from) + st_at, a.dv, tid, st);
+      move_state<DK, PB, HPC, false>(f.sm + C::kOffS, const_cast<float*>(from) + st_at, a.dv, worker(), st);
+      asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kWorkers) : "memory");  // before the state operand
     }
     // the sums of the segments before: one by one where they are few, or joined into one
     const int i0 = g.joined ? s.slot : s.slot - s.p, i1 = s.slot + (g.joined && s.p > 0 ? 1 : 0);
@@ -622,10 +626,9 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     }
     if (ok && fin != nullptr && live && s.last) {
       __syncwarp();
-      const Worker me = worker();
-      if (me.lane == 0) arrive(w_e);
-      if (wait(w_e, 0, 1))  // every warp has come this far
-        move_state<DK, PB, HPC, true>(f.sm + C::kOffS, fin + st_at, a.dv, 128 * me.cg + me.row, st);
+      // the state operand's place is free: C S^T is done, and the gate there read
+      if (C::kOwnGate || !gate || nc == 0 || wait(w_z, (uint32_t)((nc - 1) & 1), 1))
+        move_state<DK, PB, HPC, true>(f.sm + C::kOffS, fin + st_at, a.dv, worker(), st);
     }
   }
   const Worker at_end = worker();
