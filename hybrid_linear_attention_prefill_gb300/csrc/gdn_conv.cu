@@ -7,7 +7,8 @@
 // and written once (4 bytes) for 2 K + ~6 operations, so HBM bandwidth bounds it.  A thread owns
 // four consecutive channels (an 8-byte access a token: with eight, its weights and window leave
 // room for too few loads in flight) and walks a run of tokens with the last K - 1 inputs in
-// registers, so that only a run's first K - 1 inputs are read twice.
+// registers, so that only a run's first K - 1 inputs are read twice.  72,102 tokens of 8,192
+// channels: 371 us, 6.37 TB/s; 4,096 tokens: 27.2 us.
 #include "gdn_internal.h"
 #include "gdn_vec.cuh"
 

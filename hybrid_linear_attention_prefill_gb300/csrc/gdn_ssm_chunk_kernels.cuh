@@ -54,8 +54,8 @@ __device__ __forceinline__ size_t seg_at(int slot, int nhb, int hb, int tid) {
 }
 
 // The state of the CTA's heads between memory (rows of DK values, the heads one after the other) and the workers'
-// registers, by way of a piece of shared memory of each warp's own (in the state operand's place): its 32 rows, up to 16
-// columns at a time, 16-byte pieces XORed with the row so that both orders are free of bank conflicts.
+// registers, by way of a piece of shared memory of each warp's own (in the state operand's place): its 32 rows, up to
+// 16 columns at a time, 16-byte pieces XORed with the row so that both orders are free of bank conflicts.
 template <int DK, int PB, int HPC, bool kStore>
 __device__ __forceinline__ void move_state(unsigned char* place, float* mem, int dv, const Worker& me,
                                            float (&st)[DK / 4]) {
@@ -115,9 +115,10 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
   const Frame f = make_frame<C>(smem_raw);
   // Completed by the MMAs, once a chunk each: scores; (w x)^T B of half 0 and C S^T; (w x)^T B of half 1; y.  By
   // copies: the two stages, C, the gate's tile.  By the worker warps: the first operands of a chunk (the state, w x),
-  // the second (w x), the gate read, y read, the outputs out of the x tile, y scaled and M.  By the table warp: a chunk's
-  // tables made and its stage loaded.  Every waiter waits for every phase in turn, and no phase after it can end before
-  // it has looked (a parity only names the last phase that ended): what leads to the next one waits for the waiter.
+  // the second (w x), the gate read, y read, the outputs out of the x tile, y scaled and M.  By the table warp: a
+  // chunk's tables made and its stage loaded.  Every waiter waits for every phase in turn, and no phase after it can
+  // end before it has looked (a parity only names the last phase that ended): what leads to the next one waits for
+  // the waiter.
   uint64_t *b_sc = f.bars, *b_in = f.bars + 1, *b_d1 = f.bars + 2, *b_y = f.bars + 3, *b_st = f.bars + 4,
            *b_c = f.bars + 6, *b_z = f.bars + 7, *w_a = f.bars + 8, *w_b = f.bars + 9, *w_z = f.bars + 10,
            *w_y = f.bars + 11, *w_s = f.bars + 12, *b_tab = f.bars + 13, *w_m = f.bars + 14;
@@ -508,8 +509,8 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       tc::fence_before();
       __syncwarp();
       if (lane == 0) arrive(w_m);
-      // Some of the gate through silu while the state's product runs: what the registers have room for (32 ragged prompts:
-      // 595 us with none, 580 with eight columns, 620 with sixteen).
+      // Some of the gate through silu while the state's product runs: what the registers have room for (32 ragged
+      // prompts: 587 us with none, 560 with eight columns, 595 with sixteen).
       constexpr int kEarly = C::kOwnGate ? kP / 4 : 0;
       float2 ge[kEarly + 1][4];
       if (C::kOwnGate && gate) {

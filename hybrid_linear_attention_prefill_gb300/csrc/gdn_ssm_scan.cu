@@ -3,7 +3,7 @@
 //
 // A CTA carries the state of its heads through a segment's chunks one after the other.  Where sequences
 // and heads are too few to fill the device, sequences are cut into segments: one pass sums every segment
-// from a zero state (x, B and dt only, about a quarter of a chunk's time), and the output pass runs every segment
+// from a zero state (x, B and dt only, about 0.3 of a chunk's time), and the output pass runs every segment
 // from the sums before it (with many segments gdn_ssm_join_kernel makes start states of them first).  The
 // later kernels are programmatic dependents: they set up beside the one before.
 #include <algorithm>
@@ -34,8 +34,9 @@ struct Plan {
 };
 
 // Heads a CTA and the segments' length, from the sizes alone (a packed batch's lengths are on the device:
-// taken as equal).  In units of an output pass's chunk step: a CTA costs its chunks and about one more to start
-// and drain, a quarter of a step a chunk and 0.8 in the pass of the sums, and the join about one.
+// taken as equal).  In units of an output pass's chunk step (4.2 us at 128 x 128): a CTA costs its chunks and about one
+// more to start and drain, 0.25 of a step a chunk and 0.8 in the pass of the sums, and the join about one.  The choice
+// does not hang on these (from 0.1 to 0.6 of a step a chunk it is the same for 1,024, 4,096 and 16,381 tokens).
 Plan make_plan(int B, int T, int Hk, int Hv, int dv, bool packed, int sms) {
   Plan p;
   p.hpc = dv < 128 && (Hv / Hk) % 2 == 0 ? 2 : 1;
