@@ -269,23 +269,34 @@ __device__ __forceinline__ Tables make_tables(const float (&d)[4], float a_log2,
   return t;
 }
 
-// w x of sixteen tokens t .. t + 15 of state rows row0 .. + 31 as three bf16 terms into columns col,
-// col + 32 and col + 64 (two tokens a column) of the warp's lanes: the A operand of the state's product.
-// The terms take fp32's 24 bits eight at a time, so nothing is lost.
-__device__ __forceinline__ void split_xw(const unsigned char* xt, const float* w, int lane, int row0, int t,
-                                         uint32_t col) {
-  const float2 w0 = *reinterpret_cast<const float2*>(w + t + 2 * (lane & 3));
-  const float2 w1 = *reinterpret_cast<const float2*>(w + t + 8 + 2 * (lane & 3));
+// x of sixteen tokens t .. t + 15 and state rows row0 .. + 31 as a warp multiplies it by w (in shared memory beside
+// running MMAs both take hundreds of cycles, so they are loaded some time before they are split).
+struct XwTiles {
+  uint32_t x[2][4];
+  float2 w[2];
+};
+__device__ __forceinline__ void load_xw(XwTiles& v, const unsigned char* xt, const float* w, int lane, int row0, int t) {
   const uint32_t tok = (uint32_t)(t + ((lane >> 4) << 3) + (lane & 7));  // this lane's row of the four 8 x 8 tiles
-#pragma unroll 1  // (the kernels are long already)
+#pragma unroll
   for (int rh = 0; rh < 2; ++rh) {
     const int r = row0 + 16 * rh + (lane & 8);
-    uint32_t x[4], hi[4], mid[4], lo[4];
-    ldsm_x4_t(x, xt + (r >> 6) * 16384 + tc::sw128(tok, (uint32_t)(r & 63) >> 3));
+    ldsm_x4_t(v.x[rh], xt + (r >> 6) * 16384 + tc::sw128(tok, (uint32_t)(r & 63) >> 3));
+  }
+  v.w[0] = *reinterpret_cast<const float2*>(w + t + 2 * (lane & 3));
+  v.w[1] = *reinterpret_cast<const float2*>(w + t + 8 + 2 * (lane & 3));
+}
+
+// w x as three bf16 terms into columns col, col + 32 and col + 64 (two tokens a column) of the warp's lanes: the A
+// operand of the state's product.  The terms take fp32's 24 bits eight at a time, so nothing is lost.
+__device__ __forceinline__ void split_xw(const XwTiles& tiles, uint32_t col) {
+#pragma unroll
+  for (int rh = 0; rh < 2; ++rh) {
+    const uint32_t(&x)[4] = tiles.x[rh];
+    uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // tiles (tokens 0..7, 8..15) x (rows 0..7, 8..15), rows innermost
       const float2 v =
-          mul2(make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)), i < 2 ? w0 : w1);
+          mul2(make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)), tiles.w[i >> 1]);
       const uint32_t a = __float_as_uint(v.x), b = __float_as_uint(v.y);
       hi[i] = __byte_perm(a, b, 0x7632);
       const float2 m = fma2(make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)),

@@ -397,6 +397,9 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       if (!C::kOwnGate && gate && c > 0) {  // the gate there is read
         if (!wait(w_z, (uint32_t)((c - 1) & 1), 1)) return false;
       }
+      XwTiles xw;
+      if (32 * me.q4 < C::kRows)
+        load_xw(xw, stage + C::kOffX, f.tabs + head_of(me.row) * 3 * kQ + 2 * kQ, me.lane, 32 * me.q4, 16 * me.cg);
       if (me.row < C::kRows) {
 #pragma unroll
         for (int i = 0; i < C::kSC; i += 8) {
@@ -407,9 +410,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                          pack_bf16(st[i + 6], st[i + 7]));
         }
       }
-      if (32 * me.q4 < C::kRows)
-        split_xw(stage + C::kOffX, f.tabs + head_of(me.row) * 3 * kQ + 2 * kQ, me.lane, 32 * me.q4, 16 * me.cg,
-                 lanes_of(me) + kColXw + 8 * me.cg);
+      if (32 * me.q4 < C::kRows) split_xw(xw, lanes_of(me) + kColXw + 8 * me.cg);
       tmem_st_wait();
       tc::fence_proxy_async();
       tc::fence_before();
@@ -424,14 +425,16 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       unsigned char* xt = f.sm + (c & 1) * C::kStage + C::kOffX;
 
       // ---- w x of the other 64 tokens ------------------------------------------------------------------
-      if (!(ok = settle(seen_in, b_in, par, 1))) break;  // (w x)^T B of the first 64 and C S^T
-      tc::fence_after();
-      const uint32_t seen_sc = peek(b_sc, par);
+      uint32_t seen_sc;
       {
         const Worker me = worker();
+        XwTiles xw;
         if (32 * me.q4 < C::kRows)
-          split_xw(xt, f.tabs + head_of(me.row) * 3 * kQ + 2 * kQ, me.lane, 32 * me.q4, 64 + 16 * me.cg,
-                   lanes_of(me) + kColXw + 8 * me.cg);
+          load_xw(xw, xt, f.tabs + head_of(me.row) * 3 * kQ + 2 * kQ, me.lane, 32 * me.q4, 64 + 16 * me.cg);
+        if (!(ok = settle(seen_in, b_in, par, 1))) break;  // (w x)^T B of the first 64 and C S^T
+        tc::fence_after();
+        seen_sc = peek(b_sc, par);
+        if (32 * me.q4 < C::kRows) split_xw(xw, lanes_of(me) + kColXw + 8 * me.cg);
         tmem_st_wait();
         tc::fence_before();
         bulk_wait_read();  // the chunk before's outputs have left its x tile
@@ -793,7 +796,11 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
       if (!ok) break;
       if (32 * q4 < C::kRows) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) split_xw(xt, w, lane, 32 * q4, 64 * hf + 16 * cg, tq + xw_col(c, hf) + 8 * cg);
+        for (int hf = 0; hf < 2; ++hf) {
+          XwTiles xw;
+          load_xw(xw, xt, w, lane, 32 * q4, 64 * hf + 16 * cg);
+          split_xw(xw, tq + xw_col(c, hf) + 8 * cg);
+        }
       }
       if (c > 0) update(c - 1);
       if (!ok) break;
