@@ -8,7 +8,7 @@
 // four consecutive channels (an 8-byte access a token: with eight, its weights and window leave
 // room for too few loads in flight) and walks a run of tokens with the last K - 1 inputs in
 // registers, so that only a run's first K - 1 inputs are read twice.  72,102 tokens of 8,192
-// channels: 371 us, 6.37 TB/s; 4,096 tokens: 27.2 us.
+// channels: 367 us, 6.44 TB/s; 4,096 tokens: 27.2 us.
 #include "gdn_internal.h"
 #include "gdn_vec.cuh"
 
@@ -201,13 +201,13 @@ template <int K, bool SILU>
 cudaError_t conv_k(const void* x, long long xs, const void* weight, const void* bias, const int32_t* cu,
                    const void* init, void* out, void* fin, int B, int T, int Ttot, int C, cudaStream_t st) {
   using bf = __nv_bfloat16;
-  // Runs of 64 tokens read a twentieth of the inputs twice; shorter ones where they would not give every SM its
-  // blocks half over again (72,102 tokens of 8,192 channels: 373 us with 64, 379 with 32, 412 with 16; 4,096 tokens
-  // take 32: 27.5 us, with 16 29.1).
+  // Runs of 128 tokens read a fortieth of the inputs twice; shorter ones where they would not give every SM its blocks
+  // half over again (72,102 tokens of 8,192 channels: 367 us with 128, 373 with 64, 379 with 32, 412 with 16; 4,096
+  // tokens take 32: 27.5 us, with 16 29.1).
   const int cb = (C / 4 + kConvThreads - 1) / kConvThreads;
-  int run = 64;
+  int run = 128;
   while (run > kConvBatch && 2LL * (Ttot / run) * cb < 3LL * kConvBlocks * device_sms()) run >>= 1;
-  const int runs = (Ttot + run - 1) / run;
+  const int runs = (int)(((long long)Ttot + run - 1) / run);
   const unsigned gx = (unsigned)runs + (fin != nullptr ? (unsigned)B : 0u);
   gdn_conv_kernel<K, SILU><<<dim3(gx, cb), kConvThreads, 0, st>>>(
       static_cast<const bf*>(x), xs, static_cast<const bf*>(weight), static_cast<const bf*>(bias), cu,

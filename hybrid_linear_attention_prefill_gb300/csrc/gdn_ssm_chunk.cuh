@@ -25,9 +25,9 @@
 // of the cycles) and the latency of what they meet: a barrier's state (200 cycles beside running MMAs, hence `peek`),
 // TMEM, spilled registers, which come back from L2 (so that little is kept that can be worked out anew, and the gate
 // goes through silu only where it is used).  The MMAs take 3,840 cycles of it, the tiles' bytes about 5,600 at the
-// device's bandwidth.  32 ragged prompts of 32 heads, 72,102 tokens: 549 us, 4.43 TB/s of needed bytes.  (Warps split
-// into a group that carries the state and one that makes outputs, each with half the warps to hide its latencies: 20%
-// slower.  All of the gate through silu beside the state's product, kept in registers until the outputs: 8% slower.)
+// device's bandwidth.  32 ragged prompts of 32 heads, 72,102 tokens: 540 to 554 us, 4.4 TB/s of needed bytes.  (Warps
+// split into a group that carries the state and one that makes outputs, each with half the warps to hide its latencies:
+// 20% slower.  All of the gate through silu beside the state's product, kept in registers until the outputs: 8%.)
 //
 // Operands.  x, B and C are used as they come (bf16).  The state and M are rounded to bf16 as operands
 // (2^-9 of each term, the size of the outputs' own rounding).  The state itself stays fp32: w x is
@@ -275,7 +275,8 @@ struct XwTiles {
   uint32_t x[2][4];
   float2 w[2];
 };
-__device__ __forceinline__ void load_xw(XwTiles& v, const unsigned char* xt, const float* w, int lane, int row0, int t) {
+__device__ __forceinline__ void load_xw(XwTiles& v, const unsigned char* xt, const float* w, int lane, int row0,
+                                        int t) {
   const uint32_t tok = (uint32_t)(t + ((lane >> 4) << 3) + (lane & 7));  // this lane's row of the four 8 x 8 tiles
 #pragma unroll
   for (int rh = 0; rh < 2; ++rh) {
