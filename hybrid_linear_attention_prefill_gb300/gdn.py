@@ -535,6 +535,10 @@ def ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, cu_seqlens=None, in
     dev, (n, Hk, Hv, dk, dv), fields, out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus)
     B, T, cu = _batch(n, cu_seqlens, B, dev)
     shape = (B, Hv, dv, dk)
+    if workspace is not None:
+        _want(workspace.device == x.device and workspace.is_contiguous(),
+              f"workspace: contiguous, on the device of x, is wanted, got strides {workspace.stride()} on "
+              f"{workspace.device}")
     if final_state is None and want_final:
         final_state = torch.empty(shape, dtype=torch.float32, device=x.device)
     check(load().gdn_ssm_scan(_SSM_SCAN.pack(
