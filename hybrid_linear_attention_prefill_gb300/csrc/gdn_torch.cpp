@@ -59,8 +59,10 @@ struct Call {
     stride = t->size(0) > 1 ? t->stride(0) : width;
     return t->data_ptr();
   }
+  // The stream of a call on the current device (one on another is for the Python way, which makes that current).
   void* stream(int i) {
     PyObject* o = argv[i];
+    if (ok && c10::cuda::current_device() != dev) ok = false;
     if (!ok) return nullptr;
     if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
     if (!PyLong_Check(o)) {

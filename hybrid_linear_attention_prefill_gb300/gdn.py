@@ -305,7 +305,8 @@ def prefill(q, k, v, g, beta, cu_seqlens=None, init_state=None, *, B=None, want_
         T = Ttot // B if B else 0
     out = torch.empty((Ttot, Hv, dv), dtype=torch.bfloat16, device=q.device)
     fin = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=q.device) if want_final else None
-    check(gdn_prefill(q, k, v, g, beta, cu_seqlens, init_state, out, fin, B, T, Hk, Hv, dk, dv, stream))
+    with torch.cuda.device(q.device):
+        check(gdn_prefill(q, k, v, g, beta, cu_seqlens, init_state, out, fin, B, T, Hk, Hv, dk, dv, stream))
     return out, fin
 
 
@@ -340,7 +341,19 @@ def _raw_stream(stream, device_index) -> int:
         import torch
 
         return torch._C._cuda_getCurrentRawStream(device_index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+    if isinstance(stream, int):
+        return stream
+    of = getattr(stream, "device", None)
+    _want(of is None or of.index == device_index, f"stream: one of the device of x is wanted, got one of {of}")
+    return stream.cuda_stream
+
+
+def _call(entry, args, device_index) -> None:
+    """A C entry with its arguments packed, on this device: the entries launch on the current one."""
+    import torch
+
+    with torch.cuda.device(device_index):
+        check(entry(args))
 
 
 def gdn_conv(x, x_stride, weight, bias, cu_seqlens, init_state, out, final_state, B, T, C, K, flags,
@@ -458,11 +471,11 @@ def causal_conv(x, weight, bias=None, cu_seqlens=None, init_state=None, *, B=Non
         out = torch.empty((n, C), dtype=bf16, device=x.device)
     if final_state is None and want_final:
         final_state = torch.empty((B, K - 1, C), dtype=bf16, device=x.device)
-    check(load().gdn_conv(_CONV.pack(
+    _call(load().gdn_conv, _CONV.pack(
         x.data_ptr(), xs, _plain(weight, "weight", bf16, (C, K), dev), _plain(bias, "bias", bf16, (C,), dev), cu,
         _plain(init_state, "init_state", bf16, (B, K - 1, C), dev), _plain(out, "out", bf16, (n, C), dev),
         _plain(final_state, "final_state", bf16, (B, K - 1, C), dev), B, T, C, K, GDN_CONV_SILU if silu else 0,
-        _raw_stream(stream, dev))))
+        _raw_stream(stream, dev)), dev)
     return out, final_state
 
 
@@ -483,10 +496,10 @@ def causal_conv_step(x, weight, state, bias=None, *, silu=True, out=None, stream
     xs = _rows(x, "x", bf16, (B, C), dev)
     if out is None:
         out = torch.empty((B, C), dtype=bf16, device=x.device)
-    check(load().gdn_conv_step(_CONV_STEP.pack(
+    _call(load().gdn_conv_step, _CONV_STEP.pack(
         x.data_ptr(), xs, _plain(weight, "weight", bf16, (C, K), dev), _plain(bias, "bias", bf16, (C,), dev),
         _plain(state, "state", bf16, (B, K - 1, C), dev), _plain(out, "out", bf16, (B, C), dev), B, C, K,
-        GDN_CONV_SILU if silu else 0, _raw_stream(stream, dev))))
+        GDN_CONV_SILU if silu else 0, _raw_stream(stream, dev)), dev)
     return out
 
 
@@ -541,11 +554,11 @@ def ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, cu_seqlens=None, in
               f"{workspace.device}")
     if final_state is None and want_final:
         final_state = torch.empty(shape, dtype=torch.float32, device=x.device)
-    check(load().gdn_ssm_scan(_SSM_SCAN.pack(
+    _call(load().gdn_ssm_scan, _SSM_SCAN.pack(
         *fields, cu, _plain(init_state, "init_state", torch.float32, shape, dev), out.data_ptr(),
         _plain(final_state, "final_state", torch.float32, shape, dev), B, T, Hk, Hv, dk, dv, flags,
         0 if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))))
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)), dev)
     return out, final_state
 
 
@@ -561,9 +574,9 @@ def ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softplus=
     import torch
 
     dev, (n, Hk, Hv, dk, dv), fields, out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus)
-    check(load().gdn_ssm_step(_SSM_STEP.pack(
+    _call(load().gdn_ssm_step, _SSM_STEP.pack(
         *fields, _plain(state, "state", torch.float32, (n, Hv, dv, dk), dev), out.data_ptr(), n, Hk, Hv, dk, dv, flags,
-        _raw_stream(stream, dev))))
+        _raw_stream(stream, dev)), dev)
     return out
 
 
@@ -600,9 +613,9 @@ def add_norm(x, weight, residual=None, *, eps=1e-6, group=0, e4m3=False, out=Non
         scales = torch.empty((rows, -(-D // group) if group else 1), dtype=torch.float32, device=x.device)
     if residual is not None and residual_out is None:
         residual_out = torch.empty(shape, dtype=bf16, device=x.device)
-    check(load().gdn_add_norm(_NORM.pack(
+    _call(load().gdn_add_norm, _NORM.pack(
         x.data_ptr(), xs, _plain(residual, "residual", bf16, shape, dev), _plain(weight, "weight", bf16, (D,), dev),
         _plain(residual_out, "residual_out", bf16, shape, dev), _plain(out, "out", f8 if e4m3 else bf16, shape, dev),
         _plain(scales, "scales", torch.float32, (rows, -(-D // group) if group else 1), dev), rows, D, group, eps,
-        GDN_NORM_E4M3 if e4m3 else 0, _raw_stream(stream, dev))))
+        GDN_NORM_E4M3 if e4m3 else 0, _raw_stream(stream, dev)), dev)
     return out, scales, residual_out

@@ -51,3 +51,61 @@ def test_scan_refuses_a_workspace_that_is_not_one_piece_beside_x(entries, worksp
     assert entries.calls == []
     gdn.ssm_scan(**scan_operands(), workspace=torch.zeros(4096, dtype=torch.uint8))
     assert entries.calls == ["gdn_ssm_scan"]
+
+
+# ---- the device of a call -----------------------------------------------------------------------
+
+class OnDevice1(torch.Tensor):
+    def get_device(self):
+        return 1
+
+
+def calls_on_device_1():
+    def t(*shape, dtype=torch.bfloat16):
+        return torch.zeros(shape, dtype=dtype).as_subclass(OnDevice1)
+
+    f32 = torch.float32
+    s = dict(x=t(8, 4, 64), dt=t(8, 4, dtype=f32), A=t(4, dtype=f32), Bm=t(8, 2, 32), Cm=t(8, 2, 32))
+    return [("gdn_conv", lambda: gdn.causal_conv(t(8, 64), t(64, 4), out=t(8, 64), want_final=False)),
+            ("gdn_conv_step", lambda: gdn.causal_conv_step(t(8, 64), t(64, 4), t(8, 3, 64), out=t(8, 64))),
+            ("gdn_ssm_scan", lambda: gdn.ssm_scan(**s, out=t(8, 4, 64), want_final=False)),
+            ("gdn_ssm_step", lambda: gdn.ssm_step(**s, state=t(8, 4, 64, 32, dtype=f32), out=t(8, 4, 64))),
+            ("gdn_add_norm", lambda: gdn.add_norm(t(8, 64), t(64), out=t(8, 64)))]
+
+
+@pytest.mark.parametrize("which", range(5))
+def test_calls_run_with_the_device_of_x_as_the_current_one(monkeypatch, which):
+    """The C entries launch on the current device, so it has to be the one that the operands and the stream are of."""
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.was, current[0] = current[0], self.index
+
+        def __exit__(self, *a):
+            current[0] = self.was
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: seen.append((name, current[0])) or 0
+
+    monkeypatch.setattr(gdn, "load", lambda *a: Lib())
+    monkeypatch.setattr(gdn, "_fast", None)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    name, call = calls_on_device_1()[which]
+    call()
+    assert seen == [(name, 1)] and current == [0]
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        cuda_stream = 5
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="stream"):
+        gdn._raw_stream(Stream(), 0)
+    assert gdn._raw_stream(Stream(), 1) == 5 and gdn._raw_stream(7, 0) == 7
