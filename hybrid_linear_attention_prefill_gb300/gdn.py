@@ -286,6 +286,21 @@ def check(status: int) -> None:
         raise GdnError(status, gdn_last_cuda_error())
 
 
+def _output(shape, dtype, device, stream):
+    """A tensor for a call on `stream` to write, from that stream's memory: what the current stream freed its work
+    may still use, and what is freed to it its next tensor may take while the call runs."""
+    import torch
+
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = stream if isinstance(stream, int) else stream.cuda_stream
+        # 0 and 1 are CUDA's names of the legacy default stream
+        stream = torch.cuda.ExternalStream(raw, device) if raw > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def prefill(q, k, v, g, beta, cu_seqlens=None, init_state=None, *, B=None, want_final=True, stream=None):
     """Allocate outputs and run ``gdn_prefill`` on CUDA tensors.
 
@@ -303,8 +318,8 @@ def prefill(q, k, v, g, beta, cu_seqlens=None, init_state=None, *, B=None, want_
     else:
         B = 1 if B is None else B
         T = Ttot // B if B else 0
-    out = torch.empty((Ttot, Hv, dv), dtype=torch.bfloat16, device=q.device)
-    fin = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=q.device) if want_final else None
+    out = _output((Ttot, Hv, dv), torch.bfloat16, q.device, stream)
+    fin = _output((B, Hv, dv, dk), torch.float32, q.device, stream) if want_final else None
     with torch.cuda.device(q.device):
         check(gdn_prefill(q, k, v, g, beta, cu_seqlens, init_state, out, fin, B, T, Hk, Hv, dk, dv, stream))
     return out, fin
@@ -468,9 +483,9 @@ def causal_conv(x, weight, bias=None, cu_seqlens=None, init_state=None, *, B=Non
     xs = _rows(x, "x", bf16, (n, C), dev)
     B, T, cu = _batch(n, cu_seqlens, B, dev)
     if out is None:
-        out = torch.empty((n, C), dtype=bf16, device=x.device)
+        out = _output((n, C), bf16, x.device, stream)
     if final_state is None and want_final:
-        final_state = torch.empty((B, K - 1, C), dtype=bf16, device=x.device)
+        final_state = _output((B, K - 1, C), bf16, x.device, stream)
     _call(load().gdn_conv, _CONV.pack(
         x.data_ptr(), xs, _plain(weight, "weight", bf16, (C, K), dev), _plain(bias, "bias", bf16, (C,), dev), cu,
         _plain(init_state, "init_state", bf16, (B, K - 1, C), dev), _plain(out, "out", bf16, (n, C), dev),
@@ -495,7 +510,7 @@ def causal_conv_step(x, weight, state, bias=None, *, silu=True, out=None, stream
     (B, _), (C, K), dev = x.shape, weight.shape, x.get_device()
     xs = _rows(x, "x", bf16, (B, C), dev)
     if out is None:
-        out = torch.empty((B, C), dtype=bf16, device=x.device)
+        out = _output((B, C), bf16, x.device, stream)
     _call(load().gdn_conv_step, _CONV_STEP.pack(
         x.data_ptr(), xs, _plain(weight, "weight", bf16, (C, K), dev), _plain(bias, "bias", bf16, (C,), dev),
         _plain(state, "state", bf16, (B, K - 1, C), dev), _plain(out, "out", bf16, (B, C), dev), B, C, K,
@@ -503,7 +518,7 @@ def causal_conv_step(x, weight, state, bias=None, *, silu=True, out=None, stream
     return out
 
 
-def _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus):
+def _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus, stream):
     """Of the scan and its step: (device, sizes, the struct's fields up to dt_bias, out, flags)."""
     import torch
 
@@ -520,7 +535,7 @@ def _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus):
               _plain(D, "D", f32, (Hv,), dev), 0 if z is None else z.data_ptr(),
               0 if z is None else _rows(z, "z", bf16, shape, dev), _plain(dt_bias, "dt_bias", f32, (Hv,), dev))
     if out is None:
-        out = torch.empty((n, Hv, dv), dtype=bf16, device=x.device)
+        out = _output((n, Hv, dv), bf16, x.device, stream)
     else:
         _plain(out, "out", bf16, shape, dev)
     return dev, (n, Hk, Hv, dk, dv), fields, out, (GDN_SSM_DT_F32 if dt32 else 0) | (GDN_SSM_SOFTPLUS if softplus else 0)
@@ -545,7 +560,7 @@ def ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, cu_seqlens=None, in
             return out, final_state
     import torch
 
-    dev, (n, Hk, Hv, dk, dv), fields, out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus)
+    dev, (n, Hk, Hv, dk, dv), fields, out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus, stream)
     B, T, cu = _batch(n, cu_seqlens, B, dev)
     shape = (B, Hv, dv, dk)
     if workspace is not None:
@@ -553,7 +568,7 @@ def ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, cu_seqlens=None, in
               f"workspace: contiguous, on the device of x, is wanted, got strides {workspace.stride()} on "
               f"{workspace.device}")
     if final_state is None and want_final:
-        final_state = torch.empty(shape, dtype=torch.float32, device=x.device)
+        final_state = _output(shape, torch.float32, x.device, stream)
     _call(load().gdn_ssm_scan, _SSM_SCAN.pack(
         *fields, cu, _plain(init_state, "init_state", torch.float32, shape, dev), out.data_ptr(),
         _plain(final_state, "final_state", torch.float32, shape, dev), B, T, Hk, Hv, dk, dv, flags,
@@ -573,7 +588,7 @@ def ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softplus=
             return out
     import torch
 
-    dev, (n, Hk, Hv, dk, dv), fields, out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus)
+    dev, (n, Hk, Hv, dk, dv), fields, out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus, stream)
     _call(load().gdn_ssm_step, _SSM_STEP.pack(
         *fields, _plain(state, "state", torch.float32, (n, Hv, dv, dk), dev), out.data_ptr(), n, Hk, Hv, dk, dv, flags,
         _raw_stream(stream, dev)), dev)
@@ -604,15 +619,15 @@ def add_norm(x, weight, residual=None, *, eps=1e-6, group=0, e4m3=False, out=Non
     dev = x.get_device()
     xs = _rows(x, "x", bf16, shape, dev)
     if out is None:
-        out = torch.empty(shape, dtype=f8 if e4m3 else bf16, device=x.device)
+        out = _output(shape, f8 if e4m3 else bf16, x.device, stream)
     else:
         e4m3 = out.dtype is f8
     if not e4m3:
         scales = None
     elif scales is None:
-        scales = torch.empty((rows, -(-D // group) if group else 1), dtype=torch.float32, device=x.device)
+        scales = _output((rows, -(-D // group) if group else 1), torch.float32, x.device, stream)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty(shape, dtype=bf16, device=x.device)
+        residual_out = _output(shape, bf16, x.device, stream)
     _call(load().gdn_add_norm, _NORM.pack(
         x.data_ptr(), xs, _plain(residual, "residual", bf16, shape, dev), _plain(weight, "weight", bf16, (D,), dev),
         _plain(residual_out, "residual_out", bf16, shape, dev), _plain(out, "out", f8 if e4m3 else bf16, shape, dev),
