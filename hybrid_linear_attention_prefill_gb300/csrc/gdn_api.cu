@@ -415,15 +415,15 @@ int device_sms() {
   return n;
 }
 
-int ensure_ssm_workspace(int dev, size_t need, void** ws) {
+int ensure_ssm_workspace(int dev, size_t need, cudaStream_t st, void** ws) {
   if (dev < 0 || dev >= kMaxDevices) return GDN_ERR_ARG;
   std::lock_guard<std::mutex> lock(g_mu);
   DevBuffers& d = g_dev[dev];
   const size_t had = d.ssm_bytes;
   const int rc = ensure(d.ssm, d.ssm_bytes, need);
   if (rc != GDN_OK) return rc;
-  if (d.ssm_bytes != had) {  // a new allocation: its status words
-    const cudaError_t e = cudaMemset(d.ssm, 0, 256);
+  if (d.ssm_bytes != had) {  // a new allocation: its status words, in the order of the call that writes them
+    const cudaError_t e = cudaMemsetAsync(d.ssm, 0, 256, st);
     if (e != cudaSuccess) return set_cuda_error(e, GDN_ERR_LAUNCH);
   }
   *ws = d.ssm;

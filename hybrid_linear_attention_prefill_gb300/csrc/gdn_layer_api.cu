@@ -162,7 +162,7 @@ int gdn_ssm_scan(const gdn_ssm_scan_args* args) {
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return gdn::set_cuda_error(e, GDN_ERR_LAUNCH);
-    const int rc = gdn::ensure_ssm_workspace(dev, need, &workspace);
+    const int rc = gdn::ensure_ssm_workspace(dev, need, static_cast<cudaStream_t>(stream), &workspace);
     if (rc != GDN_OK) return rc;
   } else {
     if (!aligned(workspace, 256)) return GDN_ERR_ALIGN;

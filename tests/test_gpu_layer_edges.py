@@ -39,3 +39,18 @@ def test_outputs_come_from_the_memory_of_the_stream_of_the_call(gdn):
             del got
             fresh = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in was.values() for _ in range(4)]
             assert not was.keys() & {t.data_ptr() for t in fresh}
+
+
+def test_a_first_calls_status_survives_what_another_stream_has_to_do(gdn):
+    s = scan_inputs(gen(75), 200, 3, 1, 1, 64, 64, init=True)
+    bad = torch.tensor([0, 190, 100, 200], dtype=torch.int32, device="cuda")
+    out, fin = torch.empty_like(s["x"]), torch.empty_like(s["init_state"])
+    side = torch.cuda.Stream()
+    gdn.ssm_scan(**s, cu_seqlens=bad, out=out, final_state=fin, stream=side)
+    gdn.gdn_device_status()
+    gdn.gdn_release_workspace()
+    torch.cuda._sleep(500_000_000)  # about a quarter of a second of the default stream
+    gdn.ssm_scan(**s, cu_seqlens=bad, out=out, final_state=fin, stream=side)
+    side.synchronize()
+    rc, bits = gdn.gdn_device_status()
+    assert rc == 0 and bits == gdn.GDN_STATUS_BAD_CU_SEQLENS
