@@ -143,8 +143,8 @@ struct Cfg {
   static constexpr int kOffC = 2 * kStage;
   static constexpr int kOffS = kOffC + kNB * 16384;
   static constexpr int kSBytes = kNB * kRows * 128 > kXB * 16384 ? kNB * kRows * 128 : kXB * 16384;
-  static constexpr int kTabBytes = HPC * 4 * kQ * 4;  // L, K and w of a chunk (the pass of the sums: w of two, decays)
-  static constexpr int kBarBytes = 256;               // mbarriers, TMEM base, abort flag, decays
+  static constexpr int kTabBytes = HPC * 5 * kQ * 4;  // tables of a chunk (the pass of the sums: w of two, decays)
+  static constexpr int kBarBytes = 256;               // mbarriers, TMEM base, abort flag, decays, gaps
   static constexpr bool kOwnGate = kOffS + kSBytes + kXB * 16384 + kTabBytes + kBarBytes <= 227 * 1024;
   static constexpr int kOffZ = kOwnGate ? kOffS + kSBytes : kOffS;
   static constexpr int kOffTab = kOwnGate ? kOffZ + kXB * 16384 : kOffS + kSBytes;
@@ -240,32 +240,51 @@ __device__ __forceinline__ void to_steps(const SsmArgs& a, int n, float bias, in
   for (int u = 0; u < 4; ++u) d[u] = 4 * lane + u < n ? ssm_step_of(a, r[u], bias) : 0.f;
 }
 
-// One warp: the tables of a chunk from its steps, tokens 4 lane .. + 3 in each lane: L in units of log2, inclusive
-// of each token's own decay; K = L - log2 s; w.  The weights' exponents are sums over the tokens after each, from
-// the end: as differences of L they would carry the rounding of a strong decay's large L.
+// One warp: the tables of a chunk from its steps, tokens 4 lane .. + 3 in each lane, in units of log2.  No exponent is
+// the difference of two sums over more than 32 tokens, since it would carry the rounding of what it does not contain
+// (a strong decay's large L, before a pair of tokens whose own decay is weak).  With the chunk in blocks of 32 tokens,
+// M's exponent L_i - L_j + log2 s_j is
+//   L - K          in one block, L inclusive of a token's own decay and from its block's start, K = L - log2 s;
+//   L + gap - far  between blocks, the gap the sum over the blocks between, far = -(the sum after j in its block)
+//                  - log2 s_j.
+// The weights' exponents are sums over the tokens after each, from the chunk's end.  A token's decay below 2^-160 is 0
+// in fp32 and counts as 2^-160, which keeps L above -5,120: its rounding (2^-12) stays below that of M to bf16 (2^-9).
 struct Tables {
-  float4 L, K, w;
-  float end;  // L of the last token, in every lane
+  float4 L, K, far, w, e;  // e: 2^(the sum up to a token)
+  float2 gap;              // between the lane's block and blocks 0 and 1
+  float end;               // the sum over the chunk, in every lane
 };
 __device__ __forceinline__ Tables make_tables(const float (&d)[4], float a_log2, int lane) {
-  const float e0 = d[0] * a_log2, e1 = d[1] * a_log2, e2 = d[2] * a_log2, e3 = d[3] * a_log2;
+  constexpr float kLeast = -160.f;
+  const float e0 = max_nan(d[0] * a_log2, kLeast), e1 = max_nan(d[1] * a_log2, kLeast);
+  const float e2 = max_nan(d[2] * a_log2, kLeast), e3 = max_nan(d[3] * a_log2, kLeast);
   const float own = (e0 + e1) + (e2 + e3);
-  float from = own, upto = own;  // sums over the lanes from and up to this one
+  const int at = lane & 7, block = lane >> 3;
+  float from = own, upto = own;  // sums over the block's lanes from and up to this one
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const float y = __shfl_up_sync(0xffffffffu, upto, o), z = __shfl_down_sync(0xffffffffu, from, o);
-    if (lane >= o) upto += y;
-    if (lane + o < 32) from += z;
+  for (int o = 1; o < 8; o <<= 1) {
+    const float y = __shfl_up_sync(0xffffffffu, upto, o, 8), z = __shfl_down_sync(0xffffffffu, from, o, 8);
+    if (at >= o) upto += y;
+    if (at + o < 8) from += z;
   }
+  const float b0 = __shfl_sync(0xffffffffu, upto, 7), b1 = __shfl_sync(0xffffffffu, upto, 15);
+  const float b2 = __shfl_sync(0xffffffffu, upto, 23), b3 = __shfl_sync(0xffffffffu, upto, 31);
+  float before = __shfl_up_sync(0xffffffffu, upto, 1, 8), after = __shfl_down_sync(0xffffffffu, from, 1, 8);
+  if (at == 0) before = 0.f;
+  if (at == 7) after = 0.f;
   Tables t;
-  t.end = __shfl_sync(0xffffffffu, upto, 31);
-  float before = __shfl_up_sync(0xffffffffu, upto, 1), after = __shfl_down_sync(0xffffffffu, from, 1);
-  if (lane == 0) before = 0.f;
-  if (lane == 31) after = 0.f;
-  t.w = make_float4(exp2f(after + ((e3 + e2) + e1)) * d[0], exp2f(after + (e3 + e2)) * d[1], exp2f(after + e3) * d[2],
-                    exp2f(after) * d[3]);
+  t.end = (b0 + b1) + (b2 + b3);
+  t.gap = make_float2(block == 3 ? b1 + b2 : b1, b2);
+  const float earlier = block == 0 ? 0.f : block == 1 ? b0 : block == 2 ? b0 + b1 : (b0 + b1) + b2;
+  const float later = block == 0 ? b1 + (b2 + b3) : block == 1 ? b2 + b3 : block == 2 ? b3 : 0.f;
+  const float4 rest = make_float4(after + ((e3 + e2) + e1), after + (e3 + e2), after + e3, after);
+  const float4 s = make_float4(log2f(d[0]), log2f(d[1]), log2f(d[2]), log2f(d[3]));
+  t.w = make_float4(exp2f(later + rest.x) * d[0], exp2f(later + rest.y) * d[1], exp2f(later + rest.z) * d[2],
+                    exp2f(later + rest.w) * d[3]);
   t.L = make_float4(before + e0, before + (e0 + e1), before + ((e0 + e1) + e2), before + own);
-  t.K = make_float4(t.L.x - log2f(d[0]), t.L.y - log2f(d[1]), t.L.z - log2f(d[2]), t.L.w - log2f(d[3]));
+  t.e = make_float4(exp2f(earlier + t.L.x), exp2f(earlier + t.L.y), exp2f(earlier + t.L.z), exp2f(earlier + t.L.w));
+  t.K = make_float4(t.L.x - s.x, t.L.y - s.y, t.L.z - s.z, t.L.w - s.w);
+  t.far = make_float4(-rest.x - s.x, -rest.y - s.y, -rest.z - s.z, -rest.w - s.w);
   return t;
 }
 

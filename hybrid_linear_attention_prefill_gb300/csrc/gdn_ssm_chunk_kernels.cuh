@@ -18,7 +18,8 @@ struct Frame {
   uint32_t* tmem_slot;
   volatile int* abort_flag;
   SsmDecay* lend;  // [4 buffers][heads]: e^{L_last}
-  float* tabs;
+  float* gaps;     // [heads][4 blocks]: Tables::gap
+  float* tabs;     // [heads][L, K, far, w, e]
 };
 template <class C>
 __device__ __forceinline__ Frame make_frame(unsigned char* raw) {
@@ -29,6 +30,7 @@ __device__ __forceinline__ Frame make_frame(unsigned char* raw) {
   f.tmem_slot = reinterpret_cast<uint32_t*>(f.bars + kBars);
   f.abort_flag = reinterpret_cast<volatile int*>(f.tmem_slot + 1);
   f.lend = reinterpret_cast<SsmDecay*>(f.tmem_slot + 2);
+  f.gaps = reinterpret_cast<float*>(f.bars) + 48;  // past kBars barriers, two words and eight decays
   f.tabs = reinterpret_cast<float*>(f.sm + C::kOffTab);
   return f;
 }
@@ -289,10 +291,13 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       if (c > 0 && !wait(w_m, (uint32_t)((c - 1) & 1), 1)) break;
 #pragma unroll
       for (int hh = 0; hh < HPC; ++hh) {
-        float4* tab = reinterpret_cast<float4*>(f.tabs + hh * 3 * kQ);
+        float4* tab = reinterpret_cast<float4*>(f.tabs + hh * 5 * kQ);
         tab[lane] = t[hh].L;
         tab[32 + lane] = t[hh].K;
-        tab[64 + lane] = t[hh].w;
+        tab[64 + lane] = t[hh].far;
+        tab[96 + lane] = t[hh].w;
+        tab[128 + lane] = t[hh].e;
+        if ((lane & 7) == 0) reinterpret_cast<float2*>(f.gaps)[hh * 4 + (lane >> 3)] = t[hh].gap;
         if (lane == 0) f.lend[(c & 3) * HPC + hh] = ssm_decay(t[hh].end * 0.6931471805599453f);
       }
       __syncwarp();
@@ -399,7 +404,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       }
       XwTiles xw;
       if (32 * me.q4 < C::kRows)
-        load_xw(xw, stage + C::kOffX, f.tabs + head_of(me.row) * 3 * kQ + 2 * kQ, me.lane, 32 * me.q4, 16 * me.cg);
+        load_xw(xw, stage + C::kOffX, f.tabs + head_of(me.row) * 5 * kQ + 3 * kQ, me.lane, 32 * me.q4, 16 * me.cg);
       if (me.row < C::kRows) {
 #pragma unroll
         for (int i = 0; i < C::kSC; i += 8) {
@@ -430,7 +435,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
         const Worker me = worker();
         XwTiles xw;
         if (32 * me.q4 < C::kRows)
-          load_xw(xw, xt, f.tabs + head_of(me.row) * 3 * kQ + 2 * kQ, me.lane, 32 * me.q4, 64 + 16 * me.cg);
+          load_xw(xw, xt, f.tabs + head_of(me.row) * 5 * kQ + 3 * kQ, me.lane, 32 * me.q4, 64 + 16 * me.cg);
         if (!(ok = settle(seen_in, b_in, par, 1))) break;  // (w x)^T B of the first 64 and C S^T
         tc::fence_after();
         seen_sc = peek(b_sc, par);
@@ -448,7 +453,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       {
         const Worker me = worker();
         const uint32_t at = lanes_of(me) + kColY + C::kYC * me.cg;
-        const float e = exp2f(f.tabs[cols_of(me).h * 3 * kQ + me.row]);
+        const float e = f.tabs[cols_of(me).h * 5 * kQ + 4 * kQ + me.row];
 #pragma unroll
         for (int i0 = 0; i0 < C::kYC; i0 += 16) {
           float y[16];
@@ -471,6 +476,12 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
         const uint32_t col = lanes_of(me) + kColSc + 32 * me.cg;
         uint32_t m[8];
         if (me.cg <= me.q4) {
+          float lis[HPC];
+#pragma unroll
+          for (int hh = 0; hh < HPC; ++hh) {
+            lis[hh] = f.tabs[hh * 5 * kQ + me.row];
+            if (me.cg + 1 < me.q4) lis[hh] += f.gaps[(hh * 4 + me.q4) * 2 + me.cg];  // blocks between
+          }
 #pragma unroll 1
           for (int j0 = 0; j0 < 32; j0 += 16) {
             float sc[16];
@@ -478,12 +489,13 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
             const int upto = me.cg == me.q4 ? me.lane - j0 : 32;  // this token's last column
 #pragma unroll
             for (int hh = 0; hh < HPC; ++hh) {
-              const float* th = f.tabs + hh * 3 * kQ;
-              const float li = th[me.row];
+              const float* th = f.tabs + hh * 5 * kQ;
+              const float li = lis[hh];
+              const float* tk = th + (me.cg == me.q4 ? kQ : 2 * kQ);
               const float2 minus = make_float2(-1.f, -1.f), l2 = make_float2(li, li);
 #pragma unroll
               for (int j = 0; j < 16; j += 4) {
-                const float4 k4 = *reinterpret_cast<const float4*>(th + kQ + 32 * me.cg + j0 + j);
+                const float4 k4 = *reinterpret_cast<const float4*>(tk + 32 * me.cg + j0 + j);
                 const float2 e0 = fma2(make_float2(k4.x, k4.y), minus, l2);
                 const float2 e1 = fma2(make_float2(k4.z, k4.w), minus, l2);
                 float2 u = mul2(make_float2(sc[j], sc[j + 1]), make_float2(ex2_approx(e0.x), ex2_approx(e0.y)));

@@ -54,3 +54,39 @@ def test_a_first_calls_status_survives_what_another_stream_has_to_do(gdn):
     side.synchronize()
     rc, bits = gdn.gdn_device_status()
     assert rc == 0 and bits == gdn.GDN_STATUS_BAD_CU_SEQLENS
+
+
+# ---- strong decays --------------------------------------------------------------
+
+@pytest.mark.parametrize("dk,dv,Hk,Hv", [(64, 64, 1, 2), (128, 128, 1, 1), (32, 64, 1, 1)])
+@pytest.mark.parametrize("dt", [20.0, 50.0, 200.0, 2000.0, 1e6])
+def test_scan_long_steps(gdn, dt, dk, dv, Hk, Hv):
+    # s A of -320 to -1.6e7 a token: what is left is s_i (C_i . B_i) x_i, to the roundings of any other call
+    s = scan_inputs(gen(83), 300, 1, Hk, Hv, dk, dv, dt32=True, bias=False, init=True)
+    s["A"] = torch.full((Hv,), -16.0, device="cuda")
+    s["dt"] = dt * (0.5 + torch.rand(300, Hv, generator=gen(84))).cuda()
+    scan_check(gdn, s, 1, 300)
+
+
+@pytest.mark.parametrize("every", [0, 3, 29, 37, 64])
+@pytest.mark.parametrize("reset", [20.0, 1e4, 1e6, 1e30])
+def test_scan_resets_between_slow_decays(gdn, reset, every):
+    # single tokens of a very long step forget the state; the tokens after them decay slowly. A reset token's own
+    # input is left out, since its step would put it above all others.
+    s = scan_inputs(gen(85), 400, 1, 1, 2, 64, 64, dt32=True, bias=False, init=True)
+    s["A"] = torch.tensor([-16.0, -1.0], device="cuda")
+    at = slice(3, 4) if every == 0 else slice(1, None, every)
+    s["dt"] = torch.full((400, 2), -4.0, device="cuda") + 0.3 * rnd(gen(86), 400, 2, dtype=torch.float32)
+    s["dt"][at] = reset
+    s["x"][at] = 0
+    scan_check(gdn, s, 1, 400)
+
+
+def test_scan_nan_step_reaches_later_tokens_only(gdn):
+    # in its chunk and after it, the chunk's tokens before it left as they are
+    s = scan_inputs(gen(87), 200, 1, 1, 1, 64, 64, dt32=True, bias=False)
+    ref, _ = gdn.ssm_scan(**s)
+    s["dt"][140] = float("nan")
+    out, fin = gdn.ssm_scan(**s)
+    assert torch.equal(out[:140], ref[:140])
+    assert bool(out[140:].isnan().all()) and bool(fin.isnan().all())
