@@ -244,9 +244,10 @@ __device__ __forceinline__ void to_steps(const SsmArgs& a, int n, float bias, in
 // the difference of two sums over more than 32 tokens, since it would carry the rounding of what it does not contain
 // (a strong decay's large L, before a pair of tokens whose own decay is weak).  With the chunk in blocks of 32 tokens,
 // M's exponent L_i - L_j + log2 s_j is
-//   L - K          in one block, L inclusive of a token's own decay and from its block's start, K = L - log2 s;
+//   L - K          in one block, L inclusive of a token's own decay and from its block's start, K = L - log2 |s|;
 //   L + gap - far  between blocks, the gap the sum over the blocks between, far = -(the sum after j in its block)
-//                  - log2 s_j.
+//                  - log2 |s_j|.
+// A step below zero (there are none with softplus) leaves its sign to M and has it in w, a zero w too.
 // The weights' exponents are sums over the tokens after each, from the chunk's end.  A token's decay below 2^-160 is 0
 // in fp32 and counts as 2^-160, which keeps L above -5,120: its rounding (2^-12) stays below that of M to bf16 (2^-9).
 struct Tables {
@@ -278,14 +279,23 @@ __device__ __forceinline__ Tables make_tables(const float (&d)[4], float a_log2,
   const float earlier = block == 0 ? 0.f : block == 1 ? b0 : block == 2 ? b0 + b1 : (b0 + b1) + b2;
   const float later = block == 0 ? b1 + (b2 + b3) : block == 1 ? b2 + b3 : block == 2 ? b3 : 0.f;
   const float4 rest = make_float4(after + ((e3 + e2) + e1), after + (e3 + e2), after + e3, after);
-  const float4 s = make_float4(log2f(d[0]), log2f(d[1]), log2f(d[2]), log2f(d[3]));
+  const float4 size = make_float4(log2f(fabsf(d[0])), log2f(fabsf(d[1])), log2f(fabsf(d[2])), log2f(fabsf(d[3])));
   t.w = make_float4(exp2f(later + rest.x) * d[0], exp2f(later + rest.y) * d[1], exp2f(later + rest.z) * d[2],
                     exp2f(later + rest.w) * d[3]);
   t.L = make_float4(before + e0, before + (e0 + e1), before + ((e0 + e1) + e2), before + own);
   t.e = make_float4(exp2f(earlier + t.L.x), exp2f(earlier + t.L.y), exp2f(earlier + t.L.z), exp2f(earlier + t.L.w));
-  t.K = make_float4(t.L.x - s.x, t.L.y - s.y, t.L.z - s.z, t.L.w - s.w);
-  t.far = make_float4(-rest.x - s.x, -rest.y - s.y, -rest.z - s.z, -rest.w - s.w);
+  t.K = make_float4(t.L.x - size.x, t.L.y - size.y, t.L.z - size.z, t.L.w - size.w);
+  t.far = make_float4(-rest.x - size.x, -rest.y - size.y, -rest.z - size.z, -rest.w - size.w);
   return t;
+}
+
+// Sixteen bf16, their signs turned where those of w (in shared memory) are set.
+__device__ __forceinline__ void turn_signs(uint32_t (&m)[8], const float* w) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint2 s = *reinterpret_cast<const uint2*>(w + 2 * j);
+    m[j] ^= ((s.x & 0x80000000u) >> 16) | (s.y & 0x80000000u);
+  }
 }
 
 // x of sixteen tokens t .. t + 15 and state rows row0 .. + 31 as a warp multiplies it by w (in shared memory beside

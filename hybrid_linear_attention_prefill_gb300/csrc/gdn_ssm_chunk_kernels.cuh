@@ -507,6 +507,7 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                 m[j / 2] = pack_bf16(u.x, u.y);
                 m[j / 2 + 1] = pack_bf16(v.x, v.y);
               }
+              if (!a.softplus) turn_signs(m, th + 3 * kQ + 32 * me.cg + j0);
               tmem_st8_nowait(col + j0 + 8 * hh, m);
             }
           }

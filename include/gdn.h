@@ -424,9 +424,8 @@ int gdn_conv_step(const gdn_conv_step_args *args);
  * dk and dv are 32, 64 or 128 each.  A sequence's results do not depend on the values of other
  * sequences of a packed batch, infinities and NaN included.  Within a sequence the tokens are
  * worked on in chunks of 128 with products of matrices, so a value that is not finite makes the
- * outputs of its chunk before it not finite too.  Steps are not negative (as softplus makes them;
- * without it a negative dt + dt_bias gives NaN); a decay rate A above 0 grows the state and may
- * overflow.
+ * outputs of its chunk before it not finite too.  Without softplus a step may be below zero; like a
+ * decay rate A above 0 it grows the state, which may overflow.
  *
  * workspace: gdn_ssm_workspace_bytes(...) bytes of device memory, 256-byte aligned, not shared
  * with concurrent calls, or NULL for the library's own grow-only one (shared by the calls on a

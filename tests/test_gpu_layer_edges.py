@@ -56,7 +56,7 @@ def test_a_first_calls_status_survives_what_another_stream_has_to_do(gdn):
     assert rc == 0 and bits == gdn.GDN_STATUS_BAD_CU_SEQLENS
 
 
-# ---- strong decays --------------------------------------------------------------
+# ---- strong decays, steps below zero --------------------------------------------------------------
 
 @pytest.mark.parametrize("dk,dv,Hk,Hv", [(64, 64, 1, 2), (128, 128, 1, 1), (32, 64, 1, 1)])
 @pytest.mark.parametrize("dt", [20.0, 50.0, 200.0, 2000.0, 1e6])
@@ -90,3 +90,17 @@ def test_scan_nan_step_reaches_later_tokens_only(gdn):
     out, fin = gdn.ssm_scan(**s)
     assert torch.equal(out[:140], ref[:140])
     assert bool(out[140:].isnan().all()) and bool(fin.isnan().all())
+
+
+@pytest.mark.parametrize("dk,dv,Hk,Hv", [(64, 64, 1, 2), (128, 128, 2, 2), (32, 32, 1, 1), (128, 64, 1, 2)])
+@pytest.mark.parametrize("T", [1, 140, 1500])
+def test_scan_steps_below_zero(gdn, dk, dv, Hk, Hv, T):
+    # without softplus a step may be below zero: prompts and single tokens agree with the formula
+    s = scan_inputs(gen(88), T, 1, Hk, Hv, dk, dv, bias=False, dt32=True, init=True)
+    s["dt"] *= 0.1
+    out, fin = scan_check(gdn, s, 1, T, softplus=False)
+    if T == 140:
+        st = s["init_state"].clone()
+        for t in range(5):
+            y = gdn.ssm_step(**rows_of(s, slice(t, t + 1)), state=st, softplus=False)
+            assert float((y - out[t:t + 1]).abs().max()) <= 2.0 ** -5 * float(out.abs().max())
