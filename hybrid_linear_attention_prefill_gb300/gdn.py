@@ -62,7 +62,8 @@ EXPORTED = ("gdn_abi_version", "gdn_strerror", "gdn_last_cuda_error", "gdn_prefi
 
 _lock = threading.Lock()
 _lib = None
-_fast = None  # the gdn_torch module: the tensor wrappers' common case in C++
+_UNTRIED = object()
+_fast = _UNTRIED  # the gdn_torch module (the tensor functions' common case in C++), or None where there is none
 
 
 class GdnError(RuntimeError):
@@ -79,7 +80,7 @@ def library_path() -> str:
 
 def load(build_if_missing: bool = False):
     """Load libgdn.so (optionally building it first) and declare the signatures."""
-    global _lib, _fast
+    global _lib
     if _lib is not None:
         return _lib
     with _lock:
@@ -133,22 +134,37 @@ def load(build_if_missing: bool = False):
             getattr(lib, name).restype = i
         lib.gdn_release_workspace.argtypes = []
         lib.gdn_release_workspace.restype = None
-        _fast = _load_fast()
         _lib = lib
         return lib
 
 
+def _shorter():
+    """The gdn_torch module, loaded at a tensor function's first call (the other entries need no PyTorch), or None
+    where it was not built or does not load: the tensor functions then check in Python."""
+    global _fast
+    if _fast is _UNTRIED:
+        load()
+        with _lock:
+            if _fast is _UNTRIED:
+                _fast = _load_fast()
+    return _fast
+
+
 def _load_fast():
-    """The gdn_torch module next to the library, or None where it was not built."""
     if not os.path.exists(_build.TORCH_LIB):
         return None
     import importlib.util
+    import warnings
 
     import torch  # noqa: F401  (its libraries have to be there first)
 
-    spec = importlib.util.spec_from_file_location("gdn_torch", _build.TORCH_LIB)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    try:
+        spec = importlib.util.spec_from_file_location("gdn_torch", _build.TORCH_LIB)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except (ImportError, OSError) as e:
+        warnings.warn(f"{_build.TORCH_LIB} does not load ({e}): the tensor functions check in Python")
+        return None
     return module
 
 
@@ -468,9 +484,9 @@ def causal_conv(x, weight, bias=None, cu_seqlens=None, init_state=None, *, B=Non
     init_state: bf16 [B, K-1, C], the inputs before each sequence, oldest first.  Returns (out bf16
     [Ttot, C], final_state bf16 [B, K-1, C] or None), in `out` and `final_state` where given.
     """
-    load()
-    if _fast is not None and out is not None and (final_state is not None or not want_final):
-        rc = _fast.causal_conv(x, weight, bias, cu_seqlens, init_state, B, silu, out, final_state, stream)
+    fast = _shorter()
+    if fast is not None and out is not None and (final_state is not None or not want_final):
+        rc = fast.causal_conv(x, weight, bias, cu_seqlens, init_state, B, silu, out, final_state, stream)
         if rc is not None:
             if rc:
                 check(rc)
@@ -496,9 +512,9 @@ def causal_conv(x, weight, bias=None, cu_seqlens=None, init_state=None, *, B=Non
 
 def causal_conv_step(x, weight, state, bias=None, *, silu=True, out=None, stream=None):
     """One token of each of B sequences: x bf16 [B, C]; state bf16 [B, K-1, C], updated in place."""
-    load()
-    if _fast is not None and out is not None:
-        rc = _fast.causal_conv_step(x, weight, state, bias, silu, out, stream)
+    fast = _shorter()
+    if fast is not None and out is not None:
+        rc = fast.causal_conv_step(x, weight, state, bias, silu, out, stream)
         if rc is not None:
             if rc:
                 check(rc)
@@ -550,9 +566,9 @@ def ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, cu_seqlens=None, in
     `workspace`: a byte tensor of gdn_ssm_workspace_bytes(...), for calls that overlap or are captured.
     Returns (out bf16 [Ttot, Hv, dv], final_state fp32 [B, Hv, dv, dk] or None).
     """
-    load()
-    if _fast is not None and out is not None and (final_state is not None or not want_final):
-        rc = _fast.ssm_scan(x, dt, A, Bm, Cm, D, z, dt_bias, cu_seqlens, init_state, B, softplus, out, final_state,
+    fast = _shorter()
+    if fast is not None and out is not None and (final_state is not None or not want_final):
+        rc = fast.ssm_scan(x, dt, A, Bm, Cm, D, z, dt_bias, cu_seqlens, init_state, B, softplus, out, final_state,
                             workspace, stream)
         if rc is not None:
             if rc:
@@ -579,9 +595,9 @@ def ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, cu_seqlens=None, in
 
 def ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softplus=True, out=None, stream=None):
     """One token of each of B sequences of the scan: state fp32 [B, Hv, dv, dk], updated in place."""
-    load()
-    if _fast is not None and out is not None:
-        rc = _fast.ssm_step(x, dt, A, Bm, Cm, state, D, z, dt_bias, softplus, out, stream)
+    fast = _shorter()
+    if fast is not None and out is not None:
+        rc = fast.ssm_step(x, dt, A, Bm, Cm, state, D, z, dt_bias, softplus, out, stream)
         if rc is not None:
             if rc:
                 check(rc)
@@ -604,9 +620,9 @@ def add_norm(x, weight, residual=None, *, eps=1e-6, group=0, e4m3=False, out=Non
     `e4m3` follows from `out` where that is given.  Returns (out, scales or None, residual_out or None);
     residual_out may be `residual` itself.
     """
-    load()
-    if _fast is not None and out is not None and (residual is None or residual_out is not None):
-        rc = _fast.add_norm(x, weight, residual, eps, group, out, scales, residual_out, stream)
+    fast = _shorter()
+    if fast is not None and out is not None and (residual is None or residual_out is not None):
+        rc = fast.add_norm(x, weight, residual, eps, group, out, scales, residual_out, stream)
         if rc is not None:
             if rc:
                 check(rc)

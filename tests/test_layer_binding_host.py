@@ -1,11 +1,17 @@
 """What the tensor functions of the operators around the recurrence see to on the host: checks before any GPU work,
 the device of a call, and the library's loading (CPU only)."""
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 from hybrid_linear_attention_prefill_gb300 import build as B
 from hybrid_linear_attention_prefill_gb300 import gdn
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -109,3 +115,37 @@ def test_a_stream_of_another_device_is_refused():
     with pytest.raises(ValueError, match="stream"):
         gdn._raw_stream(Stream(), 0)
     assert gdn._raw_stream(Stream(), 1) == 5 and gdn._raw_stream(7, 0) == 7
+
+
+# ---- loading ------------------------------------------------------------------------------------
+
+def run_python(code):
+    return subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+
+
+def test_the_library_loads_without_pytorch():
+    r = run_python("import sys; sys.modules['torch'] = None\n"
+                   "from hybrid_linear_attention_prefill_gb300 import gdn\n"
+                   "gdn.load(); print(gdn.gdn_abi_version(), gdn.gdn_prefill(0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 1, 1, 32, "
+                   "32, 0))")
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.split() == [str(gdn.gdn_abi_version()), "0"]
+
+
+def test_loading_the_library_does_not_import_pytorch():
+    r = run_python("import sys\nfrom hybrid_linear_attention_prefill_gb300 import gdn\n"
+                   "gdn.load(); print('torch' in sys.modules)")
+    assert r.returncode == 0 and r.stdout.split() == ["False"], r.stderr
+
+
+@pytest.mark.parametrize("content", [b"", b"no shared object"])
+def test_the_tensor_functions_do_without_a_module_that_does_not_load(tmp_path, content):
+    bad = tmp_path / "gdn_torch.so"
+    bad.write_bytes(content)
+    r = run_python("import torch\nfrom hybrid_linear_attention_prefill_gb300 import build, gdn\n"
+                   f"build.TORCH_LIB = {str(bad)!r}\nbuild.torch_lib = lambda: {str(bad)!r}\n"
+                   "gdn.load(); z = torch.zeros\n"
+                   "try: gdn.add_norm(z(2, 8).bfloat16(), z(8).bfloat16(), out=z(2, 8).bfloat16())\n"
+                   "except ValueError as e: print(e)")
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.strip() == "CUDA tensors are wanted"  # what the checks in Python say to host tensors
