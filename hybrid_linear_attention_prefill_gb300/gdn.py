@@ -151,19 +151,18 @@ def _shorter():
 
 
 def _load_fast():
-    if not os.path.exists(_build.TORCH_LIB):
-        return None
     import importlib.util
     import warnings
 
-    import torch  # noqa: F401  (its libraries have to be there first)
-
+    path = _build.torch_lib()  # (PyTorch's libraries have to be there first)
+    if not os.path.exists(path):
+        return None
     try:
-        spec = importlib.util.spec_from_file_location("gdn_torch", _build.TORCH_LIB)
+        spec = importlib.util.spec_from_file_location("gdn_torch", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
     except (ImportError, OSError) as e:
-        warnings.warn(f"{_build.TORCH_LIB} does not load ({e}): the tensor functions check in Python")
+        warnings.warn(f"{path} does not load ({e}): the tensor functions check in Python")
         return None
     return module
 

@@ -149,3 +149,48 @@ def test_the_tensor_functions_do_without_a_module_that_does_not_load(tmp_path, c
                    "except ValueError as e: print(e)")
     assert r.returncode == 0, r.stderr
     assert r.stdout.strip() == "CUDA tensors are wanted"  # what the checks in Python say to host tensors
+
+
+def test_the_module_is_of_this_interpreter_and_this_pytorch(monkeypatch):
+    """Built against another PyTorch it could load and read its objects wrongly: its name says what it is for."""
+    path = B.torch_lib()
+    assert os.path.exists(path) and not B.module_needs_build()
+    monkeypatch.setattr(torch, "__version__", "2.0.0+other")
+    assert B.torch_lib() != path and B.module_needs_build() and not B.needs_build()
+    monkeypatch.setattr(gdn, "_fast", gdn._UNTRIED)
+    assert gdn._shorter() is None  # there is none for that PyTorch
+
+
+def test_only_the_module_is_built_for_another_pytorch(monkeypatch, tmp_path):
+    calls = []
+
+    def run(cmd, **kw):
+        calls.append(cmd)
+        if "-o" in cmd:
+            open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(B, "torch_lib", lambda: str(tmp_path / "gdn_torch.other.so"))
+    monkeypatch.setattr(subprocess, "run", run)
+    was = os.path.getmtime(B.LIB)
+    B.build()
+    assert [os.path.basename(c[0]) for c in calls] == ["g++", "g++"] and os.path.getmtime(B.LIB) == was
+    B.build()
+    assert len(calls) == 2  # it is there
+
+
+def test_a_module_that_does_not_build_is_not_tried_at_every_call(monkeypatch, tmp_path, capsys):
+    calls = []
+
+    def run(cmd, **kw):
+        calls.append(cmd)
+        return subprocess.CompletedProcess(cmd, 1, "", "no headers")
+
+    path = tmp_path / "gdn_torch.other.so"
+    path.touch()
+    os.utime(path, (0, 0))  # older than its source
+    monkeypatch.setattr(B, "torch_lib", lambda: str(path))
+    monkeypatch.setattr(subprocess, "run", run)
+    B.build()
+    B.build()
+    assert len(calls) == 1 and not path.exists() and "check in Python" in capsys.readouterr().out
