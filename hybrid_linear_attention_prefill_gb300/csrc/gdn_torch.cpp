@@ -71,10 +71,18 @@ struct Call {
     }
     return PyLong_AsVoidPtr(o);
   }
-  bool flag(int i) const { return PyObject_IsTrue(argv[i]) == 1; }
+  bool flag(int i) {
+    const int yes = PyObject_IsTrue(argv[i]);
+    if (yes < 0) ok = false;
+    return yes == 1;
+  }
 };
 
-PyObject* none() { Py_RETURN_NONE; }
+// Left to the Python checks, which meet the same arguments and raise for themselves.
+PyObject* none() {
+  PyErr_Clear();
+  Py_RETURN_NONE;
+}
 
 // A C++ exception does not cross into the interpreter: what it was is for the Python checks to say.
 template <class F>

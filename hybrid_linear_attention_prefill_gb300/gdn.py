@@ -446,6 +446,7 @@ def _plain(t, name, dtype, shape, dev) -> int:
 
 def _rows(t, name, dtype, shape, dev) -> int:
     """Row stride of a tensor of this shape whose rows are contiguous (a slice of a wider one may be)."""
+    _want(max(shape) <= 0x7fffffff, f"{name}: sizes are 32-bit, got {tuple(shape)}")
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         raise ValueError(f"{name}: a {dtype} tensor of shape {shape} on the device of x is wanted, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
@@ -466,7 +467,7 @@ def _batch(n, cu_seqlens, B, dev):
     """(sequences, tokens per sequence or in all, boundaries' address) of a dense or packed batch of n rows."""
     if cu_seqlens is None:
         B = 1 if B is None else int(B)
-        _want(B >= 0 and (n % B == 0 if B else n == 0), "the tokens have to divide into B sequences")
+        _want(0 <= B <= 0x7fffffff and (n % B == 0 if B else n == 0), "the tokens have to divide into B sequences")
         return B, n // B if B else 0, 0
     import torch
 
@@ -630,6 +631,7 @@ def add_norm(x, weight, residual=None, *, eps=1e-6, group=0, e4m3=False, out=Non
 
     bf16, f8 = torch.bfloat16, torch.float8_e4m3fn
     _want(x.dim() == 2, "x: [rows, D]")
+    _want(0 <= group <= 0x7fffffff, f"group: 0, 32, 64 or 128 columns, got {group}")
     rows, D = shape = x.shape
     dev = x.get_device()
     xs = _rows(x, "x", bf16, shape, dev)

@@ -56,6 +56,38 @@ def test_a_first_calls_status_survives_what_another_stream_has_to_do(gdn):
     assert rc == 0 and bits == gdn.GDN_STATUS_BAD_CU_SEQLENS
 
 
+# ---- arguments ----------------------------------------------------------------------------------
+
+def test_arguments_beyond_their_range_are_refused(gdn):
+    """The same errors by both ways through the binding, and the object's own where it has no truth value."""
+    class Neither:
+        def __bool__(self):
+            raise KeyError("neither")
+
+    x, w, st = rnd(gen(76), 8, 64), rnd(gen(77), 64, 4), rnd(gen(78), 8, 3, 64)
+    s = scan_inputs(gen(79), 8, 1, 1, 1, 64, 64)
+    o, so = torch.empty_like(x), torch.empty_like(s["x"])
+    q = torch.empty(8, 64, dtype=torch.float8_e4m3fn, device="cuda")
+    state = torch.zeros(8, 1, 64, 64, device="cuda")
+    for out in (None, 1):
+        kw = dict(want_final=False)
+        for n in (2 ** 70, 2 ** 32 + 1, -1, -2 ** 70):
+            with pytest.raises(ValueError):
+                gdn.causal_conv(x, w, B=n, out=out and o, **kw)
+            with pytest.raises(ValueError):
+                gdn.ssm_scan(**{**s, "init_state": None}, B=n, out=out and so, **kw)
+            with pytest.raises((ValueError, gdn.GdnError)):
+                gdn.add_norm(x, w[:, 0].contiguous(), group=n, e4m3=True, out=out and q)
+        with pytest.raises(KeyError):
+            gdn.causal_conv(x, w, silu=Neither(), out=out and o, **kw)
+        with pytest.raises(KeyError):
+            gdn.causal_conv_step(x, w, st, silu=Neither(), out=out and o)
+        with pytest.raises(KeyError):
+            gdn.ssm_scan(**s, softplus=Neither(), out=out and so, **kw)
+        with pytest.raises(KeyError):
+            gdn.ssm_step(**rows_of(s, slice(0, 8)), state=state, softplus=Neither(), out=out and so)
+
+
 # ---- strong decays, steps below zero --------------------------------------------------------------
 
 @pytest.mark.parametrize("dk,dv,Hk,Hv", [(64, 64, 1, 2), (128, 128, 1, 1), (32, 64, 1, 1)])

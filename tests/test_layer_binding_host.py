@@ -194,3 +194,20 @@ def test_a_module_that_does_not_build_is_not_tried_at_every_call(monkeypatch, tm
     B.build()
     B.build()
     assert len(calls) == 1 and not path.exists() and "check in Python" in capsys.readouterr().out
+
+
+# ---- ranges -------------------------------------------------------------------------------------
+
+def test_sizes_beyond_32_bits_are_refused(entries):
+    bf, z = torch.bfloat16, torch.zeros
+    many = z(1, 64, dtype=bf).expand(2 ** 31, 64)
+    x, w, st = z(8, 64, dtype=bf), z(64, 4, dtype=bf), z(8, 3, 64, dtype=bf)
+    none = z(0, 64, dtype=bf)
+    for call in (lambda: gdn.causal_conv(many, w), lambda: gdn.causal_conv_step(many, w, st),
+                 lambda: gdn.add_norm(many, w[:, 0]), lambda: gdn.causal_conv(none, w, B=2 ** 31),
+                 lambda: gdn.causal_conv(x, w, B=2 ** 70), lambda: gdn.add_norm(x, z(64, dtype=bf), group=2 ** 31),
+                 lambda: gdn.add_norm(x, z(64, dtype=bf), e4m3=True, group=-1),
+                 lambda: gdn.ssm_scan(**{**scan_operands(), "x": z(1, 4, 64, dtype=bf).expand(2 ** 31, 4, 64)})):
+        with pytest.raises(ValueError):
+            call()
+    assert entries.calls == []
