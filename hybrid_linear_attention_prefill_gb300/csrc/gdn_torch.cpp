@@ -243,6 +243,7 @@ PyObject* norm(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     a.weight = c.plain(1, kBf16, {D});
     a.residual = c.plain(2, kBf16, {rows, D}, true);
     a.out = c.plain(5, e4m3 ? at::ScalarType::Float8_e4m3fn : kBf16, {rows, D});
+    if (!e4m3 && argv[6] != Py_None) return none();  // scales that the call does not write
     if (e4m3) a.scales = static_cast<float*>(c.plain(6, kF32, {rows, group ? (D + group - 1) / group : 1}));
     a.residual_out = c.plain(7, kBf16, {rows, D}, true);
     a.rows = (int)rows;

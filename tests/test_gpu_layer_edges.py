@@ -88,6 +88,15 @@ def test_arguments_beyond_their_range_are_refused(gdn):
             gdn.ssm_step(**rows_of(s, slice(0, 8)), state=state, softplus=Neither(), out=out and so)
 
 
+def test_norm_returns_no_scales_with_a_bf16_output(gdn, monkeypatch):
+    x, w = rnd(gen(80), 4, 64), rnd(gen(81), 64)
+    sc = torch.full((4, 1), 7.0, device="cuda")
+    for _ in range(2):
+        out, none, _ = gdn.add_norm(x, w, scales=sc, out=torch.empty_like(x))
+        assert none is None and bool((sc == 7).all())
+        monkeypatch.setattr(gdn, "_fast", None)
+
+
 # ---- strong decays, steps below zero --------------------------------------------------------------
 
 @pytest.mark.parametrize("dk,dv,Hk,Hv", [(64, 64, 1, 2), (128, 128, 1, 1), (32, 64, 1, 1)])
