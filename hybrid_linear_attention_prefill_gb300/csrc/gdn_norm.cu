@@ -157,7 +157,7 @@ static cudaError_t add_norm_v(const void* x, long long xs, const void* residual,
                               float eps, bool e4m3, cudaStream_t st) {
   using bf = __nv_bfloat16;
   const int threads = tpr < kNormMinThreads ? kNormMinThreads : tpr;
-  const unsigned grid = (unsigned)((rows + threads / tpr - 1) / (threads / tpr));
+  const unsigned grid = (unsigned)(((long long)rows + threads / tpr - 1) / (threads / tpr));
   const int ngroups = group ? (D + group - 1) / group : 1;
   const int gshift = group == 32 ? 2 : group == 64 ? 3 : group == 128 ? 4 : kRowShift;
   const float inv_d = 1.f / (float)D;

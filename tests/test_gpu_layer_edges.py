@@ -97,6 +97,18 @@ def test_norm_returns_no_scales_with_a_bf16_output(gdn, monkeypatch):
         monkeypatch.setattr(gdn, "_fast", None)
 
 
+def test_norm_of_nearly_2_to_the_31_rows(gdn):
+    rows = 2 ** 31 - 1
+    x = torch.zeros(rows, 8, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(8, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = rnd(gen(82), 3, 8)
+    out, _, _ = gdn.add_norm(x, w, out=torch.full_like(x, 7.0))
+    assert torch.equal(out[-3:], gdn.add_norm(x[-3:], w)[0]) and not bool(out[:1000].any())
+    assert not bool(out[2 ** 30:2 ** 30 + 1000].any())
+    del x, out
+    torch.cuda.empty_cache()
+
+
 # ---- strong decays, steps below zero --------------------------------------------------------------
 
 @pytest.mark.parametrize("dk,dv,Hk,Hv", [(64, 64, 1, 2), (128, 128, 1, 1), (32, 64, 1, 1)])
