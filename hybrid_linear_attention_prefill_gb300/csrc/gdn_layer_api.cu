@@ -15,6 +15,7 @@ cudaError_t launch_add_norm(const void*, long long, const void*, const void*, vo
                             float, bool, cudaStream_t);
 cudaError_t launch_ssm_step(const SsmArgs&, float*, int, int, cudaStream_t);
 size_t ssm_scan_workspace(int, int, int, int, int, int, int);
+int ssm_scan_polls(int);
 cudaError_t launch_ssm_scan(const SsmArgs&, const int32_t*, const float*, float*, void*, int, int, int, cudaStream_t);
 }  // namespace gdn
 
@@ -136,6 +137,8 @@ size_t gdn_ssm_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv, int
   if (!ssm_sizes_ok(B, T, Hk, Hv, dk, dv)) return 0;
   return gdn::ssm_scan_workspace(B, T, Hk, Hv, dk, dv, packed);
 }
+
+int gdn_debug_ssm_wait_polls(int polls) { return gdn::ssm_scan_polls(polls); }
 
 int gdn_ssm_scan(const gdn_ssm_scan_args* args) {
   gdn::clear_cuda_error();

@@ -61,6 +61,7 @@ struct Segs {
   int len;     // chunks a segment (0: whole sequences)
   int slots;   // segments of the grid
   int joined;  // the stored states are start states (else the segments' sums)
+  uint32_t polls;  // of a wait, kMaxPolls but in tests (the output pass's whole-warp waits have the constant)
 };
 
 struct Seg {
@@ -156,7 +157,7 @@ struct Cfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 };
 
-constexpr uint32_t kMaxPolls = 1u << 22;  // of a wait; then it gives up
+constexpr uint32_t kMaxPolls = 1u << 18;  // of a wait, 3.7 us each: about a second; then it gives up
 
 // A worker thread's place, worked out anew where it is used: kept from one use to the next it would not fit the
 // registers, and with so little of the SM's memory left as L1 a spilled value comes back from L2.

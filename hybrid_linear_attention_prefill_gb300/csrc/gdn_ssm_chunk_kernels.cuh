@@ -168,11 +168,13 @@ gdn_ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
   const bool gate = a.z != nullptr;
   int gave_up = 0;  // the status bit of the wait that this warp gave up
   auto wait1 = [&](uint64_t* bar, uint32_t par, int bit) {
-    const bool done = tc::mbar_wait(bar, par, kMaxPolls);
+    const bool done = tc::mbar_wait(bar, par, g.polls);
     if (!done) gave_up = bit;
     return done;
   };
-  auto wait = [&](uint64_t* bar, uint32_t par, int bit) {  // a whole warp, together and of one mind after it
+  // A whole warp, together and of one mind after it.  (With the limit from the parameters in these loops 32 ragged
+  // prompts take 562 us, with the constant 553.)
+  auto wait = [&](uint64_t* bar, uint32_t par, int bit) {
     const bool done = __all_sync(0xffffffffu, tc::mbar_wait(bar, par, kMaxPolls)) != 0;
     if (!done) gave_up = bit;
     return done;
@@ -712,12 +714,12 @@ gdn_ssm_segment_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
   const uint32_t tmem = *f.tmem_slot;
   int gave_up = 0;  // the status bit of the wait that this warp gave up
   auto wait1 = [&](uint64_t* bar, uint32_t par, int bit) {
-    const bool done = tc::mbar_wait(bar, par, kMaxPolls);
+    const bool done = tc::mbar_wait(bar, par, g.polls);
     if (!done) gave_up = bit;
     return done;
   };
   auto wait = [&](uint64_t* bar, uint32_t par, int bit) {  // a whole warp, together and of one mind after it
-    const bool done = __all_sync(0xffffffffu, tc::mbar_wait(bar, par, kMaxPolls)) != 0;
+    const bool done = __all_sync(0xffffffffu, tc::mbar_wait(bar, par, g.polls)) != 0;
     if (!done) gave_up = bit;
     return done;
   };

@@ -7,6 +7,7 @@
 // from the sums before it (with many segments gdn_ssm_join_kernel makes start states of them first).  The
 // later kernels are programmatic dependents: they set up beside the one before.
 #include <algorithm>
+#include <atomic>
 
 #include "../../include/gdn.h"
 #include "gdn_internal.h"
@@ -26,6 +27,8 @@ namespace {
 
 constexpr int kJoinThreads = 128;
 constexpr int kAloneSegs = 8;  // segments a sequence that the output pass goes through by itself
+
+std::atomic<int> g_polls{(int)ssm::kMaxPolls};
 
 struct Plan {
   int hpc = 1;    // heads a CTA
@@ -154,6 +157,8 @@ bool token_map(CUtensorMap* m, const void* base, long long stride, long long wid
 
 }  // namespace
 
+int ssm_scan_polls(int polls) { return g_polls.exchange(polls < 0 ? (int)ssm::kMaxPolls : polls); }
+
 size_t ssm_scan_workspace(int B, int T, int Hk, int Hv, int dk, int dv, int packed) {
   const int sms = device_sms();
   // without a device: enough for any (a segment of one chunk for every chunk)
@@ -191,6 +196,7 @@ cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* in
   g.T = T;
   g.len = p.len;
   g.slots = p.slots;
+  g.polls = (uint32_t)g_polls.load(std::memory_order_relaxed);
   // With few segments a sequence the output pass goes through the sums before its own by itself (about 0.8 us each,
   // beside its first tiles' load); more are joined by a kernel (about 5 us).
   const int per = p.len * ssm::kQ;

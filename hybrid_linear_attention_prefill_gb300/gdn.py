@@ -58,7 +58,7 @@ EXPORTED = ("gdn_abi_version", "gdn_strerror", "gdn_last_cuda_error", "gdn_prefi
             "gdn_set_phase_events", "gdn_workspace_bytes", "gdn_scan_segments", "gdn_release_workspace",
             "gdn_device_status", "gdn_selftest_wait_timeout", "gdn_selftest_static_wait_timeout",
             "gdn_debug_fail_allocations", "gdn_conv", "gdn_conv_step", "gdn_ssm_scan", "gdn_ssm_workspace_bytes",
-            "gdn_ssm_step", "gdn_add_norm")
+            "gdn_debug_ssm_wait_polls", "gdn_ssm_step", "gdn_add_norm")
 
 _lock = threading.Lock()
 _lib = None
@@ -127,6 +127,8 @@ def load(build_if_missing: bool = False):
         lib.gdn_selftest_static_wait_timeout.restype = i
         lib.gdn_debug_fail_allocations.argtypes = [i]
         lib.gdn_debug_fail_allocations.restype = i
+        lib.gdn_debug_ssm_wait_polls.argtypes = [i]
+        lib.gdn_debug_ssm_wait_polls.restype = i
         lib.gdn_ssm_workspace_bytes.argtypes = [i] * 7
         lib.gdn_ssm_workspace_bytes.restype = ctypes.c_size_t
         for name in ("gdn_conv", "gdn_conv_step", "gdn_ssm_scan", "gdn_ssm_step", "gdn_add_norm"):
@@ -242,6 +244,11 @@ def gdn_selftest_static_wait_timeout(max_polls) -> int:
 def gdn_debug_fail_allocations(count) -> int:
     """Make the library's next `count` device allocations fail; returns the pending count."""
     return load().gdn_debug_fail_allocations(int(count))
+
+
+def gdn_debug_ssm_wait_polls(polls) -> int:
+    """How often a wait of the selective scan's kernels looks before it gives up; returns the limit before."""
+    return load().gdn_debug_ssm_wait_polls(int(polls))
 
 
 def gdn_release_workspace() -> None:

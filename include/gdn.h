@@ -464,6 +464,15 @@ int gdn_ssm_scan(const gdn_ssm_scan_args *args);
 size_t gdn_ssm_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv, int packed);
 
 /*
+ * gdn_debug_ssm_wait_polls -- test hook for the waits of gdn_ssm_scan's kernels: how often the
+ * thread that issues copies and products looks before it gives up (0: at once; negative: the
+ * usual limit, about a second; what waits for that thread keeps this one).  A call whose waits
+ * give up ends, with GDN_STATUS_MMA_TIMEOUT or GDN_STATUS_LOAD_TIMEOUT in its status word and
+ * nothing to be read in its outputs.  Returns the limit before.  Needs no GPU.
+ */
+int gdn_debug_ssm_wait_polls(int polls);
+
+/*
  * gdn_ssm_step -- gdn_ssm_scan for one token per sequence (x, z, out [B, Hv, dv], dt [B, Hv],
  * Bm, Cm [B, Hk, dk]); state fp32 [B, Hv, dv, dk], 16-byte aligned, updated in place.
  */

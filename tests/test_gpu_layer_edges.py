@@ -109,6 +109,30 @@ def test_norm_of_nearly_2_to_the_31_rows(gdn):
     torch.cuda.empty_cache()
 
 
+# ---- waits that run out ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,Hv,dk,dv", [(100, 1, 64, 64), (300, 2, 128, 32), (1000, 1, 128, 128),
+                                        (6000, 2, 32, 128)])
+def test_scan_whose_waits_run_out_ends_and_says_so(gdn, T, Hv, dk, dv):
+    """The issuing threads give up at once, copies in flight, and what waits for them after its own limit: in one
+    pass, two and three."""
+    s = scan_inputs(gen(89), T, 1, 1, Hv, dk, dv, init=True)
+    ref = gdn.ssm_scan(**s)
+    timeouts = gdn.GDN_STATUS_MMA_TIMEOUT | gdn.GDN_STATUS_LOAD_TIMEOUT
+    assert gdn.gdn_device_status() == (0, 0)
+    usual = gdn.gdn_debug_ssm_wait_polls(0)
+    try:
+        gdn.ssm_scan(**s)
+        rc, bits = gdn.gdn_device_status()
+        assert rc == 0 and bits & timeouts and not bits & ~timeouts
+    finally:
+        assert gdn.gdn_debug_ssm_wait_polls(-1) == 0
+    assert gdn.gdn_debug_ssm_wait_polls(usual) == usual
+    again = gdn.ssm_scan(**s)
+    assert torch.equal(again[0], ref[0]) and torch.equal(again[1], ref[1])
+    assert gdn.gdn_device_status() == (0, 0)
+
+
 # ---- strong decays, steps below zero --------------------------------------------------------------
 
 @pytest.mark.parametrize("dk,dv,Hk,Hv", [(64, 64, 1, 2), (128, 128, 1, 1), (32, 64, 1, 1)])
