@@ -12,6 +12,7 @@ run in Python.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
 import glob
 import os
 import shutil
@@ -114,8 +115,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     obj = os.path.join(BUILD, f"gdn_torch.{os.getpid()}.o")
-    if module and os.path.exists(torch_lib()):
-        os.remove(torch_lib())  # an old one must not stay where the new one does not build
+    if module:
+        with contextlib.suppress(FileNotFoundError):
+            os.remove(torch_lib())  # an old one must not stay where the new one does not build
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
         compiled = ex.submit(_compile_module, obj) if module else None
         if library:
