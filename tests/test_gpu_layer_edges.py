@@ -169,6 +169,23 @@ def test_scan_nan_step_reaches_later_tokens_only(gdn):
     assert bool(out[140:].isnan().all()) and bool(fin.isnan().all())
 
 
+@pytest.mark.parametrize("T", [300, 3000])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_scan_value_that_is_not_finite_stays_in_its_column(gdn, T, bad):
+    # from the start of its chunk on, as documented; other columns, heads and earlier chunks are left as they are
+    s = scan_inputs(gen(90), T, 1, 1, 2, 64, 64, init=True)
+    ref, rfin = gdn.ssm_scan(**s)
+    s["x"][200, 1, 5] = bad
+    out, fin = gdn.ssm_scan(**s)
+    assert not bool(out[200:, 1, 5].isfinite().any()) and not bool(fin[0, 1, 5].isfinite().any())
+    mine = torch.zeros_like(out, dtype=torch.bool)
+    mine[128:, 1, 5] = True
+    assert torch.equal(out[~mine], ref[~mine])
+    keep = torch.ones_like(fin, dtype=torch.bool)
+    keep[0, 1, 5] = False
+    assert torch.equal(fin[keep], rfin[keep])
+
+
 @pytest.mark.parametrize("dk,dv,Hk,Hv", [(64, 64, 1, 2), (128, 128, 2, 2), (32, 32, 1, 1), (128, 64, 1, 2)])
 @pytest.mark.parametrize("T", [1, 140, 1500])
 def test_scan_steps_below_zero(gdn, dk, dv, Hk, Hv, T):
