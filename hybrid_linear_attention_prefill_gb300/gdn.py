@@ -9,8 +9,8 @@ Functions keep the C names: ``gdn_prefill``, ``gdn_prefill_host``,
 ``gdn_workspace_bytes``, ``gdn_scan_segments``, ``gdn_release_workspace``.  ``prefill`` is a convenience
 wrapper that allocates the outputs with PyTorch and checks the status, and so are ``causal_conv``,
 ``causal_conv_step``, ``ssm_scan``, ``ssm_step`` and ``add_norm`` for the operators around the recurrence;
-these take tensors with their strides, check types and shapes (``ValueError``), and write into given
-output buffers where the caller has them.
+these take tensors with their strides, check types and shapes (``ValueError``), run on the tensors' device, and
+write into given output buffers where the caller has them, else into new ones of the stream that the call runs on.
 """
 
 from __future__ import annotations
@@ -570,7 +570,8 @@ def ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, cu_seqlens=None, in
 
     x, z: bf16 [Ttot, Hv, dv]; dt: bf16 or fp32 [Ttot, Hv]; A, D, dt_bias: fp32 [Hv]; Bm, Cm: bf16
     [Ttot, Hk, dk] (token rows may be slices of wider ones); init_state: fp32 [B, Hv, dv, dk].
-    `workspace`: a byte tensor of gdn_ssm_workspace_bytes(...), for calls that overlap or are captured.
+    `workspace`: a byte tensor of gdn_ssm_workspace_bytes(...) for these sizes (a smaller batch may need more),
+    zeroed once, for calls that overlap or are captured.
     Returns (out bf16 [Ttot, Hv, dv], final_state fp32 [B, Hv, dv, dk] or None).
     """
     fast = _shorter()

@@ -338,8 +338,9 @@ void gdn_release_workspace(void);
  * layers), each for prompts and for single tokens, and the norm that opens a layer.
  *
  * All pointers are DEVICE memory, owned by the caller and not retained; every call is
- * asynchronous on `stream`, never synchronises the host, and returns GDN_OK or, before
- * anything is launched, GDN_ERR_ARG / GDN_ERR_ALIGN (or GDN_ERR_LAUNCH from a launch).
+ * asynchronous on `stream`, never synchronises the host (but for a gdn_ssm_scan that has to
+ * enlarge the library's own workspace), and returns GDN_OK or, before anything is launched,
+ * GDN_ERR_ARG / GDN_ERR_ALIGN (or GDN_ERR_LAUNCH from a launch).
  * Activations are bf16; sums, states of the scan and softplus / exp values are fp32.  A
  * `*_stride` is the distance between consecutive tokens in elements, so that an operand can
  * be a slice of a wider projection or convolution output; within a token the elements are
@@ -427,12 +428,19 @@ int gdn_conv_step(const gdn_conv_step_args *args);
  * outputs of its chunk before it not finite too.  Without softplus a step may be below zero; like a
  * decay rate A above 0 it grows the state, which may overflow.
  *
- * workspace: gdn_ssm_workspace_bytes(...) bytes of device memory, 256-byte aligned, not shared
- * with concurrent calls, or NULL for the library's own grow-only one (shared by the calls on a
- * device: order calls whose work could overlap, as for gdn_prefill).  With a workspace the call
- * allocates nothing and can be captured into a CUDA graph; GDN_ERR_SCRATCH when it is too
- * small.  Its first word collects status bits; gdn_device_status reports those of the
- * library's own.
+ * The state is fp32 throughout.  For a prompt's outputs it, and the weights between the tokens of
+ * a chunk, are rounded to bf16 as operands of the matrix products (2^-9 of each term); the sums
+ * are fp32.  gdn_ssm_step rounds nothing but its output.
+ *
+ * workspace: gdn_ssm_workspace_bytes(...) bytes of device memory for the sizes of the call,
+ * 256-byte aligned, not shared with concurrent calls, or NULL for the library's own grow-only one
+ * (shared by the calls on a device: order calls whose work could overlap, as for gdn_prefill;
+ * enlarging it frees and allocates, which synchronises).  The bytes do not grow with the sizes:
+ * few sequences and heads are cut into segments, whose sums they hold, and more are not, so a
+ * smaller batch may need more.  A buffer kept over calls is sized for the largest need among them.
+ * With a workspace the call allocates nothing and can be captured into a CUDA graph;
+ * GDN_ERR_SCRATCH when it is too small.  Its first word, which the caller clears, collects status
+ * bits; gdn_device_status reports those of the library's own.
  */
 typedef struct gdn_ssm_scan_args {
   const void *x;
