@@ -186,6 +186,19 @@ def test_scan_value_that_is_not_finite_stays_in_its_column(gdn, T, bad):
     assert torch.equal(fin[keep], rfin[keep])
 
 
+@pytest.mark.parametrize("T", [300, 3000])
+@pytest.mark.parametrize("which", ["Bm", "Cm", "z"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_scan_b_c_and_gate_that_are_not_finite_reach_no_token_before(gdn, T, which, bad):
+    s = scan_inputs(gen(91), T, 1, 1, 2, 64, 64, init=True)
+    ref, _ = gdn.ssm_scan(**s)
+    s[which][200, 0, 5] = bad
+    out, _ = gdn.ssm_scan(**s)
+    assert torch.equal(out[:200], ref[:200]) and not bool(out[200, 0].isfinite().all())
+    if which != "Bm":  # C and the gate are of one token
+        assert torch.equal(out[201:], ref[201:])
+
+
 @pytest.mark.parametrize("dk,dv,Hk,Hv", [(64, 64, 1, 2), (128, 128, 2, 2), (32, 32, 1, 1), (128, 64, 1, 2)])
 @pytest.mark.parametrize("T", [1, 140, 1500])
 def test_scan_steps_below_zero(gdn, dk, dv, Hk, Hv, T):
