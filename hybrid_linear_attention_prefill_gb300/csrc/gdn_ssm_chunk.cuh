@@ -21,11 +21,11 @@
 //            S; the next chunk's S -> bf16 and w x of tokens 0..63     | MMA: y += M x, the next scores
 //            the rest of silu(z), outputs                              | MMA: the next (w x)^T B of 0..63 and C S_0^T
 //
-// What bounds a step (about 8,000 cycles at 128 x 128) is the workers' own path: its instructions (the SM issues in 57%
+// What bounds a step (about 8,000 cycles at 128 x 128) is the workers' own path: its instructions (the SM issues in 58%
 // of the cycles) and the latency of what they meet: a barrier's state (200 cycles beside running MMAs, hence `peek`),
 // TMEM, spilled registers, which come back from L2 (so that little is kept that can be worked out anew, and the gate
 // goes through silu only where it is used).  The MMAs take 3,840 cycles of it, the tiles' bytes about 5,600 at the
-// device's bandwidth.  32 ragged prompts of 32 heads, 72,102 tokens: 540 to 554 us, 4.4 TB/s of needed bytes.  (Warps
+// device's bandwidth.  32 ragged prompts of 32 heads, 72,102 tokens: 547 to 565 us, 4.4 TB/s of needed bytes.  (Warps
 // split into a group that carries the state and one that makes outputs, each with half the warps to hide its latencies:
 // 20% slower.  All of the gate through silu beside the state's product, kept in registers until the outputs: 8%.)
 //

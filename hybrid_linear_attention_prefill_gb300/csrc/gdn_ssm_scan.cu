@@ -198,7 +198,7 @@ cudaError_t launch_ssm_scan(const SsmArgs& a, const int32_t* cu, const float* in
   g.slots = p.slots;
   g.polls = (uint32_t)g_polls.load(std::memory_order_relaxed);
   // With few segments a sequence the output pass goes through the sums before its own by itself (about 0.8 us each,
-  // beside its first tiles' load); more are joined by a kernel (about 5 us).
+  // beside its first tiles' load); more are joined by a kernel (10 us by itself for 32 segments).
   const int per = p.len * ssm::kQ;
   g.joined = p.len != 0 && (T - 1) / per + 1 > kAloneSegs;
   auto run = [&](int phase) {
