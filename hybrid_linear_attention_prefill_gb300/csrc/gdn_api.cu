@@ -126,6 +126,22 @@ int ensure(void*& ptr, size_t& have, size_t need) {
   return GDN_OK;
 }
 
+// The same for a workspace whose first 256 bytes are status words: a new one's are cleared on stream `st`, in the order
+// of the call that writes them, but for the first word, which keeps the bits of the calls before.
+int ensure_workspace(void*& ptr, size_t& have, size_t need, cudaStream_t st) {
+  if (need <= have) return GDN_OK;
+  int bits = 0;
+  cudaError_t e = cudaSuccess;
+  if (ptr != nullptr && ((e = cudaDeviceSynchronize()) != cudaSuccess ||
+                         (e = cudaMemcpy(&bits, ptr, sizeof(bits), cudaMemcpyDeviceToHost)) != cudaSuccess))
+    return set_cuda_error(e, GDN_ERR_LAUNCH);
+  const int rc = ensure(ptr, have, need);
+  if (rc != GDN_OK) return rc;
+  e = cudaMemsetAsync(ptr, 0, 256, st);
+  if (e == cudaSuccess && bits != 0) e = cudaMemcpyAsync(ptr, &bits, sizeof(bits), cudaMemcpyHostToDevice, st);
+  return e == cudaSuccess ? GDN_OK : set_cuda_error(e, GDN_ERR_LAUNCH);
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // ---- two-level chunk scan (dense batches with few heads and many chunks) -----------
@@ -419,13 +435,8 @@ int ensure_ssm_workspace(int dev, size_t need, cudaStream_t st, void** ws) {
   if (dev < 0 || dev >= kMaxDevices) return GDN_ERR_ARG;
   std::lock_guard<std::mutex> lock(g_mu);
   DevBuffers& d = g_dev[dev];
-  const size_t had = d.ssm_bytes;
-  const int rc = ensure(d.ssm, d.ssm_bytes, need);
+  const int rc = ensure_workspace(d.ssm, d.ssm_bytes, need, st);
   if (rc != GDN_OK) return rc;
-  if (d.ssm_bytes != had) {  // a new allocation: its status words, in the order of the call that writes them
-    const cudaError_t e = cudaMemsetAsync(d.ssm, 0, 256, st);
-    if (e != cudaSuccess) return set_cuda_error(e, GDN_ERR_LAUNCH);
-  }
   *ws = d.ssm;
   return GDN_OK;
 }
@@ -502,7 +513,8 @@ int gdn_prefill(const void* q, const void* k, const void* v, const float* g, con
   {
     std::lock_guard<std::mutex> lock(g_mu);
     DevBuffers& d = g_dev[dev];
-    rc = ensure(d.ws, d.ws_bytes, ws_bytes_for(B, T, Hk, Hv, dk, cu_seqlens != nullptr));
+    rc = ensure_workspace(d.ws, d.ws_bytes, ws_bytes_for(B, T, Hk, Hv, dk, cu_seqlens != nullptr),
+                          static_cast<cudaStream_t>(stream));
     if (rc != GDN_OK) return rc;
     ws = d.ws;
     rc = prepare_scan(dev, B, T, Hv, dk, dv, cu_seqlens != nullptr, 0u, static_cast<cudaStream_t>(stream), plan);
@@ -591,7 +603,8 @@ int gdn_prefill_ex(const void* q, const void* k, const void* v, const float* g, 
   {
     std::lock_guard<std::mutex> lock(g_mu);
     DevBuffers& d = g_dev[dev];
-    rc = ensure(d.ws, d.ws_bytes, ws_bytes_for(B, T, Hk, Hv, dk, cu_seqlens != nullptr));
+    rc = ensure_workspace(d.ws, d.ws_bytes, ws_bytes_for(B, T, Hk, Hv, dk, cu_seqlens != nullptr),
+                          static_cast<cudaStream_t>(stream));
     if (rc != GDN_OK) return rc;
     ws = d.ws;
     rc = prepare_scan(dev, B, T, Hv, dk, dv, cu_seqlens != nullptr, flags, static_cast<cudaStream_t>(stream), plan);
@@ -647,7 +660,7 @@ int gdn_prefill_host(const void* q, const void* k, const void* v, const float* g
     dp = &d;
     rc = ensure(d.stage, d.stage_bytes, total);
     if (rc != GDN_OK) return rc;
-    rc = ensure(d.ws, d.ws_bytes, ws_bytes_for(B, T, Hk, Hv, dk, cu_seqlens != nullptr));
+    rc = ensure_workspace(d.ws, d.ws_bytes, ws_bytes_for(B, T, Hk, Hv, dk, cu_seqlens != nullptr), st);
     if (rc != GDN_OK) return rc;
     base = static_cast<unsigned char*>(d.stage);
     ws = d.ws;

@@ -27,7 +27,8 @@ bool take_injected_alloc_failure();
 int device_sms();
 
 // gdn_ssm_scan's library-owned workspace on device `dev`, grown to at least `need` bytes (its first
-// 256 bytes are status words, cleared on stream `st` when new): GDN_OK or the error code to return.
+// 256 bytes are status words, cleared on stream `st` when new but for bits already set): GDN_OK or the error code to
+// return.
 int ensure_ssm_workspace(int dev, size_t need, cudaStream_t st, void** ws);
 
 }  // namespace gdn

@@ -56,6 +56,45 @@ def test_a_first_calls_status_survives_what_another_stream_has_to_do(gdn):
     assert rc == 0 and bits == gdn.GDN_STATUS_BAD_CU_SEQLENS
 
 
+def prefill_inputs(n):
+    q = torch.nn.functional.normalize(rnd(gen(92), n, 1, 32).float(), dim=-1).bfloat16()  # keys that leave the state finite
+    return q, q, q, torch.zeros(n, 1, device="cuda"), torch.full((n, 1), 0.5, device="cuda")
+
+
+@pytest.mark.parametrize("which", ["prefill", "scan"])
+def test_status_outlives_a_larger_workspace(gdn, which):
+    bad = torch.tensor([0, 190, 100, 200], dtype=torch.int32, device="cuda")
+
+    def call(n, cu):
+        if which == "prefill":
+            return gdn.prefill(*prefill_inputs(n), cu)
+        B = 1 if cu is None else 3
+        return gdn.ssm_scan(**scan_inputs(gen(93), n, B, 1, 1, 128, 128), cu_seqlens=cu, B=B)
+
+    gdn.gdn_release_workspace()
+    call(200, bad)
+    call(60000, None)  # takes more
+    rc, bits = gdn.gdn_device_status()
+    assert rc == 0 and bits == gdn.GDN_STATUS_BAD_CU_SEQLENS
+    assert gdn.gdn_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("which", ["prefill", "scan"])
+def test_status_of_a_new_workspace_is_clear(gdn, which):
+    gdn.gdn_release_workspace()
+    torch.cuda.empty_cache()
+    used = torch.full((2 ** 30,), 255, dtype=torch.uint8, device="cuda")  # what a new allocation may find
+    small = [torch.full((2 ** 21,), 255, dtype=torch.uint8, device="cuda") for _ in range(16)]
+    torch.cuda.synchronize()
+    del used, small
+    torch.cuda.empty_cache()
+    if which == "prefill":
+        gdn.prefill(*prefill_inputs(3000))
+    else:
+        gdn.ssm_scan(**scan_inputs(gen(94), 3000, 1, 1, 1, 128, 128))
+    assert gdn.gdn_device_status() == (0, 0)
+
+
 # ---- arguments ----------------------------------------------------------------------------------
 
 def test_arguments_beyond_their_range_are_refused(gdn):
