@@ -250,7 +250,7 @@ __device__ __forceinline__ void to_steps(const SsmArgs& a, int n, float bias, in
 //                  - log2 |s_j|.
 // A step below zero (there are none with softplus) leaves its sign to M and has it in w, a zero w too.
 // The weights' exponents are sums over the tokens after each, from the chunk's end.  A token's decay below 2^-160 is 0
-// in fp32 and counts as 2^-160, which keeps L above -5,120: its rounding (2^-12) stays below that of M to bf16 (2^-9).
+// in fp32 and counts as 2^-160, which keeps L above -5,120: its roundings (2^-12) stay below that of M to bf16 (2^-9).
 struct Tables {
   float4 L, K, far, w, e;  // e: 2^(the sum up to a token)
   float2 gap;              // between the lane's block and blocks 0 and 1

@@ -453,7 +453,8 @@ def _plain(t, name, dtype, shape, dev) -> int:
 
 def _rows(t, name, dtype, shape, dev) -> int:
     """Row stride of a tensor of this shape whose rows are contiguous (a slice of a wider one may be)."""
-    _want(max(shape) <= 0x7fffffff, f"{name}: sizes are 32-bit, got {tuple(shape)}")
+    if max(shape) > 0x7fffffff:
+        raise ValueError(f"{name}: sizes are 32-bit, got {tuple(shape)}")
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         raise ValueError(f"{name}: a {dtype} tensor of shape {shape} on the device of x is wanted, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
@@ -587,10 +588,9 @@ def ssm_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, cu_seqlens=None, in
     dev, (n, Hk, Hv, dk, dv), fields, out, flags = _ssm_operands(x, dt, A, Bm, Cm, D, z, dt_bias, out, softplus, stream)
     B, T, cu = _batch(n, cu_seqlens, B, dev)
     shape = (B, Hv, dv, dk)
-    if workspace is not None:
-        _want(workspace.device == x.device and workspace.is_contiguous(),
-              f"workspace: contiguous, on the device of x, is wanted, got strides {workspace.stride()} on "
-              f"{workspace.device}")
+    if workspace is not None and (workspace.device != x.device or not workspace.is_contiguous()):
+        raise ValueError(f"workspace: contiguous, on the device of x, is wanted, got strides {workspace.stride()} on "
+                         f"{workspace.device}")
     if final_state is None and want_final:
         final_state = _output(shape, torch.float32, x.device, stream)
     _call(load().gdn_ssm_scan, _SSM_SCAN.pack(
@@ -639,7 +639,7 @@ def add_norm(x, weight, residual=None, *, eps=1e-6, group=0, e4m3=False, out=Non
 
     bf16, f8 = torch.bfloat16, torch.float8_e4m3fn
     _want(x.dim() == 2, "x: [rows, D]")
-    _want(0 <= group <= 0x7fffffff, f"group: 0, 32, 64 or 128 columns, got {group}")
+    _want(0 <= group <= 0x7fffffff, "group: 0, 32, 64 or 128 columns")
     rows, D = shape = x.shape
     dev = x.get_device()
     xs = _rows(x, "x", bf16, shape, dev)
