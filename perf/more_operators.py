@@ -166,7 +166,7 @@ def prepare(case, seed):
         for b, n in enumerate(held):
             s["table"][b, :n] = blocks[at : at + n]
             at += n
-        s["free"] = torch.zeros(total, dtype=i32, device=dev)
+        s["free"] = torch.zeros(max(total, 1), dtype=i32, device=dev)
         s["free"][: total - at] = blocks[at:]
         s["count"] = torch.tensor([total - at], dtype=i32, device=dev)
         s["slots"] = torch.empty(s["T"], dtype=i32, device=dev)
