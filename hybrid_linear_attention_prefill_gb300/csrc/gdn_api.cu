@@ -54,6 +54,8 @@ struct DevBuffers {
   size_t scan_zeroed = 0;
   void* ssm = nullptr;  // gdn_ssm_scan's workspace
   size_t ssm_bytes = 0;
+  void* attn = nullptr;  // gdn_attn's and gdn_attn_step's
+  size_t attn_bytes = 0;
   cudaStream_t aux = nullptr;  // second stream for pass A's transition run
   cudaEvent_t fork = nullptr, join = nullptr;
   int sms = 0;
@@ -431,14 +433,23 @@ int device_sms() {
   return n;
 }
 
-int ensure_ssm_workspace(int dev, size_t need, cudaStream_t st, void** ws) {
+static int ensure_own(void* DevBuffers::*ws_of, size_t DevBuffers::*bytes_of, int dev, size_t need, cudaStream_t st,
+                      void** ws) {
   if (dev < 0 || dev >= kMaxDevices) return GDN_ERR_ARG;
   std::lock_guard<std::mutex> lock(g_mu);
   DevBuffers& d = g_dev[dev];
-  const int rc = ensure_workspace(d.ssm, d.ssm_bytes, need, st);
+  const int rc = ensure_workspace(d.*ws_of, d.*bytes_of, need, st);
   if (rc != GDN_OK) return rc;
-  *ws = d.ssm;
+  *ws = d.*ws_of;
   return GDN_OK;
+}
+
+int ensure_ssm_workspace(int dev, size_t need, cudaStream_t st, void** ws) {
+  return ensure_own(&DevBuffers::ssm, &DevBuffers::ssm_bytes, dev, need, st, ws);
+}
+
+int ensure_attn_workspace(int dev, size_t need, cudaStream_t st, void** ws) {
+  return ensure_own(&DevBuffers::attn, &DevBuffers::attn_bytes, dev, need, st, ws);
 }
 
 }  // namespace gdn
@@ -854,11 +865,12 @@ int gdn_device_status(int* status) {
   if (e != cudaSuccess) return set_cuda_error(e, GDN_ERR_LAUNCH);
   if (dev < 0 || dev >= kMaxDevices) return GDN_ERR_ARG;
   // the workspaces', the static array's
-  void* words[3] = {nullptr, gdn::static_scratch_address(dev), nullptr};
+  void* words[4] = {nullptr, gdn::static_scratch_address(dev), nullptr, nullptr};
   {
     std::lock_guard<std::mutex> lock(g_mu);
     words[0] = g_dev[dev].ws;
     words[2] = g_dev[dev].ssm;
+    words[3] = g_dev[dev].attn;
   }
   e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return set_cuda_error(e, GDN_ERR_LAUNCH);
@@ -898,6 +910,7 @@ void gdn_release_workspace(void) {
   if (d.stage) cudaFree(d.stage);
   if (d.scan) cudaFree(d.scan);
   if (d.ssm) cudaFree(d.ssm);
+  if (d.attn) cudaFree(d.attn);
   if (d.fork) cudaEventDestroy(d.fork);
   if (d.join) cudaEventDestroy(d.join);
   if (d.aux) cudaStreamDestroy(d.aux);

@@ -1,9 +1,8 @@
 // C ABI of the operators around the recurrence: causal convolution, selective state space scan (each
 // for prompts and single tokens) and the norm with the residual's addition.  Argument checks here,
 // kernels in gdn_conv.cu, gdn_ssm_scan.cu, gdn_ssm_step.cu and gdn_norm.cu.
-#include "../../include/gdn.h"
+#include "gdn_args.h"
 #include "gdn_common.cuh"
-#include "gdn_internal.h"
 #include "gdn_ssm.cuh"
 
 namespace gdn {
@@ -21,22 +20,10 @@ cudaError_t launch_ssm_scan(const SsmArgs&, const int32_t*, const float*, float*
 
 namespace {
 
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a != nullptr && b != nullptr && x < y + nb && y < x + na;
-}
-
-// A bf16 operand of `tokens` rows of `width` elements: GDN_OK, or what is wrong with it.
-int check_rows(const void* p, long long stride, long long tokens, long long width) {
-  if (p == nullptr) return GDN_ERR_ARG;
-  if (tokens > 1 && stride < width) return GDN_ERR_ARG;
-  if (!aligned(p, 16) || (tokens > 1 && stride % 8 != 0)) return GDN_ERR_ALIGN;
-  return GDN_OK;
-}
-
-int done(cudaError_t e) { return e == cudaSuccess ? GDN_OK : gdn::set_cuda_error(e, GDN_ERR_LAUNCH); }
+using gdn::aligned;
+using gdn::check_rows;
+using gdn::done;
+using gdn::overlap;
 
 bool conv_sizes_ok(int B, int T, int C, int K, unsigned flags) {
   return B >= 0 && T >= 0 && C > 0 && C % 8 == 0 && K >= 2 && K <= 4 && (flags & ~GDN_CONV_SILU) == 0;

@@ -5,6 +5,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <initializer_list>
 
 #include "gdn.h"
@@ -256,11 +257,188 @@ PyObject* norm(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   });
 }
 
+constexpr at::ScalarType kI32 = at::ScalarType::Int, kE4m3 = at::ScalarType::Float8_e4m3fn;
+
+// Argument i as an integer of at least `least`.
+int whole(Call& c, int i, long least) {
+  long v = -1;
+  if (c.ok && !PyLong_Check(c.argv[i])) c.ok = false;
+  if (c.ok) v = PyLong_AsLong(c.argv[i]);
+  if (v < least || v > 0x7fffffff) c.ok = false;
+  return c.ok ? (int)v : 0;
+}
+
+// Argument i as the scores' scale, 1 / sqrt(d) for None.
+float scale_of(Call& c, int i, int64_t d) {
+  if (c.argv[i] == Py_None) return d > 0 ? (float)(1.0 / std::sqrt((double)d)) : 1.f;
+  if (!PyFloat_Check(c.argv[i])) c.ok = false;
+  return c.ok ? (float)PyFloat_AsDouble(c.argv[i]) : 0.f;
+}
+
+// A paged cache: arguments k_at, k_at + 1 and its scales s_at, s_at + 1.
+template <class A>
+void paged(Call& c, A& a, int k_at, int s_at, int64_t Hkv, int64_t d) {
+  const Tensor* k = c.tensor(k_at);
+  if (!c.ok || k->dim() != 4 || k->size(0) > 0x7fffffff || k->size(2) > 0x7fffffff) {
+    c.ok = false;
+    return;
+  }
+  const at::ScalarType type = k->scalar_type();
+  const bool e4m3 = type == kE4m3;
+  if (!e4m3 && type != kBf16) c.ok = false;
+  const int64_t blocks = k->size(0), page = k->size(2);
+  a.k_cache = c.rows(k_at, type, {blocks, Hkv, page, d}, a.k_block_stride);
+  a.v_cache = c.rows(k_at + 1, type, {blocks, Hkv, page, d}, a.v_block_stride);
+  if (e4m3) {
+    a.k_scale = static_cast<const float*>(c.plain(s_at, kF32, {Hkv}));
+    a.v_scale = static_cast<const float*>(c.plain(s_at + 1, kF32, {Hkv}));
+  } else if (c.argv[s_at] != Py_None || c.argv[s_at + 1] != Py_None) {
+    c.ok = false;
+  }
+  a.blocks = (int)blocks;
+  a.page = (int)page;
+  a.flags = e4m3 ? GDN_CACHE_E4M3 : 0;
+}
+
+template <class A>
+void workspace(Call& c, A& a, int i) {
+  if (const Tensor* w = c.tensor(i, true)) {
+    if (!w->is_contiguous() || w->nbytes() == 0) c.ok = false;
+    a.workspace = w->data_ptr();
+    a.workspace_bytes = w->nbytes();
+  }
+}
+
+// cache_plan(lens, block_table, free_blocks, free_count, cu_seqlens, page, T, slots, new_lens, new_count, refused,
+// stream)
+PyObject* plan(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 12) return none();
+    Call c(argv);
+    gdn_cache_plan_args a = {};
+    const Tensor *lens = c.tensor(0), *table = c.tensor(1), *free_blocks = c.tensor(2), *slots = c.tensor(7);
+    if (!c.ok || lens->dim() != 1 || table->dim() != 2 || free_blocks->dim() != 1 || slots->dim() != 1) return none();
+    const int64_t B = lens->size(0), W = table->size(1), capacity = free_blocks->size(0), T = slots->size(0);
+    if (B > 0x7ffffffe || W > 0x7fffffff || capacity > 0x7fffffff || T > 0x7fffffff) return none();
+    if (argv[6] != Py_None && (whole(c, 6, 0) != T || !c.ok)) return none();
+    if (argv[4] == Py_None && T != B) return none();
+    a.lens = static_cast<const int32_t*>(c.plain(0, kI32, {B}));
+    a.block_table = static_cast<int32_t*>(c.rows(1, kI32, {B, W}, a.table_stride));
+    a.free_blocks = static_cast<const int32_t*>(c.plain(2, kI32, {capacity}));
+    a.free_count = static_cast<const int32_t*>(c.plain(3, kI32, {1}));
+    a.cu_seqlens = static_cast<const int32_t*>(c.plain(4, kI32, {B + 1}, true));
+    a.slots = static_cast<int32_t*>(c.plain(7, kI32, {T}));
+    a.new_lens = static_cast<int32_t*>(c.plain(8, kI32, {B}));
+    a.new_count = static_cast<int32_t*>(c.plain(9, kI32, {1}));
+    a.refused = static_cast<int32_t*>(c.plain(10, kI32, {1}));
+    a.B = (int)B;
+    a.T = (int)T;
+    a.W = (int)W;
+    a.capacity = (int)capacity;
+    a.page = whole(c, 5, 1);
+    a.stream = c.stream(11);
+    return c.ok ? PyLong_FromLong(gdn_cache_plan(&a)) : none();
+  });
+}
+
+// cache_append(k, v, k_cache, v_cache, slots, k_scale, v_scale, stream)
+PyObject* append(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 8) return none();
+    Call c(argv);
+    gdn_cache_append_args a = {};
+    const Tensor* k = c.tensor(0);
+    if (!c.ok || k->dim() != 3 || k->size(0) > 0x7fffffff || k->size(1) > 0x7fffffff || k->size(2) > 0x7fffffff)
+      return none();
+    const int64_t T = k->size(0), Hkv = k->size(1), d = k->size(2);
+    a.k = c.rows(0, kBf16, {T, Hkv, d}, a.k_stride);
+    a.v = c.rows(1, kBf16, {T, Hkv, d}, a.v_stride);
+    paged(c, a, 2, 5, Hkv, d);
+    a.slots = static_cast<const int32_t*>(c.plain(4, kI32, {T}));
+    a.T = (int)T;
+    a.Hkv = (int)Hkv;
+    a.d = (int)d;
+    a.stream = c.stream(7);
+    return c.ok ? PyLong_FromLong(gdn_cache_append(&a)) : none();
+  });
+}
+
+// attention(q, k, v, cu_seqlens, cu_seqlens_k, B, window, sinks, scale, out, lse, workspace, stream)
+PyObject* attn(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 13) return none();
+    Call c(argv);
+    gdn_attn_args a = {};
+    const Tensor *q = c.tensor(0), *k = c.tensor(1);
+    if (!c.ok || q->dim() != 3 || k->dim() != 3) return none();
+    for (int i = 0; i < 3; ++i)
+      if (q->size(i) > 0x7fffffff || k->size(i) > 0x7fffffff) return none();
+    const int64_t T = q->size(0), Hq = q->size(1), d = q->size(2), Tk = k->size(0), Hkv = k->size(1);
+    a.q = c.rows(0, kBf16, {T, Hq, d}, a.q_stride);
+    a.k = c.rows(1, kBf16, {Tk, Hkv, d}, a.k_stride);
+    a.v = c.rows(2, kBf16, {Tk, Hkv, d}, a.v_stride);
+    if (!c.ok || !batch(c, T, 3, 5, a.cu_seqlens, a.B, a.T)) return none();
+    if (a.cu_seqlens == nullptr) {
+      if (argv[4] != Py_None || Tk % a.B != 0) return none();
+      a.Tk = (int)(Tk / a.B);
+    } else {
+      if (argv[4] == Py_None && Tk != T) return none();
+      a.cu_seqlens_k = static_cast<const int32_t*>(c.plain(4, kI32, {a.B + 1}, true));
+      a.Tk = (int)Tk;
+    }
+    a.window = whole(c, 6, 0);
+    a.sinks = whole(c, 7, 0);
+    a.scale = scale_of(c, 8, d);
+    a.out = c.plain(9, kBf16, {T, Hq, d});
+    a.lse = static_cast<float*>(c.plain(10, kF32, {T, Hq}, true));
+    workspace(c, a, 11);
+    a.Hq = (int)Hq;
+    a.Hkv = (int)Hkv;
+    a.d = (int)d;
+    a.stream = c.stream(12);
+    return c.ok ? PyLong_FromLong(gdn_attn(&a)) : none();
+  });
+}
+
+// attention_step(q, k_cache, v_cache, block_table, lens, k_scale, v_scale, window, sinks, scale, out, lse, workspace,
+// stream)
+PyObject* attn_step(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 14) return none();
+    Call c(argv);
+    gdn_attn_step_args a = {};
+    const Tensor *q = c.tensor(0), *k = c.tensor(1), *table = c.tensor(3);
+    if (!c.ok || q->dim() != 3 || k->dim() != 4 || table->dim() != 2 || table->size(1) > 0x7fffffff) return none();
+    for (int i = 0; i < 3; ++i)
+      if (q->size(i) > 0x7fffffff || k->size(i) > 0x7fffffff) return none();
+    const int64_t B = q->size(0), Hq = q->size(1), d = q->size(2), Hkv = k->size(1), W = table->size(1);
+    a.q = c.rows(0, kBf16, {B, Hq, d}, a.q_stride);
+    paged(c, a, 1, 5, Hkv, d);
+    a.block_table = static_cast<const int32_t*>(c.rows(3, kI32, {B, W}, a.table_stride));
+    a.lens = static_cast<const int32_t*>(c.plain(4, kI32, {B}));
+    a.window = whole(c, 7, 0);
+    a.sinks = whole(c, 8, 0);
+    a.scale = scale_of(c, 9, d);
+    a.out = c.plain(10, kBf16, {B, Hq, d});
+    a.lse = static_cast<float*>(c.plain(11, kF32, {B, Hq}, true));
+    workspace(c, a, 12);
+    a.B = (int)B;
+    a.Hq = (int)Hq;
+    a.Hkv = (int)Hkv;
+    a.d = (int)d;
+    a.W = (int)W;
+    a.stream = c.stream(13);
+    return c.ok ? PyLong_FromLong(gdn_attn_step(&a)) : none();
+  });
+}
+
 #define GDN_METHOD(name, f) \
   {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {GDN_METHOD("causal_conv", conv), GDN_METHOD("causal_conv_step", conv_step),
                          GDN_METHOD("ssm_scan", scan),    GDN_METHOD("ssm_step", step),
-                         GDN_METHOD("add_norm", norm),    {nullptr, nullptr, 0, nullptr}};
+                         GDN_METHOD("add_norm", norm),    GDN_METHOD("cache_plan", plan),
+                         GDN_METHOD("cache_append", append), GDN_METHOD("attention", attn),
+                         GDN_METHOD("attention_step", attn_step), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "gdn_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -8,8 +8,8 @@ Functions keep the C names: ``gdn_prefill``, ``gdn_prefill_host``,
 ``gdn_abi_version``, ``gdn_strerror``, ``gdn_last_cuda_error``,
 ``gdn_workspace_bytes``, ``gdn_scan_segments``, ``gdn_release_workspace``.  ``prefill`` is a convenience
 wrapper that allocates the outputs with PyTorch and checks the status, and so are ``causal_conv``,
-``causal_conv_step``, ``ssm_scan``, ``ssm_step`` and ``add_norm`` for the operators around the recurrence;
-these take tensors with their strides, check types and shapes (``ValueError``), run on the tensors' device, and
+``causal_conv_step``, ``ssm_scan``, ``ssm_step`` and ``add_norm`` for the operators around the recurrence, and
+``cache_plan``, ``cache_append``, ``attention`` and ``attention_step`` for the attention layers between; these take tensors with their strides, check types and shapes (``ValueError``), run on the tensors' device, and
 write into given output buffers where the caller has them, else into new ones of the stream that the call runs on.
 """
 
@@ -42,10 +42,12 @@ GDN_STATUS_PREP_LOAD_TIMEOUT = 4
 GDN_STATUS_BAD_CU_SEQLENS = 8
 GDN_STATUS_NONFINITE_STATE = 16
 GDN_STATUS_SMALL_STATE = 32
+GDN_STATUS_BAD_PAGE = 64
 GDN_CONV_SILU = 1
 GDN_SSM_SOFTPLUS = 1
 GDN_SSM_DT_F32 = 2
 GDN_NORM_E4M3 = 1
+GDN_CACHE_E4M3 = 1
 
 
 def GDN_FLAG_SEGMENTS(n: int) -> int:
@@ -58,7 +60,8 @@ EXPORTED = ("gdn_abi_version", "gdn_strerror", "gdn_last_cuda_error", "gdn_prefi
             "gdn_set_phase_events", "gdn_workspace_bytes", "gdn_scan_segments", "gdn_release_workspace",
             "gdn_device_status", "gdn_selftest_wait_timeout", "gdn_selftest_static_wait_timeout",
             "gdn_debug_fail_allocations", "gdn_conv", "gdn_conv_step", "gdn_ssm_scan", "gdn_ssm_workspace_bytes",
-            "gdn_debug_ssm_wait_polls", "gdn_ssm_step", "gdn_add_norm")
+            "gdn_debug_ssm_wait_polls", "gdn_ssm_step", "gdn_add_norm", "gdn_cache_plan", "gdn_cache_append", "gdn_attn",
+            "gdn_attn_workspace_bytes", "gdn_attn_step")
 
 _lock = threading.Lock()
 _lib = None
@@ -131,7 +134,10 @@ def load(build_if_missing: bool = False):
         lib.gdn_debug_ssm_wait_polls.restype = i
         lib.gdn_ssm_workspace_bytes.argtypes = [i] * 7
         lib.gdn_ssm_workspace_bytes.restype = ctypes.c_size_t
-        for name in ("gdn_conv", "gdn_conv_step", "gdn_ssm_scan", "gdn_ssm_step", "gdn_add_norm"):
+        lib.gdn_attn_workspace_bytes.argtypes = [i] * 4
+        lib.gdn_attn_workspace_bytes.restype = ctypes.c_size_t
+        for name in ("gdn_conv", "gdn_conv_step", "gdn_ssm_scan", "gdn_ssm_step", "gdn_add_norm", "gdn_cache_plan",
+                     "gdn_cache_append", "gdn_attn", "gdn_attn_step"):
             getattr(lib, name).argtypes = [ctypes.c_char_p]  # the packed argument struct
             getattr(lib, name).restype = i
         lib.gdn_release_workspace.argtypes = []
@@ -358,6 +364,10 @@ _CONV_STEP = struct.Struct("@PqPPPPiiiIP")
 _SSM_SCAN = struct.Struct("@PqPqPPqPqPPqPPPPPiiiiiiIPNP")
 _SSM_STEP = struct.Struct("@PqPqPPqPqPPqPPPiiiiiIP")
 _NORM = struct.Struct("@PqPPPPPiiifIP")
+_PLAN = struct.Struct("@PPqPPPPPPPiiiiiP")
+_APPEND = struct.Struct("@PqPqPqPqPPPiiiiiIP")
+_ATTN = struct.Struct("@PqPqPqPPPPiiiiiiiifIPNP")
+_ATTN_STEP = struct.Struct("@PqPqPqPPPqPPPiiiiiiiiifIPNP")
 
 
 def _addr(x) -> int:
@@ -434,6 +444,45 @@ def gdn_add_norm(x, x_stride, residual, weight, residual_out, out, scales, rows,
     """Root-mean-square norm with the residual's addition; returns the status."""
     return load().gdn_add_norm(_NORM.pack(_addr(x), x_stride, _addr(residual), _addr(weight), _addr(residual_out),
                                           _addr(out), _addr(scales), rows, D, group, eps, flags, _stream(stream)))
+
+
+def gdn_cache_plan(lens, block_table, table_stride, free_blocks, free_count, cu_seqlens, slots, new_lens, new_count,
+                   refused, B, T, W, capacity, page, stream=None) -> int:
+    """Blocks and slots of the requests' new tokens; returns the status."""
+    return load().gdn_cache_plan(_PLAN.pack(
+        _addr(lens), _addr(block_table), table_stride, _addr(free_blocks), _addr(free_count), _addr(cu_seqlens),
+        _addr(slots), _addr(new_lens), _addr(new_count), _addr(refused), B, T, W, capacity, page, _stream(stream)))
+
+
+def gdn_cache_append(k, k_stride, v, v_stride, k_cache, k_block_stride, v_cache, v_block_stride, k_scale, v_scale, slots,
+                     T, Hkv, d, page, blocks, flags, stream=None) -> int:
+    """Keys and values to their slots of a paged cache; returns the status."""
+    return load().gdn_cache_append(_APPEND.pack(
+        _addr(k), k_stride, _addr(v), v_stride, _addr(k_cache), k_block_stride, _addr(v_cache), v_block_stride,
+        _addr(k_scale), _addr(v_scale), _addr(slots), T, Hkv, d, page, blocks, flags, _stream(stream)))
+
+
+def gdn_attn(q, q_stride, k, k_stride, v, v_stride, cu_seqlens, cu_seqlens_k, out, lse, B, T, Tk, Hq, Hkv, d, window,
+             sinks, scale, flags=0, workspace=None, workspace_bytes=0, stream=None) -> int:
+    """Attention of prompts; returns the status."""
+    return load().gdn_attn(_ATTN.pack(
+        _addr(q), q_stride, _addr(k), k_stride, _addr(v), v_stride, _addr(cu_seqlens), _addr(cu_seqlens_k), _addr(out),
+        _addr(lse), B, T, Tk, Hq, Hkv, d, window, sinks, scale, flags, _addr(workspace), workspace_bytes,
+        _stream(stream)))
+
+
+def gdn_attn_workspace_bytes(B, Hq, Hkv, d) -> int:
+    return load().gdn_attn_workspace_bytes(B, Hq, Hkv, d)
+
+
+def gdn_attn_step(q, q_stride, k_cache, k_block_stride, v_cache, v_block_stride, k_scale, v_scale, block_table,
+                  table_stride, lens, out, lse, B, Hq, Hkv, d, page, blocks, W, window, sinks, scale, flags,
+                  workspace=None, workspace_bytes=0, stream=None) -> int:
+    """Attention of one token per request over a paged cache; returns the status."""
+    return load().gdn_attn_step(_ATTN_STEP.pack(
+        _addr(q), q_stride, _addr(k_cache), k_block_stride, _addr(v_cache), v_block_stride, _addr(k_scale),
+        _addr(v_scale), _addr(block_table), table_stride, _addr(lens), _addr(out), _addr(lse), B, Hq, Hkv, d, page,
+        blocks, W, window, sinks, scale, flags, _addr(workspace), workspace_bytes, _stream(stream)))
 
 
 def _want(cond, what) -> None:
@@ -659,3 +708,210 @@ def add_norm(x, weight, residual=None, *, eps=1e-6, group=0, e4m3=False, out=Non
         _plain(scales, "scales", torch.float32, (rows, -(-D // group) if group else 1), dev), rows, D, group, eps,
         GDN_NORM_E4M3 if e4m3 else 0, _raw_stream(stream, dev)), dev)
     return out, scales, residual_out
+
+
+# ---- attention over a paged cache --------------------------------------------------------------
+
+def _own_workspace(workspace, like) -> tuple:
+    """(address, bytes) of a given workspace, one piece on the device of x (an empty one has no address, and none
+    is the library's own)."""
+    if workspace is None:
+        return 0, 0
+    if workspace.device != like.device or not workspace.is_contiguous() or workspace.numel() == 0:
+        raise ValueError(f"workspace: contiguous, on the device of x, is wanted, got {tuple(workspace.shape)}, strides "
+                         f"{workspace.stride()}, on {workspace.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _int_arg(value, name, least) -> int:
+    if not isinstance(value, int) or not least <= value <= 0x7fffffff:
+        raise ValueError(f"{name}: an integer of at least {least} is wanted, got {value!r}")
+    return value
+
+
+def _table(t, name, B, dev) -> tuple:
+    """(address, columns, row stride) of block tables int32 [B, W] whose rows are contiguous."""
+    import torch
+
+    _want(t.dim() == 2, f"{name}: [B, W]")
+    W = t.shape[1]
+    stride = _rows(t, name, torch.int32, (B, W), dev)
+    return t.data_ptr(), W, stride
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev):
+    """The fields of a paged cache: (addresses and block strides, scales' addresses, page, blocks, flags)."""
+    import torch
+
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    _want(k_cache.dim() == 4 and k_cache.dtype in (torch.bfloat16, f8),
+          f"k_cache: bf16 or e4m3 [blocks, Hkv, page, d] is wanted, got {k_cache.dtype} {tuple(k_cache.shape)}")
+    e4m3 = k_cache.dtype is f8
+    blocks, _, page, _ = shape = k_cache.shape
+    _want(shape == (blocks, Hkv, page, d), f"k_cache: [blocks, {Hkv}, page, {d}] is wanted, got {tuple(shape)}")
+    where = []
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        st = t.stride()
+        if t.dtype is not k_cache.dtype or t.shape != shape or t.get_device() != dev:
+            raise ValueError(f"{name}: a {k_cache.dtype} tensor of shape {tuple(shape)} on the device of x is wanted, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        if blocks and not ((st[3] == 1 or d == 1) and (st[2] == d or page == 1) and (st[1] == page * d or Hkv == 1)):
+            raise ValueError(f"{name}: the elements of a block have to be contiguous (strides {st})")
+        where += [t.data_ptr(), st[0] if blocks > 1 else Hkv * page * d]
+    _want(max(shape) <= 0x7fffffff, f"k_cache: sizes are 32-bit, got {tuple(shape)}")
+    if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
+        raise ValueError("k_scale, v_scale: scales of the heads go with an e4m3 cache, and only with one")
+    scales = [_plain(k_scale, "k_scale", f32, (Hkv,), dev), _plain(v_scale, "v_scale", f32, (Hkv,), dev)]
+    return where, scales, page, blocks, GDN_CACHE_E4M3 if e4m3 else 0
+
+
+def cache_plan(lens, block_table, free_blocks, free_count, cu_seqlens=None, *, page, T=None, slots=None, new_lens=None,
+               new_count=None, refused=None, stream=None):
+    """New blocks for the requests that need them, put into `block_table`, and a slot for every new token.
+
+    lens: int32 [B], tokens in the cache (below 0: an idle row); block_table: int32 [B, W] (rows may be slices of
+    wider ones), updated in place; free_blocks: int32 [capacity], a stack, free_count: int32 [1], its height;
+    cu_seqlens: int32 [B+1], boundaries of the requests' new tokens among `T` (which `slots` implies where it is
+    given), None for one each.  Returns (slots int32 [T], new_lens int32 [B], new_count int32 [1], refused
+    int32 [1]: requests that got nothing), in the tensors given; new_lens may be lens and new_count free_count.
+    """
+    fast = _shorter()
+    if (fast is not None and slots is not None and new_lens is not None and new_count is not None and
+            refused is not None):
+        rc = fast.cache_plan(lens, block_table, free_blocks, free_count, cu_seqlens, page, T, slots, new_lens, new_count,
+                             refused, stream)
+        if rc is not None:
+            if rc:
+                check(rc)
+            return slots, new_lens, new_count, refused
+    import torch
+
+    i32 = torch.int32
+    _want(lens.dim() == 1 and free_blocks.dim() == 1, "lens: [B], free_blocks: [capacity]")
+    (B,), (capacity,), dev = lens.shape, free_blocks.shape, lens.get_device()
+    _want(max(B, capacity) <= 0x7fffffff, "lens, free_blocks: sizes are 32-bit")
+    _int_arg(page, "page", 1)
+    if T is None:
+        _want(slots is not None or cu_seqlens is None, "T: how many new tokens there are, or slots for them, is wanted")
+        T = slots.numel() if slots is not None else B
+    T = _int_arg(T, "T", 0)
+    _want(cu_seqlens is not None or T == B, f"T: {B} requests of one new token each are {B}, got {T}")
+    cu = 0 if cu_seqlens is None else _plain(cu_seqlens, "cu_seqlens", i32, (B + 1,), dev)
+    table, W, table_stride = _table(block_table, "block_table", B, dev)
+    fields = [_plain(lens, "lens", i32, (B,), dev), table, table_stride,
+              _plain(free_blocks, "free_blocks", i32, (capacity,), dev),
+              _plain(free_count, "free_count", i32, (1,), dev), cu]
+    made = []
+    for t, name, n in ((slots, "slots", T), (new_lens, "new_lens", B), (new_count, "new_count", 1), (refused, "refused", 1)):
+        made.append(_output((n,), i32, lens.device, stream) if t is None else t)
+        fields.append(_plain(made[-1], name, i32, (n,), dev))
+    _call(load().gdn_cache_plan, _PLAN.pack(*fields, B, T, W, capacity, page, _raw_stream(stream, dev)), dev)
+    return tuple(made)
+
+
+def cache_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, *, stream=None) -> None:
+    """Keys and values of new tokens to their slots of a paged cache.
+
+    k, v: bf16 [T, Hkv, d] (token rows may be slices of wider ones); k_cache, v_cache: bf16 or e4m3
+    [blocks, Hkv, page, d] (blocks may be further apart), updated in place; slots: int32 [T], different ones, below 0
+    for tokens to pass over; k_scale, v_scale: fp32 [Hkv], with an e4m3 cache.
+    """
+    fast = _shorter()
+    if fast is not None:
+        rc = fast.cache_append(k, v, k_cache, v_cache, slots, k_scale, v_scale, stream)
+        if rc is not None:
+            if rc:
+                check(rc)
+            return
+    import torch
+
+    bf16 = torch.bfloat16
+    _want(k.dim() == 3, "k, v: [T, Hkv, d]")
+    T, Hkv, d = shape = k.shape
+    dev = k.get_device()
+    ks, vs = _rows(k, "k", bf16, shape, dev), _rows(v, "v", bf16, shape, dev)
+    where, scales, page, blocks, flags = _cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    _call(load().gdn_cache_append, _APPEND.pack(
+        k.data_ptr(), ks, v.data_ptr(), vs, *where, *scales, _plain(slots, "slots", torch.int32, (T,), dev), T, Hkv, d,
+        page, blocks, flags, _raw_stream(stream, dev)), dev)
+
+
+def _attn_outputs(out, lse, want_lse, shape, like, dev, stream):
+    """(out, lse) and their addresses: those given, else new ones."""
+    import torch
+
+    bf16, f32 = torch.bfloat16, torch.float32
+    if out is None:
+        out = _output(shape, bf16, like.device, stream)
+    if lse is None and want_lse:
+        lse = _output(shape[:2], f32, like.device, stream)
+    return out, lse, _plain(out, "out", bf16, shape, dev), _plain(lse, "lse", f32, shape[:2], dev)
+
+
+def attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, B=None, window=0, sinks=0, scale=None, out=None, lse=None,
+              want_lse=False, workspace=None, stream=None):
+    """Causal attention of a dense batch of B sequences, or a packed one, with an optional window.
+
+    q: bf16 [T, Hq, d]; k, v: bf16 [Tk, Hkv, d] (token rows may be slices of wider ones); the queries of a sequence
+    are its last tokens, whose keys have boundaries of their own in cu_seqlens_k where they are more (or fewer).  With
+    window > 0 a query sees the last `window` tokens, itself among them, and the first `sinks`.  scale: of the
+    scores, 1 / sqrt(d) by default.  workspace: a byte tensor of gdn_attn_workspace_bytes(...), its first word
+    zeroed once, for calls that overlap or are captured.
+    Returns (out bf16 [T, Hq, d], lse fp32 [T, Hq] or None: the log of the sum of the weights).
+    """
+    fast = _shorter()
+    if fast is not None and out is not None and (lse is not None or not want_lse):
+        rc = fast.attention(q, k, v, cu_seqlens, cu_seqlens_k, B, window, sinks, scale, out, lse, workspace, stream)
+        if rc is not None:
+            if rc:
+                check(rc)
+            return out, lse
+    import torch
+
+    bf16 = torch.bfloat16
+    _want(q.dim() == 3 and k.dim() == 3, "q: [T, Hq, d], k and v: [Tk, Hkv, d]")
+    (n, Hq, d), (nk, Hkv, _), dev = q.shape, k.shape, q.get_device()
+    qs = _rows(q, "q", bf16, (n, Hq, d), dev)
+    ks, vs = (_rows(t, name, bf16, (nk, Hkv, d), dev) for t, name in ((k, "k"), (v, "v")))
+    B, T, cu = _batch(n, cu_seqlens, B, dev)
+    if cu_seqlens is None:
+        _want(cu_seqlens_k is None, "cu_seqlens_k: goes with cu_seqlens")
+        _, Tk, cuk = _batch(nk, None, B, dev)
+    else:
+        Tk, cuk = nk, _plain(cu_seqlens_k, "cu_seqlens_k", torch.int32, (B + 1,), dev)
+        _want(cu_seqlens_k is not None or n == nk, f"k: {n} tokens, as q, are wanted without cu_seqlens_k, got {nk}")
+    out, lse, out_at, lse_at = _attn_outputs(out, lse, want_lse, (n, Hq, d), q, dev, stream)
+    _call(load().gdn_attn, _ATTN.pack(
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cu, cuk, out_at, lse_at, B, T, Tk, Hq, Hkv, d,
+        _int_arg(window, "window", 0), _int_arg(sinks, "sinks", 0), d ** -0.5 if scale is None else scale, 0,
+        *_own_workspace(workspace, q), _raw_stream(stream, dev)), dev)
+    return out, lse
+
+
+def attention_step(q, k_cache, v_cache, block_table, lens, k_scale=None, v_scale=None, *, window=0, sinks=0, scale=None,
+                   out=None, lse=None, want_lse=False, workspace=None, stream=None):
+    """Attention of one token of each of B requests over a paged cache: q bf16 [B, Hq, d] (rows may be slices of
+    wider ones); the cache as in cache_append; block_table: int32 [B, W]; lens: int32 [B], tokens in the cache,
+    the new one included (below 1: the row gives 0).  The rest is as in attention."""
+    fast = _shorter()
+    if fast is not None and out is not None and (lse is not None or not want_lse):
+        rc = fast.attention_step(q, k_cache, v_cache, block_table, lens, k_scale, v_scale, window, sinks, scale, out, lse,
+                                 workspace, stream)
+        if rc is not None:
+            if rc:
+                check(rc)
+            return out, lse
+    import torch
+
+    _want(q.dim() == 3 and k_cache.dim() == 4, "q: [B, Hq, d], k_cache and v_cache: [blocks, Hkv, page, d]")
+    B, Hq, d = shape = q.shape
+    Hkv, dev = k_cache.shape[1], q.get_device()
+    qs = _rows(q, "q", torch.bfloat16, shape, dev)
+    where, scales, page, blocks, flags = _cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    table, W, table_stride = _table(block_table, "block_table", B, dev)
+    out, lse, out_at, lse_at = _attn_outputs(out, lse, want_lse, shape, q, dev, stream)
+    _call(load().gdn_attn_step, _ATTN_STEP.pack(
+        q.data_ptr(), qs, *where, *scales, table, table_stride, _plain(lens, "lens", torch.int32, (B,), dev), out_at,
+        lse_at, B, Hq, Hkv, d, page, blocks, W, _int_arg(window, "window", 0), _int_arg(sinks, "sinks", 0),
+        d ** -0.5 if scale is None else scale, flags, *_own_workspace(workspace, q), _raw_stream(stream, dev)), dev)
+    return out, lse

@@ -286,11 +286,12 @@ int gdn_prefill_static(const void *q, const void *k, const void *v,
 #define GDN_STATUS_BAD_CU_SEQLENS 8    /* cu_seqlens was not 0 = cu[0] <= ... <= cu[B] = T (entries clamped) */
 #define GDN_STATUS_NONFINITE_STATE 16  /* a final state of the fp16 state carry was not finite (see gdn_prefill) */
 #define GDN_STATUS_SMALL_STATE 32      /* a final state of the fp16 state carry stayed below 2^-12 (see gdn_prefill) */
+#define GDN_STATUS_BAD_PAGE 64         /* gdn_attn_step met a block that the cache does not have (unseen) */
 
 /*
  * gdn_device_status -- synchronise the current device, return the status bits
  * accumulated since the last call (in *status: the OR of the words of the library's
- * workspaces, gdn_prefill's and gdn_ssm_scan's, and, once gdn_prefill_static has run
+ * workspaces, gdn_prefill's, gdn_ssm_scan's and the attention's, and, once gdn_prefill_static has run
  * on the device, the fixed array's) and clear them.  Returns GDN_OK or GDN_ERR_LAUNCH.
  */
 int gdn_device_status(int *status);
@@ -536,6 +537,162 @@ typedef struct gdn_add_norm_args {
   void *stream;
 } gdn_add_norm_args;
 int gdn_add_norm(const gdn_add_norm_args *args);
+
+/* ---------------------------------------------------------------------------------------
+ * Attention, the other kind of layer between the recurrences, and its paged key-value cache.
+ * A server's step: gdn_cache_plan (blocks and slots of the new tokens), then in every layer
+ * gdn_cache_append and gdn_attn (prompts) or gdn_attn_step (one token of every request).
+ *
+ * What is said above of pointers, streams, strides, alignment and return codes holds here too.
+ * The cache of a layer is two tensors, k_cache and v_cache, [blocks, Hkv, page, d]: blocks of
+ * `page` tokens (a multiple of 16), a head's tokens of a block one after the other; bf16, or
+ * e4m3 with a scale a head (GDN_CACHE_E4M3: a value is its 8 bits times k_scale or v_scale of
+ * its head, fp32 [Hkv]).  A `*_block_stride` is the distance between blocks in elements, a
+ * multiple of 16.  A token's slot is block * page + its place in the block, below 2^31.
+ *
+ * Heads: query head h reads key head h / (Hq / Hkv); d is a multiple of 8 up to 128.
+ * ------------------------------------------------------------------------------------- */
+
+/* Flags of gdn_cache_append and gdn_attn_step. */
+#define GDN_CACHE_E4M3 1u /* the cache is e4m3 with scales, else bf16 */
+
+/*
+ * gdn_cache_plan -- new blocks for the requests that need them, and a slot for every new token.
+ *
+ *   lens         int32 [B]: tokens that each request has in the cache; below 0: an idle row
+ *   block_table  int32 [B, W], row stride table_stride: its blocks; new ones are put behind
+ *   free_blocks  int32 [capacity], the stack of free blocks; free_count int32 [1], its height
+ *   cu_seqlens   int32 [B + 1] or NULL: boundaries of the requests' new tokens among T (NULL: one
+ *                each, T = B); out-of-order entries read and write nothing out of range
+ *   slots        int32 [T]: slot of every new token; -1 for those of a request that is idle or
+ *                refused, for those behind the last request, and where the table is out of range
+ *   new_lens     int32 [B]: lens with the new tokens (may be `lens`)
+ *   new_count    int32 [1]: the stack's height after the call (may be `free_count`)
+ *   refused      int32 [1] or NULL: requests that got nothing
+ *
+ * Request b has ceil(lens / page) blocks and wants ceil((lens + new) / page).  Blocks go out from
+ * the top of the stack in the requests' order.  A request is refused as a whole (its length, its
+ * table and its blocks stay) when it would need more than W blocks, or when it needs blocks and
+ * those before it and it want more than there are; so one refused for lack of blocks takes those
+ * behind it that need blocks with it, not those that still have room.  B is at most 16,384.
+ */
+typedef struct gdn_cache_plan_args {
+  const int32_t *lens;
+  int32_t *block_table;
+  long long table_stride;
+  const int32_t *free_blocks, *free_count, *cu_seqlens;
+  int32_t *slots, *new_lens, *new_count, *refused;
+  int B, T, W, capacity, page;
+  void *stream;
+} gdn_cache_plan_args;
+int gdn_cache_plan(const gdn_cache_plan_args *args);
+
+/*
+ * gdn_cache_append -- the keys and values of T tokens, bf16 [T, Hkv, d], to their slots.
+ *
+ * Slots below 0 or past the cache are passed over.  With e4m3 a value is x / scale, rounded once and
+ * saturated (a NaN stays one).  Two tokens must not have the same slot: which of them each piece of
+ * eight values comes from is then unspecified.
+ */
+typedef struct gdn_cache_append_args {
+  const void *k;
+  long long k_stride;
+  const void *v;
+  long long v_stride;
+  void *k_cache;
+  long long k_block_stride;
+  void *v_cache;
+  long long v_block_stride;
+  const float *k_scale, *v_scale;
+  const int32_t *slots;
+  int T, Hkv, d, page, blocks;
+  unsigned flags;
+  void *stream;
+} gdn_cache_append_args;
+int gdn_cache_append(const gdn_cache_append_args *args);
+
+/*
+ * gdn_attn -- attention of prompts: causal, with an optional window and sinks:
+ *
+ *     o_i = sum_j w_ij v_j / sum_j w_ij,   w_ij = exp(scale q_i.k_j),   over the keys j that i sees
+ *
+ * The queries of a sequence are its last tokens: query i of n, with m keys, is at position
+ * p = m - n + i.  It sees the keys j <= p; with window > 0, of those the j > p - window and the
+ * j < sinks.  A query that sees no key gives 0 and an lse of minus infinity.
+ *
+ *   q, out        bf16 [T, Hq, d], [T, Hq, d];  k, v bf16 [Tk, Hkv, d];  token strides as above
+ *   cu_seqlens    int32 [B + 1] or NULL (dense: B sequences of T queries and Tk keys each; packed: T
+ *                 and Tk in all); rows of out behind the last sequence are left as they were
+ *   cu_seqlens_k  int32 [B + 1] or NULL: boundaries of the keys, where they are not the queries'
+ *   lse           fp32 [T, Hq] or NULL: log sum_j w_ij
+ *
+ * Hq / Hkv is at most 128.  Values in unseen keys and values, infinities and NaN included, change
+ * nothing.  Weights are rounded to bf16 as operands of the second product (2^-9 of each term); scores,
+ * sums and the running maximum are fp32.
+ *
+ * workspace: gdn_attn_workspace_bytes(...) bytes of device memory, 256-byte aligned, not shared with
+ * concurrent calls, or NULL for the library's own (shared by the calls on a device, as for
+ * gdn_ssm_scan).  With a workspace the call allocates nothing and can be captured into a CUDA graph.
+ * Its first word, which the caller clears, collects status bits; gdn_device_status reports those of
+ * the library's own.
+ */
+typedef struct gdn_attn_args {
+  const void *q;
+  long long q_stride;
+  const void *k;
+  long long k_stride;
+  const void *v;
+  long long v_stride;
+  const int32_t *cu_seqlens, *cu_seqlens_k;
+  void *out;
+  float *lse;
+  int B, T, Tk, Hq, Hkv, d, window, sinks;
+  float scale;
+  unsigned flags; /* 0 */
+  void *workspace;
+  size_t workspace_bytes;
+  void *stream;
+} gdn_attn_args;
+int gdn_attn(const gdn_attn_args *args);
+
+/* Bytes of workspace that gdn_attn and gdn_attn_step need for these sizes on the current device, whatever
+ * the lengths (0 on bad arguments). */
+size_t gdn_attn_workspace_bytes(int B, int Hq, int Hkv, int d);
+
+/*
+ * gdn_attn_step -- gdn_attn for one token of each of B requests over the paged cache.
+ *
+ *   q, out       bf16 [B, Hq, d]
+ *   block_table  int32 [B, W], row stride table_stride;  lens int32 [B]: tokens in the cache, the new
+ *                one included (its query is at position lens - 1); below 1: gives 0; above W * page:
+ *                counts as that
+ *   lse          fp32 [B, Hq] or NULL
+ *
+ * A block outside [0, blocks) counts as unseen and sets GDN_STATUS_BAD_PAGE; the table's entries behind
+ * a request's blocks are not read.  What the cache holds in places that are not seen changes nothing.
+ * Weights are rounded to the operands' 16-bit format, as in gdn_attn.
+ */
+typedef struct gdn_attn_step_args {
+  const void *q;
+  long long q_stride;
+  const void *k_cache;
+  long long k_block_stride;
+  const void *v_cache;
+  long long v_block_stride;
+  const float *k_scale, *v_scale;
+  const int32_t *block_table;
+  long long table_stride;
+  const int32_t *lens;
+  void *out;
+  float *lse;
+  int B, Hq, Hkv, d, page, blocks, W, window, sinks;
+  float scale;
+  unsigned flags;
+  void *workspace;
+  size_t workspace_bytes;
+  void *stream;
+} gdn_attn_step_args;
+int gdn_attn_step(const gdn_attn_step_args *args);
 
 #ifdef __cplusplus
 }
