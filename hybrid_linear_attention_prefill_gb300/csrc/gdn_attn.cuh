@@ -64,13 +64,13 @@ struct StepArgs {
 };
 
 // One query by a warp, in fp32 throughout: `key(j)` and `value(j)` give the addresses of a visible
-// token's d values, `widen(p, i, f)` eight of them from the i-th.  q: the query's values in shared memory.
+// token's d values, `widen(p, i, f)` eight of them from the i-th.  q: the query's values in global memory.
 // Lane l ends with columns 4 l .. 4 l + 3 of the sum, and every lane with the maximum and the weights' sum.
 struct RowSum {
   float o[4], m, l;
 };
 template <class Key, class Value, class Widen>
-__device__ __forceinline__ RowSum row_sum(const float* q, int d, float scale_log2, const Seen& s, Key key, Value value,
+__device__ __forceinline__ RowSum row_sum(const __nv_bfloat16* q, int d, float scale_log2, const Seen& s, Key key, Value value,
                                           Widen widen) {
   const int lane = threadIdx.x & 31;
   RowSum r = {{0.f, 0.f, 0.f, 0.f}, -INFINITY, 0.f};
@@ -83,10 +83,11 @@ __device__ __forceinline__ RowSum row_sum(const float* q, int d, float scale_log
       if (kp != nullptr) {
         float dot = 0.f;
         for (int c = 0; c < d; c += 8) {
-          float2 f[4];
+          float2 f[4], g[4];
           widen(kp, c, f);
+          widen8(*reinterpret_cast<const uint4*>(q + c), g);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) dot = fmaf(q[c + 2 * i], f[i].x, fmaf(q[c + 2 * i + 1], f[i].y, dot));
+          for (int i = 0; i < 4; ++i) dot = fmaf(g[i].x, f[i].x, fmaf(g[i].y, f[i].y, dot));
         }
         t = dot * scale_log2;
       }

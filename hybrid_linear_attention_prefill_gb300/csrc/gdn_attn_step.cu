@@ -29,14 +29,11 @@ struct WidenE4m3 {
 template <class T, class Widen>
 __global__ void __launch_bounds__(32 * kRowWarps)
 gdn_attn_step_rows_kernel(const attn::StepArgs a, int* __restrict__ err) {
-  __shared__ __align__(16) float qf[kRowWarps][attn::kMaxDim];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const int b = blockIdx.x, h = blockIdx.y * kRowWarps + warp;
   if (h >= a.Hq) return;
   const int hk = h / (a.Hq / a.Hkv);
   const __nv_bfloat16* q = a.q + b * a.qs + (long long)h * a.d;
-  for (int c = lane; c < a.d; c += 32) qf[warp][c] = __bfloat162float(q[c]);
-  __syncwarp();
   const long long most = (long long)a.W * a.page;
   const int n = a.lens[b] < most ? a.lens[b] : (int)most;
   auto at = [&](const void* c, long long stride, int j) -> const T* {
@@ -49,7 +46,7 @@ gdn_attn_step_rows_kernel(const attn::StepArgs a, int* __restrict__ err) {
   };
   const float ks = a.kscale != nullptr ? a.kscale[hk] : 1.f, vs = a.vscale != nullptr ? a.vscale[hk] : 1.f;
   const attn::RowSum r = attn::row_sum(
-      qf[warp], a.d, a.scale * ks * attn::kLog2e, attn::seen_by(a.view, n - 1), [&](int j) { return at(a.kc, a.kbs, j); },
+      q, a.d, a.scale * ks * attn::kLog2e, attn::seen_by(a.view, n - 1), [&](int j) { return at(a.kc, a.kbs, j); },
       [&](int j) { return at(a.vc, a.vbs, j); }, Widen());
   const long long row = (long long)b * a.Hq + h;
   attn::put_row(r, a.d, a.out + row * a.d, a.lse != nullptr ? a.lse + row : nullptr, vs);

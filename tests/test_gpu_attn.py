@@ -540,8 +540,11 @@ def test_attention_rows_behind_the_last_sequence(gdn):
     q[301:], k[301:], v[301:] = NAN, NAN, NAN
     gdn.attention(q, k, v, cu_of([100, 201]), out=out, lse=lse)
     assert bool((out[301:] == 7).all()) and bool((lse[301:] == 7).all())
-    want, want_lse = check_attn(gdn, q[:301], k[:301], v[:301], [100, 201])
-    assert torch.equal(out[:301], want) and torch.equal(lse[:301], want_lse)
+    # (rows beside values that are not finite are worked out apart, with other roundings: both within the tolerance)
+    for a, b in ((0, 100), (100, 301)):
+        y, mag, l, bound = R.attend(n64(q[a:b]), n64(k[a:b]), n64(v[a:b]), 128 ** -0.5)
+        close(out[a:b], y, mag, bound)
+        close_lse(lse[a:b], l, bound)
 
 
 @pytest.mark.parametrize("value", [NAN, float("inf"), -float("inf")])
