@@ -129,8 +129,9 @@ int ensure(void*& ptr, size_t& have, size_t need) {
 }
 
 // The same for a workspace whose first 256 bytes are status words: a new one's are cleared on stream `st`, in the order
-// of the call that writes them, but for the first word, which keeps the bits of the calls before.
-int ensure_workspace(void*& ptr, size_t& have, size_t need, cudaStream_t st) {
+// of the call that writes them, but for the first word, which keeps the bits of the calls before.  With `all` the rest
+// is cleared too.
+int ensure_workspace(void*& ptr, size_t& have, size_t need, cudaStream_t st, bool all = false) {
   if (need <= have) return GDN_OK;
   int bits = 0;
   cudaError_t e = cudaSuccess;
@@ -139,7 +140,7 @@ int ensure_workspace(void*& ptr, size_t& have, size_t need, cudaStream_t st) {
     return set_cuda_error(e, GDN_ERR_LAUNCH);
   const int rc = ensure(ptr, have, need);
   if (rc != GDN_OK) return rc;
-  e = cudaMemsetAsync(ptr, 0, 256, st);
+  e = cudaMemsetAsync(ptr, 0, all ? have : 256, st);
   if (e == cudaSuccess && bits != 0) e = cudaMemcpyAsync(ptr, &bits, sizeof(bits), cudaMemcpyHostToDevice, st);
   return e == cudaSuccess ? GDN_OK : set_cuda_error(e, GDN_ERR_LAUNCH);
 }
@@ -434,22 +435,22 @@ int device_sms() {
 }
 
 static int ensure_own(void* DevBuffers::*ws_of, size_t DevBuffers::*bytes_of, int dev, size_t need, cudaStream_t st,
-                      void** ws) {
+                      void** ws, bool all) {
   if (dev < 0 || dev >= kMaxDevices) return GDN_ERR_ARG;
   std::lock_guard<std::mutex> lock(g_mu);
   DevBuffers& d = g_dev[dev];
-  const int rc = ensure_workspace(d.*ws_of, d.*bytes_of, need, st);
+  const int rc = ensure_workspace(d.*ws_of, d.*bytes_of, need, st, all);
   if (rc != GDN_OK) return rc;
   *ws = d.*ws_of;
   return GDN_OK;
 }
 
 int ensure_ssm_workspace(int dev, size_t need, cudaStream_t st, void** ws) {
-  return ensure_own(&DevBuffers::ssm, &DevBuffers::ssm_bytes, dev, need, st, ws);
+  return ensure_own(&DevBuffers::ssm, &DevBuffers::ssm_bytes, dev, need, st, ws, false);
 }
 
 int ensure_attn_workspace(int dev, size_t need, cudaStream_t st, void** ws) {
-  return ensure_own(&DevBuffers::attn, &DevBuffers::attn_bytes, dev, need, st, ws);
+  return ensure_own(&DevBuffers::attn, &DevBuffers::attn_bytes, dev, need, st, ws, true);
 }
 
 }  // namespace gdn

@@ -31,7 +31,7 @@ int device_sms();
 // return.
 int ensure_ssm_workspace(int dev, size_t need, cudaStream_t st, void** ws);
 
-// The same of gdn_attn and gdn_attn_step.
+// The same of gdn_attn and gdn_attn_step (all of a new one is cleared).
 int ensure_attn_workspace(int dev, size_t need, cudaStream_t st, void** ws);
 
 }  // namespace gdn

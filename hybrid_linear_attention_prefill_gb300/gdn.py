@@ -855,8 +855,8 @@ def attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, B=None, window=0, 
     q: bf16 [T, Hq, d]; k, v: bf16 [Tk, Hkv, d] (token rows may be slices of wider ones); the queries of a sequence
     are its last tokens, whose keys have boundaries of their own in cu_seqlens_k where they are more (or fewer).  With
     window > 0 a query sees the last `window` tokens, itself among them, and the first `sinks`.  scale: of the
-    scores, 1 / sqrt(d) by default.  workspace: a byte tensor of gdn_attn_workspace_bytes(...), its first word
-    zeroed once, for calls that overlap or are captured.
+    scores, 1 / sqrt(d) by default.  workspace: a byte tensor of gdn_attn_workspace_bytes(...), zeroed once, for
+    calls that overlap or are captured.
     Returns (out bf16 [T, Hq, d], lse fp32 [T, Hq] or None: the log of the sum of the weights).
     """
     fast = _shorter()

@@ -634,8 +634,8 @@ int gdn_cache_append(const gdn_cache_append_args *args);
  * workspace: gdn_attn_workspace_bytes(...) bytes of device memory, 256-byte aligned, not shared with
  * concurrent calls, or NULL for the library's own (shared by the calls on a device, as for
  * gdn_ssm_scan).  With a workspace the call allocates nothing and can be captured into a CUDA graph.
- * Its first word, which the caller clears, collects status bits; gdn_device_status reports those of
- * the library's own.
+ * The caller clears all of it once, before its first call; its first word collects status bits, and
+ * gdn_device_status reports those of the library's own.
  */
 typedef struct gdn_attn_args {
   const void *q;
