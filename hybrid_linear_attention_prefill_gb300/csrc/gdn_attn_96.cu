@@ -1,0 +1,6 @@
+// Attention of prompts with heads of 72 to 96 columns (gdn_attn_tile.cuh).
+#include "gdn_attn_tile.cuh"
+
+namespace gdn {
+template cudaError_t launch_attn_tiles<3>(const attn::PromptArgs&, void*, cudaStream_t);
+}  // namespace gdn

@@ -1,0 +1,723 @@
+// Attention of prompts on the tensor cores (sm_103a; gdn_attn.cuh has the mathematics); one translation unit per 32
+// columns of a head instantiates it.
+//
+// A row is a query of one head.  The heads that share a key head go into one tile, 128 / G tokens of G
+// heads, so that a key is read once for all of them and a mask's edge crosses few keys.  A CTA works on
+// two such tiles side by side: while the tensor core multiplies for one, four warps take the other's
+// scores to weights, a row a thread, so that a row's maximum and sum need no exchange.
+//
+//   scores  S = Q K^T              128 x 128, operands from shared memory, into TMEM
+//   weights P = exp2(c S - m)      in the place of S, bf16, as the next product's operand in TMEM
+//   output  O += P V               128 x d in TMEM
+//
+// m is the row's running maximum, but an older one stays in use until the new one is 2^8 above it: the
+// weights are then up to 2^8 and their sums as exact as before, and O is rescaled only now and then.
+// Sums, maxima, scores and O are fp32.
+//
+// Roles, 16 warps: four for each tile's weights; four that write finished tiles out while the next item's
+// products run; one for each tile that issues MMAs, one that issues copies, one that works out the items.  They meet on
+// mbarriers only.  A CTA takes an item (256 rows of a key head) after another; the ring of key and value
+// tiles runs on across items.
+//
+// A value that is not finite in a place that a row does not see would reach the row as 0 x infinity.
+// So a finished row that is not finite is worked out again from the keys it sees alone.
+#pragma once
+
+#include <algorithm>
+#include <cfloat>
+#include <type_traits>
+
+#include "gdn_attn.cuh"
+#include "gdn_internal.h"
+#include "gdn_tc.cuh"
+#include "gdn_tmap.cuh"
+
+namespace gdn {
+
+namespace {
+
+using attn::PromptArgs;
+using attn::Seen;
+using attn::View;
+
+constexpr int kThreads = 512;
+constexpr int kOutWarp = 8, kMmaWarp = 12, kLoadWarp = 13, kItemWarp = 14;  // (and 15)
+constexpr int kKeys = 128;            // a tile
+constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns: two score tiles of 128, two outputs of 128
+constexpr int kItemSlots = 4;
+constexpr long long kPatience = 1LL << 34;  // clocks of a wait, about eight seconds; then it gives up
+// Where a CTA's dynamic shared memory starts in its window, behind the KiB that the system keeps: known here so that the
+// descriptors of the products are constants, and looked at by every CTA.
+constexpr uint32_t kSmemBase = 1024;
+constexpr float kLazy = 8.f;           // how far (log2) a maximum may be above the one in use
+
+// Shared memory: two tiles of queries, a ring of tiles of keys and values, statistics, items, barriers.  A tile is
+// 128 rows, in halves of 64 columns; products take the head's columns in 32s (past d they are zeros).
+constexpr int kHalf = 16384;
+template <int kQuarters>
+struct Cfg {
+  static constexpr int kHalves = (kQuarters + 1) / 2, kTile = kHalves * kHalf, kRing = kHalves == 2 ? 2 : 4;
+  static constexpr int kOffQ = 0, kOffK = 2 * kTile, kOffV = kOffK + kRing * kTile, kOffStat = kOffV + kRing * kTile;
+  static constexpr int kOffItem = kOffStat + 2 * 128 * 8, kOffBar = kOffItem + kItemSlots * 128;
+  static constexpr int kBars = 4 * kRing + 2 * kItemSlots + 2 * 10;
+  static constexpr int kSmem = kOffBar + kBars * 8 + 16;
+  static_assert(kSmem <= 227 * 1024 && kSmem > 116 * 1024, "one CTA an SM");
+};
+template <int N>
+using Slot = std::integral_constant<int, N>;
+// f with the ring's slot as a constant, which the products' operands are made of: an MMA whose descriptors are
+// constants is issued in less than the 64 clocks that it takes, one whose are worked out in 110.
+template <int kRing, class F>
+__device__ __forceinline__ bool in_slot(int slot, F f) {
+  if (slot == 0) return f(Slot<0>());
+  if (kRing == 2 || slot == 1) return f(Slot<1>());
+  if (slot == 2) return f(Slot<2 % kRing>());
+  return f(Slot<3 % kRing>());
+}
+
+// The keys that an item's queries see, one list: the first `sink` of the sequence (sinks, rounded up to 16; none where
+// the window reaches them), then those from `lo` on, where the first query's window starts.  A tile of keys is 128
+// places of the list; the one with the seam is loaded in boxes of 16.
+struct Item {
+  int valid;
+  int q0, n[2];  // first query (among all tokens), queries of either tile
+  int p0;        // the first one's position
+  int k0;        // the sequence's first key
+  int hk;
+  int sink, lo;
+  int tiles;     // of keys
+  int sinks;     // tiles of keys with sinks
+  int a[2], z[2];  // tiles of keys [a, z) that either tile of queries sees otherwise
+  __device__ __forceinline__ bool has(int t, int kt) const { return (kt < sinks && z[t] > 0) || (kt >= a[t] && kt < z[t]); }
+  __device__ __forceinline__ int count(int t) const { return z[t] > 0 ? sinks + z[t] - a[t] : 0; }
+  __device__ __forceinline__ int place(int key) const { return key - lo + sink; }  // of a key from `lo` on
+};
+static_assert(sizeof(Item) <= 128, "a slot");
+
+__device__ __forceinline__ void find_keys(Item& it, const View& view, int tpt) {
+  const int first = it.n[0] > 0 && it.p0 + it.n[0] > 0 ? 0 : 1;  // the first tile that sees any
+  it.lo = attn::seen_by(view, it.p0 + first * tpt).lo;
+  it.sink = (min(view.sinks, it.lo) + 15) / 16 * 16;
+  if (view.sinks == 0) it.sink = 0;
+  else if (it.sink >= it.lo) it.sink = it.lo = 0;
+  it.sinks = (it.sink + kKeys - 1) / kKeys;
+  it.tiles = 0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int pa = it.p0 + t * tpt, pb = pa + it.n[t] - 1;
+    it.a[t] = it.z[t] = 0;
+    if (it.n[t] <= 0 || pb < 0) continue;
+    const int lo = attn::seen_by(view, pa).lo;
+    it.z[t] = (it.place(pb + 1) + kKeys - 1) / kKeys;
+    it.a[t] = max(it.sinks, view.sinks > 0 && it.sink == 0 ? 0 : it.place(lo) / kKeys);
+    it.tiles = max(it.tiles, it.z[t]);
+  }
+}
+
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Whether a phase has passed, without waiting for it.
+__device__ __forceinline__ bool passed(uint64_t* bar, uint32_t par) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(par)
+      : "memory");
+  return done != 0;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+__device__ __forceinline__ void tmem_st16_start(uint32_t a, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(a),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// Bits [lo, hi) of 32, of bounds that may lie outside.
+__device__ __forceinline__ uint32_t bits(int lo, int hi) {
+  const uint32_t below_hi = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u;
+  const uint32_t below_lo = lo >= 32 ? ~0u : lo <= 0 ? 0u : (1u << lo) - 1u;
+  return below_hi & ~below_lo;
+}
+
+}  // namespace
+
+template <int kQuarters>
+__global__ void __launch_bounds__(kThreads, 1)
+gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k16,
+                     const __grid_constant__ CUtensorMap tm_v16, const attn::PromptArgs a, int items, int tpt,
+                     float scale_log2, int negate, int* __restrict__ err) {
+  using C = Cfg<kQuarters>;
+  constexpr int kTile = C::kTile, kHalves = C::kHalves, kRing = C::kRing;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* sm = smem_raw;
+  float2* stat = reinterpret_cast<float2*>(sm + C::kOffStat);  // [tile][row]: maximum in use (log2), sum
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
+  uint64_t *k_full = bars, *k_empty = k_full + kRing, *v_full = k_empty + kRing, *v_empty = v_full + kRing,
+           *item_full = v_empty + kRing, *item_empty = item_full + kItemSlots, *q_full = item_empty + kItemSlots,
+           *q_empty = q_full + 2, *s_full = q_empty + 2, *p_half = s_full + 2, *p_full = p_half + 2, *st_full = p_full + 2,
+           *o_full = st_full + 2, *o_empty = o_full + 2, *turn = o_empty + 2, *drain = turn + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.Hq / a.Hkv;
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(tmem_slot, 512);
+    tc::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      tc::mbar_init(k_full + i, 1);
+      tc::mbar_init(v_full + i, 1);
+      tc::mbar_init(k_empty + i, 2);  // by the warps of either tile
+      tc::mbar_init(v_empty + i, 2);
+    }
+    for (int i = 0; i < kItemSlots; ++i) {
+      tc::mbar_init(item_full + i, 1);
+      tc::mbar_init(item_empty + i, 15);  // twelve warps of weights and outputs, three that issue
+    }
+    for (int t = 0; t < 2; ++t) {
+      tc::mbar_init(q_full + t, 1);
+      tc::mbar_init(q_empty + t, 1);
+      tc::mbar_init(s_full + t, 1);
+      tc::mbar_init(p_half + t, 4);
+      tc::mbar_init(p_full + t, 4);
+      tc::mbar_init(st_full + t, 4);
+      tc::mbar_init(o_full + t, 1);
+      tc::mbar_init(o_empty + t, 4);
+      tc::mbar_init(turn + t, 1);
+      tc::mbar_init(drain + t, 1);
+    }
+    *abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    tc::prefetch_tensormap(&tm_q);
+    tc::prefetch_tensormap(&tm_k);
+    tc::prefetch_tensormap(&tm_v);
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;  // 0, since it is all of it
+
+  auto give_up = [&](int bit) {
+    *abort_flag = 1;
+    atomicOr(err, bit);
+  };
+  if (smem_u32(smem_raw) != kSmemBase) give_up(1);
+  // One thread's wait; false once this or another wait has run out.
+  auto wait = [&](uint64_t* bar, uint32_t par, int bit) {
+    if (tc::mbar_wait(bar, par, 8)) return true;
+    const long long since = clock64();
+    while (!*abort_flag) {
+      if (tc::mbar_wait(bar, par, 8)) return true;
+      if (clock64() - since > kPatience) give_up(bit);
+    }
+    return false;
+  };
+  // A warp's, which ends for its lanes together.
+  auto warp_wait = [&](uint64_t* bar, uint32_t par, int bit) {
+    return __all_sync(0xffffffffu, wait(bar, par, bit)) != 0;
+  };
+  // The n-th item of this CTA (one thread of a warp waits for the others' sake where `alone`).
+  auto item_at = [&](int n) { return reinterpret_cast<const Item*>(sm + C::kOffItem + (n % kItemSlots) * 128); };
+  auto item_par = [](int n) { return (uint32_t)(n / kItemSlots) & 1u; };
+
+  // The launch's 128 registers a thread are dealt out anew (2 x 168 + 88 + 88 = 4 x 128): a row of scores takes 128.
+  if (warp >= kMmaWarp) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+  if (warp == kItemWarp) {
+    // ---- the items: those of one rank of the grid after another, forwards and backwards in turn, so that
+    // the CTAs' sums are alike where the items' sizes fall steadily
+    const int per = 2 * tpt;
+    int b = 0, base = 0;  // of a packed batch: sequences and items (of a head) before
+    const int nseq = a.cu == nullptr ? (a.T + per - 1) / per : 0;
+    const int heads = a.Hkv;
+    bool more = true;
+    for (int n = 0; more; ++n) {
+      const long long idx = (long long)n * gridDim.x + (n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      int sb = -1, tile = 0, hk = 0;
+      more = idx < items;
+      if (more && a.cu == nullptr) {  // the last tiles, which see the most, first
+        const int rest = (int)(idx % ((long long)a.B * heads));
+        tile = nseq - 1 - (int)(idx / ((long long)a.B * heads));
+        sb = rest / heads;
+        hk = rest - sb * heads;
+      } else if (more) {
+        const int f = (int)(idx / heads);
+        hk = (int)(idx - (long long)f * heads);
+        while (b < a.B) {  // 32 sequences at a time
+          const int c = b + lane < a.B ? (seq_bounds(a.cu, b + lane, a.T).len + per - 1) / per : 0;
+          int sum = c;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+          }
+          const unsigned hit = __ballot_sync(0xffffffffu, base + sum > f);
+          if (hit != 0) {
+            const int l = __ffs(hit) - 1;
+            sb = b + l;
+            tile = __shfl_sync(0xffffffffu, c, l) - 1 - (f - (base + __shfl_sync(0xffffffffu, sum - c, l)));
+            break;
+          }
+          base += __shfl_sync(0xffffffffu, sum, 31);
+          b += 32;
+        }
+        more = sb >= 0;
+      }
+      if (n >= kItemSlots && !warp_wait(item_empty + n % kItemSlots, item_par(n - kItemSlots), 1)) break;
+      if (lane == 0) {
+        Item it = {};
+        it.valid = more;
+        if (more) {
+          const SeqChunk sq = seq_bounds(a.cu, sb, a.T), sk = seq_bounds(a.cuk, sb, a.Tk);
+          const int first = tile * per;
+          it.q0 = (int)sq.bos + first;
+          it.n[0] = min(tpt, sq.len - first);
+          it.n[1] = min(tpt, sq.len - first - tpt);
+          it.p0 = first + sk.len - sq.len;
+          it.k0 = (int)sk.bos;
+          it.hk = hk;
+          find_keys(it, a.view, tpt);
+        }
+        *reinterpret_cast<Item*>(sm + C::kOffItem + (n % kItemSlots) * 128) = it;
+        arrive(item_full + n % kItemSlots);
+      }
+    }
+  } else if (warp == kLoadWarp) {
+    // ---- copies: an item's queries, then its tiles of keys and values in turn
+    if (lane == 0) {
+      long long loads = 0;  // tiles of keys, and of values
+      int queries[2] = {0, 0};
+      bool ok = true;
+      // the list's places from v0 on into a slot
+      auto tile_in = [&](const CUtensorMap* whole, const CUtensorMap* part, unsigned char* to, uint64_t* full,
+                         uint64_t* empty, const Item& it, int v0) {
+        if (loads >= kRing && !wait(empty, (uint32_t)(loads / kRing - 1) & 1u, 2)) return false;
+        tc::mbar_arrive_expect_tx(full, kTile);
+        if (v0 < it.sink && v0 + kKeys > it.sink) {
+          for (int i = 0; i < kKeys; i += 16) {
+            const int tok = it.k0 + (v0 + i < it.sink ? v0 + i : it.lo + v0 + i - it.sink);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+              tc::tma_load_3d(to + h * kHalf + i * 128, part, 64 * h, it.hk, tok, full);
+          }
+        } else {
+          const int tok = it.k0 + (v0 < it.sink ? v0 : it.lo + v0 - it.sink);
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) tc::tma_load_3d(to + h * kHalf, whole, 64 * h, it.hk, tok, full);
+        }
+        return true;
+      };
+      for (int n = 0; ok; ++n) {
+        if (!(ok = wait(item_full + n % kItemSlots, item_par(n), 2))) break;
+        const Item it = *item_at(n);
+        arrive(item_empty + n % kItemSlots);
+        if (!it.valid) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || (n > 0 && !(ok = wait(q_empty + t, (n - 1) & 1, 2)))) break;
+          ++queries[t];
+          tc::mbar_arrive_expect_tx(q_full + t, kHalves * 128 * G * tpt);
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+            tc::tma_load_3d(sm + C::kOffQ + t * kTile + h * kHalf, &tm_q, 64 * h, it.hk * G, it.q0 + t * tpt,
+                            q_full + t);
+        }
+        for (int kt = 0; ok && kt < it.tiles; ++kt) {
+          const int slot = (int)(loads % kRing);
+          ok = tile_in(&tm_k, &tm_k16, sm + C::kOffK + slot * kTile, k_full + slot, k_empty + slot, it, kt * kKeys) &&
+               tile_in(&tm_v, &tm_v16, sm + C::kOffV + slot * kTile, v_full + slot, v_empty + slot, it, kt * kKeys);
+          if (ok) ++loads;
+        }
+      }
+      // what is in flight lands before the CTA ends, whoever gave up (bounded again; after a wait that gave up a
+      // tile of keys may be one ahead of its values)
+      for (int i = 0; i < kRing; ++i)
+        if (i < loads || !ok) {
+          const uint32_t p = (uint32_t)((loads - 1 - i) / kRing) & 1u;
+          for (uint32_t x = ok ? p : 0; x <= (ok ? p : 1); ++x) {
+            (void)tc::mbar_wait(k_full + i, x, 1u << 14);
+            (void)tc::mbar_wait(v_full + i, x, 1u << 14);
+          }
+        }
+      for (int t = 0; t < 2; ++t)
+        if (queries[t] > 0) (void)tc::mbar_wait(q_full + t, (uint32_t)(queries[t] - 1) & 1u, 1u << 14);
+    }
+    __syncwarp();
+  } else {
+    // ---- products, a warp for either tile of queries: the last weights' product, then the next scores in the weights'
+    // place.  The two warps take turns, so that the tensor core works on one tile while the other's weights are made
+    // (left to themselves they fall into step).  Looking at a barrier takes 200 clocks beside running products: a warp's
+    // lanes look at all that a step waits for at once, and while the other warp has its turn.
+    auto products = [&](auto tile) {
+      constexpr int t = decltype(tile)::value;
+      constexpr uint32_t id_o = tc::idesc_bf16(128, 32 * kQuarters, 0, 1), sb = kSmemBase;
+      const uint32_t id_s = tc::idesc_bf16(128, kKeys, 0, 0) | (negate ? 1u << 13 : 0u);
+      bool on = false, first = false, last = false;  // weights whose product is to come
+      int o_item = 0;                                // their item
+      uint32_t p_par = 0;
+      uint32_t tiles = 0;  // of keys, in all: the ring's slot and phase, and the turn
+      bool ok = true;
+      // Until every lane's barrier (null: none) has passed its phase, but for those of lanes that need not; the lanes whose
+      // has, 0 after giving up.
+      auto look = [&](uint64_t* bar, uint32_t par, bool must = true) -> uint32_t {
+        bool done = bar == nullptr;
+        long long since = 0;
+        for (int i = 0;; ++i) {
+          if (!done) done = must ? tc::mbar_wait(bar, par, 1) : passed(bar, par);
+          if (__all_sync(0xffffffffu, done || !must)) return __ballot_sync(0xffffffffu, done) | 1u << 31;
+          if ((i & 255) == 255) {
+            if (since == 0) since = clock64();
+            if (lane == 0 && clock64() - since > kPatience) give_up(1);
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) return 0;
+          }
+        }
+      };
+      // The pending product, with the values of slot S, the one before `tiles`; `keys`, `turn`: what else to wait for.
+      auto flush = [&](auto slot, uint64_t* keys, uint64_t* turn, uint32_t turn_par) {
+        constexpr int S = decltype(slot)::value;
+        uint64_t* bar = nullptr;
+        uint32_t par = 0;
+        if (lane == 0 && tiles > 0) bar = v_full + S, par = ((tiles - 1) / kRing) & 1u;
+        if (lane == 1) bar = keys, par = (tiles / kRing) & 1u;
+        if (lane == 2 && on) bar = p_half + t, par = p_par;
+        if (lane == 3 && on && first && o_item > 0) bar = o_empty + t, par = (uint32_t)(o_item - 1) & 1u;
+        if (lane == 4) bar = turn, par = turn_par;
+        if (lane == 5 && on) bar = p_full + t, par = p_par;  // (often there by now)
+        const uint32_t seen = look(bar, par, lane != 5);
+        if (seen == 0) return false;
+        if (!on) return true;
+        const uint64_t v = tc::sdesc(sb + C::kOffV + S * kTile, kHalf, 1024, tc::kSw128);
+        if (lane == 0) {
+          const uint32_t more = first ? 0u : 1u;
+          tc::fence_after();
+#pragma unroll
+          for (int k = 0; k < kKeys / 32; ++k)
+            tc::mma_f16_ta(kColO + t * 128, kColS + t * 128 + 8 * k, v + ((k * 2048) >> 4), id_o, k > 0 ? 1u : more);
+        }
+        __syncwarp();
+        if (!(seen >> 5 & 1u) && !look(lane == 0 ? p_full + t : nullptr, p_par)) return false;
+        if (lane == 0) {
+          tc::fence_after();
+#pragma unroll
+          for (int k = kKeys / 32; k < kKeys / 16; ++k)
+            tc::mma_f16_ta(kColO + t * 128, kColS + t * 128 + 8 * k, v + ((k * 2048) >> 4), id_o, 1u);
+          if (last) tc::commit(o_full + t);
+        }
+        __syncwarp();
+        p_par ^= 1u;
+        on = false;
+        return true;
+      };
+      auto flush_alone = [&]() {
+        return in_slot<kRing>((int)((tiles + kRing - 1) % kRing), [&](auto slot) { return flush(slot, nullptr, nullptr, 0); });
+      };
+      for (int n = 0;; ++n) {
+        if (!(ok = warp_wait(item_full + n % kItemSlots, item_par(n), 1))) break;
+        const Item* ip = item_at(n);
+        const int valid = ip->valid, all = ip->tiles, sinks = ip->z[t] > 0 ? ip->sinks : 0, from = ip->a[t], to = ip->z[t];
+        const int total = ip->count(t);
+        __syncwarp();
+        if (lane == 0) arrive(item_empty + n % kItemSlots);
+        if (!valid) break;
+        int left = total;
+        for (int kt = 0; ok && kt < all; ++kt) {
+          ok = in_slot<kRing>((int)(tiles % kRing), [&](auto slot) {
+            constexpr int S = decltype(slot)::value, before = (S + kRing - 1) % kRing;
+            const bool some = kt < sinks || (kt >= from && kt < to);
+            // (an item's first keys and queries apart, so that the last item's product does not wait for them)
+            if (!flush(Slot<before>(), kt > 0 ? k_full + S : nullptr, t == 1 || tiles > 0 ? turn + t : nullptr,
+                       t == 1 ? tiles & 1u : (tiles - 1) & 1u))
+              return false;
+            if (kt == 0) {
+              uint64_t* bar = lane == 0 ? q_full + t : lane == 1 ? k_full + S : nullptr;
+              if (!look(bar, lane == 0 ? (uint32_t)n & 1u : (tiles / kRing) & 1u)) return false;
+            }
+            if (lane == 0) {
+              if (some) {
+                const uint64_t q = tc::sdesc(sb + C::kOffQ + t * kTile, 16, 1024, tc::kSw128);
+                const uint64_t k = tc::sdesc(sb + C::kOffK + S * kTile, 16, 1024, tc::kSw128);
+                tc::fence_after();
+#pragma unroll
+                for (int i = 0; i < 2 * kQuarters; ++i) {  // (a step under a run-time condition was compiled wrong)
+                  const uint64_t off = (uint64_t)(((i >> 2) * kHalf + (i & 3) * 32) >> 4);
+                  tc::mma_bf16(kColS + t * 128, q + off, k + off, id_s, i > 0);
+                  // the other warp's turn, so that its products are there when these end
+                  if (i == kQuarters - 1) arrive(turn + 1 - t);
+                }
+                tc::commit(s_full + t);
+              } else {
+                arrive(turn + 1 - t);
+              }
+              if (some && left == 1) tc::commit(q_empty + t);
+              if (tiles > 0) tc::commit(v_empty + before);
+              tc::commit(k_empty + S);
+            }
+            __syncwarp();
+            if (some) {
+              on = true;
+              first = left == total;
+              last = --left == 0;
+              o_item = n;
+            }
+            return true;
+          });
+          ++tiles;
+        }
+        if (!ok) break;
+        if (total == 0) {  // nothing to see: the phases go by in order all the same, after what is pending
+          ok = flush_alone() && (all > 0 || look(lane == 0 ? q_full + t : nullptr, (uint32_t)n & 1u)) &&
+               (n == 0 || look(lane == 0 ? o_empty + t : nullptr, (uint32_t)(n - 1) & 1u));
+          if (!ok) break;
+          if (lane == 0) tc::commit(q_empty + t);
+          __syncwarp();
+        }
+      }
+      if (ok) ok = flush_alone();
+      if (lane == 0) {
+        tc::commit(drain + t);
+        if (!tc::mbar_wait(drain + t, 0, 1u << 16)) give_up(1);
+      }
+    };
+    if (warp == kMmaWarp) products(Slot<0>());
+    else products(Slot<1>());
+    __syncwarp();
+  }
+  } else if (warp < kOutWarp) {
+    // ---- weights: a row a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n");
+    const int t = warp >> 2, row = tid & 127, tr = row / G;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t s_at = tmem + lanes + kColS + t * 128, o_at = tmem + lanes + kColO + t * 128;
+    uint32_t s_par = 0;
+    for (int n = 0;; ++n) {
+      if (!warp_wait(item_full + n % kItemSlots, item_par(n), 1)) break;
+      const Item* ip = item_at(n);
+      const int valid = ip->valid, pa = ip->p0 + t * tpt, pb = pa + ip->n[t] - 1, off = ip->sink - ip->lo;
+      const int sink_tiles = ip->z[t] > 0 ? ip->sinks : 0, from = ip->a[t], to = ip->z[t];
+      __syncwarp();
+      if (lane == 0) arrive(item_empty + n % kItemSlots);
+      if (!valid) break;
+      float m = -INFINITY, l = 0.f;  // the maximum in use (log2), the weights' sum
+      // places of the list that the row sees: [0, sinks) and [lo, hi), and what all the tile's rows see
+      const Seen mine = attn::seen_by(a.view, pa + tr), low = attn::seen_by(a.view, pa),
+                 high = attn::seen_by(a.view, pb);
+      const int lo = mine.lo + off, hi = mine.hi + off, lo_all = high.lo + off, hi_all = low.hi + off;
+      bool ok = true;
+      for (int kt = sink_tiles > 0 ? 0 : from; kt < to; kt = kt + 1 == sink_tiles ? from : kt + 1) {
+        if (!(ok = warp_wait(s_full + t, s_par, 1))) break;
+        s_par ^= 1u;
+        tc::fence_after();
+        __syncwarp();
+        const int v0 = kt * kKeys;
+        float s[kKeys];
+        tc::tmem_ld32x4(s_at, s_at + 32, s_at + 64, s_at + 96, s);
+        if (hi_all < v0 + kKeys || (lo_all > v0 && a.view.sinks < v0 + kKeys)) {
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32) {
+            const int x = v0 + c;
+            const uint32_t see = (bits(0, a.view.sinks - x) | bits(lo - x, 32)) & bits(0, hi - x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(see >> i & 1u)) s[c + i] = -INFINITY;
+          }
+        }
+        // The weights of 32 keys relative to the maximum in use; the first beside the search for the tile's own maximum.
+        float2 sum = make_float2(0.f, 0.f);
+        uint32_t w[16];
+        auto weights = [&](int from) {
+          const float base = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 e = fma2(make_float2(s[from + 2 * i], s[from + 2 * i + 1]), make_float2(scale_log2, scale_log2),
+                                  make_float2(base, base));
+            const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+            sum = fma2(p, make_float2(1.f, 1.f), sum);
+            w[i] = pack_bf16(p.x, p.y);
+          }
+        };
+        weights(0);
+        float top4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top4[i] = fmaxf(s[i], s[i + 4]);
+#pragma unroll
+        for (int i = 8; i < kKeys; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top4[k] = max3(top4[k], s[i + k], s[i + k + 4]);
+        const float top = scale_log2 * fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
+        if (__any_sync(0xffffffffu, top > m + kLazy)) {
+          // it is far above: it takes its place, and those weights are made again
+          const float next = top > m + kLazy ? top : m;
+          if (__any_sync(0xffffffffu, m != -INFINITY)) {
+            const float f = next == m ? 1.f : ex2_approx(m - next);
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < a.d; c += 16) {
+              float r[16];
+              tc::tmem_ld16(o_at + c, r);
+              uint32_t x[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(r[i] * f);
+              tmem_st16_start(o_at + c, x);
+            }
+          }
+          m = next;
+          sum = make_float2(0.f, 0.f);
+          weights(0);
+        }
+        tmem_st16_start(s_at, w);  // in the scores' place
+        weights(32);
+        tmem_st16_start(s_at + 16, w);
+        tmem_st_wait();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(p_half + t);
+        weights(64);
+        tmem_st16_start(s_at + 32, w);
+        weights(96);
+        tmem_st16_start(s_at + 48, w);
+        l += sum.x + sum.y;
+        tmem_st_wait();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(p_full + t);
+      }
+      if (!ok || (n > 0 && !warp_wait(o_empty + t, (n - 1) & 1, 1))) break;
+      stat[t * 128 + row] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) arrive(st_full + t);
+    }
+  } else {
+    // ---- outputs: a row a thread
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+    const int row = tid & 127, tr = row / G, hr = row - tr * G;
+    const uint32_t o_at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColO;
+    uint32_t o_par[2] = {0, 0};
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      if (!warp_wait(item_full + n % kItemSlots, item_par(n), 1)) break;
+      const Item it = *item_at(n);
+      __syncwarp();
+      if (lane == 0) arrive(item_empty + n % kItemSlots);
+      if (!it.valid) break;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!(ok = warp_wait(st_full + t, n & 1, 1))) break;
+        const float2 s = stat[t * 128 + row];
+        const bool some = it.count(t) > 0;
+        if (some) {
+          if (!(ok = warp_wait(o_full + t, o_par[t], 1))) break;
+          o_par[t] ^= 1u;
+          tc::fence_after();
+        }
+        const bool live = tr < tpt && tr < it.n[t];
+        const long long tok = it.q0 + t * tpt + tr;
+        const int head = it.hk * G + hr;
+        __nv_bfloat16* out = a.out + (tok * a.Hq + head) * a.d;
+        const float inv = s.y == 0.f ? 0.f : 1.f / s.y;
+        bool odd = false;
+        for (int c = 0; c < a.d; c += 32) {
+          float r[32] = {};
+          __syncwarp();  // the load wants the lanes together, which a store of some of them may part
+          if (some) tc::tmem_ld32(o_at + t * 128 + c, r);
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            if (c + i >= a.d) break;
+            float2 f[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              f[k] = s.y == 0.f ? make_float2(0.f, 0.f)
+                                : make_float2(r[i + 2 * k] * inv, r[i + 2 * k + 1] * inv);
+              odd |= !(fabsf(f[k].x) <= FLT_MAX) || !(fabsf(f[k].y) <= FLT_MAX);
+            }
+            if (live) *reinterpret_cast<uint4*>(out + c + i) = narrow8(f);
+          }
+        }
+        if (live && a.lse != nullptr)
+          a.lse[tok * a.Hq + head] = s.y == 0.f ? -INFINITY : (s.x + log2f(s.y)) * attn::kLn2;
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(o_empty + t);
+        // rows that are not finite again, one after the other (but where the weights' sum is not: nothing else could be)
+        for (unsigned rest = __ballot_sync(0xffffffffu, odd && live && s.y <= FLT_MAX); rest != 0; rest &= rest - 1) {
+          const int r2 = 32 * (warp & 3) + __ffs(rest) - 1, tr2 = r2 / G;
+          const long long tok2 = it.q0 + t * tpt + tr2;
+          const int head2 = it.hk * G + r2 - tr2 * G;
+          const __nv_bfloat16 *k = a.k + (long long)it.k0 * a.ks + it.hk * a.d, *v = a.v + (long long)it.k0 * a.vs + it.hk * a.d;
+          const attn::RowSum sum = attn::row_sum(
+              a.q + tok2 * a.qs + (long long)head2 * a.d, a.d, negate ? -scale_log2 : scale_log2,
+              attn::seen_by(a.view, it.p0 + t * tpt + tr2), [&](int j) { return k + j * a.ks; },
+              [&](int j) { return v + j * a.vs; }, attn::WidenBf16());
+          attn::put_row(sum, a.d, a.out + (tok2 * a.Hq + head2) * a.d, nullptr, 1.f);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  __syncwarp();
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+namespace {
+
+bool head_map(CUtensorMap* m, const void* base, long long stride, int heads, int d, long long tokens, int box_heads,
+              int box_tokens) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)(tokens > 1 ? stride : (long long)heads * d) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  return make_map16(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace
+
+template <int kQuarters>
+cudaError_t launch_attn_tiles(const attn::PromptArgs& a, void* ws, cudaStream_t st) {
+  const bool packed = a.cu != nullptr;
+  const long long nq = packed ? (long long)a.T : (long long)a.B * a.T;
+  const long long nk = packed ? (long long)a.Tk : (long long)a.B * a.Tk;
+  const int G = a.Hq / a.Hkv, tpt = 128 / G, per = 2 * tpt, sms = device_sms();
+  if (sms == 0) return cudaErrorNoDevice;
+  const long long tiles = ((long long)a.T + per - 1) / per;
+  const long long items = (packed ? tiles + a.B : tiles * a.B) * a.Hkv;  // (packed: an upper bound)
+  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+  CUtensorMap q, k, v, k16, v16;
+  if (!head_map(&q, a.q, a.qs, a.Hq, a.d, nq, G, tpt)) return cudaErrorInvalidValue;
+  // without keys nothing is loaded by these
+  auto key_map = [&](CUtensorMap* m, const void* x, long long stride, int box) {
+    return nk > 0 ? head_map(m, x, stride, a.Hkv, a.d, nk, 1, box) : head_map(m, a.q, a.qs, a.Hkv, a.d, nq, 1, box);
+  };
+  if (!key_map(&k, a.k, a.ks, kKeys) || !key_map(&v, a.v, a.vs, kKeys) || !key_map(&k16, a.k, a.ks, 16) ||
+      !key_map(&v16, a.v, a.vs, 16))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = set_smem_limit_once<gdn_attn_tile_kernel<kQuarters>>(Cfg<kQuarters>::kSmem);
+  if (e != cudaSuccess) return e;
+  float c = a.scale * attn::kLog2e;
+  const int negate = c < 0.f;  // as the sign of the queries
+  c = std::max(negate ? -c : c, 0x1p-126f);  // (unseen scores are minus infinity, and 0 times that would not do)
+  gdn_attn_tile_kernel<kQuarters><<<(unsigned)std::min<long long>(items, sms), kThreads, Cfg<kQuarters>::kSmem, st>>>(
+      q, k, v, k16, v16, a, (int)items, tpt, c, negate, static_cast<int*>(ws));
+  return cudaGetLastError();
+}
+
+}  // namespace gdn
