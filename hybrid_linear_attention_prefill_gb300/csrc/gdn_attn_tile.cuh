@@ -3,8 +3,8 @@
 //
 // A row is a query of one head.  The heads that share a key head go into one tile, 128 / G tokens of G
 // heads, so that a key is read once for all of them and a mask's edge crosses few keys.  A CTA works on
-// two such tiles side by side: while the tensor core multiplies for one, four warps take the other's
-// scores to weights, a row a thread, so that a row's maximum and sum need no exchange.
+// two such tiles side by side: while the tensor core multiplies for one, eight warps take the other's
+// scores to weights, two threads a row.
 //
 //   scores  S = Q K^T              128 x 128, operands from shared memory, into TMEM
 //   weights P = exp2(c S - m)      in the place of S, bf16, as the next product's operand in TMEM
@@ -14,9 +14,8 @@
 // weights are then up to 2^8 and their sums as exact as before, and O is rescaled only now and then.
 // Sums, maxima, scores and O are fp32.
 //
-// Roles, 16 warps: four for each tile's weights; four that write finished tiles out while the next item's
-// products run; one for each tile that issues MMAs, one that issues copies, one that works out the items.  They meet on
-// mbarriers only.  A CTA takes an item (256 rows of a key head) after another; the ring of key and value
+// Roles, 20 warps: eight for each tile's weights and finished outputs; one for each tile that issues MMAs, one
+// that issues copies, one that works out the items.  They meet on mbarriers.  A CTA takes an item (256 rows of a key head) after another; the ring of key and value
 // tiles runs on across items.
 //
 // A value that is not finite in a place that a row does not see would reach the row as 0 x infinity.
@@ -40,8 +39,8 @@ using attn::PromptArgs;
 using attn::Seen;
 using attn::View;
 
-constexpr int kThreads = 512;
-constexpr int kOutWarp = 8, kMmaWarp = 12, kLoadWarp = 13, kItemWarp = 14;  // (and 15)
+constexpr int kThreads = 640;
+constexpr int kMmaWarp = 16, kLoadWarp = 18, kItemWarp = 19;  // (17: the other tile's products)
 constexpr int kKeys = 128;            // a tile
 constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns: two score tiles of 128, two outputs of 128
 constexpr int kItemSlots = 4;
@@ -58,8 +57,9 @@ template <int kQuarters>
 struct Cfg {
   static constexpr int kHalves = (kQuarters + 1) / 2, kTile = kHalves * kHalf, kRing = kHalves == 2 ? 2 : 4;
   static constexpr int kOffQ = 0, kOffK = 2 * kTile, kOffV = kOffK + kRing * kTile, kOffStat = kOffV + kRing * kTile;
-  static constexpr int kOffItem = kOffStat + 2 * 128 * 8, kOffBar = kOffItem + kItemSlots * 128;
-  static constexpr int kBars = 4 * kRing + 2 * kItemSlots + 2 * 10;
+  static constexpr int kStatBytes = 3 * 2 * 2 * 128 * 4;
+  static constexpr int kOffItem = kOffStat + kStatBytes, kOffBar = kOffItem + kItemSlots * 128;
+  static constexpr int kBars = 4 * kRing + 2 * kItemSlots + 2 * 8;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16;
   static_assert(kSmem <= 227 * 1024 && kSmem > 116 * 1024, "one CTA an SM");
 };
@@ -130,6 +130,19 @@ __device__ __forceinline__ bool passed(uint64_t* bar, uint32_t par) {
   return done != 0;
 }
 
+// The two warps of a row's threads at barrier `id`: together, and whether any thread of them has `x`.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;\n" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool any_of_pair(int id, bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\tbarrier.cta.red.or.pred p, %1, 64, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(any)
+      : "r"(id), "r"((uint32_t)x)
+      : "memory");
+  return any != 0;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
@@ -165,12 +178,11 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   constexpr int kTile = C::kTile, kHalves = C::kHalves, kRing = C::kRing;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = smem_raw;
-  float2* stat = reinterpret_cast<float2*>(sm + C::kOffStat);  // [tile][row]: maximum in use (log2), sum
+  float* stat = reinterpret_cast<float*>(sm + C::kOffStat);  // [maximum, sum, not finite][tile][half][row]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
   uint64_t *k_full = bars, *k_empty = k_full + kRing, *v_full = k_empty + kRing, *v_empty = v_full + kRing,
            *item_full = v_empty + kRing, *item_empty = item_full + kItemSlots, *q_full = item_empty + kItemSlots,
-           *q_empty = q_full + 2, *s_full = q_empty + 2, *p_half = s_full + 2, *p_full = p_half + 2, *st_full = p_full + 2,
-           *o_full = st_full + 2, *o_empty = o_full + 2, *turn = o_empty + 2, *drain = turn + 2;
+           *q_empty = q_full + 2, *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 2, *o_empty = o_full + 2, *turn = o_empty + 2, *drain = turn + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -189,17 +201,15 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
     for (int i = 0; i < kItemSlots; ++i) {
       tc::mbar_init(item_full + i, 1);
-      tc::mbar_init(item_empty + i, 15);  // twelve warps of weights and outputs, three that issue
+      tc::mbar_init(item_empty + i, 19);  // sixteen warps of weights, three that issue
     }
     for (int t = 0; t < 2; ++t) {
       tc::mbar_init(q_full + t, 1);
       tc::mbar_init(q_empty + t, 1);
       tc::mbar_init(s_full + t, 1);
-      tc::mbar_init(p_half + t, 4);
-      tc::mbar_init(p_full + t, 4);
-      tc::mbar_init(st_full + t, 4);
+      tc::mbar_init(p_full + t, 8);
       tc::mbar_init(o_full + t, 1);
-      tc::mbar_init(o_empty + t, 4);
+      tc::mbar_init(o_empty + t, 8);
       tc::mbar_init(turn + t, 1);
       tc::mbar_init(drain + t, 1);
     }
@@ -239,9 +249,9 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   auto item_at = [&](int n) { return reinterpret_cast<const Item*>(sm + C::kOffItem + (n % kItemSlots) * 128); };
   auto item_par = [](int n) { return (uint32_t)(n / kItemSlots) & 1u; };
 
-  // The launch's 128 registers a thread are dealt out anew (2 x 168 + 88 + 88 = 4 x 128): a row of scores takes 128.
+  // The launch's 128 registers a thread are dealt out anew (4 x 104 + 64 = 5 x 96).
   if (warp >= kMmaWarp) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
   if (warp == kItemWarp) {
     // ---- the items: those of one rank of the grid after another, forwards and backwards in turn, so that
     // the CTAs' sums are alike where the items' sizes fall steadily
@@ -372,22 +382,21 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       constexpr uint32_t id_o = tc::idesc_bf16(128, 32 * kQuarters, 0, 1), sb = kSmemBase;
       const uint32_t id_s = tc::idesc_bf16(128, kKeys, 0, 0) | (negate ? 1u << 13 : 0u);
       bool on = false, first = false, last = false;  // weights whose product is to come
-      int o_item = 0;                                // their item
+      int seen_items = 0;                            // items so far that this tile sees any keys of
       uint32_t p_par = 0;
       uint32_t tiles = 0;  // of keys, in all: the ring's slot and phase, and the turn
       bool ok = true;
-      // Until every lane's barrier (null: none) has passed its phase, but for those of lanes that need not; the lanes whose
-      // has, 0 after giving up.
-      auto look = [&](uint64_t* bar, uint32_t par, bool must = true) -> uint32_t {
+      // Until every lane's barrier (null: none) has passed its phase; false after giving up.
+      auto look = [&](uint64_t* bar, uint32_t par) {
         bool done = bar == nullptr;
         long long since = 0;
         for (int i = 0;; ++i) {
-          if (!done) done = must ? tc::mbar_wait(bar, par, 1) : passed(bar, par);
-          if (__all_sync(0xffffffffu, done || !must)) return __ballot_sync(0xffffffffu, done) | 1u << 31;
+          if (!done) done = tc::mbar_wait(bar, par, 1);
+          if (__all_sync(0xffffffffu, done)) return true;
           if ((i & 255) == 255) {
             if (since == 0) since = clock64();
             if (lane == 0 && clock64() - since > kPatience) give_up(1);
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) return 0;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
           }
         }
       };
@@ -398,28 +407,19 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         uint32_t par = 0;
         if (lane == 0 && tiles > 0) bar = v_full + S, par = ((tiles - 1) / kRing) & 1u;
         if (lane == 1) bar = keys, par = (tiles / kRing) & 1u;
-        if (lane == 2 && on) bar = p_half + t, par = p_par;
-        if (lane == 3 && on && first && o_item > 0) bar = o_empty + t, par = (uint32_t)(o_item - 1) & 1u;
+        if (lane == 2 && on) bar = p_full + t, par = p_par;
+        // (the item's before; items that see nothing have no phase, so that neither side can be two ahead)
+        if (lane == 3 && on && first && seen_items > 1) bar = o_empty + t, par = (uint32_t)seen_items & 1u;
         if (lane == 4) bar = turn, par = turn_par;
-        if (lane == 5 && on) bar = p_full + t, par = p_par;  // (often there by now)
-        const uint32_t seen = look(bar, par, lane != 5);
-        if (seen == 0) return false;
+        if (!look(bar, par)) return false;
         if (!on) return true;
         const uint64_t v = tc::sdesc(sb + C::kOffV + S * kTile, kHalf, 1024, tc::kSw128);
         if (lane == 0) {
           const uint32_t more = first ? 0u : 1u;
           tc::fence_after();
 #pragma unroll
-          for (int k = 0; k < kKeys / 32; ++k)
+          for (int k = 0; k < kKeys / 16; ++k)
             tc::mma_f16_ta(kColO + t * 128, kColS + t * 128 + 8 * k, v + ((k * 2048) >> 4), id_o, k > 0 ? 1u : more);
-        }
-        __syncwarp();
-        if (!(seen >> 5 & 1u) && !look(lane == 0 ? p_full + t : nullptr, p_par)) return false;
-        if (lane == 0) {
-          tc::fence_after();
-#pragma unroll
-          for (int k = kKeys / 32; k < kKeys / 16; ++k)
-            tc::mma_f16_ta(kColO + t * 128, kColS + t * 128 + 8 * k, v + ((k * 2048) >> 4), id_o, 1u);
           if (last) tc::commit(o_full + t);
         }
         __syncwarp();
@@ -476,7 +476,7 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
               on = true;
               first = left == total;
               last = --left == 0;
-              o_item = n;
+              seen_items += first;
             }
             return true;
           });
@@ -484,8 +484,7 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         if (!ok) break;
         if (total == 0) {  // nothing to see: the phases go by in order all the same, after what is pending
-          ok = flush_alone() && (all > 0 || look(lane == 0 ? q_full + t : nullptr, (uint32_t)n & 1u)) &&
-               (n == 0 || look(lane == 0 ? o_empty + t : nullptr, (uint32_t)(n - 1) & 1u));
+          ok = flush_alone() && (all > 0 || look(lane == 0 ? q_full + t : nullptr, (uint32_t)n & 1u));
           if (!ok) break;
           if (lane == 0) tc::commit(q_empty + t);
           __syncwarp();
@@ -501,39 +500,45 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     else products(Slot<1>());
     __syncwarp();
   }
-  } else if (warp < kOutWarp) {
-    // ---- weights: a row a thread
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n");
-    const int t = warp >> 2, row = tid & 127, tr = row / G;
-    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t s_at = tmem + lanes + kColS + t * 128, o_at = tmem + lanes + kColO + t * 128;
-    uint32_t s_par = 0;
+  } else {
+    // ---- weights, and a finished tile's outputs: two threads a row, each for 64 of a tile's keys (and every other 32
+    // columns of the output), in two warps that meet at a barrier of their own
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+    const int t = warp >> 3, hf = warp >> 2 & 1, quad = warp & 3, row = 32 * quad + lane, tr = row / G;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const uint32_t s_at = tmem + lanes + kColS + t * 128 + 64 * hf, p_at = tmem + lanes + kColS + t * 128 + 32 * hf,
+                   o_at = tmem + lanes + kColO + t * 128;
+    const int pair = 1 + 4 * t + quad;  // the barrier: both warps of a row come to it every time, one that gave up too
+    float *tops = stat + t * 256 + row, *sums = tops + 512, *odds = sums + 512;  // of half h: + 128 h
+    uint32_t s_par = 0, o_par = 0;
     for (int n = 0;; ++n) {
-      if (!warp_wait(item_full + n % kItemSlots, item_par(n), 1)) break;
+      bool ok = warp_wait(item_full + n % kItemSlots, item_par(n), 1);
+      if (any_of_pair(pair, !ok)) break;
       const Item* ip = item_at(n);
-      const int valid = ip->valid, pa = ip->p0 + t * tpt, pb = pa + ip->n[t] - 1, off = ip->sink - ip->lo;
+      const int valid = ip->valid, pa = ip->p0 + t * tpt, nt = ip->n[t], off = ip->sink - ip->lo;
       const int sink_tiles = ip->z[t] > 0 ? ip->sinks : 0, from = ip->a[t], to = ip->z[t];
+      const int tok0 = ip->q0 + t * tpt, k0 = ip->k0, hk = ip->hk;
       __syncwarp();
       if (lane == 0) arrive(item_empty + n % kItemSlots);
       if (!valid) break;
       float m = -INFINITY, l = 0.f;  // the maximum in use (log2), the weights' sum
       // places of the list that the row sees: [0, sinks) and [lo, hi), and what all the tile's rows see
-      const Seen mine = attn::seen_by(a.view, pa + tr), low = attn::seen_by(a.view, pa),
-                 high = attn::seen_by(a.view, pb);
-      const int lo = mine.lo + off, hi = mine.hi + off, lo_all = high.lo + off, hi_all = low.hi + off;
-      bool ok = true;
+      const Seen mine = attn::seen_by(a.view, pa + tr);
+      const int lo = mine.lo + off, hi = mine.hi + off;
+      const int lo_all = attn::seen_by(a.view, pa + nt - 1).lo + off, hi_all = attn::seen_by(a.view, pa).hi + off;
+      bool stop = false;
       for (int kt = sink_tiles > 0 ? 0 : from; kt < to; kt = kt + 1 == sink_tiles ? from : kt + 1) {
-        if (!(ok = warp_wait(s_full + t, s_par, 1))) break;
+        ok = warp_wait(s_full + t, s_par, 1);
         s_par ^= 1u;
         tc::fence_after();
         __syncwarp();
         const int v0 = kt * kKeys;
-        float s[kKeys];
-        tc::tmem_ld32x4(s_at, s_at + 32, s_at + 64, s_at + 96, s);
+        float s[64];
+        tc::tmem_ld32x2(s_at, s_at + 32, s);
         if (hi_all < v0 + kKeys || (lo_all > v0 && a.view.sinks < v0 + kKeys)) {
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 32) {
-            const int x = v0 + c;
+          for (int c = 0; c < 64; c += 32) {
+            const int x = v0 + 64 * hf + c;
             const uint32_t see = (bits(0, a.view.sinks - x) | bits(lo - x, 32)) & bits(0, hi - x);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -543,12 +548,12 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         // The weights of 32 keys relative to the maximum in use; the first beside the search for the tile's own maximum.
         float2 sum = make_float2(0.f, 0.f);
         uint32_t w[16];
-        auto weights = [&](int from) {
+        auto weights = [&](int from32) {
           const float base = m == -INFINITY ? 0.f : -m;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 e = fma2(make_float2(s[from + 2 * i], s[from + 2 * i + 1]), make_float2(scale_log2, scale_log2),
-                                  make_float2(base, base));
+            const float2 e = fma2(make_float2(s[from32 + 2 * i], s[from32 + 2 * i + 1]),
+                                  make_float2(scale_log2, scale_log2), make_float2(base, base));
             const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
             sum = fma2(p, make_float2(1.f, 1.f), sum);
             w[i] = pack_bf16(p.x, p.y);
@@ -559,18 +564,23 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
         for (int i = 0; i < 4; ++i) top4[i] = fmaxf(s[i], s[i + 4]);
 #pragma unroll
-        for (int i = 8; i < kKeys; i += 8)
+        for (int i = 8; i < 64; i += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k) top4[k] = max3(top4[k], s[i + k], s[i + k + 4]);
-        const float top = scale_log2 * fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
-        if (__any_sync(0xffffffffu, top > m + kLazy)) {
-          // it is far above: it takes its place, and those weights are made again
+        float top = scale_log2 * fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
+        // (Both warps have their scores when they meet: the other's weights go in the place of some of them.)
+        if (any_of_pair(pair, !ok || top > m + kLazy)) {
+          if ((stop = any_of_pair(pair, !ok))) break;
+          // a row's is far above: it takes its place, and those weights are made again
+          tops[128 * hf] = top;
+          pair_sync(pair);
+          top = fmaxf(top, tops[128 * (1 - hf)]);
           const float next = top > m + kLazy ? top : m;
           if (__any_sync(0xffffffffu, m != -INFINITY)) {
             const float f = next == m ? 1.f : ex2_approx(m - next);
             l *= f;
 #pragma unroll 1
-            for (int c = 0; c < a.d; c += 16) {
+            for (int c = 16 * hf; c < a.d; c += 32) {
               float r[16];
               tc::tmem_ld16(o_at + c, r);
               uint32_t x[16];
@@ -583,90 +593,73 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           sum = make_float2(0.f, 0.f);
           weights(0);
         }
-        tmem_st16_start(s_at, w);  // in the scores' place
+        tmem_st16_start(p_at, w);  // in the scores' place
         weights(32);
-        tmem_st16_start(s_at + 16, w);
-        tmem_st_wait();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) arrive(p_half + t);
-        weights(64);
-        tmem_st16_start(s_at + 32, w);
-        weights(96);
-        tmem_st16_start(s_at + 48, w);
+        tmem_st16_start(p_at + 16, w);
         l += sum.x + sum.y;
         tmem_st_wait();
         tc::fence_before();
         __syncwarp();
         if (lane == 0) arrive(p_full + t);
       }
-      if (!ok || (n > 0 && !warp_wait(o_empty + t, (n - 1) & 1, 1))) break;
-      stat[t * 128 + row] = make_float2(m, l);
-      __syncwarp();
-      if (lane == 0) arrive(st_full + t);
-    }
-  } else {
-    // ---- outputs: a row a thread
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-    const int row = tid & 127, tr = row / G, hr = row - tr * G;
-    const uint32_t o_at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColO;
-    uint32_t o_par[2] = {0, 0};
-    bool ok = true;
-    for (int n = 0; ok; ++n) {
-      if (!warp_wait(item_full + n % kItemSlots, item_par(n), 1)) break;
-      const Item it = *item_at(n);
-      __syncwarp();
-      if (lane == 0) arrive(item_empty + n % kItemSlots);
-      if (!it.valid) break;
+      if (stop) break;
+      // ---- outputs
+      sums[128 * hf] = l;
+      pair_sync(pair);
+      l += sums[128 * (1 - hf)];  // (the two in either order: the same)
+      const bool some = to > 0;
+      if (some) {
+        ok = warp_wait(o_full + t, o_par, 1);
+        o_par ^= 1u;
+        tc::fence_after();
+      }
+      const bool live = tr < tpt && tr < nt;
+      const long long tok = (long long)tok0 + tr;
+      const int head = hk * G + row - tr * G;
+      __nv_bfloat16* out = a.out + (tok * a.Hq + head) * a.d;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      bool odd = false;
+#pragma unroll 1
+      for (int c = 32 * hf; c < a.d; c += 64) {
+        float r[32] = {};
+        __syncwarp();  // the load wants the lanes together, which a store of some of them may part
+        if (some) tc::tmem_ld32(o_at + c, r);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (!(ok = warp_wait(st_full + t, n & 1, 1))) break;
-        const float2 s = stat[t * 128 + row];
-        const bool some = it.count(t) > 0;
-        if (some) {
-          if (!(ok = warp_wait(o_full + t, o_par[t], 1))) break;
-          o_par[t] ^= 1u;
-          tc::fence_after();
-        }
-        const bool live = tr < tpt && tr < it.n[t];
-        const long long tok = it.q0 + t * tpt + tr;
-        const int head = it.hk * G + hr;
-        __nv_bfloat16* out = a.out + (tok * a.Hq + head) * a.d;
-        const float inv = s.y == 0.f ? 0.f : 1.f / s.y;
-        bool odd = false;
-        for (int c = 0; c < a.d; c += 32) {
-          float r[32] = {};
-          __syncwarp();  // the load wants the lanes together, which a store of some of them may part
-          if (some) tc::tmem_ld32(o_at + t * 128 + c, r);
+        for (int i = 0; i < 32; i += 8) {
+          if (c + i >= a.d) break;
+          float2 f[4];
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            if (c + i >= a.d) break;
-            float2 f[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              f[k] = s.y == 0.f ? make_float2(0.f, 0.f)
-                                : make_float2(r[i + 2 * k] * inv, r[i + 2 * k + 1] * inv);
-              odd |= !(fabsf(f[k].x) <= FLT_MAX) || !(fabsf(f[k].y) <= FLT_MAX);
-            }
-            if (live) *reinterpret_cast<uint4*>(out + c + i) = narrow8(f);
+          for (int k = 0; k < 4; ++k) {
+            f[k] = l == 0.f ? make_float2(0.f, 0.f) : make_float2(r[i + 2 * k] * inv, r[i + 2 * k + 1] * inv);
+            odd |= !(fabsf(f[k].x) <= FLT_MAX) || !(fabsf(f[k].y) <= FLT_MAX);
           }
+          if (live) *reinterpret_cast<uint4*>(out + c + i) = narrow8(f);
         }
-        if (live && a.lse != nullptr)
-          a.lse[tok * a.Hq + head] = s.y == 0.f ? -INFINITY : (s.x + log2f(s.y)) * attn::kLn2;
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) arrive(o_empty + t);
-        // rows that are not finite again, one after the other (but where the weights' sum is not: nothing else could be)
-        for (unsigned rest = __ballot_sync(0xffffffffu, odd && live && s.y <= FLT_MAX); rest != 0; rest &= rest - 1) {
-          const int r2 = 32 * (warp & 3) + __ffs(rest) - 1, tr2 = r2 / G;
-          const long long tok2 = it.q0 + t * tpt + tr2;
-          const int head2 = it.hk * G + r2 - tr2 * G;
-          const __nv_bfloat16 *k = a.k + (long long)it.k0 * a.ks + it.hk * a.d, *v = a.v + (long long)it.k0 * a.vs + it.hk * a.d;
-          const attn::RowSum sum = attn::row_sum(
-              a.q + tok2 * a.qs + (long long)head2 * a.d, a.d, negate ? -scale_log2 : scale_log2,
-              attn::seen_by(a.view, it.p0 + t * tpt + tr2), [&](int j) { return k + j * a.ks; },
-              [&](int j) { return v + j * a.vs; }, attn::WidenBf16());
-          attn::put_row(sum, a.d, a.out + (tok2 * a.Hq + head2) * a.d, nullptr, 1.f);
+      }
+      if (live && hf == 0 && a.lse != nullptr)
+        a.lse[tok * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * attn::kLn2;
+      tc::fence_before();
+      __syncwarp();
+      if (some && lane == 0) arrive(o_empty + t);
+      // rows that are not finite again, one after the other (but where the weights' sum is not: nothing else could be)
+      odd = odd && live && l <= FLT_MAX;
+      if (any_of_pair(pair, odd || !ok)) {
+        if (any_of_pair(pair, !ok)) break;
+        odds[128 * hf] = odd ? 1.f : 0.f;
+        pair_sync(pair);
+        if (hf == 0) {
+          odd = odd || odds[128] != 0.f;
+          for (unsigned rest = __ballot_sync(0xffffffffu, odd); rest != 0; rest &= rest - 1) {
+            const int r2 = 32 * quad + __ffs(rest) - 1, tr2 = r2 / G;
+            const long long tok2 = (long long)tok0 + tr2;
+            const int head2 = hk * G + r2 - tr2 * G;
+            const __nv_bfloat16 *k = a.k + (long long)k0 * a.ks + hk * a.d, *v = a.v + (long long)k0 * a.vs + hk * a.d;
+            const attn::RowSum r = attn::row_sum(
+                a.q + tok2 * a.qs + (long long)head2 * a.d, a.d, negate ? -scale_log2 : scale_log2,
+                attn::seen_by(a.view, pa + tr2), [&](int j) { return k + j * a.ks; },
+                [&](int j) { return v + j * a.vs; }, attn::WidenBf16());
+            attn::put_row(r, a.d, a.out + (tok2 * a.Hq + head2) * a.d, nullptr, 1.f);
+          }
         }
         __syncwarp();
       }

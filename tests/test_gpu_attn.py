@@ -487,9 +487,22 @@ def test_attention_packed(gdn, lens, Hq, Hkv, d, window, sinks):
     check_attn(gdn, q, k, v, lens, window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("top,Hq,Hkv,d,window,sinks", [(80, 4, 1, 64, 0, 0), (40, 8, 2, 128, 0, 0), (150, 4, 2, 32, 20, 2),
+                                                       (300, 2, 1, 96, 60, 3)])
+def test_attention_many_sequences(gdn, top, Hq, Hkv, d, window, sinks):
+    # many more items than CTAs, with tiles that see nothing in any order among them
+    g = gen(top)
+    lens = torch.randint(0, top, (1500,), generator=g)
+    lens[torch.randint(0, 1500, (400,), generator=g)] = 1
+    klens = torch.where(torch.rand(1500, generator=g) < 0.2, torch.randint(0, top, (1500,), generator=g), lens)
+    q, k, v = slices(g, int(lens.sum()), int(klens.sum()), Hq, Hkv, d)
+    check_attn(gdn, q, k, v, lens.tolist(), klens.tolist(), window=window, sinks=sinks)
+    assert gdn.gdn_device_status() == (0, 0)
+
+
 @pytest.mark.parametrize("B,T,Hq,Hkv,d,window,sinks", [
     (1, 1, 2, 1, 64, 0, 0), (3, 65, 4, 2, 128, 0, 0), (2, 400, 8, 2, 80, 0, 0), (4, 130, 3, 3, 32, 40, 2),
-    (2, 1027, 8, 4, 128, 256, 4), (1, 3001, 8, 1, 128, 0, 0), (30, 100, 16, 8, 64, 0, 0)])
+    (2, 1027, 8, 4, 128, 256, 4), (1, 3001, 8, 1, 128, 0, 0), (5, 2500, 8, 4, 64, 130, 4), (30, 100, 16, 8, 64, 0, 0)])
 def test_attention_dense(gdn, B, T, Hq, Hkv, d, window, sinks):
     g = gen(B + T)
     q, k, v = slices(g, B * T, B * T, Hq, Hkv, d)
