@@ -23,6 +23,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_attn.cuh"
 #include "gdn_internal.h"
@@ -34,7 +35,7 @@ namespace {
 using attn::Seen;
 using attn::StepArgs;
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kCtas = 2;  // (a CTA, an SM)
 constexpr int kBlock = 16;                  // keys a warp takes at a time
 constexpr int kLeast = 2;                   // units that a run has at least, where there are so many
 constexpr int kMaxHeads = 16;               // of a key head at a time
@@ -64,48 +65,67 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint4 load_once(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// 16 or 8 bytes into shared memory, zeros where not `there`.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ uint2 load_once(const uint2* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+__device__ __forceinline__ void copy8(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(to), "l"(from), "r"(there ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+// Four e4m3 values as fp16.
+__device__ __forceinline__ void widen_e4m3(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
 }
 
-// Eight values of the cache: as they are held, and as four pairs of 16 bits.
-template <bool E4M3>
-struct Piece;
-template <>
-struct Piece<false> {
-  using Raw = uint4;
-  static constexpr int kBytes = 2;
-  __device__ static __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
-  __device__ static __forceinline__ void pairs(const Raw& r, uint32_t (&w)[4]) {
-    w[0] = r.x;
-    w[1] = r.y;
-    w[2] = r.z;
-    w[3] = r.w;
+// A warp's ring: kRing times kPer blocks of 16 keys and their values.  A row is padded or its 16-byte pieces are permuted, so that
+// eight rows' pieces of a column lie in different banks.
+template <int NT, int NC, bool E4M3>
+struct Ring {
+  static constexpr int kSize = E4M3 ? 1 : 2, kBytes = 32 * NC * kSize;  // of a value, of a row
+  static constexpr bool kXor = kBytes % 128 == 0;
+  static constexpr int kPitch = kXor ? kBytes : kBytes + 16, kTile = kBlock * kPitch, kPieces = kBytes / 16;
+  static constexpr int kPer = E4M3 ? 2 : 1, kRing = 3, kSlot = kPer * 2 * kTile;
+  static constexpr int kRow = 32 * NC + 4;  // a head's sums, padded
+  static constexpr int kOffSums = kWarps * kRing * kSlot, kOffStat = kOffSums + kWarps * 8 * kRow * 4;
+  static constexpr int kSmem = kOffStat + kWarps * 8 * 8 + 16;
+  static_assert(kSmem <= 113 * 1024, "two CTAs an SM");
+  __device__ static __forceinline__ int at(int row, int piece) {
+    return row * kPitch + 16 * (kXor ? piece ^ (row & 7) : piece);
   }
 };
-template <>
-struct Piece<true> {
-  using Raw = uint2;
-  static constexpr int kBytes = 1;
-  __device__ static __forceinline__ Raw zero() { return make_uint2(0, 0); }
-  __device__ static __forceinline__ void pairs(const Raw& r, uint32_t (&w)[4]) {
-    const uint32_t v[2] = {r.x, r.y};
+
+__device__ __forceinline__ long long inclusive(long long x, int lane) {  // the sum up to this lane
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-      w[i] = (uint32_t)h.x | (uint32_t)h.y << 16;
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-};
+  return x;
+}
+// Of numbers that are not negative: in 32 bits where they fit, which is many times as fast.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+}
 
 // What a part's sums (maximum, sum of weights) are multiplied by to be relative to `top`: nothing of a part that has
 // seen nothing (or NaN, where its sum is that).
@@ -137,202 +157,240 @@ __device__ __forceinline__ int units_of(int blocks) { return blocks > kWarps ? (
 
 }  // namespace
 
-// NT: heads in eights; NC: columns in 32s; parts: heads of a key head in groups of 8 NT.
+// NT: heads in eights; NC: columns in 32s; groups: parts of a key head's heads.
 template <int NT, int NC, bool E4M3>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
-gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, Work work, int* __restrict__ err) {
-  using P = Piece<E4M3>;
-  using Raw = typename P::Raw;
-  constexpr int NV = (NC + 1) / 2, kHeads = 8 * NT, kRow = 32 * NC + 4;  // a head's row in shared memory, padded
-  __shared__ __align__(16) float so[kWarps][kHeads][kRow];
-  __shared__ float2 stat[kWarps][kHeads];  // maximum (log2) and sum
-  __shared__ int last;
+__global__ void __launch_bounds__(kThreads, kCtas)
+gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, int wide, Work work,
+                     int* __restrict__ err) {
+  using R = Ring<NT, NC, E4M3>;
+  extern __shared__ __align__(128) unsigned char sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int G = a.Hq / a.Hkv, per_seq = a.Hkv * groups;
+  float(*so)[8][R::kRow] = reinterpret_cast<float(*)[8][R::kRow]>(sm + R::kOffSums);
+  float2(*stat)[8] = reinterpret_cast<float2(*)[8]>(sm + R::kOffStat);  // maximum (log2) and sum
+  int* last = reinterpret_cast<int*>(sm + R::kOffStat + kWarps * 8 * 8);
+  const uint32_t ring = smem_u32(sm) + warp * R::kRing * R::kSlot;
 
-  // this CTA's run of units [u0, u1), and the sequence that it begins in
-  long long total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    int u = b0 + lane < a.B ? units_of(blocks_of(a, b0 + lane).count) : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-    total += u;
+  // this CTA's run of units [u0, u1), and the sequence that it begins in: every lane counts a share of the sequences,
+  // then the lanes look at the share where the run begins
+  const int share_of = (a.B + 31) / 32;
+  long long mine = 0;
+#pragma unroll 4
+  for (int i = 0; i < share_of; ++i) {
+    const int x = lane * share_of + i;
+    mine += x < a.B ? units_of(blocks_of(a, x).count) : 0;
   }
-  total *= per_seq;
-  const long long runs = min((long long)gridDim.x, max(1LL, total / kLeast));
-  if (blockIdx.x >= runs) return;
-  long long u0 = blockIdx.x * total / runs;
-  const long long u1 = (blockIdx.x + 1) * total / runs;
-  int b = -1;
-  long long before = 0;  // units of the sequences before b
-  for (int b0 = 0; b < 0 && b0 < a.B; b0 += 32) {
-    const int u = b0 + lane < a.B ? units_of(blocks_of(a, b0 + lane).count) : 0;
-    int sum = u;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += y;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, before + (long long)sum * per_seq > u0);
-    if (hit != 0) {
-      const int l = __ffs(hit) - 1;
-      b = b0 + l;
-      before += (long long)__shfl_sync(0xffffffffu, sum - u, l) * per_seq;
-    } else {
-      before += (long long)__shfl_sync(0xffffffffu, sum, 31) * per_seq;
-    }
+  const long long upto = inclusive(mine * per_seq, lane), total = __shfl_sync(0xffffffffu, upto, 31);
+  const long long per_run = max((long long)kLeast, quotient(total + gridDim.x - 1, gridDim.x));
+  long long u0 = blockIdx.x * per_run;
+  if (u0 >= total) return;
+  const long long u1 = min(u0 + per_run, total);
+  const int l0 = __ffs(__ballot_sync(0xffffffffu, upto > u0)) - 1;
+  int b = l0 * share_of;
+  long long before = __shfl_sync(0xffffffffu, upto - mine * per_seq, l0);  // units of the sequences before b
+  for (int i = 0;; i += 32) {  // (the share has it: a sequence behind the share's last is not reached)
+    const int x = b + lane;
+    const long long u = i + lane < share_of && x < a.B ? (long long)units_of(blocks_of(a, x).count) * per_seq : 0;
+    const long long sum = before + inclusive(u, lane);
+    const unsigned hit = __ballot_sync(0xffffffffu, sum > u0);
+    const int l = hit != 0 ? __ffs(hit) - 1 : 31;
+    before = __shfl_sync(0xffffffffu, hit != 0 ? sum - u : sum, l);
+    b += hit != 0 ? l : 32;
+    if (hit != 0 || i + 32 >= share_of) break;
   }
   Blocks blk = blocks_of(a, b);
   int units = units_of(blk.count);
-  int item = (int)((u0 - before) / units), first = (int)((u0 - before) - (long long)item * units);
+  int item = (int)quotient(u0 - before, units), first = (int)((u0 - before) - (long long)item * units);
+  int todo = 0, hk = 0, h0 = 0, nh = 0;
 
-  while (u0 < u1) {
-    const int todo = (int)min((long long)(units - first), u1 - u0);
-    const int hk = item / groups, h0 = hk * G + (item - hk * groups) * heads;
-    const int nh = min(heads, (hk + 1) * G - h0);  // heads of this item
+  // ---- the item's keys and values on their way: the pages of 32 of this warp's blocks at a time, a lane each
+  int page = -1, in_page = 0, page_after = -1, in_page_after = 0;
+  // the first key of this warp's i-th block, -1 behind the last
+  auto key_of = [&](int i) {
+    const int n = (first + i) * kWarps + warp;
+    return i < todo && n < blk.count ? kBlock * (n < blk.s ? n : blk.a + n - blk.s) : -1;
+  };
+  auto look_up = [&](int i) {
+    const int key = key_of(i + lane);
+    page_after = -1;
+    if (key >= 0) {
+      const int x = key / a.page;
+      in_page_after = key - x * a.page;
+      page_after = a.table[b * a.table_stride + x];
+      if (page_after < 0 || page_after >= a.blocks) {
+        page_after = -1;
+        atomicOr(err, kBadPage);
+      }
+    }
+  };
+  auto sees = [&](int key) { return key < blk.n && (key >= blk.seen.lo || key < blk.seen.sink_end); };
+  auto sees_all = [&](int key) {
+    return key + kBlock <= blk.n && (key >= blk.seen.lo || key + kBlock <= blk.seen.sink_end);
+  };
+  int slot = 0, put_slot = 0;  // of the ring: where the next block is, where one goes
+  uint32_t filled = 0;         // which of the ring's blocks are there
+  auto fetch = [&](int i) {
+    if ((i * R::kPer & 31) == 0) {
+      page = page_after;
+      in_page = in_page_after;
+      look_up(i * R::kPer + 32);
+    }
+    int pg[R::kPer], at[R::kPer];
+    uint32_t any = 0;
+#pragma unroll
+    for (int x = 0; x < R::kPer; ++x) {
+      pg[x] = __shfl_sync(0xffffffffu, page, (i * R::kPer + x) & 31);
+      at[x] = __shfl_sync(0xffffffffu, in_page, (i * R::kPer + x) & 31);
+      any |= (uint32_t)(pg[x] >= 0) << x;
+    }
+    if (any != 0) {
+#pragma unroll
+      for (int x = 0; x < R::kPer; ++x) {
+        const int key = key_of(i * R::kPer + x);
+        const bool all = pg[x] >= 0 && sees_all(key);
+        const long long from = ((long long)hk * a.page + at[x]) * a.d;
+        const unsigned char* kp = static_cast<const unsigned char*>(a.kc) + ((long long)max(pg[x], 0) * a.kbs + from) * R::kSize;
+        const unsigned char* vp = static_cast<const unsigned char*>(a.vc) + ((long long)max(pg[x], 0) * a.vbs + from) * R::kSize;
+        const uint32_t to = ring + put_slot * R::kSlot + x * 2 * R::kTile;
+        // (a value that is not seen is not read: zero times it might not be zero)
+        if (!E4M3 || wide) {
+#pragma unroll
+          for (int e = 0; e < kBlock * R::kPieces; e += 32) {
+            const int row = (e + lane) / R::kPieces, piece = (e + lane) - row * R::kPieces;
+            const bool there = 16 * piece < a.d * R::kSize && (all || (pg[x] >= 0 && sees(key + row)));
+            const int y = there ? row * a.d * R::kSize + 16 * piece : 0;
+            copy16(to + R::at(row, piece), kp + y, there);
+            copy16(to + R::kTile + R::at(row, piece), vp + y, there);
+          }
+        } else {
+#pragma unroll 1
+          for (int e = 0; e < kBlock * R::kPieces * 2; e += 32) {
+            const int row = (e + lane) / (2 * R::kPieces), piece = (e + lane) - row * 2 * R::kPieces;
+            const bool there = 8 * piece < a.d && (all || (pg[x] >= 0 && sees(key + row)));
+            const int y = there ? row * a.d + 8 * piece : 0, z = R::at(row, piece >> 1) + 8 * (piece & 1);
+            copy8(to + z, kp + y, there);
+            copy8(to + R::kTile + z, vp + y, there);
+          }
+        }
+      }
+    }
+    copies_end();
+    filled = (filled & ~(((1u << R::kPer) - 1u) << R::kPer * put_slot)) | any << R::kPer * put_slot;
+    if (++put_slot == R::kRing) put_slot = 0;
+  };
+  auto begin = [&]() {
+    todo = (int)min((long long)(units - first), u1 - u0);
+    hk = item / groups;
+    h0 = hk * G + (item - hk * groups) * heads;
+    nh = min(heads, (hk + 1) * G - h0);  // heads of this item
+    look_up(0);
+    put_slot = slot;
+#pragma unroll 1
+    for (int i = 0; i < R::kRing - 1; ++i) fetch(i);
+  };
+  begin();
 
-    // queries: head g of each eight, the columns that this lane's pieces of a key have
-    uint32_t q[NT][NC][4];
+  while (true) {
+    // queries: head g of each eight, the columns that a product's operand has
+    uint32_t q[NT][2 * NC][2];
     float scale[NT][2];  // of heads 2 c and 2 c + 1
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const __nv_bfloat16* row = a.q + b * a.qs + (long long)(h0 + 8 * t + g) * a.d;
-      uint4 raw[NC];
+      const bool there = 8 * t + g < nh;
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int col = 32 * i + 8 * c;
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (8 * t + g < nh && col < a.d) raw[i] = *reinterpret_cast<const uint4*>(row + col);
-      }
+      for (int i = 0; i < 2 * NC; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int col = 16 * i + (E4M3 ? 4 * c + 2 * k : 2 * c + 8 * k);
+          q[t][i][k] = there && col < a.d ? *reinterpret_cast<const uint32_t*>(row + col) : 0u;
+        }
       scale[t][0] = scale[t][1] = scale_log2;
       if constexpr (E4M3) {
         // to below 2 by a power of two, which the scale takes back
         float top = 0.f;
-        float2 f[NC][4];
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          widen8(raw[i], f[i]);
+        for (int i = 0; i < 2 * NC; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(f[i][k].x), fabsf(f[i][k].y)));
-        }
+          for (int k = 0; k < 2; ++k) {
+            const float2 f = widen2(q[t][i][k]);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         int e = (int)(__float_as_uint(top) >> 23) - 127;
         e = e > 127 ? 0 : min(max(e, -100), 126);  // (infinities stay)
         const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
+        for (int i = 0; i < 2 * NC; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) q[t][i][k] = pack_f16(f[i][k].x * down, f[i][k].y * down);
+          for (int k = 0; k < 2; ++k) {
+            const float2 f = widen2(q[t][i][k]);
+            q[t][i][k] = pack_f16(f.x * down, f.y * down);
+          }
         const float ks = a.kscale[hk];
         scale[t][0] *= ks * __shfl_sync(0xffffffffu, up, 8 * c);  // lane 4 h has head h's
         scale[t][1] *= ks * __shfl_sync(0xffffffffu, up, 8 * c + 4);
-      } else {
-#pragma unroll
-        for (int i = 0; i < NC; ++i) Piece<false>::pairs(raw[i], q[t][i]);
       }
     }
 
-    float o[NT][NV][4][4] = {};
+    float o[NT][2 * NC][4] = {};
     float m[NT][2], l[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) m[t][0] = m[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.f;
 
-    const int32_t* table = a.table + b * a.table_stride;
-    // the first key of this warp's i-th block, -1 behind the last
-    auto key_of = [&](int i) {
-      const int n = (first + i) * kWarps + warp;
-      return i < todo && n < blk.count ? kBlock * (n < blk.s ? n : blk.a + n - blk.s) : -1;
-    };
-    auto page_of = [&](int key) { return key >= 0 ? table[key / a.page] : -1; };
-    // whether a block is there, and its first token's place
-    auto place = [&](int key, int page, long long& at) {
-      if (key < 0) return false;
-      if (page < 0 || page >= a.blocks) {
-        if (lane == 0) atomicOr(err, kBadPage);
-        return false;
-      }
-      at = ((long long)hk * a.page + key % a.page) * a.d;
-      return true;
-    };
-    auto sees = [&](int key) { return key < blk.n && (key >= blk.seen.lo || key < blk.seen.sink_end); };
-    auto sees_all = [&](int key) {
-      return key + kBlock <= blk.n && (key >= blk.seen.lo || key + kBlock <= blk.seen.sink_end);
-    };
-    Raw kr[NC][2], vr[NV][4];
-    auto load_k = [&](long long at, int page) {
-      const unsigned char* p = static_cast<const unsigned char*>(a.kc) + ((long long)page * a.kbs + at) * P::kBytes;
+#pragma unroll 1
+    for (int i = 0; i * R::kPer < todo; ++i) {
+      const uint32_t there = filled >> R::kPer * slot & ((1u << R::kPer) - 1u);
+      copies_wait<R::kRing - 2>();
+      __syncwarp();  // every lane's copies of these blocks are there, and the blocks before are read
+      fetch(i + R::kRing - 1);
+      __syncwarp();
+      if (there != 0) {
+        const uint32_t at = ring + slot * R::kSlot;
+        float s[R::kPer][NT][4] = {};
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int col = 32 * i + 8 * c;
+        for (int j = 0; j < (E4M3 ? NC : 2 * NC); ++j)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          kr[i][r] = col < a.d ? load_once(reinterpret_cast<const Raw*>(p + ((g + 8 * r) * a.d + col) * P::kBytes))
-                               : P::zero();
-      }
-    };
-    auto load_v = [&](long long at, int page, int key, bool all) {
-      const unsigned char* p = static_cast<const unsigned char*>(a.vc) + ((long long)page * a.vbs + at) * P::kBytes;
+          for (int x = 0; x < R::kPer; ++x) {
+            uint32_t r[4];
+            ldmatrix4(at + x * 2 * R::kTile + R::at(lane & 15, 2 * j + (lane >> 4)), r);
+            if constexpr (E4M3) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int col = 64 * i + 8 * g;
+              for (int y = 0; y < 2; ++y) {
+                uint32_t ka[4];
+                widen_e4m3(r[2 * y], ka[0], ka[2]);
+                widen_e4m3(r[2 * y + 1], ka[1], ka[3]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 2 * c + (r & 1) + 8 * (r >> 1);
-          // a value that is not seen is not read: zero times it might not be zero
-          vr[i][r] = col < a.d && (all || sees(key + row))
-                         ? load_once(reinterpret_cast<const Raw*>(p + (row * a.d + col) * P::kBytes))
-                         : P::zero();
-        }
-      }
-    };
-
-    int key = key_of(0), page = page_of(key);
-    int next_key = key_of(1), next_page = page_of(next_key);
-    long long at = 0;
-    bool there = place(key, page, at), all = there && sees_all(key);
-    if (there) {
-      load_k(at, page);
-      load_v(at, page, key, all);
-    }
-    for (int i = 0; i < todo; ++i) {
-      const int after_key = key_of(i + 2), after_page = page_of(after_key);
-      long long next_at = 0;
-      const bool next_there = place(next_key, next_page, next_at), next_all = next_there && sees_all(next_key);
-      uint32_t p[NT][2];
-      if (there) {
-        float s[NT][4] = {};
+                for (int t = 0; t < NT; ++t) mma_f16(s[x][t], ka, q[t][2 * j + y][0], q[t][2 * j + y][1]);
+              }
+            } else {
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-          uint32_t w0[4], w1[4];
-          P::pairs(kr[j][0], w0);
-          P::pairs(kr[j][1], w1);
-#pragma unroll
-          for (int st = 0; st < 2; ++st) {
-            const uint32_t ka[4] = {w0[2 * st], w1[2 * st], w0[2 * st + 1], w1[2 * st + 1]};
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              if constexpr (E4M3) mma_f16(s[t], ka, q[t][j][2 * st], q[t][j][2 * st + 1]);
-              else mma_bf16(s[t], ka, q[t][j][2 * st], q[t][j][2 * st + 1]);
+              for (int t = 0; t < NT; ++t) mma_bf16(s[x][t], r, q[t][j][0], q[t][j][1]);
             }
           }
-        }
-        if (next_there) load_k(next_at, next_page);
         bool above = false;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int x = 0; x < R::kPer; ++x) {
+          const int key = key_of(i * R::kPer + x);
+          const bool some = there >> x & 1u, all = some && sees_all(key);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            s[t][k] *= scale[t][k & 1];
-            if (!all && !sees(key + g + 8 * (k >> 1))) s[t][k] = -INFINITY;
-            above |= s[t][k] > m[t][k & 1] + kLazy;
-          }
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              s[x][t][k] *= scale[t][k & 1];
+              if (!all && (!some || !sees(key + g + 8 * (k >> 1)))) s[x][t][k] = -INFINITY;
+              above |= s[x][t][k] > m[t][k & 1] + kLazy;
+            }
+        }
         if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              float top = fmaxf(s[t][k], s[t][k + 2]);
+              float top = fmaxf(s[0][t][k], s[0][t][k + 2]);
+#pragma unroll
+              for (int x = 1; x < R::kPer; ++x) top = fmaxf(top, fmaxf(s[x][t][k], s[x][t][k + 2]));
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
               if (top > m[t][k]) {
@@ -340,119 +398,137 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
                 m[t][k] = top;
                 l[t][k] *= f;
 #pragma unroll
-                for (int v = 0; v < NV; ++v)
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) o[t][v][x][k] *= f, o[t][v][x][k + 2] *= f;
+                for (int x = 0; x < 2 * NC; ++x) o[t][x][k] *= f, o[t][x][k + 2] *= f;
               }
             }
         }
+        uint32_t p[R::kPer][NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float w[4];
+          const float base[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            w[k] = ex2_approx(s[t][k] - (m[t][k & 1] == -INFINITY ? 0.f : m[t][k & 1]));
-            l[t][k & 1] += w[k];
+          for (int x = 0; x < R::kPer; ++x) {
+            float w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              w[k] = ex2_approx(s[x][t][k] - base[k & 1]);
+              l[t][k & 1] += w[k];
+            }
+            p[x][t][0] = transposed(E4M3 ? pack_f16(w[0], w[1]) : pack_bf16(w[0], w[1]));
+            p[x][t][1] = transposed(E4M3 ? pack_f16(w[2], w[3]) : pack_bf16(w[2], w[3]));
           }
-          p[t][0] = transposed(E4M3 ? pack_f16(w[0], w[1]) : pack_bf16(w[0], w[1]));
-          p[t][1] = transposed(E4M3 ? pack_f16(w[2], w[3]) : pack_bf16(w[2], w[3]));
         }
+        const int v_row = (lane & 7) + (lane >> 4) * 8, v_piece = lane >> 3 & 1;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          uint32_t w[4][4];
+        for (int x = 0; x < R::kPer; ++x)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) P::pairs(vr[v][r], w[r]);
+          for (int j = 0; j < (E4M3 ? NC : 2 * NC); ++j) {
+            uint32_t r[4];
+            ldmatrix4_trans(at + (x * 2 + 1) * R::kTile + R::at(v_row, 2 * j + v_piece), r);
+            if constexpr (E4M3) {
+              // a lane's four bytes: two keys' two columns; keys 8 on are in the last two
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t va[4] = {__byte_perm(w[0][x], w[1][x], 0x5410), __byte_perm(w[0][x], w[1][x], 0x7632),
-                                    __byte_perm(w[2][x], w[3][x], 0x5410), __byte_perm(w[2][x], w[3][x], 0x7632)};
+              for (int y = 0; y < 2; ++y) {
+                uint32_t va[4];
+                widen_e4m3(__byte_perm(r[y], 0, 0x3120), va[0], va[1]);
+                widen_e4m3(__byte_perm(r[y + 2], 0, 0x3120), va[2], va[3]);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              if constexpr (E4M3) mma_f16(o[t][v][x], va, p[t][0], p[t][1]);
-              else mma_bf16(o[t][v][x], va, p[t][0], p[t][1]);
+                for (int t = 0; t < NT; ++t) mma_f16(o[t][2 * j + y], va, p[x][t][0], p[x][t][1]);
+              }
+            } else {
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma_bf16(o[t][j], r, p[x][t][0], p[x][t][1]);
             }
           }
-        }
-      } else if (next_there) {
-        load_k(next_at, next_page);
       }
-      if (next_there) load_v(next_at, next_page, next_key, next_all);
-      key = next_key;
-      there = next_there;
-      all = next_all;
-      next_key = after_key;
-      next_page = after_page;
+      if (++slot == R::kRing) slot = 0;
     }
 
-    // the warps' sums together
-    __syncthreads();  // the item before's are read
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float sum = l[t][k];
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        const int h = 8 * t + 2 * c + k;
-        if (g == 0) stat[warp][h] = make_float2(m[t][k], sum);
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          if (64 * v + 8 * g >= 32 * NC) continue;
-          float4* to = reinterpret_cast<float4*>(&so[warp][h][64 * v + 8 * g]);
-          to[0] = make_float4(o[t][v][0][k], o[t][v][0][k + 2], o[t][v][1][k], o[t][v][1][k + 2]);
-          to[1] = make_float4(o[t][v][2][k], o[t][v][2][k + 2], o[t][v][3][k], o[t][v][3][k + 2]);
-        }
+    // the next item's blocks are on their way while this one's sums are joined
+    const int at_b = b, at_item = item, at_hk = hk, at_h0 = h0, at_nh = nh, parts_units = units;
+    const bool from_start = first == 0, whole = from_start && todo == units;
+    const long long at_start = before + (long long)item * units;
+    u0 += todo;
+    const bool more = u0 < u1;
+    if (more) {
+      first = 0;
+      if (++item == per_seq) {
+        item = 0;
+        before += (long long)units * per_seq;
+        blk = blocks_of(a, ++b);
+        units = units_of(blk.count);
       }
-    __syncthreads();
-    const bool whole = first == 0 && todo == units;
-    const int slot = 2 * blockIdx.x + (first == 0 ? 1 : 0);
-    const float vs = E4M3 ? a.vscale[hk] : 1.f;
+      __syncwarp();
+      begin();
+    }
+
+    const int index = 2 * blockIdx.x + (from_start ? 1 : 0);
+    const float vs = E4M3 ? a.vscale[at_hk] : 1.f;
     // a head's quotient to its row (four columns), and the log of its sum
     auto put = [&](int h, int col, const float4& x, float top, float sum) {
-      const long long row = (long long)b * a.Hq + h0 + h;
+      const long long row = (long long)at_b * a.Hq + at_h0 + h;
       const float inv = sum == 0.f ? 0.f : vs / sum;
       const float2 f[2] = {{x.x * inv, x.y * inv}, {x.z * inv, x.w * inv}};
       *reinterpret_cast<uint2*>(a.out + row * a.d + col) = sum == 0.f ? make_uint2(0, 0) : narrow4(f);
       if (a.lse != nullptr && col == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * attn::kLn2;
     };
     const int quads = a.d / 4;
-    for (int x = tid; x < nh * quads; x += kThreads) {
-      const int h = x / quads, col = 4 * (x - h * quads);
-      float top = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w][h].x);
-      float4 all4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int t = 0; t < NT; ++t) {
+      __syncthreads();  // what was there before is read
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 st = stat[w][h];
-        const float f = share(st, top);
-        const float4 y = *reinterpret_cast<const float4*>(&so[w][h][col]);
-        sum = fmaf(f, st.y, sum);
-        all4 = add(all4, f, y);
+      for (int k = 0; k < 2; ++k) {
+        float sum = l[t][k];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        const int h = 2 * c + k;
+        if (g == 0) stat[warp][h] = make_float2(m[t][k], sum);
+#pragma unroll
+        for (int x = 0; x < 2 * NC; ++x) {
+          so[warp][h][16 * x + (E4M3 ? 2 * g : g)] = o[t][x][k];
+          so[warp][h][16 * x + (E4M3 ? 2 * g + 1 : g + 8)] = o[t][x][k + 2];
+        }
       }
-      if (whole) {
-        put(h, col, all4, top, sum);
-      } else {
-        *reinterpret_cast<float4*>(work.sums + ((long long)slot * kMaxHeads + h) * attn::kMaxDim + col) = all4;
-        if (col == 0) work.stats[slot * kMaxHeads + h] = make_float2(top, sum);
+      __syncthreads();
+      for (int x = tid; x < min(at_nh - 8 * t, 8) * quads; x += kThreads) {
+        const int h = x / quads, col = 4 * (x - h * quads);
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w][h].x);
+        float4 all4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 st = stat[w][h];
+          const float f = share(st, top);
+          const float4 y = *reinterpret_cast<const float4*>(&so[w][h][col]);
+          sum = fmaf(f, st.y, sum);
+          all4 = add(all4, f, y);
+        }
+        if (whole) {
+          put(8 * t + h, col, all4, top, sum);
+        } else {
+          const long long to = index * kMaxHeads + 8 * t + h;
+          *reinterpret_cast<float4*>(work.sums + to * attn::kMaxDim + col) = all4;
+          if (col == 0) work.stats[to] = make_float2(top, sum);
+        }
       }
     }
     if (!whole) {
       // the run that finishes the last part joins them all
-      const long long start = before + (long long)item * units, end = start + units;  // the item's units
-      auto run_of = [&](long long u) { return (int)(((u + 1) * runs - 1) / total); };
-      const int r0 = run_of(start), r1 = run_of(end - 1);
-      int* counter = work.counters + (long long)b * per_seq + item;
+      auto run_of = [&](long long u) { return (int)quotient(u, per_run); };
+      const int r0 = run_of(at_start), r1 = run_of(at_start + parts_units - 1);
+      int* counter = work.counters + (long long)at_b * per_seq + at_item;
       __threadfence();
       __syncthreads();
-      if (tid == 0) last = atomicAdd(counter, 1) == r1 - r0;
+      if (tid == 0) *last = atomicAdd(counter, 1) == r1 - r0;
       __syncthreads();
-      if (last) {
+      if (*last) {
         __threadfence();
         if (tid == 0) *counter = 0;
-        for (int x = tid; x < nh * quads; x += kThreads) {
+        for (int x = tid; x < at_nh * quads; x += kThreads) {
           const int h = x / quads, col = 4 * (x - h * quads);
           float top = -INFINITY, sum = 0.f;
+#pragma unroll 8
           for (int r = r0; r <= r1; ++r) top = fmaxf(top, __ldcg(&work.stats[(2 * r + (r == r0)) * kMaxHeads + h]).x);
           float4 all4 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -468,22 +544,13 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
         }
       }
     }
-
-    u0 += todo;
-    first = 0;
-    if (++item == per_seq) {
-      item = 0;
-      before += (long long)units * per_seq;
-      if (++b == a.B) break;
-      blk = blocks_of(a, b);
-      units = units_of(blk.count);
-    }
+    if (!more) break;
   }
 }
 
 namespace {
 
-int resident(int heads, int sms) { return sms * (heads <= 8 ? 3 : 2); }
+int resident(int sms) { return sms * kCtas; }
 
 // Workspace: [256 B status words][partial sums][their maxima and sums][counters].  The places do not depend on the
 // call, so that the counters are zero whatever call came before.
@@ -492,7 +559,7 @@ struct Layout {
 };
 Layout layout(int B, int Hq, int Hkv, int sms) {
   const int G = Hq / Hkv, groups = (G + kMaxHeads - 1) / kMaxHeads;
-  const size_t slots = 2 * (size_t)resident(1, sms) * kMaxHeads;
+  const size_t slots = 2 * (size_t)resident(sms) * kMaxHeads;
   Layout l;
   l.stats = 256 + slots * attn::kMaxDim * 4;
   l.counters = l.stats + slots * 8;
@@ -500,15 +567,14 @@ Layout layout(int B, int Hq, int Hkv, int sms) {
   return l;
 }
 
-template <int NT, bool E4M3>
-void launch_step(const StepArgs& a, int nc, int groups, int heads, unsigned grid, Work w, int* err, cudaStream_t st) {
-  const float c = a.scale * attn::kLog2e;
-  switch (nc) {
-    case 1: return gdn_attn_step_kernel<NT, 1, E4M3><<<grid, kThreads, 0, st>>>(a, groups, heads, c, w, err);
-    case 2: return gdn_attn_step_kernel<NT, 2, E4M3><<<grid, kThreads, 0, st>>>(a, groups, heads, c, w, err);
-    case 3: return gdn_attn_step_kernel<NT, 3, E4M3><<<grid, kThreads, 0, st>>>(a, groups, heads, c, w, err);
-    default: return gdn_attn_step_kernel<NT, 4, E4M3><<<grid, kThreads, 0, st>>>(a, groups, heads, c, w, err);
-  }
+template <int NT, int NC, bool E4M3>
+cudaError_t launch_step(const StepArgs& a, int groups, int heads, unsigned grid, Work w, int* err, cudaStream_t st) {
+  constexpr int kSmem = Ring<NT, NC, E4M3>::kSmem;
+  const cudaError_t e = set_smem_limit_once<gdn_attn_step_kernel<NT, NC, E4M3>>(kSmem);
+  if (e != cudaSuccess) return e;
+  gdn_attn_step_kernel<NT, NC, E4M3>
+      <<<grid, kThreads, kSmem, st>>>(a, groups, heads, a.scale * attn::kLog2e, a.d % 16 == 0, w, err);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -528,12 +594,21 @@ cudaError_t launch_attn_step(const StepArgs& a, bool e4m3, void* ws, cudaStream_
   Work w = {reinterpret_cast<float*>(p + 256), reinterpret_cast<float2*>(p + l.stats),
             reinterpret_cast<int*>(p + l.counters)};
   int* err = static_cast<int*>(ws);
-  const int nc = (a.d + 31) / 32;
-  const unsigned grid = (unsigned)resident(heads, sms);
-  auto run = [&](auto launch) { launch(a, nc, groups, heads, grid, w, err, st); };
-  if (heads <= 8) e4m3 ? run(launch_step<1, true>) : run(launch_step<1, false>);
-  else e4m3 ? run(launch_step<2, true>) : run(launch_step<2, false>);
-  return cudaGetLastError();
+  const unsigned grid = (unsigned)resident(sms);
+  auto run = [&](auto nt, auto e) {
+    constexpr int NT = decltype(nt)::value;
+    constexpr bool E4M3 = decltype(e)::value;
+    switch ((a.d + 31) / 32) {
+      case 1: return launch_step<NT, 1, E4M3>(a, groups, heads, grid, w, err, st);
+      case 2: return launch_step<NT, 2, E4M3>(a, groups, heads, grid, w, err, st);
+      case 3: return launch_step<NT, 3, E4M3>(a, groups, heads, grid, w, err, st);
+      default: return launch_step<NT, 4, E4M3>(a, groups, heads, grid, w, err, st);
+    }
+  };
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  if (heads <= 8) return e4m3 ? run(One(), std::true_type()) : run(One(), std::false_type());
+  return e4m3 ? run(Two(), std::true_type()) : run(Two(), std::false_type());
 }
 
 }  // namespace gdn
