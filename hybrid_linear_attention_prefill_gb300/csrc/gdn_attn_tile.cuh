@@ -68,11 +68,11 @@ using Slot = std::integral_constant<int, N>;
 // f with the ring's slot as a constant, which the products' operands are made of: an MMA whose descriptors are
 // constants is issued in less than the 64 clocks that it takes, one whose are worked out in 110.
 template <int kRing, class F>
-__device__ __forceinline__ bool in_slot(int slot, F f) {
-  if (slot == 0) return f(Slot<0>());
-  if (kRing == 2 || slot == 1) return f(Slot<1>());
-  if (slot == 2) return f(Slot<2 % kRing>());
-  return f(Slot<3 % kRing>());
+__device__ __forceinline__ void in_slot(int slot, F f) {
+  if (slot == 0) f(Slot<0>());
+  else if (kRing == 2 || slot == 1) f(Slot<1>());
+  else if (slot == 2) f(Slot<2 % kRing>());
+  else f(Slot<3 % kRing>());
 }
 
 // The keys that an item's queries see, one list: the first `sink` of the sequence (sinks, rounded up to 16; none where
@@ -88,6 +88,7 @@ struct Item {
   int tiles;     // of keys
   int sinks;     // tiles of keys with sinks
   int a[2], z[2];  // tiles of keys [a, z) that either tile of queries sees otherwise
+  int lo_all[2], hi_all[2];  // places from `lo` on that all of a tile's queries see
   __device__ __forceinline__ bool has(int t, int kt) const { return (kt < sinks && z[t] > 0) || (kt >= a[t] && kt < z[t]); }
   __device__ __forceinline__ int count(int t) const { return z[t] > 0 ? sinks + z[t] - a[t] : 0; }
   __device__ __forceinline__ int place(int key) const { return key - lo + sink; }  // of a key from `lo` on
@@ -111,6 +112,8 @@ __device__ __forceinline__ void find_keys(Item& it, const View& view, int tpt) {
     it.z[t] = (it.place(pb + 1) + kKeys - 1) / kKeys;
     it.a[t] = max(it.sinks, view.sinks > 0 && it.sink == 0 ? 0 : it.place(lo) / kKeys);
     it.tiles = max(it.tiles, it.z[t]);
+    it.lo_all[t] = it.place(attn::seen_by(view, pb).lo);
+    it.hi_all[t] = it.place(attn::seen_by(view, pa).hi);
   }
 }
 
@@ -233,10 +236,11 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   if (smem_u32(smem_raw) != kSmemBase) give_up(1);
   // One thread's wait; false once this or another wait has run out.
   auto wait = [&](uint64_t* bar, uint32_t par, int bit) {
-    if (tc::mbar_wait(bar, par, 8)) return true;
+    if (tc::mbar_wait(bar, par, 1)) return true;
     const long long since = clock64();
+#pragma unroll 1
     while (!*abort_flag) {
-      if (tc::mbar_wait(bar, par, 8)) return true;
+      if (tc::mbar_wait(bar, par, 1)) return true;
       if (clock64() - since > kPatience) give_up(bit);
     }
     return false;
@@ -265,13 +269,14 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       int sb = -1, tile = 0, hk = 0;
       more = idx < items;
       if (more && a.cu == nullptr) {  // the last tiles, which see the most, first
-        const int rest = (int)(idx % ((long long)a.B * heads));
-        tile = nseq - 1 - (int)(idx / ((long long)a.B * heads));
+        const uint32_t each = (uint32_t)a.B * heads;  // (no more than items)
+        const int rest = (int)((uint32_t)idx % each);
+        tile = nseq - 1 - (int)((uint32_t)idx / each);
         sb = rest / heads;
         hk = rest - sb * heads;
       } else if (more) {
-        const int f = (int)(idx / heads);
-        hk = (int)(idx - (long long)f * heads);
+        const int f = (int)((uint32_t)idx / (uint32_t)heads);
+        hk = (int)idx - f * heads;
         while (b < a.B) {  // 32 sequences at a time
           const int c = b + lane < a.B ? (seq_bounds(a.cu, b + lane, a.T).len + per - 1) / per : 0;
           int sum = c;
@@ -323,6 +328,7 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (loads >= kRing && !wait(empty, (uint32_t)(loads / kRing - 1) & 1u, 2)) return false;
         tc::mbar_arrive_expect_tx(full, kTile);
         if (v0 < it.sink && v0 + kKeys > it.sink) {
+#pragma unroll 1
           for (int i = 0; i < kKeys; i += 16) {
             const int tok = it.k0 + (v0 + i < it.sink ? v0 + i : it.lo + v0 + i - it.sink);
 #pragma unroll
@@ -360,16 +366,23 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
       // what is in flight lands before the CTA ends, whoever gave up (bounded again; after a wait that gave up a
       // tile of keys may be one ahead of its values)
+      auto land = [](uint64_t* bar, uint32_t par) {
+#pragma unroll 1
+        for (int i = 0; i < 1 << 14 && !tc::mbar_wait(bar, par, 1); ++i) {
+        }
+      };
+#pragma unroll 1
       for (int i = 0; i < kRing; ++i)
         if (i < loads || !ok) {
+#pragma unroll 1
           const uint32_t p = (uint32_t)((loads - 1 - i) / kRing) & 1u;
           for (uint32_t x = ok ? p : 0; x <= (ok ? p : 1); ++x) {
-            (void)tc::mbar_wait(k_full + i, x, 1u << 14);
-            (void)tc::mbar_wait(v_full + i, x, 1u << 14);
+            land(k_full + i, x);
+            land(v_full + i, x);
           }
         }
       for (int t = 0; t < 2; ++t)
-        if (queries[t] > 0) (void)tc::mbar_wait(q_full + t, (uint32_t)(queries[t] - 1) & 1u, 1u << 14);
+        if (queries[t] > 0) land(q_full + t, (uint32_t)(queries[t] - 1) & 1u);
     }
     __syncwarp();
   } else {
@@ -400,36 +413,8 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           }
         }
       };
-      // The pending product, with the values of slot S, the one before `tiles`; `keys`, `turn`: what else to wait for.
-      auto flush = [&](auto slot, uint64_t* keys, uint64_t* turn, uint32_t turn_par) {
-        constexpr int S = decltype(slot)::value;
-        uint64_t* bar = nullptr;
-        uint32_t par = 0;
-        if (lane == 0 && tiles > 0) bar = v_full + S, par = ((tiles - 1) / kRing) & 1u;
-        if (lane == 1) bar = keys, par = (tiles / kRing) & 1u;
-        if (lane == 2 && on) bar = p_full + t, par = p_par;
-        // (the item's before; items that see nothing have no phase, so that neither side can be two ahead)
-        if (lane == 3 && on && first && seen_items > 1) bar = o_empty + t, par = (uint32_t)seen_items & 1u;
-        if (lane == 4) bar = turn, par = turn_par;
-        if (!look(bar, par)) return false;
-        if (!on) return true;
-        const uint64_t v = tc::sdesc(sb + C::kOffV + S * kTile, kHalf, 1024, tc::kSw128);
-        if (lane == 0) {
-          const uint32_t more = first ? 0u : 1u;
-          tc::fence_after();
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            tc::mma_f16_ta(kColO + t * 128, kColS + t * 128 + 8 * k, v + ((k * 2048) >> 4), id_o, k > 0 ? 1u : more);
-          if (last) tc::commit(o_full + t);
-        }
-        __syncwarp();
-        p_par ^= 1u;
-        on = false;
-        return true;
-      };
-      auto flush_alone = [&]() {
-        return in_slot<kRing>((int)((tiles + kRing - 1) % kRing), [&](auto slot) { return flush(slot, nullptr, nullptr, 0); });
-      };
+      // A step is a tile of keys.  An item without any, and the end, are one too, for the product that is pending (in one
+      // place all, since what is executed between two tiles has to fit the instruction cache).
       for (int n = 0;; ++n) {
         if (!(ok = warp_wait(item_full + n % kItemSlots, item_par(n), 1))) break;
         const Item* ip = item_at(n);
@@ -437,19 +422,37 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const int total = ip->count(t);
         __syncwarp();
         if (lane == 0) arrive(item_empty + n % kItemSlots);
-        if (!valid) break;
         int left = total;
-        for (int kt = 0; ok && kt < all; ++kt) {
-          ok = in_slot<kRing>((int)(tiles % kRing), [&](auto slot) {
-            constexpr int S = decltype(slot)::value, before = (S + kRing - 1) % kRing;
-            const bool some = kt < sinks || (kt >= from && kt < to);
-            // (an item's first keys and queries apart, so that the last item's product does not wait for them)
-            if (!flush(Slot<before>(), kt > 0 ? k_full + S : nullptr, t == 1 || tiles > 0 ? turn + t : nullptr,
-                       t == 1 ? tiles & 1u : (tiles - 1) & 1u))
-              return false;
-            if (kt == 0) {
-              uint64_t* bar = lane == 0 ? q_full + t : lane == 1 ? k_full + S : nullptr;
-              if (!look(bar, lane == 0 ? (uint32_t)n & 1u : (tiles / kRing) & 1u)) return false;
+#pragma unroll 1
+        for (int kt = 0; kt < (valid ? max(all, 1) : 1); ++kt) {
+          const bool keys = valid && kt < all, some = keys && (kt < sinks || (kt >= from && kt < to));
+          const int slot = (int)(tiles % kRing), before = (int)((tiles + kRing - 1) % kRing);
+          // the pending product's values, weights and place; the keys (an item's first ones and the queries apart, so
+          // that the last item's product does not wait for them); the turn
+          uint64_t* bar = nullptr;
+          uint32_t par = 0;
+          if (lane == 0 && tiles > 0) bar = v_full + before, par = ((tiles - 1) / kRing) & 1u;
+          if (lane == 1 && keys && kt > 0) bar = k_full + slot, par = (tiles / kRing) & 1u;
+          if (lane == 2 && on) bar = p_full + t, par = p_par;
+          // (the item's before; items that see nothing have no phase, so that neither side can be two ahead)
+          if (lane == 3 && on && first && seen_items > 1) bar = o_empty + t, par = (uint32_t)seen_items & 1u;
+          if (lane == 4 && keys && (t == 1 || tiles > 0)) bar = turn + t, par = t == 1 ? tiles & 1u : (tiles - 1) & 1u;
+          if (!(ok = look(bar, par))) break;
+          in_slot<kRing>(slot, [&](auto at) {
+            constexpr int S = decltype(at)::value, kBefore = (S + kRing - 1) % kRing;
+            if (on && lane == 0) {
+              const uint64_t v = tc::sdesc(sb + C::kOffV + kBefore * kTile, kHalf, 1024, tc::kSw128);
+              const uint32_t more = first ? 0u : 1u;
+              tc::fence_after();
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                tc::mma_f16_ta(kColO + t * 128, kColS + t * 128 + 8 * k, v + ((k * 2048) >> 4), id_o, k > 0 ? 1u : more);
+              if (last) tc::commit(o_full + t);
+            }
+            __syncwarp();
+            if (valid && kt == 0) {
+              bar = lane == 0 ? q_full + t : lane == 1 && keys ? k_full + S : nullptr;
+              if (!(ok = look(bar, lane == 0 ? (uint32_t)n & 1u : (tiles / kRing) & 1u))) return;
             }
             if (lane == 0) {
               if (some) {
@@ -464,33 +467,27 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                   if (i == kQuarters - 1) arrive(turn + 1 - t);
                 }
                 tc::commit(s_full + t);
-              } else {
+              } else if (keys) {
                 arrive(turn + 1 - t);
               }
-              if (some && left == 1) tc::commit(q_empty + t);
-              if (tiles > 0) tc::commit(v_empty + before);
-              tc::commit(k_empty + S);
+              if (valid && (total > 0 ? some && left == 1 : kt == 0)) tc::commit(q_empty + t);
+              if (keys && tiles > 0) tc::commit(v_empty + kBefore);
+              if (keys) tc::commit(k_empty + S);
             }
-            __syncwarp();
-            if (some) {
-              on = true;
-              first = left == total;
-              last = --left == 0;
-              seen_items += first;
-            }
-            return true;
           });
-          ++tiles;
-        }
-        if (!ok) break;
-        if (total == 0) {  // nothing to see: the phases go by in order all the same, after what is pending
-          ok = flush_alone() && (all > 0 || look(lane == 0 ? q_full + t : nullptr, (uint32_t)n & 1u));
           if (!ok) break;
-          if (lane == 0) tc::commit(q_empty + t);
+          if (on) p_par ^= 1u;
+          on = some;
+          if (some) {
+            first = left == total;
+            last = --left == 0;
+            seen_items += first;
+          }
           __syncwarp();
+          tiles += keys;
         }
+        if (!ok || !valid) break;
       }
-      if (ok) ok = flush_alone();
       if (lane == 0) {
         tc::commit(drain + t);
         if (!tc::mbar_wait(drain + t, 0, 1u << 16)) give_up(1);
@@ -511,13 +508,14 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const int pair = 1 + 4 * t + quad;  // the barrier: both warps of a row come to it every time, one that gave up too
     float *tops = stat + t * 256 + row, *sums = tops + 512, *odds = sums + 512;  // of half h: + 128 h
     uint32_t s_par = 0, o_par = 0;
-    for (int n = 0;; ++n) {
-      bool ok = warp_wait(item_full + n % kItemSlots, item_par(n), 1);
-      if (any_of_pair(pair, !ok)) break;
+    bool ok = warp_wait(item_full, 0, 1);
+    bool stop = any_of_pair(pair, !ok);
+    for (int n = 0; !stop; ++n) {
       const Item* ip = item_at(n);
       const int valid = ip->valid, pa = ip->p0 + t * tpt, nt = ip->n[t], off = ip->sink - ip->lo;
       const int sink_tiles = ip->z[t] > 0 ? ip->sinks : 0, from = ip->a[t], to = ip->z[t];
       const int tok0 = ip->q0 + t * tpt, k0 = ip->k0, hk = ip->hk;
+      const int lo_all = ip->lo_all[t], hi_all = ip->hi_all[t];
       __syncwarp();
       if (lane == 0) arrive(item_empty + n % kItemSlots);
       if (!valid) break;
@@ -525,8 +523,6 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       // places of the list that the row sees: [0, sinks) and [lo, hi), and what all the tile's rows see
       const Seen mine = attn::seen_by(a.view, pa + tr);
       const int lo = mine.lo + off, hi = mine.hi + off;
-      const int lo_all = attn::seen_by(a.view, pa + nt - 1).lo + off, hi_all = attn::seen_by(a.view, pa).hi + off;
-      bool stop = false;
       for (int kt = sink_tiles > 0 ? 0 : from; kt < to; kt = kt + 1 == sink_tiles ? from : kt + 1) {
         ok = warp_wait(s_full + t, s_par, 1);
         s_par ^= 1u;
@@ -570,10 +566,9 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         float top = scale_log2 * fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
         // (Both warps have their scores when they meet: the other's weights go in the place of some of them.)
         if (any_of_pair(pair, !ok || top > m + kLazy)) {
-          if ((stop = any_of_pair(pair, !ok))) break;
           // a row's is far above: it takes its place, and those weights are made again
           tops[128 * hf] = top;
-          pair_sync(pair);
+          if ((stop = any_of_pair(pair, !ok))) break;
           top = fmaxf(top, tops[128 * (1 - hf)]);
           const float next = top > m + kLazy ? top : m;
           if (__any_sync(0xffffffffu, m != -INFINITY)) {
@@ -617,8 +612,8 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const long long tok = (long long)tok0 + tr;
       const int head = hk * G + row - tr * G;
       __nv_bfloat16* out = a.out + (tok * a.Hq + head) * a.d;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      bool odd = false;
+      const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+      float2 zero = make_float2(0.f, 0.f);  // or NaN, once a value is not finite
 #pragma unroll 1
       for (int c = 32 * hf; c < a.d; c += 64) {
         float r[32] = {};
@@ -626,14 +621,13 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (some) tc::tmem_ld32(o_at + c, r);
 #pragma unroll
         for (int i = 0; i < 32; i += 8) {
-          if (c + i >= a.d) break;
           float2 f[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            f[k] = l == 0.f ? make_float2(0.f, 0.f) : make_float2(r[i + 2 * k] * inv, r[i + 2 * k + 1] * inv);
-            odd |= !(fabsf(f[k].x) <= FLT_MAX) || !(fabsf(f[k].y) <= FLT_MAX);
+            f[k] = mul2(make_float2(r[i + 2 * k], r[i + 2 * k + 1]), make_float2(inv, inv));
+            zero = fma2(f[k], make_float2(0.f, 0.f), zero);
           }
-          if (live) *reinterpret_cast<uint4*>(out + c + i) = narrow8(f);
+          if (live && c + i < a.d) *reinterpret_cast<uint4*>(out + c + i) = narrow8(f);
         }
       }
       if (live && hf == 0 && a.lse != nullptr)
@@ -642,7 +636,9 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       __syncwarp();
       if (some && lane == 0) arrive(o_empty + t);
       // rows that are not finite again, one after the other (but where the weights' sum is not: nothing else could be)
-      odd = odd && live && l <= FLT_MAX;
+      // (and where nothing is seen, 0 times the sum of values that were not)
+      bool odd = !(zero.x + zero.y == 0.f) && live && l <= FLT_MAX;
+      ok = ok && warp_wait(item_full + (n + 1) % kItemSlots, item_par(n + 1), 1);
       if (any_of_pair(pair, odd || !ok)) {
         if (any_of_pair(pair, !ok)) break;
         odds[128 * hf] = odd ? 1.f : 0.f;
