@@ -13,6 +13,8 @@
 #include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "gdn_cache.h"
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
@@ -24,14 +26,16 @@ namespace gdn {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024, kPlanFew = 256;  // of a CTA; where that many do for requests and tokens
+constexpr int kPlanRun = 4;           // tokens of packed requests that a thread takes together
 constexpr int kPlanCtas = 8;          // of the cluster for many tokens
 constexpr int kPlanAlone = 4096;      // tokens that one CTA takes by itself
 constexpr int kAppendThreads = 256;
-constexpr int kAppendAhead = 4;       // tokens a thread has on their way
+constexpr int kAppendAhead = 4;       // tokens a thread has on their way, where that leaves two CTAs an SM
 
 // Sum over the threads before this one, and over all (in every thread).
 __device__ __forceinline__ long long block_scan(long long v, long long* part, long long& all) {
+  const int warps = blockDim.x / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long sum = v;
 #pragma unroll
@@ -42,7 +46,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* part, lo
   __syncthreads();  // part may still be read for the round before
   if (lane == 31) part[warp] = sum;
   __syncthreads();
-  long long w = part[lane];
+  long long w = lane < warps ? part[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, w, o);
@@ -52,6 +56,13 @@ __device__ __forceinline__ long long block_scan(long long v, long long* part, lo
   const long long before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
   return sum - v + (warp > 0 ? before : 0);
 }
+
+// x / y of x below 2^31, with 2^32 / y rounded down: one too few at most before the correction.
+__device__ __forceinline__ int over(int x, int y, uint32_t inverse) {
+  const int q = (int)__umulhi((uint32_t)x, inverse);
+  return q + (x - q * y >= y);
+}
+__device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p)); }
 
 }  // namespace
 
@@ -64,12 +75,14 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_cache_plan_kernel(const Cach
   __shared__ int lacking;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  const int threads = blockDim.x;
+  const uint32_t inverse = 0xffffffffu / (uint32_t)a.page;
   if (tid == 0) lacking = 0;
   int count = *a.free_count;
   count = count < 0 ? 0 : count > a.capacity ? a.capacity : count;
 
   long long carry = 0, taken = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < a.B; b0 += threads) {
     const int b = b0 + tid;
     long long need = 0;
     int n = -1;
@@ -84,9 +97,15 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_cache_plan_kernel(const Cach
       }
       start[b] = lo;
       held[b] = n;
-      const long long have = ((long long)n + a.page - 1) / a.page, want = ((long long)n + hi - lo + a.page - 1) / a.page;
-      able = n >= 0 && want <= a.W && (long long)n + hi - lo <= 0x7fffffffLL;
+      // (blocks that a count of tokens begins, without leaving 32 bits: those of the last token and before)
+      const bool fits = n >= 0 && (long long)n + hi - lo <= 0x7fffffffLL;
+      const int have = n > 0 ? over(n - 1, a.page, inverse) + 1 : 0;
+      const int want = fits && n + hi - lo > 0 ? over(n + hi - lo - 1, a.page, inverse) + 1 : 0;
+      able = fits && want <= a.W;
       need = able ? want - have : 0;
+      // what comes next is fetched beside the sums
+      if (n > 0 && have <= a.W && n - (have - 1) * a.page < a.page) prefetch(a.table + b * a.table_stride + have - 1);
+      if (b < count) prefetch(a.free_blocks + count - 1 - b);
     }
     long long all;
     const long long before = carry + block_scan(need, part, all);
@@ -105,49 +124,77 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_cache_plan_kernel(const Cach
   }
   __syncthreads();
   if ((tid & 31) == 0) part[tid >> 5] = taken;
-  cluster.sync();  // every CTA has read the lengths and the stack's height (and part is written)
+  // every CTA has read the lengths and the stack's height (and part is written)
+  if (ctas > 1) cluster.sync();
+  else __syncthreads();
 
   if (rank == 0) {
-    for (int b = tid; b < a.B; b += kPlanThreads) {
+    for (int b = tid; b < a.B; b += threads) {
       const int len = a.cu != nullptr ? seq_bounds(a.cu, b, a.T).len : 1;
       a.new_lens[b] = base[b] >= 0 ? held[b] + len : held[b];
     }
     if (tid == 0) {
       long long most = 0;
-      for (int w = 0; w < kPlanThreads / 32; ++w) most = part[w] > most ? part[w] : most;
+      for (int w = 0; w < threads / 32; ++w) most = part[w] > most ? part[w] : most;
       *a.new_count = count - (int)most;
       if (a.refused != nullptr) *a.refused = lacking;
     }
   }
-  // table entries: a warp a request
-  for (int b = rank * (kPlanThreads / 32) + (tid >> 5); b < a.B; b += ctas * (kPlanThreads / 32)) {
+  // table entries: a warp a request of packed ones, a thread one that gets a token
+  const bool packed = a.cu != nullptr;
+  const int per = packed ? 32 : 1, lane = packed ? tid & 31 : 0;
+  for (int b = (rank * threads + tid) / per; b < a.B; b += ctas * threads / per) {
     if (base[b] < 0) continue;
-    const int len = a.cu != nullptr ? seq_bounds(a.cu, b, a.T).len : 1;
-    const int have = (int)(((long long)held[b] + a.page - 1) / a.page);
-    const int need = (int)(((long long)held[b] + len + a.page - 1) / a.page) - have;
-    for (int i = tid & 31; i < need; i += 32)
-      a.table[b * a.table_stride + have + i] = a.free_blocks[count - 1 - base[b] - i];
+    const int n = held[b], end = n + (packed ? seq_bounds(a.cu, b, a.T).len : 1);
+    const int have = n > 0 ? over(n - 1, a.page, inverse) + 1 : 0;
+    const int need = end > 0 ? over(end - 1, a.page, inverse) + 1 - have : 0;
+    for (int i = lane; i < need; i += 32) a.table[b * a.table_stride + have + i] = a.free_blocks[count - 1 - base[b] - i];
   }
-  for (long long t = (long long)rank * kPlanThreads + tid; t < a.T; t += (long long)ctas * kPlanThreads) {
-    int b = (int)t;
-    if (a.cu != nullptr) {  // the last request that starts at or before t
+  // slots: a thread has a run of packed tokens, and looks a request or a block up where one begins
+  const int run = packed ? kPlanRun : 1;
+  const bool wide = (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0;
+  for (long long t0 = ((long long)rank * threads + tid) * run; t0 < a.T; t0 += (long long)ctas * threads * run) {
+    int b = (int)t0;
+    if (packed) {  // the last request that starts at or before t0
       int lo = 0, hi = a.B;
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (start[mid] <= t) lo = mid; else hi = mid;
+        if (start[mid] <= t0) lo = mid; else hi = mid;
       }
       b = lo;
     }
-    long long slot = -1;
-    const int len = a.cu != nullptr && a.B > 0 ? seq_bounds(a.cu, b, a.T).len : 1;
-    if (a.B > 0 && t >= start[b] && t < start[b] + (long long)len && base[b] >= 0) {
-      const long long p = held[b] + (t - start[b]);
-      const int col = (int)(p / a.page), have = (int)(((long long)held[b] + a.page - 1) / a.page);
-      const int block = col < have ? a.table[b * a.table_stride + col] : a.free_blocks[count - 1 - base[b] - (col - have)];
-      if (block >= 0) slot = (long long)block * a.page + (p - (long long)col * a.page);
-      if (slot > 0x7fffffffLL) slot = -1;
+    int4 out = make_int4(-1, -1, -1, -1);
+    int at = -1, first = 0, len = 0, n = 0, taken_before = -1, have = 0, col = -1, block = -1;
+#pragma unroll
+    for (int i = 0; i < kPlanRun; ++i) {
+      const long long t = t0 + i;
+      if (i >= run || t >= a.T || a.B == 0) break;
+      while (b + 1 < a.B && start[b + 1] <= t) ++b;
+      if (b != at) {
+        at = b;
+        first = start[b];
+        len = packed ? seq_bounds(a.cu, b, a.T).len : 1;
+        n = held[b];
+        taken_before = base[b];
+        have = n > 0 ? over(n - 1, a.page, inverse) + 1 : 0;
+        col = -1;
+      }
+      if (t < first || t >= first + (long long)len || taken_before < 0) continue;
+      const int p = n + (int)(t - first), c = over(p, a.page, inverse);
+      if (c != col) {
+        col = c;
+        block = c < have ? a.table[b * a.table_stride + c] : a.free_blocks[count - 1 - taken_before - (c - have)];
+      }
+      const long long slot = (long long)block * a.page + (p - c * a.page);
+      if (block >= 0 && slot <= 0x7fffffffLL) (&out.x)[i] = (int)slot;
     }
-    a.slots[t] = (int32_t)slot;
+    if (run == kPlanRun && wide && t0 + kPlanRun <= a.T) {
+      *reinterpret_cast<int4*>(a.slots + t0) = out;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPlanRun; ++i)
+        if (i < run && t0 + i < a.T) a.slots[t0 + i] = (&out.x)[i];
+    }
   }
 }
 
@@ -155,8 +202,13 @@ cudaError_t launch_cache_plan(const CachePlanArgs& a, cudaStream_t st) {
   const int smem = 3 * a.B * 4;
   cudaError_t e = set_smem_limit_once<gdn_cache_plan_kernel>(3 * kPlanMaxRequests * 4);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
   const unsigned ctas = a.T <= kPlanAlone ? 1 : kPlanCtas;
+  if (ctas == 1) {
+    const int threads = a.B <= kPlanFew && a.T <= (a.cu != nullptr ? kPlanRun : 1) * kPlanFew ? kPlanFew : kPlanThreads;
+    gdn_cache_plan_kernel<<<1, threads, (size_t)smem, st>>>(a);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
@@ -172,7 +224,7 @@ cudaError_t launch_cache_plan(const CachePlanArgs& a, cudaStream_t st) {
 
 // A thread has one piece of eight values of a token's heads, k and v, and walks tokens.
 // grid: (runs of tokens, pieces past one block's)
-template <bool E4M3>
+template <bool E4M3, int kAhead>
 __global__ void __launch_bounds__(kAppendThreads) gdn_cache_append_kernel(const CacheAppendArgs a, int width, int rows) {
   const int per = a.d / 8, r = threadIdx.x / width;
   const int piece = blockIdx.y * width + (threadIdx.x - r * width);
@@ -180,11 +232,11 @@ __global__ void __launch_bounds__(kAppendThreads) gdn_cache_append_kernel(const 
   const int h = piece / per, c = (piece - h * per) * 8;
   const float ks = E4M3 ? a.kscale[h] : 1.f, vs = E4M3 ? a.vscale[h] : 1.f;
   const long long most = (long long)a.blocks * a.page;
-  const long long t0 = (long long)blockIdx.x * (rows * kAppendAhead) + r;
-  uint4 kx[kAppendAhead], vx[kAppendAhead];
-  int slot[kAppendAhead];
+  const long long t0 = (long long)blockIdx.x * (rows * kAhead) + r;
+  uint4 kx[kAhead], vx[kAhead];
+  int slot[kAhead];
 #pragma unroll
-  for (int u = 0; u < kAppendAhead; ++u) {
+  for (int u = 0; u < kAhead; ++u) {
     const long long t = t0 + (long long)u * rows;
     slot[u] = -1;
     if (t < a.T) {
@@ -194,7 +246,7 @@ __global__ void __launch_bounds__(kAppendThreads) gdn_cache_append_kernel(const 
     }
   }
 #pragma unroll
-  for (int u = 0; u < kAppendAhead; ++u) {
+  for (int u = 0; u < kAhead; ++u) {
     if (slot[u] < 0 || slot[u] >= most) continue;
     const int block = slot[u] / a.page, off = slot[u] - block * a.page;
     const long long in = ((long long)h * a.page + off) * a.d + c;
@@ -221,12 +273,18 @@ __global__ void __launch_bounds__(kAppendThreads) gdn_cache_append_kernel(const 
 cudaError_t launch_cache_append(const CacheAppendArgs& a, bool e4m3, cudaStream_t st) {
   const int pieces = a.Hkv * (a.d / 8);
   const int width = pieces < kAppendThreads ? pieces : kAppendThreads, rows = kAppendThreads / width;
-  const int run = rows * kAppendAhead;
-  const dim3 grid((unsigned)((a.T + (long long)run - 1) / run), (unsigned)((pieces + width - 1) / width));
-  if (e4m3)
-    gdn_cache_append_kernel<true><<<grid, kAppendThreads, 0, st>>>(a, width, rows);
-  else
-    gdn_cache_append_kernel<false><<<grid, kAppendThreads, 0, st>>>(a, width, rows);
+  const int sms = device_sms();
+  auto launch = [&](auto ahead) {
+    constexpr int kAhead = decltype(ahead)::value;
+    const int run = rows * kAhead;
+    const dim3 grid((unsigned)((a.T + (long long)run - 1) / run), (unsigned)((pieces + width - 1) / width));
+    if (e4m3)
+      gdn_cache_append_kernel<true, kAhead><<<grid, kAppendThreads, 0, st>>>(a, width, rows);
+    else
+      gdn_cache_append_kernel<false, kAhead><<<grid, kAppendThreads, 0, st>>>(a, width, rows);
+  };
+  if ((long long)a.T * pieces >= 2LL * sms * kAppendAhead * kAppendThreads) launch(std::integral_constant<int, kAppendAhead>());
+  else launch(std::integral_constant<int, 1>());
   return cudaGetLastError();
 }
 
