@@ -37,7 +37,6 @@ using attn::StepArgs;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kCtas = 2;  // (a CTA, an SM)
 constexpr int kBlock = 16;                  // keys a warp takes at a time
-constexpr int kLeast = 2;                   // units that a run has at least, where there are so many
 constexpr int kMaxHeads = 16;               // of a key head at a time
 constexpr float kLazy = 8.f;
 constexpr int kBadPage = 64;                // GDN_STATUS_BAD_PAGE
@@ -181,14 +180,14 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
     mine += x < a.B ? units_of(blocks_of(a, x).count) : 0;
   }
   const long long upto = inclusive(mine * per_seq, lane), total = __shfl_sync(0xffffffffu, upto, 31);
-  const long long per_run = max((long long)kLeast, quotient(total + gridDim.x - 1, gridDim.x));
+  const long long per_run = quotient(total + gridDim.x - 1, gridDim.x);
   long long u0 = blockIdx.x * per_run;
   if (u0 >= total) return;
   const long long u1 = min(u0 + per_run, total);
   const int l0 = __ffs(__ballot_sync(0xffffffffu, upto > u0)) - 1;
   int b = l0 * share_of;
   long long before = __shfl_sync(0xffffffffu, upto - mine * per_seq, l0);  // units of the sequences before b
-  for (int i = 0;; i += 32) {  // (the share has it: a sequence behind the share's last is not reached)
+  for (int i = 0; share_of > 1; i += 32) {  // (the share has it: a sequence behind the share's last is not reached)
     const int x = b + lane;
     const long long u = i + lane < share_of && x < a.B ? (long long)units_of(blocks_of(a, x).count) * per_seq : 0;
     const long long sum = before + inclusive(u, lane);
@@ -278,11 +277,23 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
     filled = (filled & ~(((1u << R::kPer) - 1u) << R::kPer * put_slot)) | any << R::kPer * put_slot;
     if (++put_slot == R::kRing) put_slot = 0;
   };
+  uint32_t q[NT][2 * NC][2];  // queries: head g of each eight, the columns that a product's operand has
   auto begin = [&]() {
     todo = (int)min((long long)(units - first), u1 - u0);
     hk = item / groups;
     h0 = hk * G + (item - hk * groups) * heads;
     nh = min(heads, (hk + 1) * G - h0);  // heads of this item
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const __nv_bfloat16* row = a.q + b * a.qs + (long long)(h0 + 8 * t + g) * a.d;
+#pragma unroll
+      for (int i = 0; i < 2 * NC; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int col = 16 * i + (E4M3 ? 4 * c + 2 * k : 2 * c + 8 * k);
+          q[t][i][k] = 8 * t + g < nh && col < a.d ? *reinterpret_cast<const uint32_t*>(row + col) : 0u;
+        }
+    }
     look_up(0);
     put_slot = slot;
 #pragma unroll 1
@@ -291,20 +302,9 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
   begin();
 
   while (true) {
-    // queries: head g of each eight, the columns that a product's operand has
-    uint32_t q[NT][2 * NC][2];
     float scale[NT][2];  // of heads 2 c and 2 c + 1
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const __nv_bfloat16* row = a.q + b * a.qs + (long long)(h0 + 8 * t + g) * a.d;
-      const bool there = 8 * t + g < nh;
-#pragma unroll
-      for (int i = 0; i < 2 * NC; ++i)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int col = 16 * i + (E4M3 ? 4 * c + 2 * k : 2 * c + 8 * k);
-          q[t][i][k] = there && col < a.d ? *reinterpret_cast<const uint32_t*>(row + col) : 0u;
-        }
       scale[t][0] = scale[t][1] = scale_log2;
       if constexpr (E4M3) {
         // to below 2 by a power of two, which the scale takes back
@@ -525,22 +525,39 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
       if (*last) {
         __threadfence();
         if (tid == 0) *counter = 0;
-        for (int x = tid; x < at_nh * quads; x += kThreads) {
-          const int h = x / quads, col = 4 * (x - h * quads);
+        // their maxima and sums into shared memory, as many parts at a time as fit; a thread has four columns of a head
+        float2* const part = reinterpret_cast<float2*>(so);
+        const int fit = kWarps * 8 * R::kRow / 2 / at_nh;
+        for (int x0 = 0; x0 < at_nh * quads; x0 += kThreads) {
+          const int x = x0 + tid, h = min(x / quads, at_nh - 1), col = 4 * (x - x / quads * quads);
           float top = -INFINITY, sum = 0.f;
-#pragma unroll 8
-          for (int r = r0; r <= r1; ++r) top = fmaxf(top, __ldcg(&work.stats[(2 * r + (r == r0)) * kMaxHeads + h]).x);
           float4 all4 = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int r = r0; r <= r1; ++r) {
-            const int from = (2 * r + (r == r0)) * kMaxHeads + h;
-            const float2 st = __ldcg(&work.stats[from]);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(work.sums + (long long)from * attn::kMaxDim + col));
-            const float f = share(st, top);
-            sum = fmaf(f, st.y, sum);
-            all4 = add(all4, f, y);
+          for (int from = r0; from <= r1; from += fit) {
+            const int n = min(fit, r1 - from + 1);
+            __syncthreads();
+            for (int y = tid; y < n * at_nh; y += kThreads) {
+              const int r = from + y / at_nh;
+              part[y] = __ldcg(&work.stats[(2 * r + (r == r0)) * kMaxHeads + y % at_nh]);
+            }
+            __syncthreads();
+            float next = top;
+            for (int r = 0; r < n; ++r) next = fmaxf(next, part[r * at_nh + h].x);
+            const float keep = share(make_float2(top, 0.f), next);
+            sum *= keep;
+            all4 = add(make_float4(0.f, 0.f, 0.f, 0.f), keep, all4);
+            top = next;
+            // (the loads do not wait for the maxima)
+#pragma unroll 16
+            for (int r = 0; r < n; ++r) {
+              const int slot = (2 * (from + r) + (from + r == r0)) * kMaxHeads + h;
+              const float4 y = __ldcg(reinterpret_cast<const float4*>(work.sums + (long long)slot * attn::kMaxDim + col));
+              const float2 st = part[r * at_nh + h];
+              const float f = share(st, top);
+              sum = fmaf(f, st.y, sum);
+              all4 = add(all4, f, y);
+            }
           }
-          put(h, col, all4, top, sum);
+          if (x < at_nh * quads) put(h, col, all4, top, sum);
         }
       }
     }
