@@ -335,6 +335,58 @@ def test_step_split_over_the_device(gdn, B, top, Hq, Hkv, d, page, window, e4m3)
         assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("B,top,Hq,Hkv,d,e4m3", [(33, 300, 2, 1, 64, False), (1025, 60, 4, 2, 32, True), (3000, 40, 2, 1, 64, False),
+                                                (5000, 2, 1, 1, 8, False)])
+def test_step_many_requests(gdn, B, top, Hq, Hkv, d, e4m3):
+    g = gen(B)
+    lens = torch.randint(0, top, (B,), generator=g)
+    lens[torch.randint(0, B, (B // 3,), generator=g)] = 0
+    lens[B // 2:B // 2 + B // 20] = 0
+    lens[B // 3] = 40 * top  # one long among them
+    kc, vc, scales, table = cache_of(g, lens.tolist(), Hkv, d, 16, e4m3)
+    check_step(gdn, rnd(g, B, Hq, d), kc, vc, scales, table, lens.tolist())
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_calls_of_many_sizes_one_after_another(gdn, given):
+    # what one call leaves in a workspace is no other's concern
+    g = gen(12)
+    ws = torch.zeros(gdn.gdn_attn_workspace_bytes(400, 48, 6, 128), dtype=torch.uint8, device="cuda") if given else None
+    for B, top, Hq, Hkv, d, e4m3 in ((1, 3000, 48, 6, 128, False), (400, 30, 2, 1, 64, True), (3, 900, 40, 1, 32, False),
+                                     (1, 1, 1, 1, 8, True), (37, 700, 16, 4, 96, True), (1, 5000, 8, 8, 128, False)):
+        lens = torch.randint(top // 2, top + 1, (B,), generator=g).tolist()
+        kc, vc, scales, table = cache_of(g, lens, Hkv, d, 32, e4m3)
+        check_step(gdn, rnd(g, B, Hq, d), kc, vc, scales, table, lens, workspace=ws)
+        q, k, v = slices(g, top, top, Hq, Hkv, d) if top < 1000 else slices(g, 9, 9, Hq, Hkv, d)
+        check_attn(gdn, q, k, v, [q.shape[0]], workspace=ws)
+    assert gdn.gdn_device_status() == (0, 0)
+    if given:
+        assert int(ws[:4].view(I32)) == 0
+
+
+@pytest.mark.parametrize("d", range(8, 129, 8))
+def test_every_width(gdn, d):
+    # each column alone: a query that is one at a column, keys that are there what no other column is
+    for lens in ([3], [70]):
+        n = lens[0]
+        q = torch.eye(d).to(BF).cuda()[:, None]  # d queries of one head
+        k = torch.zeros(n, 1, d)
+        k[0, 0] = torch.arange(1, d + 1) / 8
+        v = (torch.arange(n)[:, None, None] % 5 + torch.arange(d) % 3).float()
+        k, v = k.to(BF).cuda(), v.to(BF).cuda()
+        check_attn(gdn, q, k, v, [d], [n], scale=1.0)
+        for e4m3 in (False, True):
+            kc, vc = (torch.full((8, 1, 16, d), NAN) for _ in range(2))
+            for i in range(0, n, 16):
+                m = min(16, n - i)
+                kc[i // 16, :, :m] = k[i:i + m].float().cpu().transpose(0, 1)
+                vc[i // 16, :, :m] = v[i:i + m].float().cpu().transpose(0, 1)
+            t = torch.float8_e4m3fn if e4m3 else BF
+            scales = [torch.ones(1, device="cuda")] * 2 if e4m3 else [None, None]
+            table = np.tile(np.arange(8), (d, 1))
+            check_step(gdn, q, kc.to(t).cuda(), vc.to(t).cuda(), scales, table, [n] * d, scale=1.0)
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_step_scales(gdn, e4m3):
     g = gen(4)
