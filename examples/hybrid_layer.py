@@ -1,9 +1,10 @@
-"""A stack of two hybrid layers run on the library's operators: a packed batch of prompts, then tokens one by one.
+"""A stack of three hybrid layers run on the library's operators: a packed batch of prompts, then tokens one by one.
 
 Each layer is   norm with the residual's addition (to e4m3 with a scale a row)  ->  projection  ->
-short causal convolution  ->  recurrence  ->  projection;   the recurrence is the selective state
-space scan in the first layer and the gated delta rule in the second.  The projections are plain
-torch products on the 8-bit values (bf16 holds them exactly) with the rows' scales applied after.
+mixing  ->  projection;   the mixing is a short causal convolution with the selective state space
+scan in the first layer, one with the gated delta rule in the second, and attention over a paged
+cache in the third.  The projections are plain torch products on the 8-bit values (bf16 holds them
+exactly) with the rows' scales applied after.
 
     python examples/hybrid_layer.py      # compares a prompt continued token by token with the longer prompt
 """
@@ -19,7 +20,9 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from hybrid_linear_attention_prefill_gb300 import gdn  # noqa: E402
 
 BF16, F32 = torch.bfloat16, torch.float32
+I32 = torch.int32
 HIDDEN, HK, HV, DK, DV, K = 512, 2, 4, 64, 64, 4
+PAGE, WINDOW, SINKS = 16, 128, 4  # of the attention layer: tokens of a block, tokens looked back at, first tokens kept
 EPS = 1e-6
 
 
@@ -29,7 +32,7 @@ def project(q, scales, w):
 
 
 class Layer:
-    """What both kinds share: the norm, the projections in and out, and the convolution over `channels`."""
+    """What all kinds share: the norm, and the projections in (`channels`, and some beside them) and out."""
 
     def __init__(self, gen, extra):
         def w(*shape, scale):
@@ -41,7 +44,7 @@ class Layer:
         width = -(-(self.channels + extra) // 8) * 8  # token strides are multiples of 8 elements
         self.w_in = w(width, HIDDEN, scale=HIDDEN ** -0.5)
         self.w_out = w(HIDDEN, HV * DV, scale=(HV * DV) ** -0.5)
-        self.conv_w = w(self.channels, K, scale=K ** -0.5)
+        self.conv_w = w(self.channels, K, scale=K ** -0.5)  # (the attention layer has no convolution)
         self.conv_b = w(self.channels, scale=0.1)
 
     def enter(self, h, residual):
@@ -111,6 +114,40 @@ class DeltaLayer(Layer):
         return self.leave(y), residual
 
 
+class AttentionLayer(Layer):
+    """HV query heads over HK key heads, within a window and the first tokens, over a paged cache."""
+
+    def __init__(self, gen):
+        super().__init__(gen, 0)
+
+    def split(self, c):
+        n = HV * DK
+        return [t.unflatten(1, (-1, DK)) for t in (c[:, :n], c[:, n:n + HK * DK], c[:, n + HK * DK:])]
+
+    def prompt(self, h, residual, cu):
+        x, _, residual = self.enter(h, residual)
+        q, k, v = self.split(x)
+        B, blocks = cu.numel() - 1, -(-x.shape[0] // PAGE) + 4 * cu.numel()
+        table = torch.zeros(B, blocks, dtype=I32, device="cuda")
+        free = torch.randperm(blocks, dtype=I32, device="cuda")
+        slots, lens, count, refused = gdn.cache_plan(torch.zeros(B, dtype=I32, device="cuda"), table, free,
+                                                     torch.tensor([blocks], dtype=I32, device="cuda"), cu, page=PAGE,
+                                                     T=x.shape[0])
+        cache = [torch.empty(blocks, HK, PAGE, DK, dtype=BF16, device="cuda") for _ in range(2)]
+        gdn.cache_append(k, v, *cache, slots)
+        y, _ = gdn.attention(q, k, v, cu, window=WINDOW, sinks=SINKS)
+        return self.leave(y), residual, (lens, table, free, count, cache)
+
+    def token(self, h, residual, states):
+        lens, table, free, count, cache = states
+        x, _, residual = self.enter(h, residual)
+        q, k, v = self.split(x)
+        slots = gdn.cache_plan(lens, table, free, count, page=PAGE, new_lens=lens, new_count=count)[0]
+        gdn.cache_append(k, v, *cache, slots)
+        y, _ = gdn.attention_step(q, *cache, table, lens, window=WINDOW, sinks=SINKS)
+        return self.leave(y), residual
+
+
 def prompt(layers, h, cu):
     """Hidden states after the layers (their residual added) for a packed batch, and the layers' states."""
     residual, states = torch.zeros_like(h), []
@@ -132,7 +169,7 @@ def compare(lens=(5, 130, 300), steps=6, seed=0):
     """Largest difference between prompts continued token by token and the longer prompts at once, over the
     largest value."""
     gen = torch.Generator().manual_seed(seed)
-    layers = [ScanLayer(gen), DeltaLayer(gen)]
+    layers = [ScanLayer(gen), DeltaLayer(gen), AttentionLayer(gen)]
     full = [torch.randn(n + steps, HIDDEN, generator=gen).to(BF16).cuda() for n in lens]
 
     def packed(parts):
