@@ -7,12 +7,12 @@
 // requests for itself (a few thousand integers), the cluster's barrier puts every read before the first
 // write (lengths and the stack's height may be updated in place), and the CTAs share the tokens.
 // Latency bounds it: three dependent loads and the sums beside a launch.  One token of 128 requests takes 6.1 us on a
-// GB300 where an empty launch takes about 4; 72,102 tokens of 32 prompts 10.3 us, from 20 with a cluster of four and a
-// token a thread, which looked every token's request and block up.
+// GB300 where an empty launch takes about 4, 72,102 tokens of 32 prompts 10.3 us.  (By a clock around single calls, 2 to 3
+// more: 12.9; 15.0 with a cluster of eight, 19.1 with eight and a token a thread, each of which it looked up.)
 //
 // Append.  A copy of whole 16-byte pieces (to e4m3: eight values a thread, divided by their head's scale
 // and rounded once), bound by bandwidth: 72,102 tokens of 8 heads in 89.9 us, 6.6 TB/s in and out.  128 tokens take 4.1 us
-// with a token a thread, 6.1 with the four that the long call has on their way.
+// with a token a thread (by a clock around single calls 6.9, and 8.9 with the four that the long call has on their way).
 #include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
