@@ -140,7 +140,7 @@ int gdn_attn(const gdn_attn_args* args) {
   if (B == 0) return GDN_OK;
   const bool packed = cu_seqlens != nullptr;
   const long long nq = packed ? (long long)T : (long long)B * T, nk = packed ? (long long)Tk : (long long)B * Tk;
-  if (nq > 0x7fffffffLL || nk > 0x7fffffffLL) return GDN_ERR_ARG;
+  if (nq > 0x7ffffc00LL || nk > 0x7ffffc00LL) return GDN_ERR_ARG;  // (a tile past the last token stays below 2^31)
   if (nq == 0) return GDN_OK;
   const long long wq = (long long)Hq * d, wk = (long long)Hkv * d;
   if (out == nullptr) return GDN_ERR_ARG;

@@ -63,7 +63,8 @@ def test_append_refusals(kw, code):
     (dict(v=FAKE + 8), ALIGN), (dict(out=FAR + 8), ALIGN), (dict(lse=FAR + 2), ALIGN), (dict(cu_seqlens_k=FAKE), ARG),
     (dict(cu_seqlens=FAKE, Tk=17), ARG), (dict(cu_seqlens=FAKE + 2), ALIGN), (dict(out=FAKE + 512), ARG),
     (dict(workspace=FAKE + 16), ALIGN), (dict(workspace_bytes=255), gdn.GDN_ERR_SCRATCH), (dict(B=1 << 20, T=1 << 20), ARG),
-    (dict(B=0), OK), (dict(T=0), OK)])
+    (dict(B=0), OK), (dict(T=0), OK),
+    (dict(B=1, T=2 ** 31 - 1, Tk=2 ** 31 - 1), ARG), (dict(B=2 ** 20, T=2048, Tk=1), ARG)])
 def test_attn_refusals(kw, code):
     assert gdn.gdn_attn(**{**ATTN, **kw}) == code
 
