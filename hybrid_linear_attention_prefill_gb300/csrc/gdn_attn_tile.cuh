@@ -22,11 +22,12 @@
 // What bounds it, measured on one GB300 (d = 128, clocks of an SM): a pair of key tiles takes 3,200 where its products
 // take 2,048.  A tile's round is a chain: its scores into registers 330, maxima and the vote 550, the rest of the weights
 // 350, the issuing warp's look at the barrier 300, the products 1,100 beside the other tile's, and the two tiles' chains
-// fill the tensor core to 0.58 between them (16,381 tokens, 16 heads over 2: 770 us, 1,410 TFLOP/s).  An item costs
-// another 12,000: its last product, the output's way out (4,000 to 4,900) and the next one's first tile follow one another
-// in the same warps, so a window of 1,024 (nine tiles an item) runs at 890 TFLOP/s.  Steps that brought it here, for 16,381
+// fill the tensor core to 0.58 between them (16,381 tokens, 16 heads over 2: 760 us, 1,440 TFLOP/s).  An item costs
+// another 10,000: its last product, the output's way out and the next one's first tile follow one another in the same
+// warps, so a window of 1,024 (nine tiles an item) runs at 910 TFLOP/s.  Steps that brought it here, for 16,381
 // tokens: one thread a row and one issuing warp 1,025; scores held in registers, descriptors as constants, two issuing
-// warps in turns 967; two threads a row 770.
+// warps in turns 967; two threads a row 770;
+// output through copies 760.
 //
 // A value that is not finite in a place that a row does not see would reach the row as 0 x infinity.
 // So a finished row that is not finite is worked out again from the keys it sees alone.
@@ -66,8 +67,10 @@ constexpr int kHalf = 16384;
 template <int kQuarters>
 struct Cfg {
   static constexpr int kHalves = (kQuarters + 1) / 2, kTile = kHalves * kHalf, kRing = kHalves == 2 ? 2 : 4;
-  static constexpr int kOffQ = 0, kOffK = 2 * kTile, kOffV = kOffK + kRing * kTile, kOffStat = kOffV + kRing * kTile;
-  static constexpr int kStatBytes = 3 * 2 * 2 * 128 * 4;
+  static constexpr int kOffQ = 0, kOffK = 2 * kTile, kOffV = kOffK + kRing * kTile;
+  static constexpr int kOffStage = kOffV + kRing * kTile;  // 32 rows of 32 columns of output for each warp
+  static constexpr int kOffStat = kOffStage + 16 * 2048;
+  static constexpr int kStatBytes = 2 * 2 * 128 * 4;
   static constexpr int kOffItem = kOffStat + kStatBytes, kOffBar = kOffItem + kItemSlots * 128;
   static constexpr int kBars = 4 * kRing + 2 * kItemSlots + 2 * 8;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16;
@@ -170,6 +173,16 @@ __device__ __forceinline__ void tmem_st16_start(uint32_t a, const uint32_t (&v)[
       "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+// 32 columns of a warp's rows to the output; that the copies before have been read from shared memory, or are all done.
+__device__ __forceinline__ void copy_out(const CUtensorMap* map, const void* from, int column, int head, int token) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(map),
+               "r"(column), "r"(head), "r"(token), "r"(smem_u32(from))
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+}
+__device__ __forceinline__ void copies_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
+
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
 // Bits [lo, hi) of 32, of bounds that may lie outside.
@@ -185,13 +198,14 @@ template <int kQuarters>
 __global__ void __launch_bounds__(kThreads, 1)
 gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k16,
-                     const __grid_constant__ CUtensorMap tm_v16, const attn::PromptArgs a, int items, int tpt,
+                     const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ CUtensorMap tm_out,
+                     const attn::PromptArgs a, int items, int tpt,
                      float scale_log2, int negate, int* __restrict__ err) {
   using C = Cfg<kQuarters>;
   constexpr int kTile = C::kTile, kHalves = C::kHalves, kRing = C::kRing;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = smem_raw;
-  float* stat = reinterpret_cast<float*>(sm + C::kOffStat);  // [maximum, sum, not finite][tile][half][row]
+  float* stat = reinterpret_cast<float*>(sm + C::kOffStat);  // [tile][half][row]: what a row's threads tell each other
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
   uint64_t *k_full = bars, *k_empty = k_full + kRing, *v_full = k_empty + kRing, *v_empty = v_full + kRing,
            *item_full = v_empty + kRing, *item_empty = item_full + kItemSlots, *q_full = item_empty + kItemSlots,
@@ -516,7 +530,8 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const uint32_t s_at = tmem + lanes + kColS + t * 128 + 64 * hf, p_at = tmem + lanes + kColS + t * 128 + 32 * hf,
                    o_at = tmem + lanes + kColO + t * 128;
     const int pair = 1 + 4 * t + quad;  // the barrier: both warps of a row come to it every time, one that gave up too
-    float *tops = stat + t * 256 + row, *sums = tops + 512, *odds = sums + 512;  // of half h: + 128 h
+    float* const told = stat + t * 256 + row;  // of half h: + 128 h
+    unsigned char* const stage = sm + C::kOffStage + warp * 2048;
     uint32_t s_par = 0, o_par = 0;
     bool ok = warp_wait(item_full, 0, 1);
     bool stop = any_of_pair(pair, !ok);
@@ -577,9 +592,9 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         // (Both warps have their scores when they meet: the other's weights go in the place of some of them.)
         if (any_of_pair(pair, !ok || top > m + kLazy)) {
           // a row's is far above: it takes its place, and those weights are made again
-          tops[128 * hf] = top;
+          told[128 * hf] = top;
           if ((stop = any_of_pair(pair, !ok))) break;
-          top = fmaxf(top, tops[128 * (1 - hf)]);
+          top = fmaxf(top, told[128 * (1 - hf)]);
           const float next = top > m + kLazy ? top : m;
           if (__any_sync(0xffffffffu, m != -INFINITY)) {
             const float f = next == m ? 1.f : ex2_approx(m - next);
@@ -609,9 +624,10 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
       if (stop) break;
       // ---- outputs
-      sums[128 * hf] = l;
+      pair_sync(pair);  // (the maxima there are read)
+      told[128 * hf] = l;
       pair_sync(pair);
-      l += sums[128 * (1 - hf)];  // (the two in either order: the same)
+      l += told[128 * (1 - hf)];  // (the two in either order: the same)
       const bool some = to > 0;
       if (some) {
         ok = warp_wait(o_full + t, o_par, 1);
@@ -622,6 +638,10 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const long long tok = (long long)tok0 + tr;
       const int head = hk * G + row - tr * G;
       __nv_bfloat16* out = a.out + (tok * a.Hq + head) * a.d;
+      // A warp's rows go out as one copy of 32 columns where all of them are there and are whole heads or tokens.  (Stores of
+      // a row a lane, 16 bytes of 32 lines each, hold up what the SM's other warps read and wait for: an item took 4,000
+      // clocks longer; 4,096 tokens 123.5 us against 117.4, 128 prompts of 256 233 against 218.)
+      const bool by_copy = 128 % G == 0 && (32 * quad + 31) / G < nt;
       const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
       float2 zero = make_float2(0.f, 0.f);  // or NaN, once a value is not finite
 #pragma unroll 1
@@ -629,15 +649,29 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         float r[32] = {};
         __syncwarp();  // the load wants the lanes together, which a store of some of them may part
         if (some) tc::tmem_ld32(o_at + c, r);
+        uint4 y[4];
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
+        for (int i = 0; i < 4; ++i) {
           float2 f[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            f[k] = mul2(make_float2(r[i + 2 * k], r[i + 2 * k + 1]), make_float2(inv, inv));
+            f[k] = mul2(make_float2(r[8 * i + 2 * k], r[8 * i + 2 * k + 1]), make_float2(inv, inv));
             zero = fma2(f[k], make_float2(0.f, 0.f), zero);
           }
-          if (live && c + i < a.d) *reinterpret_cast<uint4*>(out + c + i) = narrow8(f);
+          y[i] = narrow8(f);
+        }
+        if (by_copy) {
+          if (lane == 0) copies_read();
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(stage + lane * 64 + 16 * (i ^ (lane >> 1 & 3))) = y[i];
+          tc::fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) copy_out(&tm_out, stage, c, hk * G + (G > 32 ? 32 * quad % G : 0), tok0 + 32 * quad / G);
+        } else if (live) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + 8 * i < a.d) *reinterpret_cast<uint4*>(out + c + 8 * i) = y[i];
         }
       }
       if (live && hf == 0 && a.lse != nullptr)
@@ -651,10 +685,12 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       ok = ok && warp_wait(item_full + (n + 1) % kItemSlots, item_par(n + 1), 1);
       if (any_of_pair(pair, odd || !ok)) {
         if (any_of_pair(pair, !ok)) break;
-        odds[128 * hf] = odd ? 1.f : 0.f;
+        if (lane == 0) copies_done();  // rows that are written again
+        __syncwarp();
+        told[128 * hf] = odd ? 1.f : 0.f;
         pair_sync(pair);
         if (hf == 0) {
-          odd = odd || odds[128] != 0.f;
+          odd = odd || told[128] != 0.f;
           for (unsigned rest = __ballot_sync(0xffffffffu, odd); rest != 0; rest &= rest - 1) {
             const int r2 = 32 * quad + __ffs(rest) - 1, tr2 = r2 / G;
             const long long tok2 = (long long)tok0 + tr2;
@@ -670,6 +706,8 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         __syncwarp();
       }
     }
+    if (lane == 0) copies_done();
+    __syncwarp();
   }
   tc::fence_before();
   __syncthreads();
@@ -681,11 +719,12 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 namespace {
 
 bool head_map(CUtensorMap* m, const void* base, long long stride, int heads, int d, long long tokens, int box_heads,
-              int box_tokens) {
+              int box_tokens, int columns = 64) {
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)(tokens > 1 ? stride : (long long)heads * d) * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
-  return make_map16(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  const cuuint32_t box[3] = {(cuuint32_t)columns, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  return make_map16(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 3, dims, strides, box,
+                    columns == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 }  // namespace
@@ -700,7 +739,7 @@ cudaError_t launch_attn_tiles(const attn::PromptArgs& a, void* ws, cudaStream_t 
   const long long tiles = ((long long)a.T + per - 1) / per;
   const long long items = (packed ? tiles + a.B : tiles * a.B) * a.Hkv;  // (packed: an upper bound)
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
-  CUtensorMap q, k, v, k16, v16;
+  CUtensorMap q, k, v, k16, v16, out;
   if (!head_map(&q, a.q, a.qs, a.Hq, a.d, nq, G, tpt)) return cudaErrorInvalidValue;
   // without keys nothing is loaded by these
   auto key_map = [&](CUtensorMap* m, const void* x, long long stride, int box) {
@@ -709,13 +748,17 @@ cudaError_t launch_attn_tiles(const attn::PromptArgs& a, void* ws, cudaStream_t 
   if (!key_map(&k, a.k, a.ks, kKeys) || !key_map(&v, a.v, a.vs, kKeys) || !key_map(&k16, a.k, a.ks, 16) ||
       !key_map(&v16, a.v, a.vs, 16))
     return cudaErrorInvalidValue;
+  // (not used where a warp's rows are not whole heads or tokens)
+  const int rows_heads = 128 % G != 0 ? 1 : G < 32 ? G : 32;
+  if (!head_map(&out, a.out, (long long)a.Hq * a.d, a.Hq, a.d, nq, rows_heads, 32 / rows_heads, 32))
+    return cudaErrorInvalidValue;
   const cudaError_t e = set_smem_limit_once<gdn_attn_tile_kernel<kQuarters>>(Cfg<kQuarters>::kSmem);
   if (e != cudaSuccess) return e;
   float c = a.scale * attn::kLog2e;
   const int negate = c < 0.f;  // as the sign of the queries
   c = std::max(negate ? -c : c, 0x1p-126f);  // (unseen scores are minus infinity, and 0 times that would not do)
   gdn_attn_tile_kernel<kQuarters><<<(unsigned)std::min<long long>(items, sms), kThreads, Cfg<kQuarters>::kSmem, st>>>(
-      q, k, v, k16, v16, a, (int)items, tpt, c, negate, static_cast<int*>(ws));
+      q, k, v, k16, v16, out, a, (int)items, tpt, c, negate, static_cast<int*>(ws));
   return cudaGetLastError();
 }
 
