@@ -763,3 +763,102 @@ def test_streams_and_devices_memory(gdn):
     b, _ = gdn.attention_step(q1, kc, vc, t, n, stream=s)
     s.synchronize()
     assert torch.equal(a, b)
+
+
+def captured(call):
+    """A graph of the call, which has run before on the stream that it is captured from."""
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    return graph
+
+
+def step_case(gdn, g, lens, Hq, Hkv, d, e4m3, ws):
+    kc, vc, scales, table = cache_of(g, lens, Hkv, d, 32, e4m3)
+    wide = torch.full((len(lens), table.shape[1] + 3), -5, dtype=I32, device="cuda")
+    wide[:, 1:-2] = ints(table)
+    q, out = rnd(g, len(lens), Hq, d), torch.empty(len(lens), Hq, d, dtype=BF, device="cuda")
+    lse = torch.empty(len(lens), Hq, device="cuda")
+    want = check_step(gdn, q, kc, vc, scales, table, lens)
+    args = (q, kc, vc, wide[:, 1:-2], ints(lens), *scales)
+    return (lambda: gdn.attention_step(*args, out=out, lse=lse, workspace=ws)), out, lse, want
+
+
+def test_step_two_graphs_with_one_workspace(gdn):
+    g = gen(31)
+    ws = torch.zeros(gdn.gdn_attn_workspace_bytes(50, 16, 2, 128), dtype=torch.uint8, device="cuda")
+    cases = [step_case(gdn, g, lens, Hq, Hkv, d, e4m3, ws) for lens, Hq, Hkv, d, e4m3 in (
+        ([3000, 17], 16, 2, 128, False), ([900] * 50, 4, 2, 64, True))]
+    graphs = [captured(c[0]) for c in cases]
+    for i in (0, 1, 1, 0, 0, 1, 0):
+        call, out, lse, want = cases[i]
+        out.fill_(7)
+        graphs[i].replay()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_step_two_streams_at_once(gdn):
+    g = gen(32)
+    size = gdn.gdn_attn_workspace_bytes(40, 8, 2, 128)
+    cases = [step_case(gdn, g, lens, 8, 2, 128, e4m3, torch.zeros(size, dtype=torch.uint8, device="cuda"))
+             for lens, e4m3 in (([4000, 5], False), ([700] * 40, True))]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for s, (call, out, _, _) in zip(streams, cases):
+            with torch.cuda.stream(s):
+                out.fill_(7)
+                call()
+    torch.cuda.synchronize()
+    for _, out, lse, want in cases:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_captured_server_step(gdn):
+    """Plan, writing and attention of a token as one graph, replayed with new tokens; the same as call by call."""
+    g = gen(33)
+    B, Hq, Hkv, d, page, steps = 5, 8, 2, 64, 16, 40
+    lens = [0, 15, 33, 100, -1]
+    blocks = 30
+    results = []
+    tokens = [rnd(g, B, Hq + 2 * Hkv, d) for _ in range(steps)]
+    past = rnd(g, blocks, 2, Hkv, page, d)
+    for graphed in (False, True):
+        cache = past.clone()
+        held, count = ints(lens), ints([blocks - 20])
+        table = torch.full((B, 12), -1, dtype=I32, device="cuda")
+        for b, n in enumerate(lens):
+            m = max(0, -(-n // page))
+            table[b, :m] = torch.arange(blocks - 20 + 3 * b, blocks - 20 + 3 * b + m, dtype=I32, device="cuda")
+        stack = torch.arange(blocks - 20, dtype=I32, device="cuda")
+        x = torch.empty_like(tokens[0])
+        slots, refused = ints([0] * B), ints([0])
+        out = torch.empty(B, Hq, d, dtype=BF, device="cuda")
+        ws = torch.zeros(gdn.gdn_attn_workspace_bytes(B, Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+
+        def step():
+            gdn.cache_plan(held, table, stack, count, page=page, slots=slots, new_lens=held, new_count=count,
+                           refused=refused)
+            gdn.cache_append(x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], cache[:, 0], cache[:, 1], slots)
+            gdn.attention_step(x[:, :Hq], cache[:, 0], cache[:, 1], table, held, window=30, sinks=2, out=out, workspace=ws)
+
+        x.copy_(tokens[0])
+        step()
+        got = [out.clone()]
+        graph = torch.cuda.CUDAGraph()
+        if graphed:
+            with torch.cuda.graph(graph):
+                step()
+        for t in tokens[1:]:
+            x.copy_(t)
+            graph.replay() if graphed else step()
+            got.append(out.clone())
+        results.append((torch.stack(got), held.clone(), count.clone(), refused.clone(), cache))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert results[0][1].tolist()[4] == -1
