@@ -17,8 +17,10 @@
 // other, are dealt out in equal runs to as many CTAs as are resident, whatever the lengths; a warp keeps its own
 // maxima, sums and outputs, and the CTA joins its warps' where a sequence (or the run) ends, while the next one's first
 // blocks are on their way.  A sequence that is cut leaves partial sums in the workspace; the CTA that finishes its last
-// part joins them in the runs' order, so results do not depend on which that is.  More than 16 heads of a key head are
-// taken 16 at a time.
+// part joins them in the runs' order, so results do not depend on which that is.  Where there are few sequences and key
+// heads, a run stays within one: a second item, with its own queries, lookups and join, costs it 5 us (one request of 3,001
+// tokens 17.3 us, 13.0 since; of 4,096, whose units divide, 12.2 and 12.5, on the device).  More than 16 heads of a key
+// head are taken 16 at a time.
 //
 // A running maximum stays in use until a score is 2^8 above it (as for prompts), so that a step needs a vote and no
 // exchange.  With an 8-bit cache the products are of fp16: every e4m3 value is one; the queries are scaled by a power
@@ -49,6 +51,9 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps, kCtas = 2;  // (a CTA, an SM)
 constexpr int kBlock = 16;                  // keys a warp takes at a time
 constexpr int kMaxHeads = 16;               // of a key head at a time
 constexpr float kLazy = 8.f;
+// Runs lie apart where there are this many CTAs for a sequence's key head (304 CTAs; 5 requests of 8 heads 15.6 us instead
+// of 18.7, 8 requests 19.8 instead of 21.0; 18 requests, where two suffice, 40.9 instead of 40.5).
+constexpr int kFew = 4;
 constexpr int kBadPage = 64;                // GDN_STATUS_BAD_PAGE
 
 // Partial sums of a run's two ends: [2 runs][heads][d], then maxima and sums [2 runs][heads].
@@ -132,8 +137,9 @@ __device__ __forceinline__ long long inclusive(long long x, int lane) {  // the 
   return x;
 }
 // Of numbers that are not negative: in 32 bits where they fit, which is many times as fast.
+__device__ __noinline__ long long long_quotient(long long x, long long y) { return x / y; }
 __device__ __forceinline__ long long quotient(long long x, long long y) {
-  return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+  return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : long_quotient(x, y);
 }
 
 // What a part's sums (maximum, sum of weights) are multiplied by to be relative to `top`: nothing of a part that has
@@ -181,8 +187,8 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
   int* last = reinterpret_cast<int*>(sm + R::kOffStat + kWarps * 8 * 8);
   const uint32_t ring = smem_u32(sm) + warp * R::kRing * R::kSlot;
 
-  // this CTA's run of units [u0, u1), and the sequence that it begins in: every lane counts a share of the sequences,
-  // then the lanes look at the share where the run begins
+  // This CTA's run of units, and the sequence that it begins in: every lane counts a share of the sequences, then the
+  // lanes look at the share where the run begins.  With `apart` a run stays within a sequence's key head.
   const int share_of = (a.B + 31) / 32;
   long long mine = 0;
 #pragma unroll 4
@@ -190,17 +196,35 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
     const int x = lane * share_of + i;
     mine += x < a.B ? units_of(blocks_of(a, x).count) : 0;
   }
-  const long long upto = inclusive(mine * per_seq, lane), total = __shfl_sync(0xffffffffu, upto, 31);
-  const long long per_run = quotient(total + gridDim.x - 1, gridDim.x);
-  long long u0 = blockIdx.x * per_run;
+  const int units_here = (int)mine;
+  mine *= per_seq;
+  long long upto = inclusive(mine, lane), total = __shfl_sync(0xffffffffu, upto, 31);
+  long long per_run = quotient(total + gridDim.x - 1, gridDim.x);
+  const bool apart = share_of == 1 && a.B * per_seq <= (int)gridDim.x / kFew;
+  if (apart) {  // the shortest runs, in steps of a sixteenth, of which there are few enough; from here on, runs are counted
+    const int units = units_here;
+    int per = (int)per_run, runs;
+#pragma unroll 1
+    for (;; per += (per + 15) / 16) {
+      runs = (units + per - 1) / per * per_seq;
+      if (__reduce_add_sync(0xffffffffu, runs) <= (int)gridDim.x) break;
+    }
+    per_run = per;
+    mine = runs;
+    upto = inclusive(mine, lane);
+    total = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  long long u0 = apart ? blockIdx.x : blockIdx.x * per_run;
   if (u0 >= total) return;
-  const long long u1 = min(u0 + per_run, total);
+  const long long u1 = apart ? u0 + 1 : min(u0 + per_run, total);
   const int l0 = __ffs(__ballot_sync(0xffffffffu, upto > u0)) - 1;
   int b = l0 * share_of;
-  long long before = __shfl_sync(0xffffffffu, upto - mine * per_seq, l0);  // units of the sequences before b
+  long long before = __shfl_sync(0xffffffffu, upto - mine, l0);  // of the sequences before b
+#pragma unroll 1
   for (int i = 0; share_of > 1; i += 32) {  // (the share has it: a sequence behind the share's last is not reached)
     const int x = b + lane;
-    const long long u = i + lane < share_of && x < a.B ? (long long)units_of(blocks_of(a, x).count) * per_seq : 0;
+    const long long u =
+        i + lane < share_of && x < a.B ? (long long)units_of(blocks_of(a, x).count) * per_seq : 0;
     const long long sum = before + inclusive(u, lane);
     const unsigned hit = __ballot_sync(0xffffffffu, sum > u0);
     const int l = hit != 0 ? __ffs(hit) - 1 : 31;
@@ -210,7 +234,10 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
   }
   Blocks blk = blocks_of(a, b);
   int units = units_of(blk.count);
-  int item = (int)quotient(u0 - before, units), first = (int)((u0 - before) - (long long)item * units);
+  const int parts = apart ? (units + (int)per_run - 1) / (int)per_run : units;  // of an item
+  int item = (int)quotient(u0 - before, parts), first = (int)((u0 - before) - (long long)item * parts);
+  const int part_of = first;
+  if (apart) first *= (int)per_run;
   int todo = 0, hk = 0, h0 = 0, nh = 0;
 
   // ---- the item's keys and values on their way: the pages of 32 of this warp's blocks at a time, a lane each
@@ -290,7 +317,7 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
   };
   uint32_t q[NT][2 * NC][2];  // queries: head g of each eight, the columns that a product's operand has
   auto begin = [&]() {
-    todo = (int)min((long long)(units - first), u1 - u0);
+    todo = (int)min((long long)(units - first), apart ? per_run : u1 - u0);
     hk = item / groups;
     h0 = hk * G + (item - hk * groups) * heads;
     nh = min(heads, (hk + 1) * G - h0);  // heads of this item
@@ -460,7 +487,7 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
     const int at_b = b, at_item = item, at_hk = hk, at_h0 = h0, at_nh = nh, parts_units = units;
     const bool from_start = first == 0, whole = from_start && todo == units;
     const long long at_start = before + (long long)item * units;
-    u0 += todo;
+    u0 += apart ? 1 : todo;
     const bool more = u0 < u1;
     if (more) {
       first = 0;
@@ -502,6 +529,7 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
         }
       }
       __syncthreads();
+#pragma unroll 1
       for (int x = tid; x < min(at_nh - 8 * t, 8) * quads; x += kThreads) {
         const int h = x / quads, col = 4 * (x - h * quads);
         float top = -INFINITY, sum = 0.f;
@@ -528,7 +556,8 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
     if (!whole) {
       // the run that finishes the last part joins them all
       auto run_of = [&](long long u) { return (int)quotient(u, per_run); };
-      const int r0 = run_of(at_start), r1 = run_of(at_start + parts_units - 1);
+      const int r0 = apart ? (int)blockIdx.x - part_of : run_of(at_start);
+      const int r1 = apart ? r0 + parts - 1 : run_of(at_start + parts_units - 1);
       int* counter = work.counters + (long long)at_b * per_seq + at_item;
       __threadfence();
       __syncthreads();
@@ -540,19 +569,23 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
         // their maxima and sums into shared memory, as many parts at a time as fit; a thread has four columns of a head
         float2* const part = reinterpret_cast<float2*>(so);
         const int fit = kWarps * 8 * R::kRow / 2 / at_nh;
+#pragma unroll 1
         for (int x0 = 0; x0 < at_nh * quads; x0 += kThreads) {
           const int x = x0 + tid, h = min(x / quads, at_nh - 1), col = 4 * (x - x / quads * quads);
           float top = -INFINITY, sum = 0.f;
           float4 all4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
           for (int from = r0; from <= r1; from += fit) {
             const int n = min(fit, r1 - from + 1);
             __syncthreads();
+#pragma unroll 1
             for (int y = tid; y < n * at_nh; y += kThreads) {
               const int r = from + y / at_nh;
               part[y] = __ldcg(&work.stats[(2 * r + (r == r0)) * kMaxHeads + y % at_nh]);
             }
             __syncthreads();
             float next = top;
+#pragma unroll 4
             for (int r = 0; r < n; ++r) next = fmaxf(next, part[r * at_nh + h].x);
             const float keep = share(make_float2(top, 0.f), next);
             sum *= keep;
