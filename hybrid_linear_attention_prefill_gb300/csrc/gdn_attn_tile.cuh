@@ -22,12 +22,11 @@
 // What bounds it, measured on one GB300 (d = 128, clocks of an SM): a pair of key tiles takes 3,200 where its products
 // take 2,048.  A tile's round is a chain: its scores into registers 330, maxima and the vote 550, the rest of the weights
 // 350, the issuing warp's look at the barrier 300, the products 1,100 beside the other tile's, and the two tiles' chains
-// fill the tensor core to 0.58 between them (16,381 tokens, 16 heads over 2: 760 us, 1,440 TFLOP/s).  An item costs
+// fill the tensor core to 0.60 between them (16,381 tokens, 16 heads over 2: 750 us, 1,460 TFLOP/s).  An item costs
 // another 10,000: its last product, the output's way out and the next one's first tile follow one another in the same
-// warps, so a window of 1,024 (nine tiles an item) runs at 910 TFLOP/s.  Steps that brought it here, for 16,381
-// tokens: one thread a row and one issuing warp 1,025; scores held in registers, descriptors as constants, two issuing
-// warps in turns 967; two threads a row 770;
-// output through copies 760.
+// warps, so a window of 1,024 (nine tiles an item) runs at 910 TFLOP/s.  Steps that brought it here, for 16,381 tokens:
+// one thread a row and one issuing warp 1,025; scores held in registers, descriptors as constants, two issuing warps in
+// turns 967; two threads a row 770; output through copies 760; what is seldom run out of the loops' way 750.
 //
 // A value that is not finite in a place that a row does not see would reach the row as 0 x infinity.
 // So a finished row that is not finite is worked out again from the keys it sees alone.
@@ -474,7 +473,7 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
               if (last) tc::commit(o_full + t);
             }
             __syncwarp();
-            if (valid && kt == 0) {
+            if (__builtin_expect(valid && kt == 0, 0)) {
               bar = lane == 0 ? q_full + t : lane == 1 && keys ? k_full + S : nullptr;
               if (!(ok = look(bar, lane == 0 ? (uint32_t)n & 1u : (tiles / kRing) & 1u))) return;
             }
@@ -556,7 +555,7 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const int v0 = kt * kKeys;
         float s[64];
         tc::tmem_ld32x2(s_at, s_at + 32, s);
-        if (hi_all < v0 + kKeys || (lo_all > v0 && a.view.sinks < v0 + kKeys)) {
+        if (__builtin_expect(hi_all < v0 + kKeys || (lo_all > v0 && a.view.sinks < v0 + kKeys), 0)) {
 #pragma unroll
           for (int c = 0; c < 64; c += 32) {
             const int x = v0 + 64 * hf + c;
@@ -590,7 +589,7 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           for (int k = 0; k < 4; ++k) top4[k] = max3(top4[k], s[i + k], s[i + k + 4]);
         float top = scale_log2 * fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
         // (Both warps have their scores when they meet: the other's weights go in the place of some of them.)
-        if (any_of_pair(pair, !ok || top > m + kLazy)) {
+        if (__builtin_expect(any_of_pair(pair, !ok || top > m + kLazy), 0)) {
           // a row's is far above: it takes its place, and those weights are made again
           told[128 * hf] = top;
           if ((stop = any_of_pair(pair, !ok))) break;
@@ -683,7 +682,7 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       // (and where nothing is seen, 0 times the sum of values that were not)
       bool odd = !(zero.x + zero.y == 0.f) && live && l <= FLT_MAX;
       ok = ok && warp_wait(item_full + (n + 1) % kItemSlots, item_par(n + 1), 1);
-      if (any_of_pair(pair, odd || !ok)) {
+      if (__builtin_expect(any_of_pair(pair, odd || !ok), 0)) {
         if (any_of_pair(pair, !ok)) break;
         if (lane == 0) copies_done();  // rows that are written again
         __syncwarp();
