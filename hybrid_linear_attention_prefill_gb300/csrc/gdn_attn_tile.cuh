@@ -397,8 +397,8 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll 1
       for (int i = 0; i < kRing; ++i)
         if (i < loads || !ok) {
-#pragma unroll 1
           const uint32_t p = (uint32_t)((loads - 1 - i) / kRing) & 1u;
+#pragma unroll 1
           for (uint32_t x = ok ? p : 0; x <= (ok ? p : 1); ++x) {
             land(k_full + i, x);
             land(v_full + i, x);
