@@ -42,7 +42,8 @@ def sources():
 
 
 def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "gdn.h")]
+    headers = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return sources() + headers + [os.path.join(ROOT, "include", "gdn.h")]
 
 
 def _older(path: str, deps) -> bool:
