@@ -29,7 +29,8 @@
 // turns 967; two threads a row 770; output through copies 760; what is seldom run out of the loops' way 750.
 //
 // A value that is not finite in a place that a row does not see would reach the row as 0 x infinity.
-// So a finished row that is not finite is worked out again from the keys it sees alone.
+// So a finished row that is not finite is looked into, and worked out again from the keys it sees alone where the
+// values that it sees do not explain it.
 #pragma once
 
 #include <algorithm>
@@ -191,6 +192,241 @@ __device__ __forceinline__ uint32_t bits(int lo, int hi) {
   return below_hi & ~below_lo;
 }
 
+// Which of four bf16 are not finite, as their signs' bits; that of the i-th, and whether it is a NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t two) { return ((two & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ bool not_finite(const uint2& x, int i) { return not_finite(i < 2 ? x.x : x.y) >> (i & 1 ? 31 : 15) & 1u; }
+__device__ __forceinline__ bool is_nan(const uint2& x, int i) { return ((i < 2 ? x.x : x.y) >> (i & 1 ? 16 : 0) & 0x7fffu) > 0x7f80u; }
+
+// What the two warps of 32 rows look into and work out again: queries and outputs from the tile's first token and head, keys
+// and values from the sequence's first (`there` of them to the end of the tensor).
+struct Rows {
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16* out;
+  long long qs, ks, vs, os, there;
+  int d, G, row0, pa;  // of the warp's first row; position of the tile's first query
+  View view;
+  float scale_log2;
+  __device__ __forceinline__ Seen seen(int row) const { return attn::seen_by(view, pa + row / G); }
+  __device__ __forceinline__ long long at(int row, long long stride) const { return row / G * stride + row % G * d; }
+};
+
+// Whether the lane's row, which is not finite where `odd`, has to be worked out again: where a column of it is not finite
+// and the values that the row sees do not say why, or one that it does not see may have changed it.  A column is as it has
+// to be where a NaN is seen in it, or a value that is not finite is and none that is not seen.
+//
+// Only tiles at a mask's edge hold values that some row does not see, so these are read first; the others are read until
+// all columns are explained.  One such value early in a sequence makes every row behind it odd: 4,096 tokens of 32 heads
+// with a NaN among the first values take 0.24 ms instead of 0.12 (85 when every such row was worked out again), with one
+// among the last, which the rows before it in its tile do not see and have to be worked out without, 2.5.
+__device__ __forceinline__ bool unexplained(const Rows& x, const Item& it, int t, bool odd) {
+  const int lane = threadIdx.x & 31, off = it.sink - it.lo;
+  const bool has = 4 * lane < x.d;  // four columns a lane: bit l of word i is column 4 l + i
+  uint32_t bad[4] = {}, nan[4] = {}, known[4] = {}, apart[4] = {};
+#pragma unroll 1
+  for (unsigned rest = __ballot_sync(0xffffffffu, odd); rest != 0; rest &= rest - 1) {
+    const int r = __ffs(rest) - 1;
+    const uint2 y = has ? __ldcg(reinterpret_cast<const uint2*>(x.out + x.at(x.row0 + r, x.os) + 4 * lane)) : make_uint2(0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = __ballot_sync(0xffffffffu, not_finite(y, i));
+      if (lane == r) bad[i] = w;
+    }
+  }
+  const Seen seen = x.seen(x.row0 + lane);
+  auto open = [&]() {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= bad[i] & ~(nan[i] | (known[i] & ~apart[i]));
+    return w != 0;
+  };
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int kt = it.sinks > 0 ? 0 : it.a[t]; kt < it.z[t]; kt = kt + 1 == it.sinks ? it.a[t] : kt + 1) {
+      const int v0 = kt * kKeys;
+      const bool edge = it.hi_all[t] < v0 + kKeys || (it.lo_all[t] > v0 && x.view.sinks < v0 + kKeys);
+      if (edge == (pass == 1)) continue;
+      if (pass == 1 && !__any_sync(0xffffffffu, open())) break;
+#pragma unroll 1
+      for (int x0 = v0; x0 < v0 + kKeys; x0 += 8) {
+        uint2 y[8];
+        uint32_t some = 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int key = x0 + u < it.sink ? x0 + u : x0 + u - off;
+          y[u] = has && key < x.there ? *reinterpret_cast<const uint2*>(x.v + key * x.vs + 4 * lane) : make_uint2(0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) some |= not_finite(y[u].x) | not_finite(y[u].y);
+        if (!__any_sync(0xffffffffu, some != 0)) continue;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int key = x0 + u < it.sink ? x0 + u : x0 + u - off;
+          const bool sees = key < seen.hi && (key < x.view.sinks || key >= seen.lo);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t odds = __ballot_sync(0xffffffffu, not_finite(y[u], i));
+            const uint32_t nans = __ballot_sync(0xffffffffu, is_nan(y[u], i));
+            nan[i] |= sees ? nans : 0u;
+            known[i] |= sees ? odds : 0u;
+            apart[i] |= sees ? 0u : odds;
+          }
+        }
+      }
+    }
+  }
+  return open();
+}
+
+// Eight rows of a warp (the set bits of `rows`, eight at most) from the keys that they see alone, eight keys at a time:
+// scores by `mma.sync` (a lane has row g of the eight, and eight columns in a row of each 32 of queries and keys alike),
+// weights and sums in fp32, of which a lane has four columns.
+__device__ __forceinline__ void rows_again(const Rows& x, unsigned rows) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const bool has = 4 * lane < x.d;
+  const unsigned all = rows;
+  Seen mine = {0, 0, 0};
+  int own = x.row0, sink_end = 0, lo = 0x7fffffff, hi = 0;
+#pragma unroll 1
+  for (int i = 0; rows != 0; ++i, rows &= rows - 1) {
+    const int row = x.row0 + __ffs(rows) - 1;
+    const Seen s = x.seen(row);
+    sink_end = max(sink_end, s.sink_end);
+    lo = min(lo, s.lo);
+    hi = max(hi, s.hi);
+    if (g == i) own = row, mine = s;
+  }
+  uint4 q[4];
+  auto pieces = [&](const __nv_bfloat16* from, uint4 (&y)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      y[i] = 32 * i + 8 * c < x.d ? *reinterpret_cast<const uint4*>(from + 32 * i + 8 * c) : make_uint4(0, 0, 0, 0);
+  };
+  pieces(x.q + x.at(own, x.qs), q);
+  float2 o[8][2] = {};
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const int begin = part == 0 ? 0 : lo, end = part == 0 ? sink_end : hi;
+#pragma unroll 1
+    for (int j0 = begin; j0 < end; j0 += 8) {
+      uint4 k[4];
+      uint2 v[8];
+      pieces(x.k + min(j0 + g, end - 1) * x.ks, k);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        v[u] = has && j0 + u < end ? *reinterpret_cast<const uint2*>(x.v + (j0 + u) * x.vs + 4 * lane) : make_uint2(0, 0);
+      float s[4] = {0.f, 0.f, 0.f, 0.f};  // keys 2 c and 2 c + 1 in the first two
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t q0[4] = {q[i].x, 0u, q[i].y, 0u}, q1[4] = {q[i].z, 0u, q[i].w, 0u};
+        mma_bf16(s, q0, k[i].x, k[i].y);
+        mma_bf16(s, q1, k[i].z, k[i].w);
+      }
+      bool sees[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int key = j0 + 2 * c + i;
+        sees[i] = part == 0 ? key < mine.sink_end : key >= mine.lo && key < mine.hi;
+        s[i] = sees[i] ? s[i] * x.scale_log2 : -INFINITY;
+      }
+      float top = fmaxf(s[0], s[1]);
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(m, fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)));
+      const float base = top == -INFINITY ? 0.f : top, keep = exp2f(m - base);
+      m = top;
+      uint32_t some = 0;  // values that a weight of 0 does not keep out
+#pragma unroll
+      for (int u = 0; u < 8; ++u) some |= not_finite(v[u].x) | not_finite(v[u].y);
+      const bool odd = __any_sync(0xffffffffu, some != 0);
+      float w[2];
+      l *= keep;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // (weights of 2^-32 at most: sums of fewer than 2^31 finite values stay finite)
+        w[i] = sees[i] ? exp2f(s[i] - base) * 0x1p-32f : 0.f;
+        l += w[i];
+        if (odd && !sees[i]) w[i] = -1.f;
+      }
+      if (__any_sync(0xffffffffu, keep != 1.f)) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const float f = __shfl_sync(0xffffffffu, keep, 4 * r);
+          o[r][0] = mul2(o[r][0], make_float2(f, f));
+          o[r][1] = mul2(o[r][1], make_float2(f, f));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float2 a = widen2(v[u].x), b = widen2(v[u].y);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const float f = __shfl_sync(0xffffffffu, w[u & 1], 4 * r + u / 2);
+          if (odd && f < 0.f) continue;
+          o[r][0] = fma2(a, make_float2(f, f), o[r][0]);
+          o[r][1] = fma2(b, make_float2(f, f), o[r][1]);
+        }
+      }
+    }
+  }
+  l += __shfl_xor_sync(0xffffffffu, l, 1);
+  l += __shfl_xor_sync(0xffffffffu, l, 2);
+  rows = all;
+#pragma unroll
+  for (int r = 0; r < 8; ++r, rows &= rows - 1) {
+    const float sum = __shfl_sync(0xffffffffu, l, 4 * r), inv = 1.f / sum;
+    const float2 f[2] = {mul2(o[r][0], make_float2(inv, inv)), mul2(o[r][1], make_float2(inv, inv))};
+    if (rows != 0 && has)
+      *reinterpret_cast<uint2*>(x.out + x.at(x.row0 + __ffs(rows) - 1, x.os) + 4 * lane) =
+          sum == 0.f ? make_uint2(0, 0) : narrow4(f);
+  }
+}
+
+// The rows of an item that are not finite (`odd`: the lane's, whose other thread's told[128] is about), by both warps of
+// theirs.  Apart from the kernel, whose registers and instructions it would take.
+__device__ __noinline__ void odd_rows(const PromptArgs& a, const Item& it, int tpt, float scale_log2, bool odd, float* stat,
+                                      int* busy) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 3, hf = warp >> 2 & 1, quad = warp & 3;
+  const int pair = 1 + 4 * t + quad, G = a.Hq / a.Hkv;
+  float* const told = stat + t * 256 + 32 * quad + lane;
+  if (lane == 0) {
+    copies_done();  // rows that are looked at, and may be written again
+    atomicAdd(busy, 1);
+  }
+  __syncwarp();
+  Rows x;
+  const long long tok = (long long)it.q0 + t * tpt;
+  x.q = a.q + tok * a.qs + (long long)it.hk * G * a.d;
+  x.k = a.k + (long long)it.k0 * a.ks + it.hk * a.d;
+  x.v = a.v + (long long)it.k0 * a.vs + it.hk * a.d;
+  x.out = a.out + (tok * a.Hq + (long long)it.hk * G) * a.d;
+  x.qs = a.qs;
+  x.ks = a.ks;
+  x.vs = a.vs;
+  x.os = (long long)a.Hq * a.d;
+  x.there = (a.cu != nullptr ? (long long)a.Tk : (long long)a.B * a.Tk) - it.k0;
+  x.d = a.d;
+  x.G = G;
+  x.row0 = 32 * quad;
+  x.pa = it.p0 + t * tpt;
+  x.view = a.view;
+  x.scale_log2 = scale_log2;
+  told[128 * hf] = odd ? 1.f : 0.f;
+  pair_sync(pair);
+  if (hf == 0) told[0] = unexplained(x, it, t, odd || told[128] != 0.f) ? 1.f : 0.f;
+  pair_sync(pair);
+  // the two warps take those rows in turn, eight at a time
+  unsigned rest = __ballot_sync(0xffffffffu, told[0] != 0.f);
+#pragma unroll 1
+  for (int i = 0; rest != 0; ++i) {
+    unsigned eight = 0;
+    for (int n = 0; n < 8; ++n, rest &= rest - 1) eight |= rest & (0u - rest);
+    if ((i & 1) == hf) rows_again(x, eight);
+  }
+  __syncwarp();
+  if (lane == 0) atomicSub(busy, 1);
+}
+
 }  // namespace
 
 template <int kQuarters>
@@ -198,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k16,
                      const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ CUtensorMap tm_out,
-                     const attn::PromptArgs a, int items, int tpt,
+                     const __grid_constant__ attn::PromptArgs a, int items, int tpt,
                      float scale_log2, int negate, int* __restrict__ err) {
   using C = Cfg<kQuarters>;
   constexpr int kTile = C::kTile, kHalves = C::kHalves, kRing = C::kRing;
@@ -211,6 +447,7 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
            *q_empty = q_full + 2, *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 2, *o_empty = o_full + 2, *turn = o_empty + 2, *drain = turn + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* busy = reinterpret_cast<int*>(tmem_slot + 2);  // warps that work rows out again, which others wait for in patience
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
@@ -240,6 +477,7 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       tc::mbar_init(drain + t, 1);
     }
     *abort_flag = 0;
+    *busy = 0;
     tc::fence_mbar_init();
   }
   if (warp == kLoadWarp && lane == 0) {
@@ -257,14 +495,20 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     atomicOr(err, bit);
   };
   if (smem_u32(smem_raw) != kSmemBase) give_up(1);
+  // Whether a wait has run out (what it waits for may itself wait for rows that are worked out again).
+  auto run_out = [&](long long& since) {
+    if (clock64() - since <= kPatience) return false;
+    since = clock64();
+    return *static_cast<volatile int*>(busy) == 0;
+  };
   // One thread's wait; false once this or another wait has run out.
   auto wait = [&](uint64_t* bar, uint32_t par, int bit) {
     if (tc::mbar_wait(bar, par, 1)) return true;
-    const long long since = clock64();
+    long long since = clock64();
 #pragma unroll 1
     while (!*abort_flag) {
       if (tc::mbar_wait(bar, par, 1)) return true;
-      if (clock64() - since > kPatience) give_up(bit);
+      if (run_out(since)) give_up(bit);
     }
     return false;
   };
@@ -431,7 +675,7 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           if (__all_sync(0xffffffffu, done)) return true;
           if ((i & 255) == 255) {
             if (since == 0) since = clock64();
-            if (lane == 0 && clock64() - since > kPatience) give_up(1);
+            if (lane == 0 && run_out(since)) give_up(1);
             if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
           }
         }
@@ -536,12 +780,9 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     bool stop = any_of_pair(pair, !ok);
     for (int n = 0; !stop; ++n) {
       const Item* ip = item_at(n);
-      const int valid = ip->valid, pa = ip->p0 + t * tpt, nt = ip->n[t], off = ip->sink - ip->lo;
+      const int valid = ip->valid, pa = ip->p0 + t * tpt, off = ip->sink - ip->lo;
       const int sink_tiles = ip->z[t] > 0 ? ip->sinks : 0, from = ip->a[t], to = ip->z[t];
-      const int tok0 = ip->q0 + t * tpt, k0 = ip->k0, hk = ip->hk;
       const int lo_all = ip->lo_all[t], hi_all = ip->hi_all[t];
-      __syncwarp();
-      if (lane == 0) arrive(item_empty + n % kItemSlots);
       if (!valid) break;
       float m = -INFINITY, l = 0.f;  // the maximum in use (log2), the weights' sum
       // places of the list that the row sees: [0, sinks) and [lo, hi), and what all the tile's rows see
@@ -622,7 +863,8 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (lane == 0) arrive(p_full + t);
       }
       if (stop) break;
-      // ---- outputs
+      // ---- outputs (what they take of the item is read here, so that the loop above has the registers)
+      const int tok0 = ip->q0 + t * tpt, hk = ip->hk, nt = ip->n[t];
       pair_sync(pair);  // (the maxima there are read)
       told[128 * hf] = l;
       pair_sync(pair);
@@ -678,32 +920,15 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       tc::fence_before();
       __syncwarp();
       if (some && lane == 0) arrive(o_empty + t);
-      // rows that are not finite again, one after the other (but where the weights' sum is not: nothing else could be)
-      // (and where nothing is seen, 0 times the sum of values that were not)
+      // rows that are not finite are looked into (but where the weights' sum is not: nothing else could be; a row that
+      // sees nothing is among them where values beside it are not, 0 times their sum)
       bool odd = !(zero.x + zero.y == 0.f) && live && l <= FLT_MAX;
       ok = ok && warp_wait(item_full + (n + 1) % kItemSlots, item_par(n + 1), 1);
       if (__builtin_expect(any_of_pair(pair, odd || !ok), 0)) {
         if (any_of_pair(pair, !ok)) break;
-        if (lane == 0) copies_done();  // rows that are written again
-        __syncwarp();
-        told[128 * hf] = odd ? 1.f : 0.f;
-        pair_sync(pair);
-        if (hf == 0) {
-          odd = odd || told[128] != 0.f;
-          for (unsigned rest = __ballot_sync(0xffffffffu, odd); rest != 0; rest &= rest - 1) {
-            const int r2 = 32 * quad + __ffs(rest) - 1, tr2 = r2 / G;
-            const long long tok2 = (long long)tok0 + tr2;
-            const int head2 = hk * G + r2 - tr2 * G;
-            const __nv_bfloat16 *k = a.k + (long long)k0 * a.ks + hk * a.d, *v = a.v + (long long)k0 * a.vs + hk * a.d;
-            const attn::RowSum r = attn::row_sum(
-                a.q + tok2 * a.qs + (long long)head2 * a.d, a.d, negate ? -scale_log2 : scale_log2,
-                attn::seen_by(a.view, pa + tr2), [&](int j) { return k + j * a.ks; },
-                [&](int j) { return v + j * a.vs; }, attn::WidenBf16());
-            attn::put_row(r, a.d, a.out + (tok2 * a.Hq + head2) * a.d, nullptr, 1.f);
-          }
-        }
-        __syncwarp();
+        odd_rows(a, *ip, tpt, negate ? -scale_log2 : scale_log2, odd, stat, busy);
       }
+      if (lane == 0) arrive(item_empty + n % kItemSlots);
     }
     if (lane == 0) copies_done();
     __syncwarp();

@@ -627,9 +627,9 @@ int gdn_cache_append(const gdn_cache_append_args *args);
  *   lse           fp32 [T, Hq] or NULL: log sum_j w_ij
  *
  * Hq / Hkv is at most 128, and there are at most 2^31 - 1,024 queries, and keys, in all.  What unseen
- * keys and values hold, infinities and NaN included, does not reach a query (where it is not finite, the
- * queries of the tiles beside it are worked out apart, slowly and with other roundings, as those are that
- * see such a value).  Weights are rounded to bf16 as operands of the second product (2^-9 of each term);
+ * keys and values hold, infinities and NaN included, does not reach a query (where a value is not finite, the
+ * queries of the tiles beside it that do not see it are worked out apart, more slowly and with other roundings;
+ * those that * see it are not).  Weights are rounded to bf16 as operands of the second product (2^-9 of each term);
  * scores, sums and the running maximum are fp32.
  *
  * workspace: gdn_attn_workspace_bytes(...) bytes of device memory, 256-byte aligned, not shared with

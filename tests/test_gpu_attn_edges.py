@@ -1,0 +1,132 @@
+"""Attention and its cache where they can go wrong: values that are not finite, calls at once, refusals (GPU).
+
+Tolerances are those of test_gpu_attn.py.
+"""
+
+import numpy as np
+import pytest
+
+import attn_refs as R
+from test_gpu_attn import BF, I32, NAN, close, close_lse, cu_of, gen, ints, n64, rnd, slices, torch
+from test_gpu_attn import gdn  # noqa: F401  (the fixture)
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def fastest(call, n=4):
+    """Milliseconds of the fastest of n calls, after one."""
+    call()
+    times = []
+    for _ in range(n):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        call()
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b))
+    return min(times)
+
+
+# ---- prompts: values that are not finite ---------------------------------------------------------
+
+def sees(n, m, window, sinks):
+    p, j = np.arange(m - n, m)[:, None], np.arange(m)[None]
+    return (j <= p) & ((j > p - window) | (j < sinks) if window else True)
+
+
+def check_odd(gdn, q, k, v, lens, window=0, sinks=0, packed=True):
+    """Against float64 with the values that are not finite taken out, and put where they are seen: a column in which a
+    row sees a NaN, or infinities of both signs, is NaN, one in which it sees an infinity is that."""
+    out, lse = gdn.attention(q, k, v, cu_of(lens) if packed else None, B=None if packed else len(lens), window=window,
+                             sinks=sinks, want_lse=True)
+    G = q.shape[1] // k.shape[1]
+    at = 0
+    for n in lens:
+        sl = slice(at, at + n)
+        q64, k64, v64 = n64(q[sl]), n64(k[sl]), n64(v[sl])
+        y, mag, l, bound = R.attend(q64, k64, v64, q.shape[2] ** -0.5, window, sinks)
+        seen = sees(n, n, window, sinks).astype(np.float64)
+        got, kind = n64(out[sl]), {}
+        for what, there in (("nan", np.isnan(v64)), ("up", np.isposinf(v64)), ("down", np.isneginf(v64))):
+            kind[what] = np.stack([seen @ there[:, h // G] > 0 for h in range(q.shape[1])], 1)
+        nan = kind["nan"] | (kind["up"] & kind["down"])
+        assert np.array_equal(np.isnan(got), nan)
+        assert np.array_equal(np.isposinf(got), kind["up"] & ~nan) and np.array_equal(np.isneginf(got), kind["down"] & ~nan)
+        odd = ~np.isfinite(got)
+        close(torch.from_numpy(np.where(odd, 0.0, got)), np.where(odd, 0.0, y), np.where(odd, 0.0, mag), bound)
+        close_lse(lse[sl], l, bound)
+        at += n
+    return out
+
+
+ODD = [  # lens, Hq, Hkv, d, window, sinks
+    ([700], 4, 1, 64, 0, 0), ([300, 1, 520], 8, 2, 128, 0, 0), ([900], 2, 2, 80, 0, 0), ([260, 400], 5, 1, 32, 0, 0),
+    ([1100], 4, 1, 128, 200, 0), ([1100], 4, 2, 64, 130, 5), ([640, 300], 16, 1, 104, 150, 140), ([500], 128, 1, 16, 60, 1),
+]
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d,window,sinks", ODD)
+@pytest.mark.parametrize("what", ["first", "middle", "last", "both", "every 128", "every 300", "columns", "all", "huge"])
+def test_attention_values_that_are_not_finite(gdn, lens, Hq, Hkv, d, window, sinks, what):
+    g = gen(sum(lens) + d)
+    T = sum(lens)
+    q, k, v = slices(g, T, T, Hq, Hkv, d)
+    h = Hkv - 1
+    if what == "first":  # seen by every row of the first sequence
+        v[0, h, 3] = NAN
+        v[0, 0, d - 1] = -INF
+    elif what == "middle":
+        v[lens[0] // 2, h, 5] = INF
+        v[lens[0] // 2 + 1, 0, 6] = NAN
+    elif what == "last":  # beside the next sequence's rows, or at the end
+        v[lens[0] - 1, h, 0] = NAN
+        v[T - 1, 0] = INF
+    elif what == "both":  # of both signs, in one column and in two
+        v[10, h, 1], v[200, h, 1], v[lens[0] - 3, h, 2], v[lens[0] - 60, h, 4] = INF, -INF, -INF, INF
+    elif what == "every 128":
+        v[::128, h, 2] = NAN
+        v[64::128, 0, 7] = INF
+    elif what == "every 300":  # (a window forgets them)
+        v[7::300, h, :2] = INF
+        v[180::300, 0, 1] = NAN
+    elif what == "columns":
+        for c in range(d):
+            v[(c * 37) % T, h, c] = (NAN, INF, -INF)[c % 3]
+    elif what == "all":
+        v[:, h] = NAN
+        v[:, 0, ::2] = INF
+    else:  # finite, but their weighted sums are not before the division
+        v[:, h, :3] = 2e38
+        v[T // 2, 0, 1] = NAN
+    check_odd(gdn, q, k, v, lens, window, sinks)
+    assert gdn.gdn_device_status() == (0, 0)
+
+
+def test_attention_a_value_that_is_not_finite_is_quick(gdn):
+    # rows that see it are looked into, not worked out one by one
+    g = gen(3)
+    q, k, v = rnd(g, 4096, 32, 128), rnd(g, 4096, 8, 128), rnd(g, 4096, 8, 128)
+    out = torch.empty_like(q)
+    clean = fastest(lambda: gdn.attention(q, k, v, out=out))
+    for at in (0, 1000, 4095, slice(None)):
+        odd = v.clone()
+        odd[at, :, 3] = NAN
+        assert fastest(lambda: gdn.attention(q, k, odd, out=out)) < 40 * clean  # 700 and more where every row was
+
+
+def test_attention_keys_that_are_not_finite(gdn):
+    # a score that is not a number reaches its row whole, the others not at all
+    g = gen(4)
+    q, k, v = rnd(g, 700, 4, 64), rnd(g, 700, 2, 64), rnd(g, 700, 2, 64)
+    want, _ = gdn.attention(q, k, v, window=200, sinks=3)
+    k[300, 1, 5] = NAN
+    v[300, 0, 0] = NAN
+    out, lse = gdn.attention(q, k, v, window=200, sinks=3, want_lse=True)
+    assert bool(out[300:500, 2:].isnan().all()) and bool(lse[300:500, 2:].isnan().all())
+    assert bool(out[300:500, :2, 0].isnan().all())
+    for rest in (out[:300], out[500:], out[300:500, :2, 1:]):
+        assert bool(rest.isfinite().all())
+    assert bool(torch.isfinite(lse[:, :2]).all())
+    assert torch.equal(out[640:], want[640:])  # (tiles far from the edge of what sees it)
