@@ -43,6 +43,7 @@ cudaError_t launch_decode(const void*, const void*, const void*, const float*, c
 namespace {
 
 constexpr int kMaxDevices = 64;
+constexpr int kAttnStreams = 16;  // that keep a workspace (about 6 MB); another takes over the one longest unused
 
 struct DevBuffers {
   void* ws = nullptr;
@@ -54,8 +55,15 @@ struct DevBuffers {
   size_t scan_zeroed = 0;
   void* ssm = nullptr;  // gdn_ssm_scan's workspace
   size_t ssm_bytes = 0;
-  void* attn = nullptr;  // gdn_attn's and gdn_attn_step's
+  void* attn = nullptr;  // the status words of gdn_attn and gdn_attn_step
   size_t attn_bytes = 0;
+  // gdn_attn_step's workspaces, a stream's each, so that calls on different streams may overlap
+  struct OfStream {
+    unsigned long long id = 0, used = 0;  // of the stream (no other ever has it); the last call's number
+    void* ws = nullptr;
+    size_t bytes = 0;
+  } attn_of[kAttnStreams];
+  unsigned long long attn_calls = 0;
   cudaStream_t aux = nullptr;  // second stream for pass A's transition run
   cudaEvent_t fork = nullptr, join = nullptr;
   int sms = 0;
@@ -129,9 +137,8 @@ int ensure(void*& ptr, size_t& have, size_t need) {
 }
 
 // The same for a workspace whose first 256 bytes are status words: a new one's are cleared on stream `st`, in the order
-// of the call that writes them, but for the first word, which keeps the bits of the calls before.  With `all` the rest
-// is cleared too.
-int ensure_workspace(void*& ptr, size_t& have, size_t need, cudaStream_t st, bool all = false) {
+// of the call that writes them, but for the first word, which keeps the bits of the calls before.
+int ensure_workspace(void*& ptr, size_t& have, size_t need, cudaStream_t st) {
   if (need <= have) return GDN_OK;
   int bits = 0;
   cudaError_t e = cudaSuccess;
@@ -140,7 +147,7 @@ int ensure_workspace(void*& ptr, size_t& have, size_t need, cudaStream_t st, boo
     return set_cuda_error(e, GDN_ERR_LAUNCH);
   const int rc = ensure(ptr, have, need);
   if (rc != GDN_OK) return rc;
-  e = cudaMemsetAsync(ptr, 0, all ? have : 256, st);
+  e = cudaMemsetAsync(ptr, 0, 256, st);
   if (e == cudaSuccess && bits != 0) e = cudaMemcpyAsync(ptr, &bits, sizeof(bits), cudaMemcpyHostToDevice, st);
   return e == cudaSuccess ? GDN_OK : set_cuda_error(e, GDN_ERR_LAUNCH);
 }
@@ -434,23 +441,59 @@ int device_sms() {
   return n;
 }
 
-static int ensure_own(void* DevBuffers::*ws_of, size_t DevBuffers::*bytes_of, int dev, size_t need, cudaStream_t st,
-                      void** ws, bool all) {
+int ensure_ssm_workspace(int dev, size_t need, cudaStream_t st, void** ws) {
   if (dev < 0 || dev >= kMaxDevices) return GDN_ERR_ARG;
   std::lock_guard<std::mutex> lock(g_mu);
   DevBuffers& d = g_dev[dev];
-  const int rc = ensure_workspace(d.*ws_of, d.*bytes_of, need, st, all);
+  const int rc = ensure_workspace(d.ssm, d.ssm_bytes, need, st);
   if (rc != GDN_OK) return rc;
-  *ws = d.*ws_of;
+  *ws = d.ssm;
   return GDN_OK;
 }
 
-int ensure_ssm_workspace(int dev, size_t need, cudaStream_t st, void** ws) {
-  return ensure_own(&DevBuffers::ssm, &DevBuffers::ssm_bytes, dev, need, st, ws, false);
-}
-
-int ensure_attn_workspace(int dev, size_t need, cudaStream_t st, void** ws) {
-  return ensure_own(&DevBuffers::attn, &DevBuffers::attn_bytes, dev, need, st, ws, true);
+int own_attn_workspace(int dev, size_t need, cudaStream_t st, AttnOwn& own) {
+  if (dev < 0 || dev >= kMaxDevices) return GDN_ERR_ARG;
+  own.hold = std::unique_lock<std::mutex>(g_mu);
+  DevBuffers& d = g_dev[dev];
+  cudaError_t e;
+  if (d.attn == nullptr || need > 0) {
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    e = cudaStreamIsCapturing(st, &capture);
+    if (e != cudaSuccess) return set_cuda_error(e, GDN_ERR_LAUNCH);
+    if (capture != cudaStreamCaptureStatusNone) return GDN_ERR_SCRATCH;
+  }
+  if (d.attn == nullptr) {  // cleared before any stream uses it
+    const int rc = ensure_workspace(d.attn, d.attn_bytes, 256, st);
+    if (rc != GDN_OK) return rc;
+    if ((e = cudaStreamSynchronize(st)) != cudaSuccess) return set_cuda_error(e, GDN_ERR_LAUNCH);
+  }
+  own.status = static_cast<int*>(d.attn);
+  if (need == 0) return GDN_OK;
+  unsigned long long id = 0;
+  if ((e = cudaStreamGetId(st, &id)) != cudaSuccess) return set_cuda_error(e, GDN_ERR_LAUNCH);
+  DevBuffers::OfStream* s = nullptr;
+  for (DevBuffers::OfStream& x : d.attn_of)
+    if (x.ws != nullptr && x.id == id) s = &x;
+  const bool known = s != nullptr;
+  if (!known) {
+    s = &d.attn_of[0];
+    for (DevBuffers::OfStream& x : d.attn_of)
+      if (x.used < s->used) s = &x;
+    // what another stream has begun there ends first
+    if (s->ws != nullptr && (e = cudaDeviceSynchronize()) != cudaSuccess) return set_cuda_error(e, GDN_ERR_LAUNCH);
+  }
+  if (!known || need > s->bytes) {
+    const int rc = ensure(s->ws, s->bytes, need);
+    if (rc != GDN_OK) return rc;
+    s->id = id;
+    if ((e = cudaMemsetAsync(s->ws, 0, s->bytes, st)) != cudaSuccess) {
+      s->id = 0;  // (no stream's)
+      return set_cuda_error(e, GDN_ERR_LAUNCH);
+    }
+  }
+  s->used = ++d.attn_calls;
+  own.ws = s->ws;
+  return GDN_OK;
 }
 
 }  // namespace gdn
@@ -912,6 +955,8 @@ void gdn_release_workspace(void) {
   if (d.scan) cudaFree(d.scan);
   if (d.ssm) cudaFree(d.ssm);
   if (d.attn) cudaFree(d.attn);
+  for (const DevBuffers::OfStream& s : d.attn_of)
+    if (s.ws) cudaFree(s.ws);
   if (d.fork) cudaEventDestroy(d.fork);
   if (d.join) cudaEventDestroy(d.join);
   if (d.aux) cudaStreamDestroy(d.aux);

@@ -2,5 +2,5 @@
 #include "gdn_attn_tile.cuh"
 
 namespace gdn {
-template cudaError_t launch_attn_tiles<2>(const attn::PromptArgs&, void*, cudaStream_t);
+template cudaError_t launch_attn_tiles<2>(const attn::PromptArgs&, int*, cudaStream_t);
 }  // namespace gdn

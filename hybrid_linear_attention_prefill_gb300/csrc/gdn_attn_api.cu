@@ -7,8 +7,8 @@
 #include "gdn_cache.h"
 
 namespace gdn {
-cudaError_t launch_attn(const attn::PromptArgs&, void*, cudaStream_t);
-cudaError_t launch_attn_step(const attn::StepArgs&, bool, void*, cudaStream_t);
+cudaError_t launch_attn(const attn::PromptArgs&, int*, cudaStream_t);
+cudaError_t launch_attn_step(const attn::StepArgs&, bool, void*, int*, cudaStream_t);
 size_t attn_step_workspace(int, int, int, int);
 }  // namespace gdn
 
@@ -34,18 +34,20 @@ int check_cache(const void* p, long long stride, int Hkv, int d, int page, int b
   return GDN_OK;
 }
 
-// The call's workspace: the given one, or the library's own.
-int workspace_for(void* given, size_t given_bytes, size_t need, void* stream, void** ws) {
+// The call's workspace of `need` bytes: the given one, whose first word is for status bits, or the library's own, of which
+// `status_only` wants no more than those.
+int workspace_for(void* given, size_t given_bytes, size_t need, bool status_only, void* stream, gdn::AttnOwn& own) {
   if (given != nullptr) {
     if (!aligned(given, 256)) return GDN_ERR_ALIGN;
     if (given_bytes < need) return GDN_ERR_SCRATCH;
-    *ws = given;
+    own.ws = given;
+    own.status = static_cast<int*>(given);
     return GDN_OK;
   }
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return gdn::set_cuda_error(e, GDN_ERR_LAUNCH);
-  return gdn::ensure_attn_workspace(dev, need, static_cast<cudaStream_t>(stream), ws);
+  return gdn::own_attn_workspace(dev, status_only ? 0 : need, static_cast<cudaStream_t>(stream), own);
 }
 
 }  // namespace
@@ -155,8 +157,8 @@ int gdn_attn(const gdn_attn_args* args) {
   if (nk > 0 && (overlap(k, ((size_t)(nk - 1) * k_stride + wk) * 2, out, no) ||
                  overlap(v, ((size_t)(nk - 1) * v_stride + wk) * 2, out, no)))
     return GDN_ERR_ARG;
-  void* ws = nullptr;
-  if ((rc = workspace_for(given, given_bytes, 256, stream, &ws)) != GDN_OK) return rc;
+  gdn::AttnOwn own;
+  if ((rc = workspace_for(given, given_bytes, 256, true, stream, own)) != GDN_OK) return rc;
   gdn::attn::PromptArgs a;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k = static_cast<const __nv_bfloat16*>(k);
@@ -176,7 +178,7 @@ int gdn_attn(const gdn_attn_args* args) {
   a.d = d;
   a.view = {window, sinks};
   a.scale = scale;
-  return done(gdn::launch_attn(a, ws, static_cast<cudaStream_t>(stream)));
+  return done(gdn::launch_attn(a, own.status, static_cast<cudaStream_t>(stream)));
 }
 
 int gdn_attn_step(const gdn_attn_step_args* args) {
@@ -202,8 +204,9 @@ int gdn_attn_step(const gdn_attn_step_args* args) {
       !aligned(v_scale, 4))
     return GDN_ERR_ALIGN;
   if (overlap(q, ((size_t)(B - 1) * q_stride + (size_t)Hq * d) * 2, out, (size_t)B * Hq * d * 2)) return GDN_ERR_ARG;
-  void* ws = nullptr;
-  if ((rc = workspace_for(given, given_bytes, gdn::attn_step_workspace(B, Hq, Hkv, d), stream, &ws)) != GDN_OK) return rc;
+  gdn::AttnOwn own;
+  if ((rc = workspace_for(given, given_bytes, gdn::attn_step_workspace(B, Hq, Hkv, d), false, stream, own)) != GDN_OK)
+    return rc;
   gdn::attn::StepArgs a;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.qs = q_stride;
@@ -227,7 +230,7 @@ int gdn_attn_step(const gdn_attn_step_args* args) {
   a.W = W;
   a.view = {window, sinks};
   a.scale = scale;
-  return done(gdn::launch_attn_step(a, e4m3, ws, static_cast<cudaStream_t>(stream)));
+  return done(gdn::launch_attn_step(a, e4m3, own.ws, own.status, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

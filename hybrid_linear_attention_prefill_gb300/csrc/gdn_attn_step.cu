@@ -614,7 +614,7 @@ namespace {
 
 int resident(int sms) { return sms * kCtas; }
 
-// Workspace: [256 B status words][partial sums][their maxima and sums][counters].  The places do not depend on the
+// Workspace: [256 B, a caller's status words][partial sums][their maxima and sums][counters].  The places do not depend on the
 // call, so that the counters are zero whatever call came before.
 struct Layout {
   size_t stats, counters, total;
@@ -646,7 +646,7 @@ size_t attn_step_workspace(int B, int Hq, int Hkv, int d) {
   return layout(B, Hq, Hkv, sms > 0 ? sms : 256).total;  // (without a device: enough for any)
 }
 
-cudaError_t launch_attn_step(const StepArgs& a, bool e4m3, void* ws, cudaStream_t st) {
+cudaError_t launch_attn_step(const StepArgs& a, bool e4m3, void* ws, int* status, cudaStream_t st) {
   const int sms = device_sms();
   if (sms == 0) return cudaErrorNoDevice;
   const int G = a.Hq / a.Hkv, groups = (G + kMaxHeads - 1) / kMaxHeads, heads = (G + groups - 1) / groups;
@@ -655,16 +655,15 @@ cudaError_t launch_attn_step(const StepArgs& a, bool e4m3, void* ws, cudaStream_
   unsigned char* p = static_cast<unsigned char*>(ws);
   Work w = {reinterpret_cast<float*>(p + 256), reinterpret_cast<float2*>(p + l.stats),
             reinterpret_cast<int*>(p + l.counters)};
-  int* err = static_cast<int*>(ws);
   const unsigned grid = (unsigned)resident(sms);
   auto run = [&](auto nt, auto e) {
     constexpr int NT = decltype(nt)::value;
     constexpr bool E4M3 = decltype(e)::value;
     switch ((a.d + 31) / 32) {
-      case 1: return launch_step<NT, 1, E4M3>(a, groups, heads, grid, w, err, st);
-      case 2: return launch_step<NT, 2, E4M3>(a, groups, heads, grid, w, err, st);
-      case 3: return launch_step<NT, 3, E4M3>(a, groups, heads, grid, w, err, st);
-      default: return launch_step<NT, 4, E4M3>(a, groups, heads, grid, w, err, st);
+      case 1: return launch_step<NT, 1, E4M3>(a, groups, heads, grid, w, status, st);
+      case 2: return launch_step<NT, 2, E4M3>(a, groups, heads, grid, w, status, st);
+      case 3: return launch_step<NT, 3, E4M3>(a, groups, heads, grid, w, status, st);
+      default: return launch_step<NT, 4, E4M3>(a, groups, heads, grid, w, status, st);
     }
   };
   using One = std::integral_constant<int, 1>;

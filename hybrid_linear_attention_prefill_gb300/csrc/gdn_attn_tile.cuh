@@ -954,7 +954,7 @@ bool head_map(CUtensorMap* m, const void* base, long long stride, int heads, int
 }  // namespace
 
 template <int kQuarters>
-cudaError_t launch_attn_tiles(const attn::PromptArgs& a, void* ws, cudaStream_t st) {
+cudaError_t launch_attn_tiles(const attn::PromptArgs& a, int* status, cudaStream_t st) {
   const bool packed = a.cu != nullptr;
   const long long nq = packed ? (long long)a.T : (long long)a.B * a.T;
   const long long nk = packed ? (long long)a.Tk : (long long)a.B * a.Tk;
@@ -982,7 +982,7 @@ cudaError_t launch_attn_tiles(const attn::PromptArgs& a, void* ws, cudaStream_t 
   const int negate = c < 0.f;  // as the sign of the queries
   c = std::max(negate ? -c : c, 0x1p-126f);  // (unseen scores are minus infinity, and 0 times that would not do)
   gdn_attn_tile_kernel<kQuarters><<<(unsigned)std::min<long long>(items, sms), kThreads, Cfg<kQuarters>::kSmem, st>>>(
-      q, k, v, k16, v16, out, a, (int)items, tpt, c, negate, static_cast<int*>(ws));
+      q, k, v, k16, v16, out, a, (int)items, tpt, c, negate, status);
   return cudaGetLastError();
 }
 

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stddef.h>
 
+#include <mutex>
+
 namespace gdn {
 
 // The calling thread's record of the CUDA error behind its last GDN_ERR_LAUNCH or
@@ -31,7 +33,15 @@ int device_sms();
 // return.
 int ensure_ssm_workspace(int dev, size_t need, cudaStream_t st, void** ws);
 
-// The same of gdn_attn and gdn_attn_step (all of a new one is cleared).
-int ensure_attn_workspace(int dev, size_t need, cudaStream_t st, void** ws);
+// The library's own workspace of an attention call: the device's status words, and for `need` bytes (0: none) a place of
+// the stream's own, zero where it has not been used.  GDN_OK, or the error code to return; GDN_ERR_SCRATCH while the
+// stream is being captured, where something would have to be allocated or a place of the stream's given to a graph that
+// any stream may run.  The library's buffers are held as they are until `hold` goes: after the launch.
+struct AttnOwn {
+  int* status = nullptr;
+  void* ws = nullptr;
+  std::unique_lock<std::mutex> hold;
+};
+int own_attn_workspace(int dev, size_t need, cudaStream_t st, AttnOwn& own);
 
 }  // namespace gdn

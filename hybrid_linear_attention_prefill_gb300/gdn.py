@@ -856,7 +856,7 @@ def attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, B=None, window=0, 
     are its last tokens, whose keys have boundaries of their own in cu_seqlens_k where they are more (or fewer).  With
     window > 0 a query sees the last `window` tokens, itself among them, and the first `sinks`.  scale: of the
     scores, 1 / sqrt(d) by default.  workspace: a byte tensor of gdn_attn_workspace_bytes(...), zeroed once, for
-    calls that overlap or are captured.
+    calls that are captured; without one the library has one for each stream.
     Returns (out bf16 [T, Hq, d], lse fp32 [T, Hq] or None: the log of the sum of the weights).
     """
     fast = _shorter()

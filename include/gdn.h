@@ -339,8 +339,8 @@ void gdn_release_workspace(void);
  * layers), each for prompts and for single tokens, and the norm that opens a layer.
  *
  * All pointers are DEVICE memory, owned by the caller and not retained; every call is
- * asynchronous on `stream`, never synchronises the host (but for a gdn_ssm_scan that has to
- * enlarge the library's own workspace), and returns GDN_OK or, before anything is launched,
+ * asynchronous on `stream`, never synchronises the host (but for a gdn_ssm_scan, gdn_attn or
+ * gdn_attn_step that has to make or enlarge the library's own workspace), and returns GDN_OK or, before anything is launched,
  * GDN_ERR_ARG / GDN_ERR_ALIGN (or GDN_ERR_LAUNCH from a launch).
  * Activations are bf16; sums, states of the scan and softplus / exp values are fp32.  A
  * `*_stride` is the distance between consecutive tokens in elements, so that an operand can
@@ -629,12 +629,14 @@ int gdn_cache_append(const gdn_cache_append_args *args);
  * Hq / Hkv is at most 128, and there are at most 2^31 - 1,024 queries, and keys, in all.  What unseen
  * keys and values hold, infinities and NaN included, does not reach a query (where a value is not finite, the
  * queries of the tiles beside it that do not see it are worked out apart, more slowly and with other roundings;
- * those that * see it are not).  Weights are rounded to bf16 as operands of the second product (2^-9 of each term);
+ * those that see it are not).  Weights are rounded to bf16 as operands of the second product (2^-9 of each term);
  * scores, sums and the running maximum are fp32.
  *
  * workspace: gdn_attn_workspace_bytes(...) bytes of device memory, 256-byte aligned, not shared with
- * concurrent calls, or NULL for the library's own (shared by the calls on a device, as for
- * gdn_ssm_scan).  With a workspace the call allocates nothing and can be captured into a CUDA graph.
+ * concurrent calls, or NULL for the library's own, of which each of up to 16 streams has one (another takes
+ * over the one longest unused, and synchronises the device for it), so that calls on different streams may
+ * overlap.  With a workspace the call allocates nothing and can be captured into a CUDA graph; without one
+ * the capture of a gdn_attn_step, and of a device's first call, is refused with GDN_ERR_SCRATCH.
  * The caller clears all of it once, before its first call; its first word collects status bits, and
  * gdn_device_status reports those of the library's own.
  */

@@ -130,3 +130,111 @@ def test_attention_keys_that_are_not_finite(gdn):
         assert bool(rest.isfinite().all())
     assert bool(torch.isfinite(lse[:, :2]).all())
     assert torch.equal(out[640:], want[640:])  # (tiles far from the edge of what sees it)
+
+
+# ---- the library's own workspaces ----------------------------------------------------------------
+
+def step_of(gdn, g, lens, Hq, Hkv, d, page=16):
+    """A step's call without a workspace, its output and what that has to be."""
+    W = -(-max(lens) // page)
+    kc, vc = rnd(g, W * len(lens), Hkv, page, d), rnd(g, W * len(lens), Hkv, page, d)
+    table = torch.randperm(W * len(lens), generator=g).to(I32).cuda().reshape(len(lens), W)
+    q, n = rnd(g, len(lens), Hq, d), ints(lens)
+    out, lse = torch.empty_like(q), torch.empty(len(lens), Hq, device="cuda")
+    ws = torch.zeros(gdn.gdn_attn_workspace_bytes(len(lens), Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+    want = [x.clone() for x in gdn.attention_step(q, kc, vc, table, n, want_lse=True, workspace=ws)]
+    return (lambda **kw: gdn.attention_step(q, kc, vc, table, n, out=out, lse=lse, **kw)), out, lse, want
+
+
+def test_steps_on_streams_at_once_without_a_workspace(gdn):
+    # few CTAs each, so that they run beside one another, with parts of their own that share no counter
+    g = gen(5)
+    cases = [step_of(gdn, g, [n], 8, 1, 128) for n in (4000, 2500, 900, 3300)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(20):
+        torch.cuda.synchronize()
+        wrong = []
+        for s in streams:
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(400_000)
+        for _ in range(8):
+            for s, (call, out, lse, want) in zip(streams, cases):
+                with torch.cuda.stream(s):
+                    out.fill_(7)
+                    call()
+                    wrong.append((out != want[0]).any() | (lse != want[1]).any())
+        torch.cuda.synchronize()
+        assert not any(bool(w) for w in wrong)
+    for call, out, lse, want in cases:  # and afterwards, one by one
+        call()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_steps_on_more_streams_than_have_a_workspace(gdn):
+    g = gen(6)
+    cases = [step_of(gdn, g, lens, 4, 2, 64) for lens in ([1500], [40] * 700, [300, 2000])]  # (the second wants more room)
+    streams = [torch.cuda.Stream() for _ in range(20)]
+    raw = {s.cuda_stream for s in streams}
+    assert len(raw) == 20
+    torch.cuda.synchronize()
+    for turn in range(4):
+        for i, s in enumerate(streams):
+            call, out, lse, want = cases[(i + turn) % 3]
+            with torch.cuda.stream(s):
+                out.fill_(7)
+                call()
+            s.synchronize()
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    gdn.gdn_release_workspace()
+    for call, out, lse, want in cases:
+        call()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert gdn.gdn_device_status() == (0, 0)
+
+
+def test_bad_blocks_on_any_stream_are_reported(gdn):
+    g = gen(7)
+    kc, vc = rnd(g, 4, 1, 16, 64), rnd(g, 4, 1, 16, 64)
+    q, n, table = rnd(g, 1, 2, 64), ints([40]), ints([[0, 4, 1]])
+    gdn.gdn_device_status()
+    for s in (torch.cuda.current_stream(), torch.cuda.Stream(), torch.cuda.Stream()):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            gdn.attention_step(q, kc, vc, table, n)
+        assert gdn.gdn_device_status() == (0, gdn.GDN_STATUS_BAD_PAGE) and gdn.gdn_device_status() == (0, 0)
+
+
+def test_a_step_without_a_workspace_is_not_captured(gdn):
+    g = gen(8)
+    call, out, lse, want = step_of(gdn, g, [700], 4, 2, 64)
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out.fill_(3)
+        with pytest.raises(gdn.GdnError, match=str(gdn.GDN_ERR_SCRATCH)):
+            call()
+    graph.replay()
+    assert bool((out == 3).all())
+    call()
+    assert torch.equal(out, want[0])
+
+
+def test_a_prompt_without_a_workspace_is_captured_after_the_first_call(gdn):
+    g = gen(9)
+    q, k, v = rnd(g, 300, 4, 64), rnd(g, 300, 2, 64), rnd(g, 300, 2, 64)
+    out = torch.empty_like(q)
+    gdn.gdn_release_workspace()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out.fill_(3)
+        with pytest.raises(gdn.GdnError, match=str(gdn.GDN_ERR_SCRATCH)):
+            gdn.attention(q, k, v, out=out)
+    want = gdn.attention(q, k, v)[0]
+    step_of(gdn, g, [40] * 3000, 4, 2, 64)[0]()  # (a large step moves nothing that the graph holds)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.attention(q, k, v, out=out)
+    step_of(gdn, g, [40] * 6000, 4, 2, 64)[0]()
+    out.fill_(7)
+    graph.replay()
+    assert torch.equal(out, want)
