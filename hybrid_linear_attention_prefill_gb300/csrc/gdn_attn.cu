@@ -1,7 +1,27 @@
 // Attention of prompts: the kernel for the width of a head (gdn_attn_tile.cuh).
+#include <atomic>
+
+#include "../../include/gdn.h"
 #include "gdn_attn.cuh"
+#include "gdn_internal.h"
 
 namespace gdn {
+
+namespace {
+std::atomic<int> g_base_said{0};
+}  // namespace
+
+cudaError_t attn_smem_base(int* bytes) {
+  static std::atomic<int> known[64] = {};
+  int dev = 0;
+  cudaError_t e;
+  if ((*bytes = g_base_said.load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if (dev < 64 && (*bytes = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(bytes, cudaDevAttrReservedSharedMemoryPerBlock, dev);
+  if (e == cudaSuccess && dev < 64) known[dev].store(*bytes, std::memory_order_relaxed);
+  return e;
+}
 
 template <int kQuarters>
 cudaError_t launch_attn_tiles(const attn::PromptArgs& a, int* status, cudaStream_t st);
@@ -16,3 +36,5 @@ cudaError_t launch_attn(const attn::PromptArgs& a, int* status, cudaStream_t st)
 }
 
 }  // namespace gdn
+
+extern "C" int gdn_debug_attn_smem_base(int bytes) { return gdn::g_base_said.exchange(bytes > 0 ? bytes : 0); }

@@ -57,7 +57,7 @@ constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns: two score tiles of 
 constexpr int kItemSlots = 4;
 constexpr long long kPatience = 1LL << 34;  // clocks of a wait, about eight seconds; then it gives up
 // Where a CTA's dynamic shared memory starts in its window, behind the KiB that the system keeps: known here so that the
-// descriptors of the products are constants, and looked at by every CTA.
+// descriptors of the products are constants, asked for by the host before a launch, and looked at by every CTA.
 constexpr uint32_t kSmemBase = 1024;
 constexpr float kLazy = 8.f;           // how far (log2) a maximum may be above the one in use
 
@@ -976,8 +976,11 @@ cudaError_t launch_attn_tiles(const attn::PromptArgs& a, int* status, cudaStream
   const int rows_heads = 128 % G != 0 ? 1 : G < 32 ? G : 32;
   if (!head_map(&out, a.out, (long long)a.Hq * a.d, a.Hq, a.d, nq, rows_heads, 32 / rows_heads, 32))
     return cudaErrorInvalidValue;
-  const cudaError_t e = set_smem_limit_once<gdn_attn_tile_kernel<kQuarters>>(Cfg<kQuarters>::kSmem);
+  cudaError_t e = set_smem_limit_once<gdn_attn_tile_kernel<kQuarters>>(Cfg<kQuarters>::kSmem);
   if (e != cudaSuccess) return e;
+  int base = 0;
+  if ((e = attn_smem_base(&base)) != cudaSuccess) return e;
+  if (base != (int)kSmemBase) return cudaErrorNotSupported;
   float c = a.scale * attn::kLog2e;
   const int negate = c < 0.f;  // as the sign of the queries
   c = std::max(negate ? -c : c, 0x1p-126f);  // (unseen scores are minus infinity, and 0 times that would not do)

@@ -44,4 +44,8 @@ struct AttnOwn {
 };
 int own_attn_workspace(int dev, size_t need, cudaStream_t st, AttnOwn& own);
 
+// Where a kernel's dynamic shared memory starts on the current device, if it has no other: the bytes that the system keeps
+// before it, or what gdn_debug_attn_smem_base says.
+cudaError_t attn_smem_base(int* bytes);
+
 }  // namespace gdn

@@ -61,7 +61,7 @@ EXPORTED = ("gdn_abi_version", "gdn_strerror", "gdn_last_cuda_error", "gdn_prefi
             "gdn_device_status", "gdn_selftest_wait_timeout", "gdn_selftest_static_wait_timeout",
             "gdn_debug_fail_allocations", "gdn_conv", "gdn_conv_step", "gdn_ssm_scan", "gdn_ssm_workspace_bytes",
             "gdn_debug_ssm_wait_polls", "gdn_ssm_step", "gdn_add_norm", "gdn_cache_plan", "gdn_cache_append", "gdn_attn",
-            "gdn_attn_workspace_bytes", "gdn_attn_step")
+            "gdn_attn_workspace_bytes", "gdn_attn_step", "gdn_debug_attn_smem_base")
 
 _lock = threading.Lock()
 _lib = None
@@ -134,6 +134,8 @@ def load(build_if_missing: bool = False):
         lib.gdn_debug_ssm_wait_polls.restype = i
         lib.gdn_ssm_workspace_bytes.argtypes = [i] * 7
         lib.gdn_ssm_workspace_bytes.restype = ctypes.c_size_t
+        lib.gdn_debug_attn_smem_base.argtypes = [i]
+        lib.gdn_debug_attn_smem_base.restype = i
         lib.gdn_attn_workspace_bytes.argtypes = [i] * 4
         lib.gdn_attn_workspace_bytes.restype = ctypes.c_size_t
         for name in ("gdn_conv", "gdn_conv_step", "gdn_ssm_scan", "gdn_ssm_step", "gdn_add_norm", "gdn_cache_plan",
@@ -255,6 +257,11 @@ def gdn_debug_fail_allocations(count) -> int:
 def gdn_debug_ssm_wait_polls(polls) -> int:
     """How often a wait of the selective scan's kernels looks before it gives up; returns the limit before."""
     return load().gdn_debug_ssm_wait_polls(int(polls))
+
+
+def gdn_debug_attn_smem_base(nbytes) -> int:
+    """Test hook: what gdn_attn takes a device to keep of a block's shared memory (0: what it says); the setting before."""
+    return load().gdn_debug_attn_smem_base(int(nbytes))
 
 
 def gdn_release_workspace() -> None:

@@ -659,6 +659,14 @@ typedef struct gdn_attn_args {
 } gdn_attn_args;
 int gdn_attn(const gdn_attn_args *args);
 
+/*
+ * gdn_debug_attn_smem_base -- test hook: gdn_attn's kernels are made for devices whose system keeps 1,024
+ * bytes of a block's shared memory, and the call is refused elsewhere (GDN_ERR_LAUNCH, before anything is
+ * launched).  With bytes > 0 the library takes that for what the device says, until a call with 0.  Returns
+ * what was set before.  Needs no GPU.
+ */
+int gdn_debug_attn_smem_base(int bytes);
+
 /* Bytes of workspace that gdn_attn and gdn_attn_step need for these sizes on the current device, whatever
  * the lengths (0 on bad arguments). */
 size_t gdn_attn_workspace_bytes(int B, int Hq, int Hkv, int d);

@@ -238,3 +238,22 @@ def test_a_prompt_without_a_workspace_is_captured_after_the_first_call(gdn):
     out.fill_(7)
     graph.replay()
     assert torch.equal(out, want)
+
+
+# ---- devices that prompts' kernels are not made for ------------------------------------------------
+
+def test_another_start_of_shared_memory_is_refused(gdn):
+    g = gen(10)
+    q, k, v = rnd(g, 100, 4, 64), rnd(g, 100, 2, 64), rnd(g, 100, 2, 64)
+    out, lse = torch.full_like(q, 3), torch.full((100, 4), 3.0, device="cuda")
+    assert gdn.gdn_debug_attn_smem_base(2048) == 0
+    try:
+        with pytest.raises(gdn.GdnError, match=str(gdn.GDN_ERR_LAUNCH)):
+            gdn.attention(q, k, v, out=out, lse=lse)
+    finally:
+        assert gdn.gdn_debug_attn_smem_base(0) == 2048
+    assert bool((out == 3).all()) and bool((lse == 3).all()) and gdn.gdn_device_status() == (0, 0)
+    assert gdn.gdn_debug_attn_smem_base(1024) == 0  # what it is
+    want = gdn.attention(q, k, v, out=out)[0].clone()
+    assert gdn.gdn_debug_attn_smem_base(0) == 1024
+    assert torch.equal(gdn.attention(q, k, v)[0], want) and bool(want.isfinite().all())
