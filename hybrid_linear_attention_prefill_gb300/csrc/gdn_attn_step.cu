@@ -22,9 +22,12 @@
 // tokens 17.3 us, 13.0 since; of 4,096, whose units divide, 12.2 and 12.5, on the device).  More than 16 heads of a key
 // head are taken 16 at a time.
 //
+// Over a bf16 cache a weight is two bf16 operands, its upper 16 bits and what they leave: 2^-16 of it is lost, not the 2^-9
+// of one operand, and the tensor cores, which wait for bytes, take the second product in their stride.
+//
 // A running maximum stays in use until a score is 2^8 above it (as for prompts), so that a step needs a vote and no
 // exchange.  With an 8-bit cache the products are of fp16: every e4m3 value is one; the queries are scaled by a power
-// of two a head to fit; weights are rounded to 11 bits instead of 8.  fp16 loses bits below 2^-14, so the weights are
+// of two a head to fit; weights are rounded to 11 bits, next to the values' 4.  fp16 loses bits below 2^-14, so the weights are
 // held relative to 2^-7 of the maximum: up to 2^15 then, and each is off by 2^-25, 2^-32 of their sum, at most.
 //
 // Measured on one GB300, L2 flushed between calls: 128 ragged requests (1.16 GB of keys and values) 199 us, of which 18
@@ -109,6 +112,12 @@ __device__ __forceinline__ void widen_e4m3(uint32_t x, uint32_t& lo, uint32_t& h
       "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
       : "=r"(lo), "=r"(hi)
       : "r"(x));
+}
+
+// What is left of a weight without its lower 16 bits.  A weight above 0 leaves something above 0, so that an infinity among
+// the values stays one.
+__device__ __forceinline__ float cut_off(float w) {
+  return fmaxf(w - __uint_as_float(__float_as_uint(w) & 0xffff0000u), fminf(w, 0x1p-126f));
 }
 
 // A warp's ring: kRing times kPer blocks of 16 keys and their values.  A row is padded or its 16-byte pieces are permuted, so that
@@ -441,7 +450,7 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
               }
             }
         }
-        uint32_t p[R::kPer][NT][2];
+        uint32_t p[R::kPer][NT][2], rest[R::kPer][NT][2];  // weights, and with bf16 what their rounding leaves
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const float base[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
@@ -453,8 +462,15 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
               w[k] = ex2_approx(s[x][t][k] - base[k & 1]);
               l[t][k & 1] += w[k];
             }
-            p[x][t][0] = transposed(E4M3 ? pack_f16(w[0], w[1]) : pack_bf16(w[0], w[1]));
-            p[x][t][1] = transposed(E4M3 ? pack_f16(w[2], w[3]) : pack_bf16(w[2], w[3]));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              if constexpr (E4M3) {
+                p[x][t][k] = transposed(pack_f16(w[2 * k], w[2 * k + 1]));
+              } else {
+                p[x][t][k] = transposed(__byte_perm(__float_as_uint(w[2 * k]), __float_as_uint(w[2 * k + 1]), 0x7632));
+                rest[x][t][k] = transposed(pack_bf16(cut_off(w[2 * k]), cut_off(w[2 * k + 1])));
+              }
+            }
           }
         }
         const int v_row = (lane & 7) + (lane >> 4) * 8, v_piece = lane >> 3 & 1;
@@ -476,7 +492,10 @@ gdn_attn_step_kernel(const StepArgs a, int groups, int heads, float scale_log2, 
               }
             } else {
 #pragma unroll
-              for (int t = 0; t < NT; ++t) mma_bf16(o[t][j], r, p[x][t][0], p[x][t][1]);
+              for (int t = 0; t < NT; ++t) {
+                mma_bf16(o[t][j], r, p[x][t][0], p[x][t][1]);
+                mma_bf16(o[t][j], r, rest[x][t][0], rest[x][t][1]);
+              }
             }
           }
       }

@@ -682,7 +682,7 @@ size_t gdn_attn_workspace_bytes(int B, int Hq, int Hkv, int d);
  *
  * A block outside [0, blocks) counts as unseen and sets GDN_STATUS_BAD_PAGE; the table's entries behind
  * a request's blocks are not read.  What the cache holds in places that are not seen changes nothing.
- * Weights are rounded to the operands' 16-bit format, as in gdn_attn.
+ * Weights keep 16 bits over a bf16 cache, 11 over an e4m3 one.
  */
 typedef struct gdn_attn_step_args {
   const void *q;

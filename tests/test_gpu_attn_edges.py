@@ -257,3 +257,49 @@ def test_another_start_of_shared_memory_is_refused(gdn):
     want = gdn.attention(q, k, v, out=out)[0].clone()
     assert gdn.gdn_debug_attn_smem_base(0) == 1024
     assert torch.equal(gdn.attention(q, k, v)[0], want) and bool(want.isfinite().all())
+
+
+# ---- one token: what the weights keep -----------------------------------------------------------
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d,window,sinks", [([3000] * 3, 8, 2, 128, 0, 0), ([700, 41, 2048], 20, 1, 64, 0, 0),
+                                                        ([900, 1500], 4, 4, 80, 300, 5)])
+def test_step_weights_over_a_bf16_cache(gdn, lens, Hq, Hkv, d, window, sinks):
+    """A weight is 2^-16 of it off at most as two operands (the upper 16 bits and the rest, cut and rounded to 8), besides
+    the fp32 rounding that `bound` is for: an output is its own rounding to bf16, 2^-8, and that."""
+    g = gen(d)
+    W = -(-max(lens) // 32)
+    kc, vc = rnd(g, W * len(lens), Hkv, 32, d), rnd(g, W * len(lens), Hkv, 32, d)
+    table = torch.randperm(W * len(lens), generator=g).reshape(len(lens), W)
+    q = rnd(g, len(lens), Hq, d)
+    out, lse = gdn.attention_step(q, kc, vc, ints(table.tolist()), ints(lens), window=window, sinks=sinks, want_lse=True)
+    for b, n in enumerate(lens):
+        k, v = (R.paged(n64(c), table[b].tolist(), n) for c in (kc, vc))
+        y, mag, l, bound = R.attend(n64(q[b:b + 1]), k, v, d ** -0.5, window, sinks)
+        err, tol = np.abs(n64(out[b:b + 1]) - y), 2.0 ** -8 * np.abs(y) + (2.0 ** -16 + 2 * bound) * mag
+        assert np.all(err <= tol), np.max(err / tol)
+        close_lse(lse[b:b + 1], l, bound)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_step_infinities_that_are_seen(gdn, e4m3):
+    """An infinity among the values is one in the output, whatever of its weight the operands hold; two signs are NaN."""
+    g = gen(11)
+    kc, vc = rnd(g, 8, 1, 16, 64), rnd(g, 8, 1, 16, 64)
+    q = rnd(g, 2, 8, 64)
+    one = [torch.ones(1, device="cuda")] * 2 if e4m3 else []
+    vc[1, 0, 3, 5], vc[2, 0, 1, 5], vc[5, 0, 0, 7] = INF, -INF, -INF
+    kc[6] = 0  # weights of a power of two, that one operand holds
+    q[1] = 0
+    vc[6, 0, 2, 9], vc[7, 0, 15, 9] = INF, INF
+    if e4m3:  # (which has no infinities, only NaN)
+        kc, vc = (c.to(torch.float8_e4m3fn) for c in (kc, vc))
+    out, lse = gdn.attention_step(q, kc, vc, ints([list(range(8))] * 2), ints([128, 128]), *one, want_lse=True)
+    if e4m3:
+        want = vc.float().isnan().any(0).any(1).expand(2, 8, 64)
+        assert torch.equal(out.isnan(), want) and bool(out.isfinite()[~want].all())
+    else:
+        assert bool(out[:, :, 5].isnan().all()) and bool(torch.isneginf(out[:, :, 7]).all())
+        assert bool(torch.isposinf(out[:, :, 9]).all())
+        keep = [c for c in range(64) if c not in (5, 7, 9)]
+        assert bool(out[:, :, keep].isfinite().all())
+    assert bool(lse.isfinite().all())
