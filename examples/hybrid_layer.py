@@ -34,7 +34,7 @@ def project(q, scales, w):
 class Layer:
     """What all kinds share: the norm, and the projections in (`channels`, and some beside them) and out."""
 
-    def __init__(self, gen, extra):
+    def __init__(self, gen, extra, conv=True):
         def w(*shape, scale):
             return (torch.randn(shape, generator=gen) * scale).to(BF16).cuda()
 
@@ -44,8 +44,9 @@ class Layer:
         width = -(-(self.channels + extra) // 8) * 8  # token strides are multiples of 8 elements
         self.w_in = w(width, HIDDEN, scale=HIDDEN ** -0.5)
         self.w_out = w(HIDDEN, HV * DV, scale=(HV * DV) ** -0.5)
-        self.conv_w = w(self.channels, K, scale=K ** -0.5)  # (the attention layer has no convolution)
-        self.conv_b = w(self.channels, scale=0.1)
+        if conv:
+            self.conv_w = w(self.channels, K, scale=K ** -0.5)
+            self.conv_b = w(self.channels, scale=0.1)
 
     def enter(self, h, residual):
         q, scales, residual = gdn.add_norm(h, self.norm, residual, eps=EPS, e4m3=True)
@@ -118,7 +119,7 @@ class AttentionLayer(Layer):
     """HV query heads over HK key heads, within a window and the first tokens, over a paged cache."""
 
     def __init__(self, gen):
-        super().__init__(gen, 0)
+        super().__init__(gen, 0, conv=False)
 
     def split(self, c):
         n = HV * DK

@@ -102,7 +102,6 @@ struct Item {
   int sinks;     // tiles of keys with sinks
   int a[2], z[2];  // tiles of keys [a, z) that either tile of queries sees otherwise
   int lo_all[2], hi_all[2];  // places from `lo` on that all of a tile's queries see
-  __device__ __forceinline__ bool has(int t, int kt) const { return (kt < sinks && z[t] > 0) || (kt >= a[t] && kt < z[t]); }
   __device__ __forceinline__ int count(int t) const { return z[t] > 0 ? sinks + z[t] - a[t] : 0; }
   __device__ __forceinline__ int place(int key) const { return key - lo + sink; }  // of a key from `lo` on
 };
@@ -132,18 +131,6 @@ __device__ __forceinline__ void find_keys(Item& it, const View& view, int tpt) {
 
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// Whether a phase has passed, without waiting for it.
-__device__ __forceinline__ bool passed(uint64_t* bar, uint32_t par) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(par)
-      : "memory");
-  return done != 0;
 }
 
 // The two warps of a row's threads at barrier `id`: together, and whether any thread of them has `x`.
@@ -516,11 +503,11 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   auto warp_wait = [&](uint64_t* bar, uint32_t par, int bit) {
     return __all_sync(0xffffffffu, wait(bar, par, bit)) != 0;
   };
-  // The n-th item of this CTA (one thread of a warp waits for the others' sake where `alone`).
+  // The n-th item of this CTA.
   auto item_at = [&](int n) { return reinterpret_cast<const Item*>(sm + C::kOffItem + (n % kItemSlots) * 128); };
   auto item_par = [](int n) { return (uint32_t)(n / kItemSlots) & 1u; };
 
-  // The launch's 128 registers a thread are dealt out anew (4 x 104 + 64 = 5 x 96).
+  // The launch's 96 registers a thread are dealt out anew (16 warps x 104 + 4 x 64 = 20 x 96).
   if (warp >= kMmaWarp) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
   if (warp == kItemWarp) {
@@ -727,7 +714,9 @@ gdn_attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 const uint64_t k = tc::sdesc(sb + C::kOffK + S * kTile, 16, 1024, tc::kSw128);
                 tc::fence_after();
 #pragma unroll
-                for (int i = 0; i < 2 * kQuarters; ++i) {  // (a step under a run-time condition was compiled wrong)
+                for (int i = 0; i < 2 * kQuarters; ++i) {
+                  // (A constant number of steps.  With each under a condition of its own, i below a run-time count, those
+                  // past the fourth were built to multiply an earlier step's queries; why is not known.)
                   const uint64_t off = (uint64_t)(((i >> 2) * kHalf + (i & 3) * 32) >> 4);
                   tc::mma_bf16(kColS + t * 128, q + off, k + off, id_s, i > 0);
                   // the other warp's turn, so that its products are there when these end
