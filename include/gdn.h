@@ -636,7 +636,8 @@ int gdn_cache_append(const gdn_cache_append_args *args);
  * concurrent calls, or NULL for the library's own, of which each of up to 16 streams has one (another takes
  * over the one longest unused, and synchronises the device for it), so that calls on different streams may
  * overlap.  With a workspace the call allocates nothing and can be captured into a CUDA graph; without one
- * the capture of a gdn_attn_step, and of a device's first call, is refused with GDN_ERR_SCRATCH.
+ * the capture of a gdn_attn_step, and of a device's first call, is refused with GDN_ERR_SCRATCH (a graph of
+ * a gdn_attn without one holds the library's status words, which gdn_release_workspace frees).
  * The caller clears all of it once, before its first call; its first word collects status bits, and
  * gdn_device_status reports those of the library's own.
  */

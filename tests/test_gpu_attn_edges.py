@@ -3,6 +3,8 @@
 Tolerances are those of test_gpu_attn.py.
 """
 
+import threading
+
 import numpy as np
 import pytest
 
@@ -143,7 +145,7 @@ def step_of(gdn, g, lens, Hq, Hkv, d, page=16):
     out, lse = torch.empty_like(q), torch.empty(len(lens), Hq, device="cuda")
     ws = torch.zeros(gdn.gdn_attn_workspace_bytes(len(lens), Hq, Hkv, d), dtype=torch.uint8, device="cuda")
     want = [x.clone() for x in gdn.attention_step(q, kc, vc, table, n, want_lse=True, workspace=ws)]
-    return (lambda **kw: gdn.attention_step(q, kc, vc, table, n, out=out, lse=lse, **kw)), out, lse, want
+    return (lambda **kw: gdn.attention_step(q, kc, vc, table, n, **{"out": out, "lse": lse, **kw})), out, lse, want
 
 
 def test_steps_on_streams_at_once_without_a_workspace(gdn):
@@ -238,6 +240,87 @@ def test_a_prompt_without_a_workspace_is_captured_after_the_first_call(gdn):
     out.fill_(7)
     graph.replay()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("own_streams", [False, True])
+def test_steps_from_threads_at_once_without_a_workspace(gdn, own_streams):
+    """Threads whose calls want ever more room: what one enlarges, another may be about to use."""
+    g = gen(12)
+    sizes = ([9], [30] * 900, [2000], [20] * 2500, [700] * 3, [5] * 5000)
+    cases = [step_of(gdn, g, lens, 4, 2, 64) for lens in sizes]
+    gdn.gdn_release_workspace()
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream() if own_streams else torch.cuda.default_stream()
+            with torch.cuda.stream(s):
+                for n in range(12):
+                    q_call, _, _, want = cases[(i + n) % len(cases)]
+                    out = torch.empty_like(want[0])
+                    got, _ = q_call(out=out if n % 2 else None, lse=None)
+                    s.synchronize()
+                    if not (torch.equal(got, want[0])):
+                        wrong.append((i, n))
+        except Exception as e:  # noqa: BLE001  (said by the assertion below)
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == []
+    assert gdn.gdn_device_status() == (0, 0)
+
+
+# ---- the smallest calls --------------------------------------------------------------------------
+
+def test_calls_with_nothing_in_them(gdn):
+    g = gen(13)
+    none = ints([]).reshape(2, 0)
+    cache = torch.empty(0, 2, 16, 64, dtype=BF, device="cuda")
+    for lens in ([0, 0], [-5, 0], [40, 3]):  # no columns, no blocks: nothing is seen
+        for given in (False, True):
+            out = torch.full((2, 4, 64), 3, dtype=BF, device="cuda") if given else None
+            out, lse = gdn.attention_step(rnd(g, 2, 4, 64), cache, cache, none, ints(lens), out=out, want_lse=True)
+            assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+    q = rnd(g, 0, 4, 64)
+    assert gdn.attention(q, q[:, :2], q[:, :2])[0].shape == (0, 4, 64)
+    assert gdn.attention(q, q[:, :2], q[:, :2], ints([0, 0, 0]), want_lse=True)[1].shape == (0, 4)
+    assert gdn.attention_step(q, cache, cache, ints([]).reshape(0, 3), ints([]))[0].shape == (0, 4, 64)
+    gdn.cache_append(q[:, :2], q[:, :2], cache, cache, ints([]))
+    gdn.cache_append(rnd(g, 3, 2, 64), rnd(g, 3, 2, 64), cache, cache, ints([0, 1, 2]))  # nowhere to go
+    out = torch.full((5, 4, 64), 3, dtype=BF, device="cuda")
+    gdn.attention(rnd(g, 5, 4, 64), rnd(g, 5, 2, 64), rnd(g, 5, 2, 64), ints([0, 0, 0]), out=out)  # no sequence has any
+    assert bool((out == 3).all()) and gdn.gdn_device_status() == (0, 0)
+
+
+def test_a_step_with_more_tokens_than_columns(gdn):
+    g = gen(14)
+    kc, vc = rnd(g, 9, 2, 16, 64), rnd(g, 9, 2, 16, 64)
+    q, table = rnd(g, 1, 4, 64), [[4, 0, 7]]
+    out, lse = gdn.attention_step(q, kc, vc, ints(table), ints([2 ** 31 - 1]), want_lse=True)
+    want, want_lse = gdn.attention_step(q, kc, vc, ints(table), ints([48]), want_lse=True)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 1, 0), (1, 2 ** 31 - 1), (0, 2 ** 31 - 1)])
+def test_the_largest_windows_and_sinks(gdn, window, sinks):
+    g = gen(15)
+    q, k, v = rnd(g, 300, 4, 64), rnd(g, 300, 2, 64), rnd(g, 300, 2, 64)
+    want, want_lse = gdn.attention(q, k, v, want_lse=True)  # all of them see everything before them
+    out, lse = gdn.attention(q, k, v, window=window, sinks=sinks, want_lse=True)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    kc, vc = (t[:288].unflatten(0, (18, 16)).transpose(1, 2).contiguous() for t in (k, v))
+    table, n = ints([list(range(18))]), ints([288])
+    want, want_lse = gdn.attention_step(q[:1], kc, vc, table, n, want_lse=True)
+    out, lse = gdn.attention_step(q[:1], kc, vc, table, n, window=window, sinks=sinks, want_lse=True)
+    y, mag, l, bound = R.attend(n64(q[:1]), n64(k[:288]), n64(v[:288]), 64 ** -0.5)
+    for o, s in ((out, lse), (want, want_lse)):
+        close(o, y, mag, bound)
+        close_lse(s, l, bound)
 
 
 # ---- devices that prompts' kernels are not made for ------------------------------------------------
