@@ -10,8 +10,8 @@
 // The ring keeps 128 KB of an SM on their way whatever the products do, and a warp meets no other until its sequence
 // ends; a block's place in the cache is looked up by a lane for 32 blocks at a time.  (Loads straight into registers
 // kept as many bytes on their way with bf16, half as many with e4m3, whose products also took twice the instructions:
-// 160 us for 32 long requests over an 8-bit cache, 111 now.)  With an 8-bit cache two blocks are taken together, since the
-// chain of one block's steps, not the bytes, bound it (136 us).
+// 160 us for 32 long requests over an 8-bit cache where the ring took 111.)  With an 8-bit cache two blocks are taken
+// together, since the chain of one block's steps, not the bytes, bound it (136 us where two took 111).
 //
 // Work.  A unit is 64 keys, 16 for each warp of a CTA.  The units of all sequences and key heads, one after the
 // other, are dealt out in equal runs to as many CTAs as are resident, whatever the lengths; a warp keeps its own
@@ -30,10 +30,10 @@
 // of two a head to fit; weights are rounded to 11 bits, next to the values' 4.  fp16 loses bits below 2^-14, so the weights are
 // held relative to 2^-7 of the maximum: up to 2^15 then, and each is off by 2^-25, 2^-32 of their sum, at most.
 //
-// Measured on one GB300, L2 flushed between calls: 128 ragged requests (1.16 GB of keys and values) 199 us, of which 18
-// are the flushed lines' way out (184 without), 6.3 TB/s; 32 long requests over an 8-bit cache (531 MB) 97 us without,
-// 5.5 TB/s; a window of 1,024 for 128 requests (541 MB) 91 us.  A call costs about 12 us beside its bytes: launch, three
-// dependent first reads (lengths, table, keys), the last join.  One request of 4,096 tokens takes 17 us (32 parts a head).
+// Measured on one GB300, L2 cold, call after call: 128 ragged requests (1.16 GB of keys and values) 182 us, 6.4 TB/s; 32
+// long requests over an 8-bit cache (531 MB) 91.5 us, 5.8 TB/s; a window of 1,024 for 128 requests (541 MB) 90.8 us; one
+// request of 4,096 tokens 12.3 us (32 parts a head).  A call costs about 12 us beside its bytes: launch, three dependent
+// first reads (lengths, table, keys), the last join.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 

@@ -22,11 +22,12 @@
 // What bounds it, measured on one GB300 (d = 128, clocks of an SM): a pair of key tiles takes 3,200 where its products
 // take 2,048.  A tile's round is a chain: its scores into registers 330, maxima and the vote 550, the rest of the weights
 // 350, the issuing warp's look at the barrier 300, the products 1,100 beside the other tile's, and the two tiles' chains
-// fill the tensor core to 0.60 between them (16,381 tokens, 16 heads over 2: 750 us, 1,460 TFLOP/s).  An item costs
-// another 10,000: its last product, the output's way out and the next one's first tile follow one another in the same
-// warps, so a window of 1,024 (nine tiles an item) runs at 910 TFLOP/s.  Steps that brought it here, for 16,381 tokens:
-// one thread a row and one issuing warp 1,025; scores held in registers, descriptors as constants, two issuing warps in
-// turns 967; two threads a row 770; output through copies 760; what is seldom run out of the loops' way 750.
+// fill the tensor core to 0.60 between them (16,381 tokens, 16 heads over 2: 787 us, 1,400 TFLOP/s, call after call,
+// when the clock falls to 1.75 GHz; 745 with pauses).  An item costs another 10,000: its last product, the output's way
+// out and the next one's first tile follow one another in the same warps, so a window of 1,024 (nine tiles an item) runs
+// at 880 TFLOP/s.  Steps that brought it here, for 16,381 tokens with pauses: one thread a row and one issuing warp
+// 1,025; scores held in registers, descriptors as constants, two issuing warps in turns 967; two threads a row 770; output
+// through copies 760; what is seldom run out of the loops' way 750.
 //
 // A value that is not finite in a place that a row does not see would reach the row as 0 x infinity.
 // So a finished row that is not finite is looked into, and worked out again from the keys it sees alone where the
