@@ -280,8 +280,8 @@ int gdn_prefill_static(const void *q, const void *k, const void *v,
  * gdn_prefill_ws the word is the first 4 bytes of the caller's workspace; with
  * gdn_prefill_static it is the first word of the fixed array.
  */
-#define GDN_STATUS_MMA_TIMEOUT 1       /* the state-carry kernel gave up waiting for an MMA phase */
-#define GDN_STATUS_LOAD_TIMEOUT 2      /* the state-carry kernel gave up waiting for a tile load */
+#define GDN_STATUS_MMA_TIMEOUT 1       /* the state-carry kernel (or gdn_ssm_scan's, gdn_attn's) gave up waiting for an MMA phase */
+#define GDN_STATUS_LOAD_TIMEOUT 2      /* the same, waiting for a tile load */
 #define GDN_STATUS_PREP_LOAD_TIMEOUT 4 /* the preparation kernel gave up waiting (tile load or Gram product) */
 #define GDN_STATUS_BAD_CU_SEQLENS 8    /* cu_seqlens was not 0 = cu[0] <= ... <= cu[B] = T (entries clamped) */
 #define GDN_STATUS_NONFINITE_STATE 16  /* a final state of the fp16 state carry was not finite (see gdn_prefill) */
